@@ -11,6 +11,9 @@ The compute lives in the CUDA library ``libgdn_qdq.so`` (C ABI in
   gdn_two_precision_fwd  two-precision profile: fp32 anchor, E4M3 read copy for outputs
   gdn_two_precision_bwd  its window-wise adjoint (straight-through read copy)
   fake_qdq_e4m3 / fake_qdq_int8   the grouped QDQ primitive
+  kv8_append / kv8_attention      8-bit paged cache of K and V, and the attention that reads it
+  kv8_fork / kv8_reserve / kv8_free / kv8_compact / kv8_copy_pages   its pages, by reference count
+  beam_select / beam_reorder      beam search: selection, and the states that follow it
 
 ``synth`` holds the seeded synthetic-input generators.
 """
@@ -21,3 +24,5 @@ from .api import (fake_qdq_e4m3, fake_qdq_int8, gdn_bwd_workspace_bytes, gdn_chu
                   make_problem, make_two_precision_problem, split_ctx)
 from ._lib import GdnError, load  # noqa: F401
 from .autograd import gdn_chunk_qdq  # noqa: F401
+from .serve import (beam_reorder, beam_select, kv8_append, kv8_attention, kv8_compact,  # noqa: F401
+                    kv8_copy_pages, kv8_fork, kv8_free, kv8_pool, kv8_reserve, kv8_workspace_bytes)

@@ -65,6 +65,37 @@ class GdnTwoPrecisionProblem(ctypes.Structure):
 
 
 _TP = ctypes.POINTER(GdnTwoPrecisionProblem)
+
+
+class GdnKv8Problem(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_int64), ("rows", ctypes.c_int64), ("total", ctypes.c_int64),
+        ("tokens", ctypes.c_int32), ("cols", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("group", ctypes.c_int32), ("dim", ctypes.c_int32), ("page", ctypes.c_int32),
+        ("mode", ctypes.c_int32), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p),
+        ("x_row", ctypes.c_int64), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+        ("v_row", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+    ]
+
+
+class GdnKv8Pool(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int32),
+        ("page", ctypes.c_int32), ("planes", ctypes.c_int32), ("heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+    ]
+
+
+class GdnBeamProblem(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("stride", ctypes.c_int64), ("beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("eos", ctypes.c_int32),
+    ]
+
+
+_KP, _KL, _BP = (ctypes.POINTER(t) for t in (GdnKv8Problem, GdnKv8Pool, GdnBeamProblem))
 SIGNATURES = {
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_abi_version": (ctypes.c_int, []),
@@ -90,6 +121,19 @@ SIGNATURES = {
     "gdn_two_precision_bwd_workspace_bytes": (_SZ, [_TP]),
     "gdn_two_precision_bwd": (ctypes.c_int, [_TP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _SZ, _P]),
+    "gdn_kv8_validate": (ctypes.c_int, [_KP]),
+    "gdn_kv8_append": (ctypes.c_int, [_KP, _P, _P, _P, _P, _P, _P, _P]),
+    "gdn_kv8_workspace_bytes": (_SZ, [_KP]),
+    "gdn_kv8_attention": (ctypes.c_int, [_KP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_kv8_pool_workspace_bytes": (_SZ, [_KL]),
+    "gdn_kv8_copy_pages": (ctypes.c_int, [_KL, _P, _P, _P, _P, _I64, _P]),
+    "gdn_kv8_fork": (ctypes.c_int, [_KL, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_kv8_reserve": (ctypes.c_int, [_KL, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_kv8_compact": (ctypes.c_int, [_KL, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_beam_validate": (ctypes.c_int, [_BP]),
+    "gdn_beam_workspace_bytes": (_SZ, [_BP]),
+    "gdn_beam_select": (ctypes.c_int, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_beam_reorder": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _P, _I64, ctypes.c_int32, _P]),
 }
 
 _lock = threading.Lock()

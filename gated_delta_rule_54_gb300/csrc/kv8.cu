@@ -1,0 +1,287 @@
+// The 8-bit paged cache: entry points, append, and attention.
+#include <math.h>
+
+#include "kv8.cuh"
+#include "launch.h"
+
+namespace gdn {
+
+namespace {
+
+// Append.  One CTA per (row, touched page, head, K or V): the new tokens of that
+// page are read once into registers (CH chunks of eight bf16 per thread), their
+// maximum is the block's, and their codes go out as 8-byte stores.  The bytes
+// are the bf16 tokens in and the codes out; the old codes of the page are read
+// and written only when the new tokens raise its scale.
+template <int MODE, int DIM, int NT, int CH>
+__global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int blocks) {
+  constexpr int C8 = DIM / 8;
+  __shared__ float red[NT / 32];
+  const int64_t r = blockIdx.x / blocks;
+  const int h = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
+  int64_t base;
+  int n;
+  kv8_row(p, r, base, n);
+  const int64_t st = p.lengths[r];
+  if (st < 0) return;
+  const int64_t b = st / p.page + blockIdx.x % blocks;
+  const int64_t lo = st > b * p.page ? st : b * p.page;
+  const int64_t hi = st + n < (b + 1) * p.page ? st + n : (b + 1) * p.page;
+  if (lo >= hi || b >= p.cols) return;
+  const int64_t id = p.table[r * p.cols + b];
+  if (id < 0 || id >= p.pages) return;
+  const int64_t tile = (kv * p.pages + id) * p.heads + h;
+  const __nv_bfloat16* x =
+      kv ? p.v + kv8_at(p, r, base, lo - st, p.v_row, p.v_token) + h * p.v_head
+         : p.x + kv8_at(p, r, base, lo - st, p.x_row, p.x_token) + h * p.x_head;
+  const int64_t step = kv ? p.v_token : p.x_token;
+  const int chunks = (int)(hi - lo) * C8, old = (int)(lo - b * p.page);
+
+  uint4 u[CH];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * NT;
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (c < chunks) u[i] = *reinterpret_cast<const uint4*>(x + (c / C8) * step + (c % C8) * 8);
+  }
+  const float was = old > 0 ? p.scales[tile] : 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    float f[8];
+    bf16x8(u[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+  }
+  m = warp_max(m);
+  if constexpr (NT > 32) {
+    if (tid % 32 == 0) red[tid / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) m = fmaxf(m, red[i]);
+  } else {
+    __syncwarp();
+  }
+  float now = fmaxf(was, __fdiv_rn(m, QdqMax<MODE>::value)), rcp = __frcp_rn(now);
+  if (isinf(rcp)) now = rcp = 0.f;
+
+  uint8_t* out = p.codes + tile * p.page * DIM;
+  if (now > was) {
+    for (int c = tid; c < old * C8; c += NT) {
+      const uint2 w = *reinterpret_cast<const uint2*>(out + c * 8);
+      const float4 a = qdq_code4_values<MODE>(w.x), e = qdq_code4_values<MODE>(w.y);
+      *reinterpret_cast<uint2*>(out + c * 8) =
+          make_uint2(kv8_code4<MODE>(__fmul_rn(a.x, was), __fmul_rn(a.y, was),
+                                     __fmul_rn(a.z, was), __fmul_rn(a.w, was), rcp),
+                     kv8_code4<MODE>(__fmul_rn(e.x, was), __fmul_rn(e.y, was),
+                                     __fmul_rn(e.z, was), __fmul_rn(e.w, was), rcp));
+    }
+  }
+  if (tid == 0 && (now != was || old == 0)) p.scales[tile] = now;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * NT;
+    if (c < chunks) {
+      float f[8];
+      bf16x8(u[i], f);
+      *reinterpret_cast<uint2*>(out + (old * C8 + c) * 8) = make_uint2(
+          kv8_code4<MODE>(f[0], f[1], f[2], f[3], rcp), kv8_code4<MODE>(f[4], f[5], f[6], f[7], rcp));
+    }
+  }
+}
+
+template <int MODE, int DIM>
+gdn_status run_append(const Kv8Params& p, cudaStream_t st) {
+  // pages that n consecutive positions can touch
+  const int blocks = (p.tokens + p.page - 2) / p.page + 1;
+  if (p.rows * blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)(p.rows * blocks), (unsigned)p.heads, 2);
+  const int chunks = (p.tokens < p.page ? p.tokens : p.page) * (DIM / 8);
+  if (chunks <= 32)
+    kv8_append_kernel<MODE, DIM, 32, 1><<<grid, 32, 0, st>>>(p, blocks);
+  else if (chunks <= 128)
+    kv8_append_kernel<MODE, DIM, 128, 1><<<grid, 128, 0, st>>>(p, blocks);
+  else if (chunks <= 512)
+    kv8_append_kernel<MODE, DIM, 128, 4><<<grid, 128, 0, st>>>(p, blocks);
+  else
+    kv8_append_kernel<MODE, DIM, 256, 8><<<grid, 256, 0, st>>>(p, blocks);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// Attention, one warp per (query token, query head), one key at a time.
+template <int MODE, int DIM>
+__global__ void __launch_bounds__(128) kv8_attention_kernel(const Kv8Params p) {
+  constexpr int PER = DIM / 32;
+  const int lane = threadIdx.x % 32, hq = p.heads * p.group;
+  const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  if (item >= p.total * hq) return;
+  const int64_t tok = item / hq;
+  const int h = (int)(item % hq), hk = h / p.group;
+  int64_t r, base;
+  int n;
+  if (p.cu) {
+    int64_t a = 0, b = p.rows - 1;
+    while (a < b) {
+      const int64_t mid = (a + b) / 2;
+      if (p.cu[mid + 1] > tok) b = mid; else a = mid + 1;
+    }
+    r = a;
+  } else {
+    r = tok / p.tokens;
+  }
+  kv8_row(p, r, base, n);
+  const int64_t i = tok - base;
+  if (i < 0 || i >= n) return;
+  const int64_t cap = (int64_t)p.cols * p.page;
+  const int64_t len = p.lengths[r], pos = len - n + i;
+  int64_t end = len < cap ? len : cap;
+  if (p.causal && pos + 1 < end) end = pos + 1;
+  int64_t begin = p.window > 0 ? pos - p.window + 1 : 0;
+  if (begin < 0) begin = 0;
+  const __nv_bfloat16* x = p.x + kv8_at(p, r, base, i, p.x_row, p.x_token) + h * p.x_head;
+  float q[PER], acc[PER];
+  for (int j = 0; j < PER; ++j) {
+    q[j] = __bfloat162float(x[lane * PER + j]) * p.scale;
+    acc[j] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int64_t j = begin; j < end; ++j) {
+    const int64_t id = p.table[r * p.cols + j / p.page];
+    if (id < 0 || id >= p.pages) continue;
+    const int64_t kt = id * p.heads + hk, vt = kt + p.pages * p.heads;
+    const uint8_t* kc = p.codes + (kt * p.page + j % p.page) * DIM + lane * PER;
+    const uint8_t* vc = p.codes + (vt * p.page + j % p.page) * DIM + lane * PER;
+    float s = 0.f;
+    for (int e = 0; e < PER; ++e) s = fmaf(q[e], qdq_code_value<MODE>(kc[e]), s);
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    s *= p.scales[kt];
+    const float top = fmaxf(m, s), a = __expf(m - top), w = __expf(s - top);
+    l = l * a + w;
+    const float vs = w * p.scales[vt];
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], a, vs * qdq_code_value<MODE>(vc[e]));
+    m = top;
+  }
+  for (int e = 0; e < PER; ++e)
+    p.o[(tok * hq + h) * DIM + lane * PER + e] = __float2bfloat16_rn(l > 0.f ? acc[e] / l : 0.f);
+  if (p.lse && lane == 0) p.lse[tok * hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+gdn_status validate_kv8(const gdn_kv8_problem* p) {
+  if (!p) return GDN_ERR_INVALID_ARG;
+  if (p->pages < 0 || p->rows < 0 || p->total < 0 || p->tokens < 0 || p->cols < 0 ||
+      p->heads <= 0 || p->group <= 0 || p->window < 0 || (p->causal != 0 && p->causal != 1))
+    return GDN_ERR_INVALID_ARG;
+  if (p->mode != GDN_QDQ_E4M3 && p->mode != GDN_QDQ_INT8)
+    return p->mode == GDN_QDQ_NONE ? GDN_ERR_UNSUPPORTED_MODE : GDN_ERR_INVALID_ARG;
+  if (p->dtype != GDN_DTYPE_BF16) {
+    if (p->dtype == GDN_DTYPE_FP16 || p->dtype == GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED_DTYPE;
+    return GDN_ERR_INVALID_ARG;
+  }
+  if (p->dim != 64 && p->dim != 128) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128)
+    return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (!p->cu_seqlens && p->total != p->rows * p->tokens) return GDN_ERR_INVALID_ARG;
+  if (p->rows == 0 && p->total > 0) return GDN_ERR_INVALID_ARG;
+  // positions are 32-bit; heads are a grid dimension; page ids are 32-bit
+  if ((int64_t)p->cols * p->page > 0x7fffffffLL || p->pages > 0x7fffffffLL ||
+      p->rows > 0x7fffffffLL || p->total > 0x7fffffffLL ||
+      (int64_t)p->heads * p->group > 65535)
+    return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (!isfinite(p->scale)) return GDN_ERR_INVALID_ARG;
+  for (const int64_t s : {p->x_row, p->x_token, p->x_head, p->v_row, p->v_token, p->v_head})
+    if (s % 8 != 0) return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
+Kv8Params params_of(const gdn_kv8_problem& p) {
+  Kv8Params k = {};
+  k.pages = p.pages, k.rows = p.rows, k.total = p.total;
+  k.x_row = p.x_row, k.x_token = p.x_token, k.x_head = p.x_head;
+  k.v_row = p.v_row, k.v_token = p.v_token, k.v_head = p.v_head;
+  k.tokens = p.tokens, k.cols = p.cols, k.heads = p.heads, k.group = p.group, k.page = p.page;
+  k.causal = p.causal, k.window = p.window, k.scale = p.scale;
+  k.cu = p.cu_seqlens;
+  return k;
+}
+
+bool off16(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if ((uintptr_t)q & 15) return true;
+  return false;
+}
+bool off4(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if ((uintptr_t)q & 3) return true;
+  return false;
+}
+
+}  // namespace
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_kv8_validate(const gdn_kv8_problem* p) { return validate_kv8(p); }
+
+size_t gdn_kv8_workspace_bytes(const gdn_kv8_problem* p) {
+  if (validate_kv8(p) != GDN_OK) return 0;
+  return 0;
+}
+
+gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v, uint8_t* codes,
+                          float* scales, const int32_t* table, const int32_t* start,
+                          void* stream) {
+  const gdn_status s = validate_kv8(p);
+  if (s != GDN_OK) return s;
+  if (p->total == 0 || p->pages == 0 || p->cols == 0 || p->tokens == 0) return GDN_OK;
+  if (!k || !v || !codes || !scales || !table || !start) return GDN_ERR_INVALID_ARG;
+  if (off16({k, v, codes}) || off4({scales, table, start, p->cu_seqlens}))
+    return GDN_ERR_MISALIGNED;
+  Kv8Params prm = params_of(*p);
+  prm.x = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  prm.codes = codes, prm.scales = scales, prm.table = table, prm.lengths = start;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p->mode == GDN_QDQ_E4M3)
+    return p->dim == 128 ? run_append<GDN_QDQ_E4M3, 128>(prm, st)
+                         : run_append<GDN_QDQ_E4M3, 64>(prm, st);
+  return p->dim == 128 ? run_append<GDN_QDQ_INT8, 128>(prm, st)
+                       : run_append<GDN_QDQ_INT8, 64>(prm, st);
+}
+
+gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint8_t* codes,
+                             const float* scales, const int32_t* table, const int32_t* lengths,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const gdn_status s = validate_kv8(p);
+  if (s != GDN_OK) return s;
+  if (p->total == 0) return GDN_OK;
+  if (!q || !o || !lengths) return GDN_ERR_INVALID_ARG;
+  if (p->pages > 0 && p->cols > 0 && (!codes || !scales || !table)) return GDN_ERR_INVALID_ARG;
+  if (off16({q, codes, o}) || off4({scales, table, lengths, lse, p->cu_seqlens}) ||
+      ((uintptr_t)workspace & 255))
+    return GDN_ERR_MISALIGNED;
+  const size_t need = gdn_kv8_workspace_bytes(p);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  Kv8Params prm = params_of(*p);
+  prm.x = static_cast<const __nv_bfloat16*>(q);
+  prm.codes = const_cast<uint8_t*>(codes), prm.scales = const_cast<float*>(scales);
+  prm.table = table, prm.lengths = lengths;
+  prm.o = static_cast<__nv_bfloat16*>(o), prm.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t warps = p->total * p->heads * p->group;
+  if (warps > 4 * 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
+  const unsigned grid = (unsigned)((warps + 3) / 4);
+  if (p->mode == GDN_QDQ_E4M3) {
+    if (p->dim == 128) kv8_attention_kernel<GDN_QDQ_E4M3, 128><<<grid, 128, 0, st>>>(prm);
+    else kv8_attention_kernel<GDN_QDQ_E4M3, 64><<<grid, 128, 0, st>>>(prm);
+  } else {
+    if (p->dim == 128) kv8_attention_kernel<GDN_QDQ_INT8, 128><<<grid, 128, 0, st>>>(prm);
+    else kv8_attention_kernel<GDN_QDQ_INT8, 64><<<grid, 128, 0, st>>>(prm);
+  }
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -435,6 +435,180 @@ gdn_status gdn_two_precision_bwd(const gdn_two_precision_problem* p, const void*
                                  float* dbeta, float* dg, float* dh0, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/*
+ * Serving beside the recurrent layers: an 8-bit paged cache of K and V, the
+ * attention that reads it, and beam search.
+ *
+ * Cache.  One layer's cache is
+ *   codes   u8  [2, pages, heads, page, dim]   0: K, 1: V
+ *   scales  f32 [2, pages, heads]              value = code * scale
+ * i.e. one scale per block of `page` tokens and head, by the quantization rule
+ * of fake_qdq_*.  A pool over layers has a leading [layers]; page ids are the
+ * same in every layer.  Row r holds lengths[r] tokens; token j lies in page
+ * table[r, j / page] at slot j % page.  Ids outside [0, pages) are never
+ * followed: a token there is not written, and as a key it does not exist.
+ * Slots past a row's length may hold anything.
+ */
+typedef struct {
+  int64_t pages;              /* pages of the cache                              */
+  int64_t rows;               /* sequences                                       */
+  int64_t total;              /* tokens of q (k, v) over all rows                */
+  int32_t tokens;             /* a row's tokens (packed: an upper bound)         */
+  int32_t cols;               /* columns of the table                            */
+  int32_t heads;              /* K/V heads                                       */
+  int32_t group;              /* query heads per K/V head (attention)            */
+  int32_t dim;                /* head dim: 64 or 128                             */
+  int32_t page;               /* tokens per page: 16, 32, 64 or 128              */
+  int32_t mode;               /* gdn_qdq_mode of the codes: E4M3 or INT8         */
+  int32_t dtype;              /* gdn_dtype of q, k, v: BF16                      */
+  int32_t causal;             /* 1: a query sees keys up to its own position     */
+  int32_t window;             /* > 0: and only the last `window` of those        */
+  float scale;                /* factor of q . k                                 */
+  const int32_t* cu_seqlens;  /* device [rows + 1] (packed), or NULL: total ==
+                                 rows * tokens                                   */
+  /* strides in elements of q (attention) or k (append), and of v (append): row
+     (ignored when packed), token, head; the last dim is contiguous.  Multiples
+     of 8 elements.                                                              */
+  int64_t x_row, x_token, x_head;
+  int64_t v_row, v_token, v_head;
+} gdn_kv8_problem;
+
+/* Host-only validation (no CUDA call). */
+gdn_status gdn_kv8_validate(const gdn_kv8_problem* p);
+
+/*
+ * Append: row r's new tokens take positions start[r] .. start[r] + n_r - 1
+ * (n_r = tokens, or cu[r + 1] - cu[r]).  Per touched (page, head), x the new
+ * tokens in it and the slots before them old:
+ *   s_old = scale if there are old slots, else 0;   a = max |x|
+ *   s = max(s_old, fl(a / M));  r = fl(1 / s)   (r infinite: s = r = 0)
+ *   code(new) = rne(fl(x r));  if s > s_old: code(old) = rne(fl(fl(code s_old) r))
+ * so a block keeps one scale while it fills; the old codes are rounded again
+ * only when a larger token arrives.  A page written here must belong to one
+ * row only (gdn_kv8_fork keeps it so).
+ *   k, v  bf16 [rows, tokens, heads, dim] or packed [total, heads, dim], strided
+ *   start i32 [rows]    table i32 [rows, cols]    codes, scales: one layer's
+ */
+gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v,
+                          uint8_t* codes, float* scales, const int32_t* table,
+                          const int32_t* start, void* stream);
+
+/*
+ * Attention over the cache.  Row r's n_r queries are the last n_r of its
+ * lengths[r] tokens (their K and V are in the cache): query i stands at
+ * position t = lengths[r] - n_r + i and sees key j in [0, lengths[r]) with
+ * j <= t (causal) and j > t - window (window > 0).  Query head h reads K/V
+ * head h / group.
+ *   o   = sum_j softmax_j(scale q . K_j) V_j        bf16
+ *   lse = log sum_j exp(scale q . K_j)              f32 (or NULL)
+ * A query that sees no key (also: t < 0) has o = 0 and lse = -inf.  Sums and
+ * softmax statistics are fp32; probabilities enter the V product in fp16.
+ *   q   bf16 [rows, tokens, heads * group, dim] or packed [total, ...], strided
+ *   o   bf16 [total, heads * group, dim] contiguous,  lse f32 [total, heads * group]
+ *   workspace  gdn_kv8_workspace_bytes(p) bytes, 256-byte aligned
+ */
+size_t gdn_kv8_workspace_bytes(const gdn_kv8_problem* p);
+
+gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint8_t* codes,
+                             const float* scales, const int32_t* table, const int32_t* lengths,
+                             void* o, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Pages.  refs[p] counts the holders of page p (rows and whatever else the
+ * caller counts); 0 = free.  A row holds the first ceil(lengths / page) pages
+ * of its table row.  A partly filled page has one holder.  All outputs are new
+ * arrays (no overlap with the inputs), table entries past a row's pages are -1,
+ * and choices are fixed: fresh pages are the lowest free ones, given in row
+ * order.  `missing` counts pages that were wanted and not there (their table
+ * entries are -1).
+ */
+typedef struct {
+  int64_t pages;        /* pages of the pool                                     */
+  int64_t rows;         /* 1 .. 4096                                             */
+  int32_t cols;         /* columns of the tables                                 */
+  int32_t page;         /* tokens per page                                       */
+  int32_t planes;       /* layers * 2                                            */
+  int32_t heads, dim;   /* a page of one plane is heads * page * dim bytes       */
+} gdn_kv8_pool;
+
+size_t gdn_kv8_pool_workspace_bytes(const gdn_kv8_pool* p);
+
+/* Copies page src[i] to page dst[i], codes and scales, in all planes.  Pages of
+ * dst are distinct and none of them is in src. */
+gdn_status gdn_kv8_copy_pages(const gdn_kv8_pool* p, uint8_t* codes, float* scales,
+                              const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* New row r takes the sequence of old row parents[r] (-1: it becomes empty);
+ * sequences that no row takes are released.  Whole pages are shared; the partly
+ * filled last page stays with the sequence's lowest new row and is copied to a
+ * fresh page for the others.  With parents NULL, drop u8 [rows] gives the rows
+ * to empty and the others keep theirs. */
+gdn_status gdn_kv8_fork(const gdn_kv8_pool* p, uint8_t* codes, float* scales,
+                        const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                        const int32_t* parents, const uint8_t* drop, int32_t* table_out,
+                        int32_t* lengths_out, int32_t* refs_out, int32_t* missing, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Room for extra[r] more tokens of each row: lengths_out = lengths + extra, and
+ * fresh pages for what no page of the row holds yet (extra < 0 counts as 0; no
+ * row grows past cols * page tokens, and pages that would be needed there count
+ * as missing). */
+gdn_status gdn_kv8_reserve(const gdn_kv8_pool* p, const int32_t* table, const int32_t* lengths,
+                           const int32_t* refs, const int32_t* extra, int32_t* table_out,
+                           int32_t* lengths_out, int32_t* refs_out, int32_t* missing,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Moves the live pages at or above n to the free pages below n (the i-th lowest
+ * to the i-th lowest), n = live[0] = the number of live pages, so that pages n
+ * and above are free. */
+gdn_status gdn_kv8_compact(const gdn_kv8_pool* p, uint8_t* codes, float* scales,
+                           const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                           int32_t* table_out, int32_t* refs_out, int32_t* live, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Beam selection.  For each batch item the K best of its candidates: beam w
+ * (unfinished) with token v scores fl(fl(x - m) + fl(score_w - log sum exp(x - m))),
+ * x its logits and m their maximum; a finished beam has one candidate, itself
+ * with token `eos` and its score.  Order: score descending, then beam, then
+ * logit descending, then token.  Where there are fewer than K candidates the
+ * rest score -inf (token 0, or eos of a finished beam).  NaN logits count as
+ * -inf, +inf as the largest finite number.
+ *   logits   bf16 or f32 [batch, beams, vocab], row stride `stride` elements
+ *   scores   f32 [batch, beams]      finished u8 [batch, beams] or NULL
+ *   out      scores f32, parents i32 (batch * beams + beam: a row index),
+ *            tokens i32, finished u8: [batch, K]
+ */
+typedef struct {
+  int64_t batch;
+  int64_t stride;       /* elements from one row of logits to the next           */
+  int32_t beams;        /* 1 .. 32                                               */
+  int32_t vocab;        /* >= 1                                                  */
+  int32_t k;            /* 1 .. 32                                               */
+  int32_t dtype;        /* GDN_DTYPE_BF16 or GDN_DTYPE_FP32                      */
+  int32_t eos;          /* token that finishes a beam; -1: none does             */
+} gdn_beam_problem;
+
+gdn_status gdn_beam_validate(const gdn_beam_problem* p);
+size_t gdn_beam_workspace_bytes(const gdn_beam_problem* p);
+
+gdn_status gdn_beam_select(const gdn_beam_problem* p, const void* logits, const float* scores,
+                           const uint8_t* finished, float* scores_out, int32_t* parents,
+                           int32_t* tokens, uint8_t* finished_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Row r of every state becomes row parents[r] (-1: zeros).  n states, state i
+ * of row_bytes[i] bytes a row (a multiple of 16).  dst[i] may be src[i] (in
+ * place: rows that keep themselves are not touched); then parents stay within
+ * groups of `beams` consecutive rows (others are not followed: the row stays).
+ * Any other overlap is an error.  src, dst and row_bytes are host arrays.
+ */
+gdn_status gdn_beam_reorder(int32_t n, const void* const* src, void* const* dst,
+                            const int64_t* row_bytes, const int32_t* parents, int64_t rows,
+                            int32_t beams, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
