@@ -148,8 +148,8 @@ int gdn_abi_version(void) { return GDN_QDQ_ABI_VERSION; }
 
 int gdn_device_error(int reset) {
   const int f = fwd_device_error(reset != 0), b = bwd_device_error(reset != 0);
-  const int u = fused_device_error(reset != 0);
-  return (f < 0 || b < 0 || u < 0) ? -1 : (f | b | u);
+  const int u = fused_device_error(reset != 0), k = kv8_device_error(reset != 0);
+  return (f < 0 || b < 0 || u < 0 || k < 0) ? -1 : (f | b | u | k);
 }
 
 gdn_status gdn_validate(const gdn_problem* p) { return validate(p); }

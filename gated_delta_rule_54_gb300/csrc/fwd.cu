@@ -1465,6 +1465,20 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols,
+                 uint64_t rows, uint64_t tiles, uint64_t row_bytes, uint32_t box_cols,
+                 uint32_t box_rows, CUtensorMapSwizzle sw) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, tiles};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int fwd_device_error(bool reset) {
   int v = 0;
   if (cudaMemcpyFromSymbol(&v, g_fwd_device_error, sizeof(int)) != cudaSuccess) return -1;

@@ -185,6 +185,7 @@ gdn_status validate_kv8(const gdn_kv8_problem* p) {
   // positions are 32-bit; heads are a grid dimension; page ids are 32-bit
   if ((int64_t)p->cols * p->page > 0x7fffffffLL || p->pages > 0x7fffffffLL ||
       p->rows > 0x7fffffffLL || p->total > 0x7fffffffLL ||
+      2 * p->pages * p->heads > 0x7fffffffLL || p->rows * p->heads > 0x7fffffffLL ||
       (int64_t)p->heads * p->group > 65535)
     return GDN_ERR_UNSUPPORTED_SHAPE;
   if (!isfinite(p->scale)) return GDN_ERR_INVALID_ARG;
@@ -203,6 +204,9 @@ Kv8Params params_of(const gdn_kv8_problem& p) {
   k.cu = p.cu_seqlens;
   return k;
 }
+
+// one 16-row tile holds a row's queries of a K/V head
+bool few_rows(const gdn_kv8_problem& p) { return (int64_t)p.tokens * p.group <= 16; }
 
 bool off16(std::initializer_list<const void*> ptrs) {
   for (const void* q : ptrs)
@@ -227,7 +231,7 @@ gdn_status gdn_kv8_validate(const gdn_kv8_problem* p) { return validate_kv8(p); 
 
 size_t gdn_kv8_workspace_bytes(const gdn_kv8_problem* p) {
   if (validate_kv8(p) != GDN_OK) return 0;
-  return 0;
+  return few_rows(*p) ? kv8_decode_workspace(params_of(*p), p->dim) : 0;
 }
 
 gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v, uint8_t* codes,
@@ -271,6 +275,7 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
   prm.table = table, prm.lengths = lengths;
   prm.o = static_cast<__nv_bfloat16*>(o), prm.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (few_rows(*p)) return launch_kv8_decode(prm, p->mode, p->dim, workspace, st);
   const int64_t warps = p->total * p->heads * p->group;
   if (warps > 4 * 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
   const unsigned grid = (unsigned)((warps + 3) / 4);

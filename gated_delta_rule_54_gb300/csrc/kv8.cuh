@@ -21,6 +21,13 @@ struct Kv8Params {
   float scale;
 };
 
+// Keys of a row that any of its queries sees: positions [begin, end).
+struct Kv8Span {
+  int64_t base;     // first packed token (queries)
+  int n, len;       // queries, tokens
+  int begin, end;
+};
+
 __device__ __forceinline__ int kv8_clamp(int64_t x, int64_t lo, int64_t hi) {
   return (int)(x < lo ? lo : x > hi ? hi : x);
 }
@@ -45,6 +52,87 @@ __device__ __forceinline__ int64_t kv8_at(const Kv8Params& p, int64_t r, int64_t
   return p.cu ? (base + i) * token : r * row + i * token;
 }
 
+__device__ __forceinline__ Kv8Span kv8_span(const Kv8Params& p, int64_t r) {
+  Kv8Span s;
+  kv8_row(p, r, s.base, s.n);
+  s.len = p.lengths[r];
+  const int64_t first = (int64_t)s.len - s.n;  // position of the first query
+  s.end = kv8_clamp(s.len, 0, (int64_t)p.cols * p.page);
+  s.begin = p.window > 0 ? kv8_clamp(first - p.window + 1, 0, s.end) : 0;
+  if (s.n == 0) s.begin = s.end = 0;
+  return s;
+}
+
+// Keys that query i of the row sees: [begin, end).
+__device__ __forceinline__ void kv8_seen(const Kv8Params& p, const Kv8Span& s, int i, int& begin,
+                                         int& end) {
+  const int64_t pos = (int64_t)s.len - s.n + i;
+  end = p.causal ? kv8_clamp(pos + 1, 0, s.end) : pos < 0 ? 0 : s.end;
+  begin = p.window > 0 ? kv8_clamp(pos - p.window + 1, 0, s.end) : 0;
+}
+
+// Code bytes to fp16 pairs: of the bytes b0 b1 b2 b3 of w, even = (b0, b2) and
+// odd = (b1, b3).  An E4M3 byte s eeee mmm moved to the fp16 fields reads
+// value * 2^-8, subnormals included, and exactly; no byte gives an infinity or
+// NaN, so what lies in slots without a token (weight 0) cannot spoil a sum.  An
+// INT8 byte c is 1024 + (c + 128) in fp16 less 1152, exactly.
+template <int MODE>
+__device__ __forceinline__ void kv8_half2(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if constexpr (MODE == GDN_QDQ_E4M3) {
+    even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+    odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+  } else {
+    const uint32_t e = (w & 0x00ff00ffu) ^ 0x64806480u, o = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&e), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&o), off);
+    even = *reinterpret_cast<const uint32_t*>(&a);
+    odd = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+// what kv8_half2 leaves out of the value, as a power of two
+template <int MODE>
+constexpr float kKv8Shift = MODE == GDN_QDQ_E4M3 ? 8.f : 0.f;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A power of two that brings a row of q with this largest magnitude to [2^8, 2^9)
+// in fp16 (its small elements then keep at least 33 bits below the largest), and
+// its inverse.
+__device__ __forceinline__ void kv8_q_factor(float most, float& to, float& back) {
+  int e = (int)(__float_as_uint(most) >> 23) - 127;
+  e = e < -100 ? -100 : e > 120 ? 120 : e;
+  to = __uint_as_float((uint32_t)(8 - e + 127) << 23);
+  back = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void bf16x8(uint4 u, float (&x)[8]) {
   float a[2];
   bf16x2(u.x, a), x[0] = a[0], x[1] = a[1];
@@ -67,5 +155,10 @@ __device__ __forceinline__ uint32_t kv8_code4(float a, float b, float c, float d
            ((uint32_t)qdq_code<MODE>(c, rcp) << 16) | ((uint32_t)qdq_code<MODE>(d, rcp) << 24);
   }
 }
+
+// Launchers (arguments validated).
+size_t kv8_decode_workspace(const Kv8Params& p, int dim);
+gdn_status launch_kv8_decode(const Kv8Params& p, int mode, int dim, void* workspace,
+                             cudaStream_t st);
 
 }  // namespace gdn

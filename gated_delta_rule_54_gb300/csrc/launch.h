@@ -50,12 +50,18 @@ gdn_status launch_fwd(const gdn_problem& p, const Dims& d, const void* q, const 
 // gave up (cleared when reset); -1 if the flag could not be read
 int fwd_device_error(bool reset);
 int bwd_device_error(bool reset);
+int kv8_device_error(bool reset);
 
 // 2-D row-major TMA map: `cols` elements per row (contiguous), `rows` rows of
 // `row_bytes` bytes; boxes of box_cols x box_rows elements; false on failure
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols,
               uint64_t rows, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows,
               CUtensorMapSwizzle sw);
+
+// the same with a third dimension: `tiles` tiles of `rows` rows, contiguous; boxes of one tile
+bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols,
+                 uint64_t rows, uint64_t tiles, uint64_t row_bytes, uint32_t box_cols,
+                 uint32_t box_rows, CUtensorMapSwizzle sw);
 
 gdn_status launch_kda(const gdn_problem& p, const Dims& d, const void* q, const void* k,
                       const void* v, const float* beta, const float* g, const float* h0,
