@@ -1,4 +1,4 @@
-// The 8-bit paged cache: entry points, append, and attention.
+// The 8-bit paged cache: append, and the entry points of append and attention.
 #include <math.h>
 
 #include "kv8.cuh"
@@ -108,64 +108,6 @@ gdn_status run_append(const Kv8Params& p, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// Attention, one warp per (query token, query head), one key at a time.
-template <int MODE, int DIM>
-__global__ void __launch_bounds__(128) kv8_attention_kernel(const Kv8Params p) {
-  constexpr int PER = DIM / 32;
-  const int lane = threadIdx.x % 32, hq = p.heads * p.group;
-  const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  if (item >= p.total * hq) return;
-  const int64_t tok = item / hq;
-  const int h = (int)(item % hq), hk = h / p.group;
-  int64_t r, base;
-  int n;
-  if (p.cu) {
-    int64_t a = 0, b = p.rows - 1;
-    while (a < b) {
-      const int64_t mid = (a + b) / 2;
-      if (p.cu[mid + 1] > tok) b = mid; else a = mid + 1;
-    }
-    r = a;
-  } else {
-    r = tok / p.tokens;
-  }
-  kv8_row(p, r, base, n);
-  const int64_t i = tok - base;
-  if (i < 0 || i >= n) return;
-  const int64_t cap = (int64_t)p.cols * p.page;
-  const int64_t len = p.lengths[r], pos = len - n + i;
-  int64_t end = len < cap ? len : cap;
-  if (p.causal && pos + 1 < end) end = pos + 1;
-  int64_t begin = p.window > 0 ? pos - p.window + 1 : 0;
-  if (begin < 0) begin = 0;
-  const __nv_bfloat16* x = p.x + kv8_at(p, r, base, i, p.x_row, p.x_token) + h * p.x_head;
-  float q[PER], acc[PER];
-  for (int j = 0; j < PER; ++j) {
-    q[j] = __bfloat162float(x[lane * PER + j]) * p.scale;
-    acc[j] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = begin; j < end; ++j) {
-    const int64_t id = p.table[r * p.cols + j / p.page];
-    if (id < 0 || id >= p.pages) continue;
-    const int64_t kt = id * p.heads + hk, vt = kt + p.pages * p.heads;
-    const uint8_t* kc = p.codes + (kt * p.page + j % p.page) * DIM + lane * PER;
-    const uint8_t* vc = p.codes + (vt * p.page + j % p.page) * DIM + lane * PER;
-    float s = 0.f;
-    for (int e = 0; e < PER; ++e) s = fmaf(q[e], qdq_code_value<MODE>(kc[e]), s);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scales[kt];
-    const float top = fmaxf(m, s), a = __expf(m - top), w = __expf(s - top);
-    l = l * a + w;
-    const float vs = w * p.scales[vt];
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], a, vs * qdq_code_value<MODE>(vc[e]));
-    m = top;
-  }
-  for (int e = 0; e < PER; ++e)
-    p.o[(tok * hq + h) * DIM + lane * PER + e] = __float2bfloat16_rn(l > 0.f ? acc[e] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[tok * hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
 gdn_status validate_kv8(const gdn_kv8_problem* p) {
   if (!p) return GDN_ERR_INVALID_ARG;
   if (p->pages < 0 || p->rows < 0 || p->total < 0 || p->tokens < 0 || p->cols < 0 ||
@@ -231,7 +173,8 @@ gdn_status gdn_kv8_validate(const gdn_kv8_problem* p) { return validate_kv8(p); 
 
 size_t gdn_kv8_workspace_bytes(const gdn_kv8_problem* p) {
   if (validate_kv8(p) != GDN_OK) return 0;
-  return few_rows(*p) ? kv8_decode_workspace(params_of(*p), p->dim) : 0;
+  return few_rows(*p) ? kv8_decode_workspace(params_of(*p), p->dim)
+                      : kv8_prefill_workspace(params_of(*p), p->dim);
 }
 
 gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v, uint8_t* codes,
@@ -276,17 +219,7 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
   prm.o = static_cast<__nv_bfloat16*>(o), prm.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows(*p)) return launch_kv8_decode(prm, p->mode, p->dim, workspace, st);
-  const int64_t warps = p->total * p->heads * p->group;
-  if (warps > 4 * 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
-  if (p->mode == GDN_QDQ_E4M3) {
-    if (p->dim == 128) kv8_attention_kernel<GDN_QDQ_E4M3, 128><<<grid, 128, 0, st>>>(prm);
-    else kv8_attention_kernel<GDN_QDQ_E4M3, 64><<<grid, 128, 0, st>>>(prm);
-  } else {
-    if (p->dim == 128) kv8_attention_kernel<GDN_QDQ_INT8, 128><<<grid, 128, 0, st>>>(prm);
-    else kv8_attention_kernel<GDN_QDQ_INT8, 64><<<grid, 128, 0, st>>>(prm);
-  }
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch_kv8_prefill(prm, p->mode, p->dim, workspace, st);
 }
 
 }  // extern "C"

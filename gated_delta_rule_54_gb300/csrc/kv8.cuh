@@ -160,5 +160,9 @@ __device__ __forceinline__ uint32_t kv8_code4(float a, float b, float c, float d
 size_t kv8_decode_workspace(const Kv8Params& p, int dim);
 gdn_status launch_kv8_decode(const Kv8Params& p, int mode, int dim, void* workspace,
                              cudaStream_t st);
+size_t kv8_prefill_workspace(const Kv8Params& p, int dim);
+gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* workspace,
+                              cudaStream_t st);
+int kv8_prefill_device_error(bool reset);
 
 }  // namespace gdn

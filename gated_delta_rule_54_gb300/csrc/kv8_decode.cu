@@ -711,7 +711,8 @@ int kv8_device_error(bool reset) {
     const int z = 0;
     if (cudaMemcpyToSymbol(g_kv8_device_error, &z, sizeof(int)) != cudaSuccess) return -1;
   }
-  return v;
+  const int u = kv8_prefill_device_error(reset);
+  return u < 0 ? -1 : v | u;
 }
 
 }  // namespace gdn

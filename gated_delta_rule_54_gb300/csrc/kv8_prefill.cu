@@ -1,0 +1,592 @@
+// Attention of many query rows over the 8-bit paged cache, on the tensor cores.
+//
+// The query rows of a (row, K/V head) are its queries times the query heads that
+// share the head, query-major; a CTA takes 256 of them, as two tiles of 128, so
+// that one conversion of a block of keys serves both.  Per 128 keys and tile:
+//     S = Q K^T   (tcgen05, fp16 x fp16 -> fp32 in TMEM)
+//     P = 2^(s - reference)  (one thread per query row; written over S as fp16)
+//     O += P V    (tcgen05 with P from TMEM)
+// Warps 0-3 and 4-7 are the rows of the two tiles; warps 8-11 turn code bytes
+// into fp16 (exact) and place them as swizzled operand tiles; one lane of warp 12
+// issues the products, those of one tile while the rows of the other compute.
+//
+// Products of fp16 codes bound it together with shared memory: per 128 keys the
+// two tiles' operands are read at the rate of the products, and the converted
+// tiles are written besides.
+//
+// Scales.  s_j = q . code_j * (scale * ks(block of j)), and V's scale joins the
+// exponent: P_j = 2^(s_j + log2 vs - mv), so that fp16 holds it for any scales;
+// the denominator takes a block's sum times 2^(mv - log2 vs - m).  mv follows the
+// maximum of s_j + log2 vs only when that grows by more than 2^8 (fp16 has the
+// room), and then O is rescaled in TMEM.
+#include <cuda.h>
+
+#include "kv8.cuh"
+#include "launch.h"
+#include "tc.cuh"
+
+namespace gdn {
+
+namespace {
+
+__device__ int g_kv8_prefill_error;
+
+constexpr int kKeys = 128, kRows = 256;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
+
+struct PrefillArgs {
+  Kv8Params p;
+  float* ws;   // splits > 1: parts [block][split][256][DIM + 1 ...]
+  int blocks;  // 256-row blocks of a row's queries
+  int splits;  // CTAs that share the keys of a block
+};
+
+// fp16 x fp16 -> fp32
+constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B: row i of A in lane i, two fp16 per column
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc));
+}
+// 32 consecutive fp32 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = __float_as_uint(v[i]), b[i] = __float_as_uint(v[16 + i]);
+  tmem_st16(taddr, a);
+  tmem_st16(taddr + 16, b);
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
+// Tile layout: panels of 64 columns, 128-byte rows, 16-byte units swizzled by
+// row & 7 (see tc.cuh).  Columns are stored in the order in which kv8_half2 gives
+// them: of each four, 0 2 1 3.  Unit u (16 bytes = 8 columns) of a row:
+__device__ __forceinline__ uint32_t unit_at(int row, int u) {
+  return (uint32_t)((u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+}
+
+template <int MODE, int DIM>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int kTileBytes = kKeys * DIM * 2;
+  constexpr uint32_t kCols = 512;  // S0 S1 O0 O1
+  constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone;
+  __shared__ float2 meta[4][8];  // per 16 keys of a tile: K scale, log2 of V scale
+  __shared__ int valid[4];       // bit c: these 16 keys have a page
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const Kv8Params& p = a.p;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char *sQ = smem, *sK = smem + 2 * kTileBytes, *sV = smem + 4 * kTileBytes;
+
+  // ---- which rows and keys (long blocks of rows first) ----
+  const int64_t rh = p.rows * p.heads;
+  const int split = blockIdx.x % a.splits;
+  const int64_t x = blockIdx.x / a.splits;
+  const int block = a.blocks - 1 - (int)(x / rh);
+  const int64_t r = x % rh / p.heads;
+  const int h = (int)(x % rh % p.heads);
+  const Kv8Span sp = kv8_span(p, r);
+  const int64_t rows = (int64_t)sp.n * p.group, row0 = (int64_t)block * kRows;
+  if (row0 >= rows) return;
+  const int here = (int)(rows - row0 < kRows ? rows - row0 : kRows);
+  const bool two = here > 128;
+  int ka, kb;  // tiles of keys
+  {
+    int b0, e0, b1, e1;
+    kv8_seen(p, sp, (int)(row0 / p.group), b0, e0);
+    kv8_seen(p, sp, (int)((row0 + here - 1) / p.group), b1, e1);
+    // begins and ends both grow along the rows
+    ka = b0 / kKeys;
+    kb = e1 > b0 ? (e1 + kKeys - 1) / kKeys : ka;
+    const int64_t n = kb - ka;
+    kb = ka + (int)(n * (split + 1) / a.splits);
+    ka = ka + (int)(n * split / a.splits);
+  }
+  const int nt = kb - ka;
+
+  if (warp == 0) tmem_alloc(&tmem_slot, kCols);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
+      mbar_init(&kfree[i], 1), mbar_init(&vfree[i], 1);
+      mbar_init(&sfull[i], 1), mbar_init(&pready[i], 128);
+    }
+    mbar_init(&odone, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+
+  // ---- queries: one thread per row; what it keeps for the softmax ----
+  const int i_row = warp < kSoftWarps ? tid : 0;  // row of the block
+  float rowfac = 0.f;
+  int beg = 0, end = 0;
+  const int qi = (int)((row0 + i_row) / p.group), hg = (int)((row0 + i_row) % p.group);
+  const bool mine = warp < kSoftWarps && i_row < here;
+  if (warp < kSoftWarps) {
+    unsigned char* to = sQ + (i_row / 128) * kTileBytes;
+    const int row = i_row % 128;
+    const __nv_bfloat16* x8 = p.x + kv8_at(p, r, sp.base, qi, p.x_row, p.x_token) +
+                              (h * p.group + hg) * p.x_head;
+    float most = 0.f;
+    if (mine) {
+      kv8_seen(p, sp, qi, beg, end);
+#pragma unroll 4
+      for (int u = 0; u < DIM / 8; ++u) {
+        float f[8];
+        bf16x8(*reinterpret_cast<const uint4*>(x8 + 8 * u), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+      }
+    }
+    float up, back;
+    kv8_q_factor(most, up, back);
+    rowfac = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
+    if (p.scale < 0.f) up = -up;
+#pragma unroll 4
+    for (int u = 0; u < DIM / 8; ++u) {
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (mine) bf16x8(*reinterpret_cast<const uint4*>(x8 + 8 * u), f);
+      *reinterpret_cast<uint4*>(to + unit_at(row, u)) =
+          make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
+                     pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
+    }
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* stop = &abort_flag;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity)) return true;
+    *stop = 1;
+    return false;
+  };
+
+  float l = 0.f, m = -INFINITY, mv = -INFINITY;
+  bool done = false;  // this thread went through all its tiles
+
+  if (warp < kSoftWarps) {
+    // ======================= softmax =======================
+    const int t = warp / 4;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + t * kKeys, o_col = lane_base + 256 + t * 128;
+    // keys that every row of this tile sees
+    int in0 = 0, in1 = 0;
+    {
+      const int64_t last = row0 + (t * 128 + 127 < here ? t * 128 + 127 : here - 1);
+      int b0, e0, b1, e1;
+      kv8_seen(p, sp, (int)((row0 + t * 128) / p.group), b0, e0);
+      kv8_seen(p, sp, (int)(last / p.group), b1, e1);
+      in0 = b1, in1 = e0;
+    }
+    bool ok = t == 0 || two;
+    const bool run = ok;
+    for (int i = 0; i < nt && ok; ++i) {
+      if (*stop || !__all_sync(0xffffffffu, wait(&sfull[t], i & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int j0 = (ka + i) * kKeys;
+      const int have = valid[i & 3];
+      const bool mask = have != 0xff || j0 < in0 || j0 + kKeys > in1;
+      // largest product of every 16 keys
+      float pm[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld32(s_col + 32 * c, v);
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int j = j0 + 32 * c + e;
+            if (j < beg || j >= end || !(have >> (2 * c + e / 16) & 1)) v[e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float top = v[16 * f];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) top = fmaxf(top, v[16 * f + e]);
+          pm[2 * c + f] = top;
+        }
+      }
+      float fac[8], off[8];
+      float nm = m, nv = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float2 sc = meta[i & 3][c];
+        fac[c] = rowfac * sc.x;
+        off[c] = sc.y;
+        const float top = pm[c] > -INFINITY ? pm[c] * fac[c] : -INFINITY;
+        nm = fmaxf(nm, top);
+        nv = fmaxf(nv, top + sc.y);
+      }
+      const float um = nm == -INFINITY ? 0.f : nm;
+      l *= ex2_approx_f(m - um);
+      m = nm;
+      if (__any_sync(0xffffffffu, nv > mv + 8.f)) {
+        const float to = fmaxf(mv, nv), f = ex2_approx_f(mv - (to == -INFINITY ? 0.f : to));
+        mv = to;
+        if (i > 0) {  // the products into O so far have completed with S
+#pragma unroll
+          for (int c = 0; c < DIM / 32; ++c) {
+            float v[32];
+            tmem_ld32(o_col + 32 * c, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= f;
+            tmem_st32(o_col + 32 * c, v);
+          }
+        }
+      }
+      const float uv = mv == -INFINITY ? 0.f : mv;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld32(s_col + 32 * c, v);
+        uint32_t pk[16];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int b = 2 * c + f;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float w0 = ex2_approx_f(fmaf(v[16 * f + e], fac[b], off[b]));
+            float w1 = ex2_approx_f(fmaf(v[16 * f + e + 1], fac[b], off[b]));
+            if (mask) {
+              const int j = j0 + 16 * b + e;
+              const bool page = have >> b & 1;
+              if (j < beg || j >= end || !page) w0 = 0.f;
+              if (j + 1 < beg || j + 1 >= end || !page) w1 = 0.f;
+            }
+            sum0 += w0, sum1 += w1;
+            pk[8 * f + e / 2] = pack_f16(w0, w1);
+          }
+          l = fmaf(sum0 + sum1, ex2_approx_f(-off[b] - um), l);
+        }
+        tmem_st16(s_col + 16 * c, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&pready[t]);
+    }
+    done = ok && run;
+  } else if (warp < kSoftWarps + kConvWarps) {
+    // ======================= codes to fp16 =======================
+    const int ct = tid - kSoftWarps * 32;
+    // quads of lanes read 64 bytes of a row; eight lanes store to eight banks groups
+    const int cw = ct / 32;
+    const int unit = DIM == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
+    const int sub = DIM == 128 ? ((lane >> 2) & 1) | ((lane >> 4) & 1) << 1 : lane >> 2;
+    constexpr int kPer = DIM == 128 ? 8 : 4, kStep = DIM == 128 ? 16 : 32, kSub = DIM == 128 ? 4 : 8;
+    const int myrow = cw * kSub + sub;
+    auto ids = [&](int tile, int (&id)[kPer]) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int j = tile * kKeys + myrow + e * kStep;
+        id[e] = -1;
+        if (j < sp.end) id[e] = p.table[r * p.cols + j / p.page];
+        if (id[e] >= p.pages) id[e] = -1;
+      }
+    };
+    auto load = [&](int tile, int kv, const int (&id)[kPer], uint4 (&u)[kPer]) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int j = tile * kKeys + myrow + e * kStep;
+        u[e] = make_uint4(0, 0, 0, 0);
+        if (id[e] >= 0)
+          u[e] = *reinterpret_cast<const uint4*>(
+              p.codes + (((kv * p.pages + id[e]) * p.heads + h) * p.page + j % p.page) * DIM + 16 * unit);
+      }
+    };
+    auto store = [&](unsigned char* to, const uint4 (&u)[kPer]) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int row = myrow + e * kStep;
+        uint4 lo, hi;
+        kv8_half2<MODE>(u[e].x, lo.x, lo.y);
+        kv8_half2<MODE>(u[e].y, lo.z, lo.w);
+        kv8_half2<MODE>(u[e].z, hi.x, hi.y);
+        kv8_half2<MODE>(u[e].w, hi.z, hi.w);
+        *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
+        *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
+      }
+    };
+    int id[kPer];
+    uint4 ku[kPer], vu[kPer];
+    if (nt > 0) {
+      ids(ka, id);
+      load(ka, 0, id, ku);
+      load(ka, 1, id, vu);
+    }
+    for (int i = 0; i < nt; ++i) {
+      const int b = i & 1;
+      const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
+      // scales of this tile's blocks of 16 keys
+      float2 sc = make_float2(0.f, -INFINITY);
+      bool page = false;
+      if (ct < 8) {
+        const int j = (ka + i) * kKeys + 16 * ct;
+        const int64_t at = j < sp.end ? p.table[r * p.cols + j / p.page] : -1;
+        page = at >= 0 && at < p.pages;
+        if (page) {
+          const int64_t tile = at * p.heads + h;
+          sc = make_float2(p.scales[tile], lg2_approx(p.scales[tile + p.pages * p.heads]));
+        }
+      }
+      if (i + 1 < nt) ids(ka + i + 1, id);
+      if (*stop || !wait(&kfree[b], free_parity)) break;
+      if (cw == 0) {
+        const unsigned bits = __ballot_sync(0xffffffffu, page);
+        if (ct < 8) meta[i & 3][ct] = sc;
+        if (ct == 0) valid[i & 3] = (int)bits;
+      }
+      store(sK + b * kTileBytes, ku);
+      fence_proxy_async();
+      mbar_arrive(&kfull[b]);
+      if (i + 1 < nt) load(ka + i + 1, 0, id, ku);
+      if (*stop || !wait(&vfree[b], free_parity)) break;
+      store(sV + b * kTileBytes, vu);
+      fence_proxy_async();
+      mbar_arrive(&vfull[b]);
+      if (i + 1 < nt) load(ka + i + 1, 1, id, vu);
+    }
+  } else if (lane == 0 && nt > 0) {
+    // ======================= products =======================
+    const uint64_t q0 = sdesc(smem_u32(sQ), 16, 1024), q1 = sdesc(smem_u32(sQ + kTileBytes), 16, 1024);
+    auto qk = [&](int t, int i) {
+      const uint64_t k = sdesc(smem_u32(sK + (i & 1) * kTileBytes), 16, 1024);
+#pragma unroll
+      for (int s = 0; s < DIM / 16; ++s) {
+        const uint32_t off = (s >> 2) * (kKeys * 128) + (s & 3) * 32;
+        umma(tmem + t * kKeys, dadd(t ? q1 : q0, off), dadd(k, off), kIdQK, s > 0);
+      }
+      umma_commit(&sfull[t]);
+    };
+    auto pv = [&](int t, int i) {
+      const uint64_t v = sdesc(smem_u32(sV + (i & 1) * kTileBytes), kKeys * 128, 1024);
+#pragma unroll
+      for (int s = 0; s < kKeys / 16; ++s)
+        umma_ts(tmem + 256 + t * 128, tmem + t * kKeys + 8 * s, dadd(v, s * 2048), kIdPV, i > 0 || s > 0);
+    };
+    bool ok = wait(&kfull[0], 0);
+    if (ok) {
+      tc_fence_after();
+      qk(0, 0);
+      if (two) qk(1, 0);
+      umma_commit(&kfree[0]);
+    }
+    for (int i = 0; i < nt && ok; ++i) {
+      const int b = i & 1, nb = (i + 1) & 1;
+      const uint32_t par = (i >> 1) & 1;
+      ok = !*stop && wait(&vfull[b], par) && wait(&pready[0], i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      pv(0, i);
+      if (i + 1 < nt) {
+        ok = wait(&kfull[nb], ((i + 1) >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        qk(0, i + 1);
+      }
+      if (two) {
+        ok = !*stop && wait(&pready[1], i & 1);
+        if (!ok) break;
+        tc_fence_after();
+        pv(1, i);
+        if (i + 1 < nt) qk(1, i + 1);
+      }
+      umma_commit(&vfree[b]);
+      if (i + 1 < nt) umma_commit(&kfree[nb]);
+    }
+    umma_commit(&odone);  // completes with every product issued
+    wait(&odone, 0);
+  }
+
+  // ---- outputs ----
+  if (warp < kSoftWarps) {
+    const int t = warp / 4;
+    const bool any = nt > 0 && done;
+    bool ok = true;
+    if (any) {
+      ok = __all_sync(0xffffffffu, wait(&odone, 0));
+      tc_fence_after();
+    }
+    const uint32_t o_col = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + t * 128;
+    const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
+    const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + hg;
+    float* part = a.ws + ((int64_t)blockIdx.x * kRows + i_row) * (DIM + 4);
+    if ((nt == 0 || done) && ok) {
+#pragma unroll
+      for (int c = 0; c < DIM / 32; ++c) {
+        float v[32];
+        if (any) {
+          tmem_ld32(o_col + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+        if (mine) {
+          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            // where nothing was seen the factor is 0 and O holds finite sums or zeros
+            const float f0 = v[e] * fac, f1 = v[e + 2] * fac, f2 = v[e + 1] * fac, f3 = v[e + 3] * fac;
+            const float f4 = v[e + 4] * fac, f5 = v[e + 6] * fac, f6 = v[e + 5] * fac, f7 = v[e + 7] * fac;
+            if (a.splits == 1) {
+              *reinterpret_cast<uint4*>(p.o + at * DIM + 32 * c + e) =
+                  make_uint4(pack_bf16(f0, f1), pack_bf16(f2, f3), pack_bf16(f4, f5), pack_bf16(f6, f7));
+            } else {
+              *reinterpret_cast<float4*>(part + 32 * c + e) = make_float4(f0, f1, f2, f3);
+              *reinterpret_cast<float4*>(part + 32 * c + e + 4) = make_float4(f4, f5, f6, f7);
+            }
+          }
+        }
+      }
+      if (mine) {
+        if (a.splits > 1) part[DIM] = lse2;
+        else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && abort_flag) atomicOr(&g_kv8_prefill_error, 1);
+  if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
+// Joins the parts of a block's rows: one warp per row, in order of the splits.
+template <int DIM>
+__global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const __grid_constant__ PrefillArgs a) {
+  const Kv8Params& p = a.p;
+  const int lane = threadIdx.x % 32, i = blockIdx.y * 8 + threadIdx.x / 32;
+  const int64_t rh = p.rows * p.heads, x = blockIdx.x;
+  const int block = a.blocks - 1 - (int)(x / rh);
+  const int64_t r = x % rh / p.heads;
+  const int h = (int)(x % rh % p.heads);
+  const Kv8Span sp = kv8_span(p, r);
+  const int64_t row = (int64_t)block * kRows + i;
+  if (row >= (int64_t)sp.n * p.group) return;
+  const float* part = a.ws + (x * a.splits * kRows + i) * (DIM + 4);
+  constexpr int64_t step = (int64_t)kRows * (DIM + 4);
+  float top = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, part[s * step + DIM]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int s = 0; s < a.splits && top > -INFINITY; ++s) {
+    const float c = ex2_approx_f(part[s * step + DIM] - top);
+    l += c;
+    if (lane < DIM / 4) {
+      const float4 v = *reinterpret_cast<const float4*>(part + s * step + 4 * lane);
+      o.x = fmaf(c, v.x, o.x), o.y = fmaf(c, v.y, o.y), o.z = fmaf(c, v.z, o.z), o.w = fmaf(c, v.w, o.w);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t at = (sp.base + row / p.group) * (p.heads * p.group) + h * p.group + row % p.group;
+  if (lane < DIM / 4)
+    *reinterpret_cast<uint2*>(p.o + at * DIM + 4 * lane) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (p.lse && lane == 0) p.lse[at] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+int64_t blocks_of(const Kv8Params& p) {
+  return ((int64_t)p.tokens * p.group + kRows - 1) / kRows;
+}
+// CTAs per block of rows: where the blocks do not fill 152 SMs, the keys are
+// split, down to two tiles each
+int splits_of(const Kv8Params& p) {
+  int64_t keys = (int64_t)p.cols * p.page;
+  if (p.window > 0 && (int64_t)p.window + p.tokens < keys) keys = (int64_t)p.window + p.tokens;
+  const int64_t ctas = blocks_of(p) * p.rows * p.heads, tiles = (keys + kKeys - 1) / kKeys;
+  int64_t n = ctas > 0 ? 152 / ctas : 1;
+  if (n > tiles / 2) n = tiles / 2;
+  return n < 1 ? 1 : (int)n;
+}
+
+template <int MODE, int DIM>
+gdn_status run(const PrefillArgs& a, cudaStream_t st) {
+  const Kv8Params& p = a.p;
+  const int64_t blocks = (int64_t)a.blocks * p.rows * p.heads;
+  if (blocks * a.splits > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
+  constexpr int bytes = 6 * kKeys * DIM * 2 + 1024;
+  auto kern = kv8_prefill_kernel<MODE, DIM>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  kern<<<(unsigned)(blocks * a.splits), kThreads, bytes, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  if (a.splits == 1) return GDN_OK;
+  kv8_prefill_join_kernel<DIM><<<dim3((unsigned)blocks, kRows / 8), 256, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t kv8_prefill_workspace(const Kv8Params& p, int dim) {
+  const int splits = splits_of(p);
+  if (splits == 1) return 0;
+  return (size_t)(blocks_of(p) * p.rows * p.heads) * splits * kRows * (dim + 4) * sizeof(float);
+}
+
+gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* workspace,
+                              cudaStream_t st) {
+  PrefillArgs a;
+  a.p = p;
+  a.ws = static_cast<float*>(workspace);
+  a.blocks = (int)blocks_of(p);
+  a.splits = splits_of(p);
+  if (mode == GDN_QDQ_E4M3)
+    return dim == 128 ? run<GDN_QDQ_E4M3, 128>(a, st) : run<GDN_QDQ_E4M3, 64>(a, st);
+  return dim == 128 ? run<GDN_QDQ_INT8, 128>(a, st) : run<GDN_QDQ_INT8, 64>(a, st);
+}
+
+int kv8_prefill_device_error(bool reset) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_kv8_prefill_error, sizeof(int)) != cudaSuccess) return -1;
+  if (reset && v) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_kv8_prefill_error, &z, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+}  // namespace gdn
