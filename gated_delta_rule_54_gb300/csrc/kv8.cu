@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int b
   kv8_row(p, r, base, n);
   const int64_t st = p.lengths[r];
   if (st < 0) return;
-  const int64_t b = st / p.page + blockIdx.x % blocks;
+  const int64_t b = (st >> p.shift) + blockIdx.x % blocks;
   const int64_t lo = st > b * p.page ? st : b * p.page;
   const int64_t hi = st + n < (b + 1) * p.page ? st + n : (b + 1) * p.page;
   if (lo >= hi || b >= p.cols) return;
@@ -142,6 +142,7 @@ Kv8Params params_of(const gdn_kv8_problem& p) {
   k.x_row = p.x_row, k.x_token = p.x_token, k.x_head = p.x_head;
   k.v_row = p.v_row, k.v_token = p.v_token, k.v_head = p.v_head;
   k.tokens = p.tokens, k.cols = p.cols, k.heads = p.heads, k.group = p.group, k.page = p.page;
+  k.shift = __builtin_ctz((unsigned)p.page);
   k.causal = p.causal, k.window = p.window, k.scale = p.scale;
   k.cu = p.cu_seqlens;
   return k;

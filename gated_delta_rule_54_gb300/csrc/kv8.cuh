@@ -17,7 +17,7 @@ struct Kv8Params {
   float* lse;
   int64_t pages, rows, total;
   int64_t x_row, x_token, x_head, v_row, v_token, v_head;
-  int tokens, cols, heads, group, page, causal, window;
+  int tokens, cols, heads, group, page, shift, causal, window;  // page == 1 << shift
   float scale;
 };
 

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   float w_ks = 0.f, w_lv = -INFINITY;
   const int two = p.page < kTile;  // two pages per tile
   auto issue = [&](int st) {
-    const int j0 = pc.tile * kTile, first = j0 / p.page;
+    const int j0 = pc.tile * kTile, first = j0 >> p.shift;
     if (pc.r != w_r || pc.h != w_h || first >= w_base + 32 || first < w_base) {
       w_r = pc.r, w_h = pc.h, w_base = first;
       const int at = first + lane;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       mbar_expect_tx(&bars[warp][st],
                      (uint32_t)(per * 2 * ((id0 >= 0) + (two && id1 >= 0))));
       if (id0 >= 0) {
-        const int z = id0 * p.heads + pc.h, y = j0 % p.page;
+        const int z = id0 * p.heads + pc.h, y = j0 & (p.page - 1);
         tma_load_3d(k, &a.map, 0, y, z, &bars[warp][st]);
         tma_load_3d(k + kBytes, &a.map, 0, y, z + (int)(p.pages * p.heads), &bars[warp][st]);
       }
@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   float lsum[2], m[2], mv[2];
   Kv8Span sp;
   int64_t part = -1;  // segment left in registers at the end
-  const int hq = p.heads * p.group;
   int64_t u_done = lo;
   for (int64_t u = lo; u < hi && !bad;) {
     const int64_t u0 = cc.u0, u1 = u0 + (cc.t1 - cc.t0);

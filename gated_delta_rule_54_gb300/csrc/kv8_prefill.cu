@@ -33,7 +33,10 @@ __device__ int g_kv8_prefill_error;
 
 constexpr int kKeys = 128, kRows = 256;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
+constexpr int kThreads = 512;  // four warpgroups; of the last, one lane issues the products
+// registers per thread of the warpgroups: together what the launch gave (4 x 128)
+constexpr int kSoftRegs = 176, kConvRegs = 112, kIssueRegs = 48;
+static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs == 4 * 128, "register shares");
 
 struct PrefillArgs {
   Kv8Params p;
@@ -54,22 +57,53 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc));
 }
-// 32 consecutive fp32 columns of this thread's lane
+// 32 consecutive fp32 columns of this thread's lane; valid after tmem_wait_ld of them
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// waits for this thread's loads; the values pass through so that no use moves before it
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                 "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+                 "+f"(v[31])
+               :
+               : "memory");
+}
+// two fp32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -78,13 +112,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) a[i] = __float_as_uint(v[i]), b[i] = __float_as_uint(v[16 + i]);
-  tmem_st16(taddr, a);
-  tmem_st16(taddr + 16, b);
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
@@ -97,15 +124,17 @@ __device__ __forceinline__ uint32_t unit_at(int row, int u) {
   return (uint32_t)((u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
 }
 
-template <int MODE, int DIM>
+// CH: blocks of a tile of keys that have scales of their own (two at least)
+template <int MODE, int DIM, int CH>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int kTileBytes = kKeys * DIM * 2;
   constexpr uint32_t kCols = 512;  // S0 S1 O0 O1
+  constexpr int BK = kKeys / CH;   // keys of a block
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone;
-  __shared__ float2 meta[4][8];  // per 16 keys of a tile: K scale, log2 of V scale
-  __shared__ int valid[4];       // bit c: these 16 keys have a page
+  __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
+  __shared__ int valid[4];        // bit c: the block has a page
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -199,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   };
 
   float l = 0.f, m = -INFINITY, mv = -INFINITY;
-  bool done = false;  // this thread went through all its tiles
 
   if (warp < kSoftWarps) {
+    set_regs_up<kSoftRegs>();
     // ======================= softmax =======================
     const int t = warp / 4;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -215,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       kv8_seen(p, sp, (int)(last / p.group), b1, e1);
       in0 = b1, in1 = e0;
     }
-    bool ok = t == 0 || two;
-    const bool run = ok;
-    for (int i = 0; i < nt && ok; ++i) {
+    const bool run = t == 0 || two;  // the tile has rows
+    bool ok = true;
+    for (int i = 0; i < nt && run; ++i) {
       if (*stop || !__all_sync(0xffffffffu, wait(&sfull[t], i & 1))) {
         ok = false;
         break;
@@ -225,38 +254,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       tc_fence_after();
       const int j0 = (ka + i) * kKeys;
       const int have = valid[i & 3];
-      const bool mask = have != 0xff || j0 < in0 || j0 + kKeys > in1;
-      // largest product of every 16 keys
-      float pm[8];
+      float v[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld32(s_col + 32 * c, v);
-        if (mask) {
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int j = j0 + 32 * c + e;
-            if (j < beg || j >= end || !(have >> (2 * c + e / 16) & 1)) v[e] = -INFINITY;
-          }
-        }
+      for (int c = 0; c < 4; ++c) tmem_wait_ld(v[c]);
+      if (have != (1 << CH) - 1 || j0 < in0 || j0 + kKeys > in1) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          float top = v[16 * f];
-#pragma unroll
-          for (int e = 1; e < 16; ++e) top = fmaxf(top, v[16 * f + e]);
-          pm[2 * c + f] = top;
+        for (int e = 0; e < kKeys; ++e) {
+          const int j = j0 + e;
+          if (j < beg || j >= end || !(have >> (e / BK) & 1)) v[e / 32][e % 32] = -INFINITY;
         }
       }
-      float fac[8], off[8];
+      // largest product of each block
+      float fac[CH], off[CH];
       float nm = m, nv = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < CH; ++c) {
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = v[(c * BK + q) / 32][(c * BK + q) % 32];
+#pragma unroll
+          for (int e = q + 4; e < BK; e += 4) top[q] = fmaxf(top[q], v[(c * BK + e) / 32][(c * BK + e) % 32]);
+        }
         const float2 sc = meta[i & 3][c];
-        fac[c] = rowfac * sc.x;
+        // (a factor of 0 would make -inf of a masked key a NaN)
+        fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
         off[c] = sc.y;
-        const float top = pm[c] > -INFINITY ? pm[c] * fac[c] : -INFINITY;
-        nm = fmaxf(nm, top);
-        nv = fmaxf(nv, top + sc.y);
+        const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac[c];
+        nm = fmaxf(nm, x);
+        nv = fmaxf(nv, x + sc.y);
       }
       const float um = nm == -INFINITY ? 0.f : nm;
       l *= ex2_approx_f(m - um);
@@ -265,51 +293,87 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         const float to = fmaxf(mv, nv), f = ex2_approx_f(mv - (to == -INFINITY ? 0.f : to));
         mv = to;
         if (i > 0) {  // the products into O so far have completed with S
+#pragma unroll 1
+          for (int c = 0; c < DIM / 16; ++c) {
+            float w[16];
+            tmem_ld16(o_col + 16 * c, w);
+            uint32_t u[16];
 #pragma unroll
-          for (int c = 0; c < DIM / 32; ++c) {
-            float v[32];
-            tmem_ld32(o_col + 32 * c, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= f;
-            tmem_st32(o_col + 32 * c, v);
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(w[e] * f);
+            tmem_st16(o_col + 16 * c, u);
           }
         }
       }
       const float uv = mv == -INFINITY ? 0.f : mv;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+      for (int c = 0; c < CH; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+      float2 sum[CH];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_ld32(s_col + 32 * c, v);
         uint32_t pk[16];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int b = 2 * c + f;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float w0 = ex2_approx_f(fmaf(v[16 * f + e], fac[b], off[b]));
-            float w1 = ex2_approx_f(fmaf(v[16 * f + e + 1], fac[b], off[b]));
-            if (mask) {
-              const int j = j0 + 16 * b + e;
-              const bool page = have >> b & 1;
-              if (j < beg || j >= end || !page) w0 = 0.f;
-              if (j + 1 < beg || j + 1 >= end || !page) w1 = 0.f;
-            }
-            sum0 += w0, sum1 += w1;
-            pk[8 * f + e / 2] = pack_f16(w0, w1);
-          }
-          l = fmaf(sum0 + sum1, ex2_approx_f(-off[b] - um), l);
+        for (int e = 0; e < 32; e += 2) {
+          const int b = (32 * c + e) / BK;
+          const float2 x = fma2(make_float2(v[c][e], v[c][e + 1]), make_float2(fac[b], fac[b]),
+                                make_float2(off[b], off[b]));
+          const float2 w = make_float2(ex2_approx_f(x.x), ex2_approx_f(x.y));
+          sum[b] = (32 * c + e) % BK == 0 ? w : add2(sum[b], w);
+          pk[e / 2] = pack_f16(w.x, w.y);
         }
         tmem_st16(s_col + 16 * c, pk);
       }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) l = fmaf(sum[c].x + sum[c].y, ex2_approx_f(-off[c] - um), l);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&pready[t]);
     }
-    done = ok && run;
+
+    // ---- outputs ----
+    const bool any = nt > 0 && run && ok;
+    if (any) {
+      ok = __all_sync(0xffffffffu, wait(&odone, 0));
+      tc_fence_after();
+    }
+    const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
+    const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + hg;
+    float* part = a.ws + ((int64_t)blockIdx.x * kRows + i_row) * (DIM + 4);
+    if ((nt == 0 || run) && ok) {
+#pragma unroll
+      for (int c = 0; c < DIM / 32; ++c) {
+        float v[32];
+        if (any) {
+          tmem_ld32(o_col + 32 * c, v);
+          tmem_wait_ld(v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+        if (mine) {
+          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            // where nothing was seen the factor is 0 and O holds finite sums or zeros
+            const float f0 = v[e] * fac, f1 = v[e + 2] * fac, f2 = v[e + 1] * fac, f3 = v[e + 3] * fac;
+            const float f4 = v[e + 4] * fac, f5 = v[e + 6] * fac, f6 = v[e + 5] * fac, f7 = v[e + 7] * fac;
+            if (a.splits == 1) {
+              *reinterpret_cast<uint4*>(p.o + at * DIM + 32 * c + e) =
+                  make_uint4(pack_bf16(f0, f1), pack_bf16(f2, f3), pack_bf16(f4, f5), pack_bf16(f6, f7));
+            } else {
+              *reinterpret_cast<float4*>(part + 32 * c + e) = make_float4(f0, f1, f2, f3);
+              *reinterpret_cast<float4*>(part + 32 * c + e + 4) = make_float4(f4, f5, f6, f7);
+            }
+          }
+        }
+      }
+      if (mine) {
+        if (a.splits > 1) part[DIM] = lse2;
+        else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
+      }
+    }
   } else if (warp < kSoftWarps + kConvWarps) {
+    set_regs_down<kConvRegs>();
     // ======================= codes to fp16 =======================
     const int ct = tid - kSoftWarps * 32;
     // quads of lanes read 64 bytes of a row; eight lanes store to eight banks groups
@@ -323,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       for (int e = 0; e < kPer; ++e) {
         const int j = tile * kKeys + myrow + e * kStep;
         id[e] = -1;
-        if (j < sp.end) id[e] = p.table[r * p.cols + j / p.page];
+        if (j < sp.end) id[e] = p.table[r * p.cols + (j >> p.shift)];
         if (id[e] >= p.pages) id[e] = -1;
       }
     };
@@ -334,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         u[e] = make_uint4(0, 0, 0, 0);
         if (id[e] >= 0)
           u[e] = *reinterpret_cast<const uint4*>(
-              p.codes + (((kv * p.pages + id[e]) * p.heads + h) * p.page + j % p.page) * DIM + 16 * unit);
+              p.codes + (((kv * p.pages + id[e]) * p.heads + h) * p.page + (j & (p.page - 1))) * DIM + 16 * unit);
       }
     };
     auto store = [&](unsigned char* to, const uint4 (&u)[kPer]) {
@@ -350,51 +414,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
       }
     };
-    int id[kPer];
+    // what a step needs was asked for a step before: page ids for the codes and
+    // scales of the next tile, those for this one
+    int id[kPer], sid = -1;
     uint4 ku[kPer], vu[kPer];
+    float2 sc = make_float2(0.f, 0.f);
+    bool page = false;
+    auto scale_id = [&](int tile) {
+      const int j = tile * kKeys + BK * ct;
+      sid = -1;
+      if (ct < CH && j < sp.end) sid = p.table[r * p.cols + (j >> p.shift)];
+    };
+    auto scale = [&]() {
+      page = sid >= 0 && sid < p.pages;
+      sc = make_float2(0.f, 1.f);
+      if (page) {
+        const int64_t tile = (int64_t)sid * p.heads + h;
+        sc = make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
+      }
+    };
     if (nt > 0) {
       ids(ka, id);
       load(ka, 0, id, ku);
       load(ka, 1, id, vu);
+      scale_id(ka);
+      scale();
+      if (nt > 1) {
+        ids(ka + 1, id);
+        scale_id(ka + 1);
+      }
     }
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
       const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-      // scales of this tile's blocks of 16 keys
-      float2 sc = make_float2(0.f, -INFINITY);
-      bool page = false;
-      if (ct < 8) {
-        const int j = (ka + i) * kKeys + 16 * ct;
-        const int64_t at = j < sp.end ? p.table[r * p.cols + j / p.page] : -1;
-        page = at >= 0 && at < p.pages;
-        if (page) {
-          const int64_t tile = at * p.heads + h;
-          sc = make_float2(p.scales[tile], lg2_approx(p.scales[tile + p.pages * p.heads]));
-        }
-      }
-      if (i + 1 < nt) ids(ka + i + 1, id);
       if (*stop || !wait(&kfree[b], free_parity)) break;
       if (cw == 0) {
         const unsigned bits = __ballot_sync(0xffffffffu, page);
-        if (ct < 8) meta[i & 3][ct] = sc;
+        if (ct < CH) meta[i & 3][ct] = make_float2(sc.x, lg2_approx(sc.y));
         if (ct == 0) valid[i & 3] = (int)bits;
       }
       store(sK + b * kTileBytes, ku);
       fence_proxy_async();
       mbar_arrive(&kfull[b]);
-      if (i + 1 < nt) load(ka + i + 1, 0, id, ku);
+      if (i + 1 < nt) {
+        load(ka + i + 1, 0, id, ku);
+        scale();
+      }
       if (*stop || !wait(&vfree[b], free_parity)) break;
       store(sV + b * kTileBytes, vu);
       fence_proxy_async();
       mbar_arrive(&vfull[b]);
       if (i + 1 < nt) load(ka + i + 1, 1, id, vu);
+      if (i + 2 < nt) {
+        ids(ka + i + 2, id);
+        scale_id(ka + i + 2);
+      }
     }
-  } else if (lane == 0 && nt > 0) {
+  } else {
+    set_regs_down<kIssueRegs>();
+  }
+  if (warp == kSoftWarps + kConvWarps && lane == 0 && nt > 0) {
     // ======================= products =======================
     const uint64_t q0 = sdesc(smem_u32(sQ), 16, 1024), q1 = sdesc(smem_u32(sQ + kTileBytes), 16, 1024);
     auto qk = [&](int t, int i) {
       const uint64_t k = sdesc(smem_u32(sK + (i & 1) * kTileBytes), 16, 1024);
-#pragma unroll
+#pragma unroll 2
       for (int s = 0; s < DIM / 16; ++s) {
         const uint32_t off = (s >> 2) * (kKeys * 128) + (s & 3) * 32;
         umma(tmem + t * kKeys, dadd(t ? q1 : q0, off), dadd(k, off), kIdQK, s > 0);
@@ -403,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     };
     auto pv = [&](int t, int i) {
       const uint64_t v = sdesc(smem_u32(sV + (i & 1) * kTileBytes), kKeys * 128, 1024);
-#pragma unroll
+#pragma unroll 2
       for (int s = 0; s < kKeys / 16; ++s)
         umma_ts(tmem + 256 + t * 128, tmem + t * kKeys + 8 * s, dadd(v, s * 2048), kIdPV, i > 0 || s > 0);
     };
@@ -441,53 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     wait(&odone, 0);
   }
 
-  // ---- outputs ----
-  if (warp < kSoftWarps) {
-    const int t = warp / 4;
-    const bool any = nt > 0 && done;
-    bool ok = true;
-    if (any) {
-      ok = __all_sync(0xffffffffu, wait(&odone, 0));
-      tc_fence_after();
-    }
-    const uint32_t o_col = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + t * 128;
-    const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
-    const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + hg;
-    float* part = a.ws + ((int64_t)blockIdx.x * kRows + i_row) * (DIM + 4);
-    if ((nt == 0 || done) && ok) {
-#pragma unroll
-      for (int c = 0; c < DIM / 32; ++c) {
-        float v[32];
-        if (any) {
-          tmem_ld32(o_col + 32 * c, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        }
-        if (mine) {
-          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            // where nothing was seen the factor is 0 and O holds finite sums or zeros
-            const float f0 = v[e] * fac, f1 = v[e + 2] * fac, f2 = v[e + 1] * fac, f3 = v[e + 3] * fac;
-            const float f4 = v[e + 4] * fac, f5 = v[e + 6] * fac, f6 = v[e + 5] * fac, f7 = v[e + 7] * fac;
-            if (a.splits == 1) {
-              *reinterpret_cast<uint4*>(p.o + at * DIM + 32 * c + e) =
-                  make_uint4(pack_bf16(f0, f1), pack_bf16(f2, f3), pack_bf16(f4, f5), pack_bf16(f6, f7));
-            } else {
-              *reinterpret_cast<float4*>(part + 32 * c + e) = make_float4(f0, f1, f2, f3);
-              *reinterpret_cast<float4*>(part + 32 * c + e + 4) = make_float4(f4, f5, f6, f7);
-            }
-          }
-        }
-      }
-      if (mine) {
-        if (a.splits > 1) part[DIM] = lse2;
-        else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
-      }
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -543,13 +580,13 @@ int splits_of(const Kv8Params& p) {
   return n < 1 ? 1 : (int)n;
 }
 
-template <int MODE, int DIM>
+template <int MODE, int DIM, int CH>
 gdn_status run(const PrefillArgs& a, cudaStream_t st) {
   const Kv8Params& p = a.p;
   const int64_t blocks = (int64_t)a.blocks * p.rows * p.heads;
   if (blocks * a.splits > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
   constexpr int bytes = 6 * kKeys * DIM * 2 + 1024;
-  auto kern = kv8_prefill_kernel<MODE, DIM>;
+  auto kern = kv8_prefill_kernel<MODE, DIM, CH>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
   kern<<<(unsigned)(blocks * a.splits), kThreads, bytes, st>>>(a);
@@ -574,9 +611,14 @@ gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* works
   a.ws = static_cast<float*>(workspace);
   a.blocks = (int)blocks_of(p);
   a.splits = splits_of(p);
+  // pages of 64 and 128 tokens: two scales per tile of keys (their per-row work is
+  // four times that of one per 16 keys otherwise)
+  auto pick = [&](auto two, auto eight) { return p.page >= 64 ? two(a, st) : eight(a, st); };
   if (mode == GDN_QDQ_E4M3)
-    return dim == 128 ? run<GDN_QDQ_E4M3, 128>(a, st) : run<GDN_QDQ_E4M3, 64>(a, st);
-  return dim == 128 ? run<GDN_QDQ_INT8, 128>(a, st) : run<GDN_QDQ_INT8, 64>(a, st);
+    return dim == 128 ? pick(run<GDN_QDQ_E4M3, 128, 2>, run<GDN_QDQ_E4M3, 128, 8>)
+                      : pick(run<GDN_QDQ_E4M3, 64, 2>, run<GDN_QDQ_E4M3, 64, 8>);
+  return dim == 128 ? pick(run<GDN_QDQ_INT8, 128, 2>, run<GDN_QDQ_INT8, 128, 8>)
+                    : pick(run<GDN_QDQ_INT8, 64, 2>, run<GDN_QDQ_INT8, 64, 8>);
 }
 
 int kv8_prefill_device_error(bool reset) {
