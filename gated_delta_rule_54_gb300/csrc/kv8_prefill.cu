@@ -6,9 +6,10 @@
 //     S = Q K^T   (tcgen05, fp16 x fp16 -> fp32 in TMEM)
 //     P = 2^(s - reference)  (one thread per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
-// Warps 0-3 and 4-7 are the rows of the two tiles; warps 8-11 turn code bytes
-// into fp16 (exact) and place them as swizzled operand tiles; one lane of warp 12
-// issues the products, those of one tile while the rows of the other compute.
+// Warp 13 brings the codes of 128 keys by TMA (a box per page); warps 8-11 turn them
+// into fp16 (exact), as swizzled operand tiles; one lane of warp 12 issues the
+// products, those of one tile while the rows of the other compute; warps 0-3 and
+// 4-7 are the rows of the two tiles.
 //
 // Products of fp16 codes bound it together with shared memory: per 128 keys the
 // two tiles' operands are read at the rate of the products, and the converted
@@ -33,13 +34,14 @@ __device__ int g_kv8_prefill_error;
 
 constexpr int kKeys = 128, kRows = 256;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 512;  // four warpgroups; of the last, one lane issues the products
+constexpr int kThreads = 512;  // four warpgroups; of the last, warp 12 issues and warp 13 loads
 // registers per thread of the warpgroups: together what the launch gave (4 x 128)
-constexpr int kSoftRegs = 176, kConvRegs = 112, kIssueRegs = 48;
+constexpr int kSoftRegs = 200, kConvRegs = 64, kIssueRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs == 4 * 128, "register shares");
 
 struct PrefillArgs {
   Kv8Params p;
+  CUtensorMap map;  // codes, a page of a head per box
   float* ws;   // splits > 1: parts [block][split][256][DIM + 1 ...]
   int blocks;  // 256-row blocks of a row's queries
   int splits;  // CTAs that share the keys of a block
@@ -50,12 +52,25 @@ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] B: row i of A in lane i, two fp16 per column
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+// Products with descriptors given as the low word (start address and LBO) and the
+// common high word, so that stepping through a tile is one 32-bit add.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // SBO 1024, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc));
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
+}
+// A in TMEM: row i in lane i, two fp16 per column
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %4};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
 }
 // 32 consecutive fp32 columns of this thread's lane; valid after tmem_wait_ld of them
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -133,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone;
+  __shared__ __align__(8) uint64_t cfull[2], cfree[2];  // codes of K, of V
   __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
   __shared__ int valid[4];        // bit c: the block has a page
   __shared__ uint32_t tmem_slot;
@@ -141,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned char *sQ = smem, *sK = smem + 2 * kTileBytes, *sV = smem + 4 * kTileBytes;
+  unsigned char* sC = smem + 6 * kTileBytes;  // codes: K, V
 
   // ---- which rows and keys (long blocks of rows first) ----
   const int64_t rh = p.rows * p.heads;
@@ -174,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
       mbar_init(&kfree[i], 1), mbar_init(&vfree[i], 1);
       mbar_init(&sfull[i], 1), mbar_init(&pready[i], 128);
+      mbar_init(&cfull[i], 1), mbar_init(&cfree[i], kConvWarps * 32);
     }
     mbar_init(&odone, 1);
     abort_flag = 0;
@@ -375,121 +393,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   } else if (warp < kSoftWarps + kConvWarps) {
     set_regs_down<kConvRegs>();
     // ======================= codes to fp16 =======================
-    const int ct = tid - kSoftWarps * 32;
-    // quads of lanes read 64 bytes of a row; eight lanes store to eight banks groups
-    const int cw = ct / 32;
+    // a lane takes 16 codes at a time; the two rows of eight neighbouring lanes are
+    // chosen so that their loads and their stores each fall on different banks
+    const int ct = tid - kSoftWarps * 32, cw = ct / 32;
+    constexpr int kPer = DIM / 16, kStep = 2048 / DIM;
     const int unit = DIM == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
-    const int sub = DIM == 128 ? ((lane >> 2) & 1) | ((lane >> 4) & 1) << 1 : lane >> 2;
-    constexpr int kPer = DIM == 128 ? 8 : 4, kStep = DIM == 128 ? 16 : 32, kSub = DIM == 128 ? 4 : 8;
-    const int myrow = cw * kSub + sub;
-    auto ids = [&](int tile, int (&id)[kPer]) {
+    const int r8 = DIM == 128 ? (lane >> 4 & 1) * 2 : lane >> 2;
+    // 128-byte rows: (0 5) (1 4) (2 7) (3 6), the even warps the first of each two pairs
+    const int row0c = DIM == 128 ? (cw / 2) * 8 + (((r8 + (cw & 1)) ^ ((lane >> 2 & 1) ? 5 : 0)))
+                                 : cw * 8 + r8;
+    auto convert = [&](const unsigned char* from, unsigned char* to) {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        const int j = tile * kKeys + myrow + e * kStep;
-        id[e] = -1;
-        if (j < sp.end) id[e] = p.table[r * p.cols + (j >> p.shift)];
-        if (id[e] >= p.pages) id[e] = -1;
-      }
-    };
-    auto load = [&](int tile, int kv, const int (&id)[kPer], uint4 (&u)[kPer]) {
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int j = tile * kKeys + myrow + e * kStep;
-        u[e] = make_uint4(0, 0, 0, 0);
-        if (id[e] >= 0)
-          u[e] = *reinterpret_cast<const uint4*>(
-              p.codes + (((kv * p.pages + id[e]) * p.heads + h) * p.page + (j & (p.page - 1))) * DIM + 16 * unit);
-      }
-    };
-    auto store = [&](unsigned char* to, const uint4 (&u)[kPer]) {
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int row = myrow + e * kStep;
+        const int row = row0c + e * kStep;
+        const int at = DIM == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
+                                  : row * 64 + ((unit ^ (row >> 1 & 3)) << 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(from + at);
         uint4 lo, hi;
-        kv8_half2<MODE>(u[e].x, lo.x, lo.y);
-        kv8_half2<MODE>(u[e].y, lo.z, lo.w);
-        kv8_half2<MODE>(u[e].z, hi.x, hi.y);
-        kv8_half2<MODE>(u[e].w, hi.z, hi.w);
+        kv8_half2<MODE>(u.x, lo.x, lo.y);
+        kv8_half2<MODE>(u.y, lo.z, lo.w);
+        kv8_half2<MODE>(u.z, hi.x, hi.y);
+        kv8_half2<MODE>(u.w, hi.z, hi.w);
         *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
         *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
       }
+      fence_proxy_async();
     };
-    // what a step needs was asked for a step before: page ids for the codes and
-    // scales of the next tile, those for this one
-    int id[kPer], sid = -1;
-    uint4 ku[kPer], vu[kPer];
-    float2 sc = make_float2(0.f, 0.f);
-    bool page = false;
-    auto scale_id = [&](int tile) {
-      const int j = tile * kKeys + BK * ct;
-      sid = -1;
-      if (ct < CH && j < sp.end) sid = p.table[r * p.cols + (j >> p.shift)];
-    };
-    auto scale = [&]() {
-      page = sid >= 0 && sid < p.pages;
-      sc = make_float2(0.f, 1.f);
-      if (page) {
-        const int64_t tile = (int64_t)sid * p.heads + h;
-        sc = make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
-      }
-    };
-    if (nt > 0) {
-      ids(ka, id);
-      load(ka, 0, id, ku);
-      load(ka, 1, id, vu);
-      scale_id(ka);
-      scale();
-      if (nt > 1) {
-        ids(ka + 1, id);
-        scale_id(ka + 1);
-      }
-    }
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
       const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-      if (*stop || !wait(&kfree[b], free_parity)) break;
-      if (cw == 0) {
-        const unsigned bits = __ballot_sync(0xffffffffu, page);
-        if (ct < CH) meta[i & 3][ct] = make_float2(sc.x, lg2_approx(sc.y));
-        if (ct == 0) valid[i & 3] = (int)bits;
-      }
-      store(sK + b * kTileBytes, ku);
-      fence_proxy_async();
+      if (*stop || !wait(&cfull[0], i & 1) || !wait(&kfree[b], free_parity)) break;
+      convert(sC, sK + b * kTileBytes);
       mbar_arrive(&kfull[b]);
-      if (i + 1 < nt) {
-        load(ka + i + 1, 0, id, ku);
-        scale();
-      }
-      if (*stop || !wait(&vfree[b], free_parity)) break;
-      store(sV + b * kTileBytes, vu);
-      fence_proxy_async();
+      mbar_arrive(&cfree[0]);
+      if (*stop || !wait(&cfull[1], i & 1) || !wait(&vfree[b], free_parity)) break;
+      convert(sC + kKeys * DIM, sV + b * kTileBytes);
       mbar_arrive(&vfull[b]);
-      if (i + 1 < nt) load(ka + i + 1, 1, id, vu);
-      if (i + 2 < nt) {
-        ids(ka + i + 2, id);
-        scale_id(ka + i + 2);
-      }
+      mbar_arrive(&cfree[1]);
     }
   } else {
     set_regs_down<kIssueRegs>();
   }
-  if (warp == kSoftWarps + kConvWarps && lane == 0 && nt > 0) {
+  if (warp == kSoftWarps + kConvWarps + 1) {
+    // ======================= codes by TMA =======================
+    // page ids and scales were asked for a tile before
+    const int boxes = kKeys >> p.shift;
+    auto page_of = [&](int tile) {
+      const int j = tile * kKeys + (lane << p.shift);
+      return lane < boxes && j < sp.end ? p.table[r * p.cols + (j >> p.shift)] : -1;
+    };
+    auto scale_of = [&](int id) {
+      if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
+      const int64_t tile = (int64_t)id * p.heads + h;
+      return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
+    };
+    int id = -1, id1 = -1, issued[2] = {0, 0};
+    float2 sc = make_float2(0.f, 0.f);
+    if (nt > 0) id = page_of(ka), sc = scale_of(id);
+    if (nt > 1) id1 = page_of(ka + 1);
+    for (int i = 0; i < nt; ++i) {
+      const bool have = id >= 0 && id < p.pages;
+      // block c of the scales lies in page c >> (log2 of blocks per page)
+      const int from = (lane * BK) >> p.shift;
+      const float ks = __shfl_sync(0xffffffffu, sc.x, from & 31);
+      const float vs = __shfl_sync(0xffffffffu, sc.y, from & 31);
+      const bool there = __shfl_sync(0xffffffffu, (int)have, from & 31);
+      const unsigned bits = __ballot_sync(0xffffffffu, there && lane < CH);
+      const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have)) * (DIM << p.shift);
+      bool ok = true;
+      #pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = __all_sync(0xffffffffu, !*stop && wait(&cfree[kv], (i & 1) ^ 1));
+        if (!ok) break;
+        if (kv == 0) {
+          if (lane < CH) meta[i & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
+          if (lane == 0) valid[i & 3] = (int)bits;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(&cfull[kv], bytes);
+        __syncwarp();
+        issued[kv] = i + 1;
+        if (have)
+          tma_load_3d(sC + kv * kKeys * DIM + (lane << p.shift) * DIM, &a.map, 0, 0,
+                      (int)((kv * p.pages + id) * p.heads + h), &cfull[kv]);
+      }
+      if (!ok) break;
+      id = id1;
+      sc = i + 1 < nt ? scale_of(id) : sc;
+      id1 = i + 2 < nt ? page_of(ka + i + 2) : -1;
+    }
+    // no copy is in flight when the CTA ends, whatever ended the loop
+    if (issued[0] > 0) mbar_wait(&cfull[0], (issued[0] - 1) & 1);
+    if (issued[1] > 0) mbar_wait(&cfull[1], (issued[1] - 1) & 1);
+  } else if (warp == kSoftWarps + kConvWarps && lane == 0 && nt > 0) {
     // ======================= products =======================
-    const uint64_t q0 = sdesc(smem_u32(sQ), 16, 1024), q1 = sdesc(smem_u32(sQ + kTileBytes), 16, 1024);
+    const uint32_t dq = desc_lo(smem_u32(sQ), 16), dk = desc_lo(smem_u32(sK), 16);
+    const uint32_t dv = desc_lo(smem_u32(sV), kKeys * 128);
+    constexpr uint32_t kTileStep = kTileBytes >> 4;
     auto qk = [&](int t, int i) {
-      const uint64_t k = sdesc(smem_u32(sK + (i & 1) * kTileBytes), 16, 1024);
-#pragma unroll 2
+      const uint32_t q = dq + t * kTileStep, k = dk + (i & 1) * kTileStep;
+#pragma unroll
       for (int s = 0; s < DIM / 16; ++s) {
-        const uint32_t off = (s >> 2) * (kKeys * 128) + (s & 3) * 32;
-        umma(tmem + t * kKeys, dadd(t ? q1 : q0, off), dadd(k, off), kIdQK, s > 0);
+        const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
+        umma_ss(tmem + t * kKeys, q + off, k + off, kIdQK, s > 0);
       }
       umma_commit(&sfull[t]);
     };
     auto pv = [&](int t, int i) {
-      const uint64_t v = sdesc(smem_u32(sV + (i & 1) * kTileBytes), kKeys * 128, 1024);
-#pragma unroll 2
+      const uint32_t v = dv + (i & 1) * kTileStep;
+#pragma unroll
       for (int s = 0; s < kKeys / 16; ++s)
-        umma_ts(tmem + 256 + t * 128, tmem + t * kKeys + 8 * s, dadd(v, s * 2048), kIdPV, i > 0 || s > 0);
+        umma_ts(tmem + 256 + t * 128, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), kIdPV,
+                i > 0 || s > 0);
     };
     bool ok = wait(&kfull[0], 0);
     if (ok) {
@@ -581,11 +596,17 @@ int splits_of(const Kv8Params& p) {
 }
 
 template <int MODE, int DIM, int CH>
-gdn_status run(const PrefillArgs& a, cudaStream_t st) {
+gdn_status run(PrefillArgs& a, cudaStream_t st) {
   const Kv8Params& p = a.p;
+  a.map = CUtensorMap();
+  if (p.pages > 0 &&
+      !make_map_3d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, DIM, p.page,
+                   (uint64_t)(2 * p.pages * p.heads), DIM, DIM, p.page,
+                   DIM == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return GDN_ERR_CUDA;
   const int64_t blocks = (int64_t)a.blocks * p.rows * p.heads;
   if (blocks * a.splits > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  constexpr int bytes = 6 * kKeys * DIM * 2 + 1024;
+  constexpr int bytes = (6 * 2 + 2) * kKeys * DIM + 1024;
   auto kern = kv8_prefill_kernel<MODE, DIM, CH>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
