@@ -52,6 +52,12 @@ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t lead;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
+  return lead != 0;
+}
 // Products with descriptors given as the low word (start address and LBO) and the
 // common high word, so that stepping through a tile is one 32-bit add.
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // SBO 1024, 128-byte swizzle
@@ -154,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);  // uniform
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned char *sQ = smem, *sK = smem + 2 * kTileBytes, *sV = smem + 4 * kTileBytes;
   unsigned char* sC = smem + 6 * kTileBytes;  // codes: K, V
@@ -209,25 +216,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     const int row = i_row % 128;
     const __nv_bfloat16* x8 = p.x + kv8_at(p, r, sp.base, qi, p.x_row, p.x_token) +
                               (h * p.group + hg) * p.x_head;
-    float most = 0.f;
-    if (mine) {
-      kv8_seen(p, sp, qi, beg, end);
-#pragma unroll 4
-      for (int u = 0; u < DIM / 8; ++u) {
-        float f[8];
-        bf16x8(*reinterpret_cast<const uint4*>(x8 + 8 * u), f);
+    if (mine) kv8_seen(p, sp, qi, beg, end);
+    uint4 q[DIM / 8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
-      }
+    for (int u = 0; u < DIM / 8; ++u)
+      q[u] = mine ? *reinterpret_cast<const uint4*>(x8 + 8 * u) : make_uint4(0, 0, 0, 0);
+    float most = 0.f;
+#pragma unroll
+    for (int u = 0; u < DIM / 8; ++u) {
+      float f[8];
+      bf16x8(q[u], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
     }
     float up, back;
     kv8_q_factor(most, up, back);
     rowfac = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
     if (p.scale < 0.f) up = -up;
-#pragma unroll 4
+#pragma unroll
     for (int u = 0; u < DIM / 8; ++u) {
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (mine) bf16x8(*reinterpret_cast<const uint4*>(x8 + 8 * u), f);
+      float f[8];
+      bf16x8(q[u], f);
       *reinterpret_cast<uint4*>(to + unit_at(row, u)) =
           make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
                      pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
@@ -238,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  volatile int* stop = &abort_flag;
+  // every wait is bounded, so when one gives up the other roles' do as well
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait(bar, parity)) return true;
-    *stop = 1;
+    abort_flag = 1;
     return false;
   };
 
@@ -265,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     const bool run = t == 0 || two;  // the tile has rows
     bool ok = true;
     for (int i = 0; i < nt && run; ++i) {
-      if (*stop || !__all_sync(0xffffffffu, wait(&sfull[t], i & 1))) {
+      if (!__all_sync(0xffffffffu, wait(&sfull[t], i & 1))) {
         ok = false;
         break;
       }
@@ -422,11 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     for (int i = 0; i < nt; ++i) {
       const int b = i & 1;
       const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-      if (*stop || !wait(&cfull[0], i & 1) || !wait(&kfree[b], free_parity)) break;
+      if (!wait(&cfull[0], i & 1) || !wait(&kfree[b], free_parity)) break;
       convert(sC, sK + b * kTileBytes);
       mbar_arrive(&kfull[b]);
       mbar_arrive(&cfree[0]);
-      if (*stop || !wait(&cfull[1], i & 1) || !wait(&vfree[b], free_parity)) break;
+      if (!wait(&cfull[1], i & 1) || !wait(&vfree[b], free_parity)) break;
       convert(sC + kKeys * DIM, sV + b * kTileBytes);
       mbar_arrive(&vfull[b]);
       mbar_arrive(&cfree[1]);
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     const int boxes = kKeys >> p.shift;
     auto page_of = [&](int tile) {
       const int j = tile * kKeys + (lane << p.shift);
-      return lane < boxes && j < sp.end ? p.table[r * p.cols + (j >> p.shift)] : -1;
+      return lane < boxes && j < sp.end ? p.table[(int64_t)r * p.cols + (j >> p.shift)] : -1;
     };
     auto scale_of = [&](int id) {
       if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       bool ok = true;
       #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        ok = __all_sync(0xffffffffu, !*stop && wait(&cfree[kv], (i & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, wait(&cfree[kv], (i & 1) ^ 1));
         if (!ok) break;
         if (kv == 0) {
           if (lane < CH) meta[i & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
@@ -485,61 +494,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     // no copy is in flight when the CTA ends, whatever ended the loop
     if (issued[0] > 0) mbar_wait(&cfull[0], (issued[0] - 1) & 1);
     if (issued[1] > 0) mbar_wait(&cfull[1], (issued[1] - 1) & 1);
-  } else if (warp == kSoftWarps + kConvWarps && lane == 0 && nt > 0) {
+  } else if (warp == kSoftWarps + kConvWarps && nt > 0) {
     // ======================= products =======================
-    const uint32_t dq = desc_lo(smem_u32(sQ), 16), dk = desc_lo(smem_u32(sK), 16);
-    const uint32_t dv = desc_lo(smem_u32(sV), kKeys * 128);
+    // The whole warp goes through this, so that descriptors stay in uniform
+    // registers; one elected lane issues.
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+    const uint32_t dq = desc_lo(base, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
+    const uint32_t dv = desc_lo(base + 4 * kTileBytes, kKeys * 128);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
+    const bool lead = elect_one();
     auto qk = [&](int t, int i) {
       const uint32_t q = dq + t * kTileStep, k = dk + (i & 1) * kTileStep;
+      if (lead) {
 #pragma unroll
-      for (int s = 0; s < DIM / 16; ++s) {
-        const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
-        umma_ss(tmem + t * kKeys, q + off, k + off, kIdQK, s > 0);
+        for (int s = 0; s < DIM / 16; ++s) {
+          const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
+          umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
+        }
+        umma_commit(&sfull[t]);
       }
-      umma_commit(&sfull[t]);
+      __syncwarp();
     };
     auto pv = [&](int t, int i) {
       const uint32_t v = dv + (i & 1) * kTileStep;
+      if (lead) {
 #pragma unroll
-      for (int s = 0; s < kKeys / 16; ++s)
-        umma_ts(tmem + 256 + t * 128, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), kIdPV,
-                i > 0 || s > 0);
+        for (int s = 0; s < kKeys / 16; ++s)
+          umma_ts(tm + 256 + t * 128, tm + t * kKeys + 8 * s, v + s * (2048 >> 4), kIdPV,
+                  i > 0 || s > 0);
+      }
+      __syncwarp();
     };
-    bool ok = wait(&kfull[0], 0);
+    auto commit = [&](uint64_t* bar) {
+      if (lead) umma_commit(bar);
+      __syncwarp();
+    };
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait(bar, parity));
+    };
+    bool ok = all_wait(&kfull[0], 0);
     if (ok) {
       tc_fence_after();
       qk(0, 0);
       if (two) qk(1, 0);
-      umma_commit(&kfree[0]);
+      commit(&kfree[0]);
     }
     for (int i = 0; i < nt && ok; ++i) {
       const int b = i & 1, nb = (i + 1) & 1;
       const uint32_t par = (i >> 1) & 1;
-      ok = !*stop && wait(&vfull[b], par) && wait(&pready[0], i & 1);
+      ok = all_wait(&vfull[b], par) && all_wait(&pready[0], i & 1);
       if (!ok) break;
       tc_fence_after();
       pv(0, i);
       if (i + 1 < nt) {
-        ok = wait(&kfull[nb], ((i + 1) >> 1) & 1);
+        ok = all_wait(&kfull[nb], ((i + 1) >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         qk(0, i + 1);
       }
       if (two) {
-        ok = !*stop && wait(&pready[1], i & 1);
+        ok = all_wait(&pready[1], i & 1);
         if (!ok) break;
         tc_fence_after();
         pv(1, i);
         if (i + 1 < nt) qk(1, i + 1);
       }
-      umma_commit(&vfree[b]);
-      if (i + 1 < nt) umma_commit(&kfree[nb]);
+      commit(&vfree[b]);
+      if (i + 1 < nt) commit(&kfree[nb]);
     }
-    umma_commit(&odone);  // completes with every product issued
+    commit(&odone);  // completes with every product issued
     wait(&odone, 0);
   }
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
