@@ -95,7 +95,8 @@ class GdnBeamProblem(ctypes.Structure):
     ]
 
 
-_KP, _KL, _BP = (ctypes.POINTER(t) for t in (GdnKv8Problem, GdnKv8Pool, GdnBeamProblem))
+# these take the structure (by reference) or its packed bytes
+_KP = _KL = _BP = _P
 SIGNATURES = {
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_abi_version": (ctypes.c_int, []),

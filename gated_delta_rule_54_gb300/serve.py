@@ -8,17 +8,31 @@ page.  Everything runs on the current stream and nothing waits for the host.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional, Sequence
 
 import torch
 
-from ._lib import (DTYPES, QDQ_MODES, GdnBeamProblem, GdnError, GdnKv8Pool, GdnKv8Problem, check,
-                   load)
-from .api import _ptr, _stream
+from . import _lib
+from ._lib import DTYPES, QDQ_MODES, GdnError, load
 
-_i32 = torch.int32
-_byref = ctypes.byref
+_i32, _u8, _f32, _bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_MODES = {k: v for k, v in QDQ_MODES.items() if v}
+_XTYPES = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"], torch.float32: DTYPES["fp32"]}
+# gdn_kv8_problem, gdn_kv8_pool and gdn_beam_problem as the C compiler lays them out
+_KV8 = struct.Struct("@3q10ifP6q").pack
+_POOL = struct.Struct("@2q5i0q").pack
+_BEAM = struct.Struct("@2q5i0q").pack
+_TOO_SMALL = -5  # GDN_ERR_WORKSPACE_TOO_SMALL
+
+
+def _fns():
+    return _lib._lib or load()
+
+
+def _raise(fn, status):
+    raise GdnError(fn, status)
 
 
 def _need(cond, text):
@@ -26,11 +40,18 @@ def _need(cond, text):
         raise ValueError(text)
 
 
-def _flat(name, t, dtype, device):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device == device,
-          "%s must be a CUDA tensor on %s" % (name, device))
-    _need(t.dtype == dtype, "%s must be %s" % (name, dtype))
-    _need(t.is_contiguous(), "%s must be contiguous" % name)
+def _plain(t, dtype, dev):
+    """t is a contiguous tensor of this type on CUDA device number dev."""
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _say(dev, *named):
+    """Raises for the first of (name, tensor, dtype) that is not plain."""
+    for name, t, dtype in named:
+        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev,
+              "%s must be a CUDA tensor on cuda:%d" % (name, dev))
+        _need(t.dtype == dtype, "%s must be %s" % (name, dtype))
+        _need(t.is_contiguous(), "%s must be contiguous" % name)
 
 
 def kv8_pool(layers, pages, heads, dim, page=64, device="cuda"):
@@ -39,56 +60,59 @@ def kv8_pool(layers, pages, heads, dim, page=64, device="cuda"):
             torch.zeros(layers, 2, pages, heads, dtype=torch.float32, device=device))
 
 
-def _strides(x):
+def _strides(x, shape):
     """(row, token, head) strides in elements of [rows, tokens, heads, dim] or [total, heads, dim]."""
-    s, n = x.stride(), x.shape
-    _need(s[-1] == 1 or n[-1] == 1, "the last dim must be contiguous")
-    s = [a if b > 1 else 0 for a, b in zip(s, n)]
-    return (s[0], s[1], s[2]) if x.dim() == 4 else (0, s[0], s[1])
+    s = x.stride()
+    _need(s[-1] == 1 or shape[-1] == 1, "the last dim must be contiguous")
+    if len(shape) == 4:
+        a, b, c = s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0
+        return a, b, c
+    return 0, s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0
 
 
 def _problem(x, v, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, scale, causal,
-             window) -> GdnKv8Problem:
-    dev = codes.device
-    _flat("codes", codes, torch.uint8, dev)
-    _flat("scales", scales, torch.float32, dev)
-    _flat("table", table, _i32, dev)
-    _flat("lengths", lengths, _i32, dev)
-    _need(codes.dim() == 5 and codes.shape[0] == 2, "codes must be [2, pages, heads, page, dim]")
-    _, pages, heads, page, dim = codes.shape
-    _need(scales.shape == codes.shape[:3], "scales must be [2, pages, heads]")
-    _need(table.dim() == 2 and lengths.shape == (table.shape[0],),
-          "table must be [rows, columns] and lengths [rows]")
-    _need(x.is_cuda and x.device == dev, "q, k, v must be on %s" % dev)
-    _need(mode in QDQ_MODES, "mode must be one of %s, got %r" % (sorted(QDQ_MODES), mode))
-    p = GdnKv8Problem()
-    p.pages, p.rows, p.cols = pages, table.shape[0], table.shape[1]
-    p.heads, p.dim, p.page = heads, dim, page
+             window):
+    """The packed gdn_kv8_problem."""
+    dev = codes.get_device()
+    if not (_plain(codes, _u8, dev) and _plain(scales, _f32, dev) and _plain(table, _i32, dev)
+            and _plain(lengths, _i32, dev) and dev >= 0):
+        _need(dev >= 0, "codes must be a CUDA tensor")
+        _say(dev, ("codes", codes, _u8), ("scales", scales, _f32), ("table", table, _i32),
+             ("lengths", lengths, _i32))
+    cs, shape = codes.shape, x.shape
+    _need(len(cs) == 5 and cs[0] == 2, "codes must be [2, pages, heads, page, dim]")
+    _, pages, heads, page, dim = cs
+    rows, cols = table.shape if table.dim() == 2 else (-1, -1)
+    _need(scales.shape == cs[:3], "scales must be [2, pages, heads]")
+    _need(rows >= 0 and lengths.shape == (rows,), "table must be [rows, columns] and lengths [rows]")
+    _need(x.get_device() == dev, "q, k, v must be on cuda:%d" % dev)
+    m = _MODES.get(mode)
+    _need(m is not None, "mode must be one of %s, got %r" % (sorted(_MODES), mode))
     if cu_seqlens is None:
-        _need(x.dim() == 4 and x.shape[0] == p.rows, "expected [rows, tokens, heads, dim]")
-        p.total, p.tokens = x.shape[0] * x.shape[1], x.shape[1]
+        _need(len(shape) == 4 and shape[0] == rows, "expected [rows, tokens, heads, dim]")
+        tokens, cu = shape[1], 0
+        total = rows * tokens
     else:
-        _flat("cu_seqlens", cu_seqlens, _i32, dev)
-        _need(x.dim() == 3, "expected packed [total, heads, dim]")
-        _need(cu_seqlens.shape == (p.rows + 1,), "cu_seqlens must be [rows + 1]")
-        p.total = x.shape[0]
-        p.tokens = min(x.shape[0], x.shape[0] if max_seqlen is None else int(max_seqlen))
-        p.cu_seqlens = cu_seqlens.data_ptr()
-    _need(x.shape[-1] == dim, "head dim %d is not the cache's %d" % (x.shape[-1], dim))
-    _need(heads > 0 and x.shape[-2] % heads == 0 and x.shape[-2] > 0,
-          "%d heads cannot share %d K/V heads" % (x.shape[-2], heads))
-    p.group = x.shape[-2] // heads
-    p.mode = QDQ_MODES[mode]
-    p.dtype = DTYPES.get({torch.bfloat16: "bf16", torch.float16: "fp16",
-                          torch.float32: "fp32"}.get(x.dtype), 99)
-    p.causal, p.window, p.scale = int(bool(causal)), int(window), scale
-    p.x_row, p.x_token, p.x_head = _strides(x)
+        _say(dev, ("cu_seqlens", cu_seqlens, _i32))
+        _need(len(shape) == 3, "expected packed [total, heads, dim]")
+        _need(cu_seqlens.shape == (rows + 1,), "cu_seqlens must be [rows + 1]")
+        total = tokens = shape[0]
+        if max_seqlen is not None and max_seqlen < tokens:
+            tokens = int(max_seqlen)
+        cu = cu_seqlens.data_ptr()
+    xh = shape[-2]
+    _need(shape[-1] == dim, "head dim %d is not the cache's %d" % (shape[-1], dim))
+    _need(heads > 0 and xh > 0 and xh % heads == 0,
+          "%d heads cannot share %d K/V heads" % (xh, heads))
+    strides = _strides(x, shape)
+    more = strides
     if v is not None:
-        _need(v.is_cuda and v.device == dev and v.dtype == x.dtype and v.shape == x.shape,
+        _need(v.get_device() == dev and v.dtype is x.dtype and v.shape == shape,
               "k and v must have the same shape, type and device")
-        _need(p.group == 1, "k and v must have the cache's heads")
-        p.v_row, p.v_token, p.v_head = _strides(v)
-    return p
+        _need(xh == heads, "k and v must have the cache's heads")
+        more = _strides(v, shape)
+    return _KV8(pages, rows, total, tokens, cols, heads, xh // heads, dim, page, m,
+                _XTYPES.get(x.dtype, 99), causal, window, scale, cu, *strides, *more)
 
 
 def kv8_append(k, v, codes, scales, table, start, cu_seqlens=None, max_seqlen=None, mode="e4m3"):
@@ -99,10 +123,11 @@ def kv8_append(k, v, codes, scales, table, start, cu_seqlens=None, max_seqlen=No
     multiples of 8, last dim contiguous.  codes, scales: one layer's cache.  A page's scale is
     max |x| / 448 (E4M3) or / 127 (INT8) over its tokens so far; where a new token raises it,
     the page's older codes are rounded again."""
-    p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, True, 0)
-    check("gdn_kv8_append", load().gdn_kv8_append(
-        _byref(p), k.data_ptr(), v.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-        table.data_ptr(), start.data_ptr(), _stream(codes.device)))
+    p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, 1, 0)
+    st = _fns().gdn_kv8_append(p, k.data_ptr(), v.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                               table.data_ptr(), start.data_ptr(), _raw_stream(codes.get_device()))
+    if st:
+        _raise("gdn_kv8_append", st)
 
 
 def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=None, mode="e4m3",
@@ -117,86 +142,96 @@ def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=
     its own position (``causal``), and with ``window`` > 0 only the last ``window`` of them.
     scale defaults to dim ** -0.5.  Returns o bf16 like q and, with ``need_lse``, the log of
     the sum of exponentials f32 [..., query heads]; a query that sees nothing gets 0 and -inf."""
-    dev = codes.device
     p = _problem(q, None, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode,
-                 codes.shape[-1] ** -0.5 if scale is None else float(scale), causal, window)
-    lib = load()
+                 codes.shape[-1] ** -0.5 if scale is None else scale, 1 if causal else 0, window)
+    dev = codes.get_device()
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(q.shape, dtype=_bf16, device=codes.device)
     else:
-        _flat("out", out, torch.bfloat16, dev)
+        _say(dev, ("out", out, _bf16))
         _need(out.shape == q.shape, "out must have q's shape")
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if need_lse else None
-    need = lib.gdn_kv8_workspace_bytes(_byref(p))
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    check("gdn_kv8_attention", lib.gdn_kv8_attention(
-        _byref(p), q.data_ptr(), codes.data_ptr(), scales.data_ptr(), table.data_ptr(),
-        lengths.data_ptr(), out.data_ptr(), lse.data_ptr() if need_lse else None,
-        _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream(dev)))
+    lse = torch.empty(q.shape[:-1], dtype=_f32, device=codes.device) if need_lse else None
+    lib = _fns()
+
+    def call(ws):
+        return lib.gdn_kv8_attention(
+            p, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), table.data_ptr(),
+            lengths.data_ptr(), out.data_ptr(), lse.data_ptr() if need_lse else None,
+            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+            _raw_stream(dev))
+
+    st = call(workspace)
+    if st == _TOO_SMALL and workspace is None:
+        st = call(torch.empty(lib.gdn_kv8_workspace_bytes(p), dtype=_u8, device=codes.device))
+    if st:
+        _raise("gdn_kv8_attention", st)
     return (out, lse) if need_lse else out
 
 
 def kv8_workspace_bytes(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=None,
                         mode="e4m3", window=0) -> int:
     """Bytes of the workspace that kv8_attention takes for these arguments."""
-    p = _problem(q, None, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, 1.0, True,
-                 window)
-    return int(load().gdn_kv8_workspace_bytes(_byref(p)))
+    return int(_fns().gdn_kv8_workspace_bytes(
+        _problem(q, None, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, 1.0, 1,
+                 window)))
 
 
-def _pool_problem(codes, scales, table, lengths, refs) -> GdnKv8Pool:
-    dev = codes.device
-    _flat("codes", codes, torch.uint8, dev)
-    _flat("scales", scales, torch.float32, dev)
-    _need(codes.dim() == 6 and codes.shape[1] == 2,
-          "codes must be [layers, 2, pages, heads, page, dim]")
-    _need(scales.shape == codes.shape[:4], "scales must be [layers, 2, pages, heads]")
-    p = GdnKv8Pool()
-    p.planes, p.pages, p.heads, p.page, p.dim = 2 * codes.shape[0], *codes.shape[2:]
-    p.rows, p.cols = 1, 0
+def _pool_problem(codes, scales, table=None, lengths=None, refs=None):
+    """The packed gdn_kv8_pool."""
+    dev = codes.get_device()
+    if not (_plain(codes, _u8, dev) and _plain(scales, _f32, dev) and dev >= 0):
+        _need(dev >= 0, "codes must be a CUDA tensor")
+        _say(dev, ("codes", codes, _u8), ("scales", scales, _f32))
+    cs = codes.shape
+    _need(len(cs) == 6 and cs[1] == 2, "codes must be [layers, 2, pages, heads, page, dim]")
+    _need(scales.shape == cs[:4], "scales must be [layers, 2, pages, heads]")
+    rows, cols = 1, 0
     if table is not None:
-        _flat("table", table, _i32, dev)
-        _flat("lengths", lengths, _i32, dev)
-        _flat("refs", refs, _i32, dev)
-        _need(table.dim() == 2 and lengths.shape == (table.shape[0],),
+        if not (_plain(table, _i32, dev) and _plain(lengths, _i32, dev) and _plain(refs, _i32, dev)):
+            _say(dev, ("table", table, _i32), ("lengths", lengths, _i32), ("refs", refs, _i32))
+        rows, cols = table.shape if table.dim() == 2 else (-1, -1)
+        _need(rows >= 0 and lengths.shape == (rows,),
               "table must be [rows, columns] and lengths [rows]")
-        _need(refs.shape == (p.pages,), "refs must be [pages]")
-        p.rows, p.cols = table.shape
-    return p
+        _need(refs.shape == (cs[2],), "refs must be [pages]")
+    return _POOL(cs[2], rows, cols, cs[4], 2 * cs[0], cs[3], cs[5])
 
 
 def _pool_workspace(p, workspace, device):
     if workspace is None:
-        workspace = torch.empty(load().gdn_kv8_pool_workspace_bytes(_byref(p)), dtype=torch.uint8,
-                                device=device)
+        workspace = torch.empty(_fns().gdn_kv8_pool_workspace_bytes(p), dtype=_u8, device=device)
     return workspace
 
 
 def kv8_copy_pages(codes, scales, src, dst):
     """Page src[i] is copied to page dst[i], in every layer: codes and scales, in place.  The
     pages of dst are distinct and none of them is in src.  src, dst int32 [n] on the device."""
-    dev = codes.device
-    p = _pool_problem(codes, scales, None, None, None)
-    _flat("src", src, _i32, dev)
-    _flat("dst", dst, _i32, dev)
+    p, dev = _pool_problem(codes, scales), codes.get_device()
+    _say(dev, ("src", src, _i32), ("dst", dst, _i32))
     _need(src.dim() == 1 and src.shape == dst.shape, "src and dst must be [n]")
-    check("gdn_kv8_copy_pages", load().gdn_kv8_copy_pages(
-        _byref(p), codes.data_ptr(), scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
-        src.numel(), _stream(dev)))
+    st = _fns().gdn_kv8_copy_pages(p, codes.data_ptr(), scales.data_ptr(), src.data_ptr(),
+                                   dst.data_ptr(), src.numel(), _raw_stream(dev))
+    if st:
+        _raise("gdn_kv8_copy_pages", st)
 
 
 def _fork(codes, scales, table, lengths, parents, drop, refs, workspace):
-    dev = codes.device
     p = _pool_problem(codes, scales, table, lengths, refs)
-    ws = _pool_workspace(p, workspace, dev)
-    out = torch.empty_like(table), torch.empty_like(lengths), torch.empty_like(refs)
-    missing = torch.empty(1, dtype=_i32, device=dev)
-    check("gdn_kv8_fork", load().gdn_kv8_fork(
-        _byref(p), codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        refs.data_ptr(), _ptr(parents), _ptr(drop), out[0].data_ptr(), out[1].data_ptr(),
-        out[2].data_ptr(), missing.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
-    return (*out, missing)
+    which, dtype = (parents, _i32) if drop is None else (drop, torch.bool)
+    dev = codes.get_device()
+    if not (_plain(which, dtype, dev) and which.shape == lengths.shape):
+        _say(dev, ("parents" if drop is None else "rows", which, dtype))
+        _need(False, "parents (rows) must have one entry per row")
+    ws = _pool_workspace(p, workspace, codes.device)
+    t, n, r = torch.empty_like(table), torch.empty_like(lengths), torch.empty_like(refs)
+    missing = torch.empty(1, dtype=_i32, device=codes.device)
+    st = _fns().gdn_kv8_fork(
+        p, codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+        refs.data_ptr(), parents.data_ptr() if drop is None else None,
+        None if drop is None else drop.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
+        missing.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st:
+        _raise("gdn_kv8_fork", st)
+    return t, n, r, missing
 
 
 def kv8_fork(codes, scales, table, lengths, parents, refs, workspace=None):
@@ -206,16 +241,12 @@ def kv8_fork(codes, scales, table, lengths, parents, refs, workspace=None):
     the sequence and is copied, in every layer, to the lowest free pages for the others.
     Sequences that no row takes are released.  Returns new (table, lengths, refs, missing):
     missing int32 [1] counts the copies there was no free page for."""
-    _flat("parents", parents, _i32, codes.device)
-    _need(parents.shape == lengths.shape, "parents must be [rows]")
     return _fork(codes, scales, table, lengths, parents, None, refs, workspace)
 
 
 def kv8_free(codes, scales, table, lengths, rows, refs, workspace=None):
     """Releases the sequences of the rows where ``rows`` (bool [rows]) holds.  Returns new
     (table, lengths, refs)."""
-    _flat("rows", rows, torch.bool, codes.device)
-    _need(rows.shape == lengths.shape, "rows must be bool [rows]")
     return _fork(codes, scales, table, lengths, None, rows, refs, workspace)[:3]
 
 
@@ -223,33 +254,37 @@ def kv8_reserve(codes, scales, table, lengths, extra, refs, workspace=None):
     """Room for extra[r] (int32 [rows]) more tokens of each row: the lowest free pages, in row
     order.  Returns new (table, lengths, refs, missing) with lengths + extra; the tokens are
     then written by kv8_append at the old lengths."""
-    dev = codes.device
     p = _pool_problem(codes, scales, table, lengths, refs)
-    _flat("extra", extra, _i32, dev)
+    dev = codes.get_device()
+    _say(dev, ("extra", extra, _i32))
     _need(extra.shape == lengths.shape, "extra must be [rows]")
-    ws = _pool_workspace(p, workspace, dev)
-    out = torch.empty_like(table), torch.empty_like(lengths), torch.empty_like(refs)
-    missing = torch.empty(1, dtype=_i32, device=dev)
-    check("gdn_kv8_reserve", load().gdn_kv8_reserve(
-        _byref(p), table.data_ptr(), lengths.data_ptr(), refs.data_ptr(), extra.data_ptr(),
-        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), missing.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(dev)))
-    return (*out, missing)
+    ws = _pool_workspace(p, workspace, codes.device)
+    t, n, r = torch.empty_like(table), torch.empty_like(lengths), torch.empty_like(refs)
+    missing = torch.empty(1, dtype=_i32, device=codes.device)
+    st = _fns().gdn_kv8_reserve(
+        p, table.data_ptr(), lengths.data_ptr(), refs.data_ptr(), extra.data_ptr(), t.data_ptr(),
+        n.data_ptr(), r.data_ptr(), missing.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(dev))
+    if st:
+        _raise("gdn_kv8_reserve", st)
+    return t, n, r, missing
 
 
 def kv8_compact(codes, scales, table, lengths, refs, workspace=None):
     """Live pages move to the start of the pool, in every layer: with n of them, the i-th
     lowest at or above n goes to the i-th lowest free page below n.  Returns new
     (table, refs, live) with live int32 [1] = n.  Page ids held elsewhere become stale."""
-    dev = codes.device
     p = _pool_problem(codes, scales, table, lengths, refs)
-    ws = _pool_workspace(p, workspace, dev)
-    out = torch.empty_like(table), torch.empty_like(refs), torch.empty(1, dtype=_i32, device=dev)
-    check("gdn_kv8_compact", load().gdn_kv8_compact(
-        _byref(p), codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        refs.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(),
-        ws.numel(), _stream(dev)))
-    return out
+    ws = _pool_workspace(p, workspace, codes.device)
+    t, r = torch.empty_like(table), torch.empty_like(refs)
+    live = torch.empty(1, dtype=_i32, device=codes.device)
+    st = _fns().gdn_kv8_compact(
+        p, codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+        refs.data_ptr(), t.data_ptr(), r.data_ptr(), live.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(codes.get_device()))
+    if st:
+        _raise("gdn_kv8_compact", st)
+    return t, r, live
 
 
 def beam_select(logits, scores, finished=None, k: Optional[int] = None, eos=-1, workspace=None):
@@ -260,37 +295,40 @@ def beam_select(logits, scores, finished=None, k: Optional[int] = None, eos=-1, 
     A candidate scores scores + log_softmax(logits); a finished beam has one, itself with token
     ``eos``.  Order: score, then beam, then logit, then token.  Returns (scores f32, parents
     int32 = batch * beams + beam, tokens int32, finished bool), each [batch, k]."""
-    dev = logits.device
-    _need(logits.is_cuda and logits.dim() == 3, "logits must be [batch, beams, vocab] on CUDA")
+    dev = logits.get_device()
+    _need(dev >= 0 and logits.dim() == 3, "logits must be [batch, beams, vocab] on CUDA")
     b, w, v = logits.shape
     s = logits.stride()
     _need(v == 1 or s[2] == 1, "the vocabulary must be contiguous")
     row = s[1] if w > 1 else s[0] if b > 1 else v
-    _need(w == 1 or b == 1 or s[0] == w * s[1], "rows of logits must be evenly spaced")
-    _flat("scores", scores, torch.float32, dev)
+    _need(w == 1 or b == 1 or s[0] == w * row, "rows of logits must be evenly spaced")
+    if not _plain(scores, _f32, dev):
+        _say(dev, ("scores", scores, _f32))
     _need(scores.shape == (b, w), "scores must be [batch, beams]")
     if finished is not None:
-        _flat("finished", finished, torch.bool, dev)
+        if not _plain(finished, torch.bool, dev):
+            _say(dev, ("finished", finished, torch.bool))
         _need(finished.shape == (b, w), "finished must be [batch, beams]")
-    p = GdnBeamProblem()
-    p.batch, p.stride, p.beams, p.vocab = b, row, w, v
-    p.k = w if k is None else int(k)
-    p.dtype = DTYPES.get({torch.bfloat16: "bf16", torch.float16: "fp16",
-                          torch.float32: "fp32"}.get(logits.dtype), 99)
-    p.eos = int(eos)
-    lib = load()
-    check("gdn_beam_validate", lib.gdn_beam_validate(_byref(p)))
-    out = torch.empty(3, b, p.k, dtype=_i32, device=dev)
-    done = torch.empty(b, p.k, dtype=torch.bool, device=dev)
+    k = w if k is None else int(k)
+    p = _BEAM(b, row, w, v, k, _XTYPES.get(logits.dtype, 99), int(eos))
+    lib = _fns()
+    st = lib.gdn_beam_validate(p)
+    if st:
+        _raise("gdn_beam_validate", st)
+    on = logits.device
+    best = torch.empty(b, k, dtype=_f32, device=on)
+    parents = torch.empty(b, k, dtype=_i32, device=on)
+    tokens = torch.empty(b, k, dtype=_i32, device=on)
+    done = torch.empty(b, k, dtype=torch.bool, device=on)
     if workspace is None:
-        workspace = torch.empty(lib.gdn_beam_workspace_bytes(_byref(p)), dtype=torch.uint8,
-                                device=dev)
-    best, parents, tokens = out.unbind(0)
-    best = best.view(torch.float32)
-    check("gdn_beam_select", lib.gdn_beam_select(
-        _byref(p), logits.data_ptr(), scores.data_ptr(), _ptr(finished), best.data_ptr(),
-        parents.data_ptr(), tokens.data_ptr(), done.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream(dev)))
+        workspace = torch.empty(lib.gdn_beam_workspace_bytes(p), dtype=_u8, device=on)
+    st = lib.gdn_beam_select(
+        p, logits.data_ptr(), scores.data_ptr(),
+        None if finished is None else finished.data_ptr(), best.data_ptr(), parents.data_ptr(),
+        tokens.data_ptr(), done.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _raw_stream(dev))
+    if st:
+        _raise("gdn_beam_select", st)
     return best, parents, tokens, done
 
 
@@ -303,21 +341,25 @@ def beam_reorder(states: Sequence[torch.Tensor], parents, beams: int, out=None):
     dst = list(states if out is None else out)
     if not states:
         return dst
-    dev, rows = states[0].device, states[0].shape[0]
-    _flat("parents", parents, _i32, dev)
+    dev, rows = states[0].get_device(), states[0].shape[0]
+    if not _plain(parents, _i32, dev):
+        _say(dev, ("parents", parents, _i32))
     _need(parents.numel() == rows, "parents must have one entry per row")
     _need(len(dst) == len(states), "out must have one buffer per state")
-    n = len(dst)
-    a, b, size = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
-    for i, (x, y) in enumerate(zip(states, dst)):
-        _need(x.is_cuda and x.device == dev and x.is_contiguous() and x.shape[0] == rows,
-              "states must be contiguous [rows, ...] on one device")
-        _need(y is x or (y.shape == x.shape and y.dtype == x.dtype and y.device == dev
+    n, src, to, size = len(dst), [], [], []
+    for x, y in zip(states, dst):
+        _need(x.get_device() == dev and dev >= 0 and x.is_contiguous() and x.shape[0] == rows,
+              "states must be contiguous [rows, ...] on one CUDA device")
+        _need(y is x or (y.shape == x.shape and y.dtype is x.dtype and y.get_device() == dev
                          and y.is_contiguous()), "out must match the states")
-        a[i], b[i] = x.data_ptr(), y.data_ptr()
-        size[i] = x.numel() // rows * x.element_size() if rows else 0
-    check("gdn_beam_reorder", load().gdn_beam_reorder(n, a, b, size, parents.data_ptr(), rows,
-                                                      int(beams), _stream(dev)))
+        src.append(x.data_ptr())
+        to.append(y.data_ptr())
+        size.append(x.numel() // rows * x.element_size() if rows else 0)
+    pack = struct.Struct("%dQ" % n).pack
+    st = _fns().gdn_beam_reorder(n, pack(*src), pack(*to), pack(*size), parents.data_ptr(), rows,
+                                 int(beams), _raw_stream(dev))
+    if st:
+        _raise("gdn_beam_reorder", st)
     return dst
 
 
