@@ -13,6 +13,7 @@ Contents
   decode.py      decode QAT step (state QDQ before every token), numpy fp64
   kda.py         KDA recurrence (decay per key channel) with state QDQ, numpy fp64
   two_precision.py  two-precision GDN profile: fp32 anchor + E4M3 read copy, numpy fp64
+  serve.py       8-bit paged cache, attention over it, its pages, beam search; numpy
 
 The C part is compiled with gcc into ``oracle/liboracle.so`` by ``build()``.
 """
