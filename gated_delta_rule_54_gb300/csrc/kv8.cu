@@ -8,17 +8,18 @@ namespace gdn {
 
 namespace {
 
-// Append.  One CTA per (row, touched page, head, K or V): the new tokens of that
-// page are read once into registers (CH chunks of eight bf16 per thread), their
-// maximum is the block's, and their codes go out as 8-byte stores.  The bytes
-// are the bf16 tokens in and the codes out; the old codes of the page are read
-// and written only when the new tokens raise its scale.
+// Append.  A CTA takes a touched page of a row and some of its 2 * heads blocks (K
+// and V of a head): the new tokens of a block are read once into registers (CH
+// chunks of eight bf16 per thread, the next block's while this one is worked on),
+// their maximum is the block's, and their codes go out as 8-byte stores.  The
+// bytes are the bf16 tokens in and the codes out; the old codes of the page are
+// read and written only when the new tokens raise its scale.
 template <int MODE, int DIM, int NT, int CH>
-__global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int blocks) {
+__global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int blocks, int per) {
   constexpr int C8 = DIM / 8;
-  __shared__ float red[NT / 32];
+  __shared__ float red[2][NT / 32];
   const int64_t r = blockIdx.x / blocks;
-  const int h = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   int64_t base;
   int n;
   kv8_row(p, r, base, n);
@@ -30,62 +31,77 @@ __global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int b
   if (lo >= hi || b >= p.cols) return;
   const int64_t id = p.table[r * p.cols + b];
   if (id < 0 || id >= p.pages) return;
-  const int64_t tile = (kv * p.pages + id) * p.heads + h;
-  const __nv_bfloat16* x =
-      kv ? p.v + kv8_at(p, r, base, lo - st, p.v_row, p.v_token) + h * p.v_head
-         : p.x + kv8_at(p, r, base, lo - st, p.x_row, p.x_token) + h * p.x_head;
-  const int64_t step = kv ? p.v_token : p.x_token;
+  const int64_t xat = kv8_at(p, r, base, lo - st, p.x_row, p.x_token);
+  const int64_t vat = kv8_at(p, r, base, lo - st, p.v_row, p.v_token);
   const int chunks = (int)(hi - lo) * C8, old = (int)(lo - b * p.page);
+  const int first = blockIdx.y * per, last = min(first + per, 2 * p.heads);
 
-  uint4 u[CH];
-  float m = 0.f;
+  // block i: head i / 2, K or V
+  auto tile_of = [&](int i) { return ((i & 1) * p.pages + id) * p.heads + i / 2; };
+  auto load = [&](int i, uint4 (&u)[CH], float& was) {
+    const __nv_bfloat16* x = i & 1 ? p.v + vat + (i / 2) * p.v_head : p.x + xat + (i / 2) * p.x_head;
+    const int64_t step = i & 1 ? p.v_token : p.x_token;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * NT;
-    u[i] = make_uint4(0, 0, 0, 0);
-    if (c < chunks) u[i] = *reinterpret_cast<const uint4*>(x + (c / C8) * step + (c % C8) * 8);
-  }
-  const float was = old > 0 ? p.scales[tile] : 0.f;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    float f[8];
-    bf16x8(u[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
-  }
-  m = warp_max(m);
-  if constexpr (NT > 32) {
-    if (tid % 32 == 0) red[tid / 32] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) m = fmaxf(m, red[i]);
-  } else {
-    __syncwarp();
-  }
-  float now = fmaxf(was, __fdiv_rn(m, QdqMax<MODE>::value)), rcp = __frcp_rn(now);
-  if (isinf(rcp)) now = rcp = 0.f;
-
-  uint8_t* out = p.codes + tile * p.page * DIM;
-  if (now > was) {
-    for (int c = tid; c < old * C8; c += NT) {
-      const uint2 w = *reinterpret_cast<const uint2*>(out + c * 8);
-      const float4 a = qdq_code4_values<MODE>(w.x), e = qdq_code4_values<MODE>(w.y);
-      *reinterpret_cast<uint2*>(out + c * 8) =
-          make_uint2(kv8_code4<MODE>(__fmul_rn(a.x, was), __fmul_rn(a.y, was),
-                                     __fmul_rn(a.z, was), __fmul_rn(a.w, was), rcp),
-                     kv8_code4<MODE>(__fmul_rn(e.x, was), __fmul_rn(e.y, was),
-                                     __fmul_rn(e.z, was), __fmul_rn(e.w, was), rcp));
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * NT;
+      u[j] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) u[j] = __ldg(reinterpret_cast<const uint4*>(x + (c / C8) * step + (c % C8) * 8));
     }
-  }
-  if (tid == 0 && (now != was || old == 0)) p.scales[tile] = now;
+    was = old > 0 ? p.scales[tile_of(i)] : 0.f;
+  };
+  uint4 next[CH];
+  float next_was;
+  load(first, next, next_was);
+  for (int i = first; i < last; ++i) {
+    uint4 u[CH];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * NT;
-    if (c < chunks) {
+    for (int j = 0; j < CH; ++j) u[j] = next[j];
+    const float was = next_was;
+    if (i + 1 < last) load(i + 1, next, next_was);
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
       float f[8];
-      bf16x8(u[i], f);
-      *reinterpret_cast<uint2*>(out + (old * C8 + c) * 8) = make_uint2(
-          kv8_code4<MODE>(f[0], f[1], f[2], f[3], rcp), kv8_code4<MODE>(f[4], f[5], f[6], f[7], rcp));
+      bf16x8(u[j], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+    }
+    m = warp_max(m);
+    if constexpr (NT > 32) {
+      float(&part)[NT / 32] = red[i & 1];
+      if (tid % 32 == 0) part[tid / 32] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, part[w]);
+    } else {
+      __syncwarp();  // every lane has read the block's scale
+    }
+    float now = fmaxf(was, __fdiv_rn(m, QdqMax<MODE>::value)), rcp = __frcp_rn(now);
+    if (isinf(rcp)) now = rcp = 0.f;
+
+    const int64_t tile = tile_of(i);
+    uint8_t* out = p.codes + tile * p.page * DIM;
+    if (now > was) {
+      for (int c = tid; c < old * C8; c += NT) {
+        const uint2 w = *reinterpret_cast<const uint2*>(out + c * 8);
+        const float4 a = qdq_code4_values<MODE>(w.x), e = qdq_code4_values<MODE>(w.y);
+        *reinterpret_cast<uint2*>(out + c * 8) =
+            make_uint2(kv8_code4<MODE>(__fmul_rn(a.x, was), __fmul_rn(a.y, was),
+                                       __fmul_rn(a.z, was), __fmul_rn(a.w, was), rcp),
+                       kv8_code4<MODE>(__fmul_rn(e.x, was), __fmul_rn(e.y, was),
+                                       __fmul_rn(e.z, was), __fmul_rn(e.w, was), rcp));
+      }
+    }
+    if (tid == 0 && (now != was || old == 0)) p.scales[tile] = now;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * NT;
+      if (c < chunks) {
+        float f[8];
+        bf16x8(u[j], f);
+        *reinterpret_cast<uint2*>(out + (old * C8 + c) * 8) = make_uint2(
+            kv8_code4<MODE>(f[0], f[1], f[2], f[3], rcp), kv8_code4<MODE>(f[4], f[5], f[6], f[7], rcp));
+      }
     }
   }
 }
@@ -95,16 +111,19 @@ gdn_status run_append(const Kv8Params& p, cudaStream_t st) {
   // pages that n consecutive positions can touch
   const int blocks = (p.tokens + p.page - 2) / p.page + 1;
   if (p.rows * blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid((unsigned)(p.rows * blocks), (unsigned)p.heads, 2);
+  // blocks per CTA: up to 8 while 152 SMs still get eight CTAs each
+  int per = 1;
+  while (per < 8 && per < 2 * p.heads && p.rows * blocks * 2 * p.heads / (2 * per) >= 152 * 8) per *= 2;
+  const dim3 grid((unsigned)(p.rows * blocks), (unsigned)((2 * p.heads + per - 1) / per));
   const int chunks = (p.tokens < p.page ? p.tokens : p.page) * (DIM / 8);
   if (chunks <= 32)
-    kv8_append_kernel<MODE, DIM, 32, 1><<<grid, 32, 0, st>>>(p, blocks);
+    kv8_append_kernel<MODE, DIM, 32, 1><<<grid, 32, 0, st>>>(p, blocks, per);
   else if (chunks <= 128)
-    kv8_append_kernel<MODE, DIM, 128, 1><<<grid, 128, 0, st>>>(p, blocks);
+    kv8_append_kernel<MODE, DIM, 128, 1><<<grid, 128, 0, st>>>(p, blocks, per);
   else if (chunks <= 512)
-    kv8_append_kernel<MODE, DIM, 128, 4><<<grid, 128, 0, st>>>(p, blocks);
+    kv8_append_kernel<MODE, DIM, 128, 4><<<grid, 128, 0, st>>>(p, blocks, per);
   else
-    kv8_append_kernel<MODE, DIM, 256, 8><<<grid, 256, 0, st>>>(p, blocks);
+    kv8_append_kernel<MODE, DIM, 256, 8><<<grid, 256, 0, st>>>(p, blocks, per);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

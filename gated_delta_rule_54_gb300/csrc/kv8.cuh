@@ -108,14 +108,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A power of two that brings a row of q with this largest magnitude to [2^8, 2^9)
-// in fp16 (its small elements then keep at least 33 bits below the largest), and
-// its inverse.
+// A power of two that brings a row of q with this largest magnitude to [2^E, 2^(E+1)),
+// and its inverse.  (In fp16 with E = 8 a row's small elements keep at least 33 bits
+// below its largest.)
+template <int E>
 __device__ __forceinline__ void kv8_q_factor(float most, float& to, float& back) {
   int e = (int)(__float_as_uint(most) >> 23) - 127;
   e = e < -100 ? -100 : e > 120 ? 120 : e;
-  to = __uint_as_float((uint32_t)(8 - e + 127) << 23);
-  back = __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+  to = __uint_as_float((uint32_t)(E - e + 127) << 23);
+  back = __uint_as_float((uint32_t)(e - E + 127) << 23);
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -151,8 +152,13 @@ __device__ __forceinline__ uint32_t kv8_code4(float a, float b, float c, float d
         make_float2(__fmul_rn(c, rcp), __fmul_rn(d, rcp)), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   } else {
-    return (uint32_t)qdq_code<MODE>(a, rcp) | ((uint32_t)qdq_code<MODE>(b, rcp) << 8) |
-           ((uint32_t)qdq_code<MODE>(c, rcp) << 16) | ((uint32_t)qdq_code<MODE>(d, rcp) << 24);
+    // |x rcp| is at most 127 (1 + 2^-22) where rcp comes from a scale of at least
+    // max |x| / 127, so no clamp is needed; adding 1.5 * 2^23 rounds to the nearest
+    // integer, ties to even, which is then the low byte
+    constexpr float kInt = 12582912.f;
+    const uint32_t i0 = __float_as_uint(__fmul_rn(a, rcp) + kInt), i1 = __float_as_uint(__fmul_rn(b, rcp) + kInt);
+    const uint32_t i2 = __float_as_uint(__fmul_rn(c, rcp) + kInt), i3 = __float_as_uint(__fmul_rn(d, rcp) + kInt);
+    return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
   }
 }
 

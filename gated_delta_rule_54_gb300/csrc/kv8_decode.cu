@@ -13,9 +13,10 @@
 // give one CTA per segment instead, and then nothing is left to join.
 //
 // A warp runs by itself: a ring of S tiles (K and V, by TMA, 128- or 64-byte
-// swizzle) that its lane 0 refills, products m16n8k16 in fp16 with fp32 sums (the
-// codes are exact in fp16; q keeps its bits by a power of two per row), and an
-// online softmax.  A block's V scale multiplies the probabilities, so these run
+// swizzle) that its lane 0 refills, warp products with fp32 sums, and an online
+// softmax.  E4M3 scores come from the codes as they are, with q as a sum of two
+// E4M3 numbers; INT8 codes, and those of V, are exact in fp16 (q keeps its bits by
+// a power of two per row).  A block's V scale multiplies the probabilities, so these run
 // against a second maximum, of score + log2(scale), and stay within [0, 1] for
 // any scales.
 #include <cuda.h>
@@ -35,8 +36,9 @@ constexpr int kSegmentTiles = 64;  // tables up to this many tiles: one CTA per 
 struct DecodeArgs {
   Kv8Params p;
   CUtensorMap map;
-  float* ws;
-  int whole;  // one CTA per segment
+  float* ws;        // parts: two slots per warp of the grid
+  int64_t* before;  // tiles (of one K/V head) before each row
+  int whole;        // one CTA per segment
 };
 
 template <int DIM>
@@ -133,10 +135,13 @@ __device__ __forceinline__ int64_t out_row(const Kv8Params& p, const Kv8Span& s,
   return (s.base + i / p.group) * (p.heads * p.group) + h * p.group + i % p.group;
 }
 
-template <int MODE, int DIM, int S>
+// TWO: a page holds half a tile.  R8: at most eight query rows.
+template <int MODE, int DIM, int S, bool TWO, bool R8>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     kv8_decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int KSTEPS = DIM / 16, NT = DIM / 8;      // 16-byte chunks of a row; n tiles of V
+  constexpr int NE = R8 ? 1 : 2;                      // query rows of a thread: g, g + 8
+  constexpr bool F8 = MODE == GDN_QDQ_E4M3;           // scores from the codes as they are
   constexpr int kBytes = kTile * DIM;                 // K or V of a tile
   constexpr int kRowMask = DIM == 128 ? 7 : 3, kRowShift = DIM == 128 ? 0 : 1;
   extern __shared__ unsigned char smem_raw[];
@@ -178,6 +183,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lo < hi) pc = locate(p, lo, lane);
     }
   }
+  if (!a.whole && blockIdx.x == 0 && warp == 0) {
+    // tiles before each row, for the join
+    int64_t before = 0;
+    for (int64_t r0 = 0; r0 < p.rows; r0 += 32) {
+      int64_t mine = r0 + lane < p.rows ? tiles_of(kv8_span(p, r0 + lane)) : 0, x = mine;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (r0 + lane < p.rows) a.before[r0 + lane] = before + x - mine;
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) a.before[p.rows] = before;
+  }
   // rows that see nothing at all: zeros, written by some warp
   for (int64_t r = (int64_t)blockIdx.x * kWarps + warp; r < p.rows; r += (int64_t)gridDim.x * kWarps) {
     const Kv8Span s = kv8_span(p, r);
@@ -193,7 +212,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   int w_id = -1, w_base = 0, w_h = -1;
   int64_t w_r = -1;
   float w_ks = 0.f, w_lv = -INFINITY;
-  const int two = p.page < kTile;  // two pages per tile
   auto issue = [&](int st) {
     const int j0 = pc.tile * kTile, first = j0 >> p.shift;
     if (pc.r != w_r || pc.h != w_h || first >= w_base + 32 || first < w_base) {
@@ -213,22 +231,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int from = first - w_base;
     const int id0 = __shfl_sync(0xffffffffu, w_id, from);
     const float ks0 = __shfl_sync(0xffffffffu, w_ks, from), lv0 = __shfl_sync(0xffffffffu, w_lv, from);
-    const int id1 = __shfl_sync(0xffffffffu, w_id, from + two);
-    const float ks1 = __shfl_sync(0xffffffffu, w_ks, from + two);
-    const float lv1 = __shfl_sync(0xffffffffu, w_lv, from + two);
+    const int id1 = TWO ? __shfl_sync(0xffffffffu, w_id, from + 1) : id0;
+    const float ks1 = TWO ? __shfl_sync(0xffffffffu, w_ks, from + 1) : ks0;
+    const float lv1 = TWO ? __shfl_sync(0xffffffffu, w_lv, from + 1) : lv0;
     if (lane == 0) {
       meta[warp][st] = make_float4(ks0, lv0, ks1, lv1);
       valid[warp][st] = (id0 >= 0) | (id1 >= 0) << 1;
       unsigned char* k = ring + st * 2 * kBytes;
-      const int per = two ? kBytes / 2 : kBytes;
+      constexpr int per = TWO ? kBytes / 2 : kBytes;
       mbar_expect_tx(&bars[warp][st],
-                     (uint32_t)(per * 2 * ((id0 >= 0) + (two && id1 >= 0))));
+                     (uint32_t)(per * 2 * ((id0 >= 0) + (TWO && id1 >= 0))));
       if (id0 >= 0) {
         const int z = id0 * p.heads + pc.h, y = j0 & (p.page - 1);
         tma_load_3d(k, &a.map, 0, y, z, &bars[warp][st]);
         tma_load_3d(k + kBytes, &a.map, 0, y, z + (int)(p.pages * p.heads), &bars[warp][st]);
       }
-      if (two && id1 >= 0) {
+      if (TWO && id1 >= 0) {
         const int z = id1 * p.heads + pc.h;
         tma_load_3d(k + kBytes / 2, &a.map, 0, 0, z, &bars[warp][st]);
         tma_load_3d(k + kBytes + kBytes / 2, &a.map, 0, 0, z + (int)(p.pages * p.heads),
@@ -247,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   int st = 0;
   uint32_t parity = 0;
   float oacc[NT][4];
-  float lsum[2], m[2], mv[2];
+  float lsum[NE], m[NE], mv[NE];
   Kv8Span sp;
   int64_t part = -1;  // segment left in registers at the end
   int64_t u_done = lo;
@@ -256,19 +274,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int64_t stop = u1 < hi ? u1 : hi;
     sp = kv8_span(p, cc.r);
     const int rows = sp.n * p.group;
-    // q fragments: rows g and g + 8, element pairs in the order kv8_half2 gives K's
-    uint32_t qf[KSTEPS][4];
-    float rowfac[2];
-    int beg[2], end[2];
+    // q fragments.  INT8: fp16, element pairs in the order kv8_half2 gives K's.  E4M3:
+    // q as the sum of two E4M3 numbers, which is exact for elements down to 2^-10
+    // of the row's largest (8 bits = 4 + 4) and off by 2^-18 of it below; the second
+    // ones are rows 8-15 of the same fragment where these are free (R8), else one
+    // of their own.
+    constexpr int QF = F8 ? (R8 ? DIM / 32 : DIM / 16) : KSTEPS;
+    uint32_t qf[QF][4];
+    float rowfac[NE];
+    int beg[NE], end[NE];
     {
-      uint2 raw[2][KSTEPS];
-      float most[2] = {0.f, 0.f};
+      uint2 raw[NE][KSTEPS];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < NE; ++e) {
+        float most = 0.f;
         const int i = g + 8 * e;
         const int qi = i / p.group;
         const bool have = i < rows;
-        if (have) kv8_seen(p, sp, qi, beg[e], end[e]); else beg[e] = end[e] = 0;
+        beg[e] = end[e] = 0;
+        if (have) kv8_seen(p, sp, qi, beg[e], end[e]);
         const __nv_bfloat16* x = p.x + kv8_at(p, cc.r, sp.base, qi, p.x_row, p.x_token) +
                                  (cc.h * p.group + i % p.group) * p.x_head + 4 * t;
 #pragma unroll
@@ -276,19 +300,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           raw[e][c] = have ? *reinterpret_cast<const uint2*>(x + 16 * c) : make_uint2(0, 0);
           float f[4];
           bf16x4(raw[e][c], f);
-          most[e] = fmaxf(most[e], fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+          most = fmaxf(most, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
         }
-        most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], 1));
-        most[e] = fmaxf(most[e], __shfl_xor_sync(0xffffffffu, most[e], 2));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
         float to, back;
-        kv8_q_factor(most[e], to, back);
-        rowfac[e] = back * p.scale * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
+        kv8_q_factor<F8 ? 7 : 8>(most, to, back);
+        rowfac[e] = back * p.scale * kLog2eF;
 #pragma unroll
         for (int c = 0; c < KSTEPS; ++c) {
           float f[4];
           bf16x4(raw[e][c], f);
-          qf[c][e] = pack_f16(f[0] * to, f[2] * to);
-          qf[c][2 + e] = pack_f16(f[1] * to, f[3] * to);
+          if constexpr (F8) {
+            // k 16 c + 4 t ..: register 2 (c & 1) of row g, 2 (c & 1) + 1 of row g + 8
+            float2 h0, h1;
+            const uint32_t hi = e4m3_code2(f[0], f[1], to, h0) | (uint32_t)e4m3_code2(f[2], f[3], to, h1) << 16;
+            float2 l0, l1;
+            const uint32_t lo = e4m3_code2(f[0] * to - h0.x, f[1] * to - h0.y, 1.f, l0) |
+                                (uint32_t)e4m3_code2(f[2] * to - h1.x, f[3] * to - h1.y, 1.f, l1) << 16;
+            if constexpr (R8) {
+              qf[c / 2][2 * (c & 1)] = hi, qf[c / 2][2 * (c & 1) + 1] = lo;
+            } else {
+              qf[c / 2][2 * (c & 1) + e] = hi, qf[DIM / 32 + c / 2][2 * (c & 1) + e] = lo;
+            }
+          } else {
+            qf[c][e] = pack_f16(f[0] * to, f[2] * to);
+            qf[c][2 + e] = pack_f16(f[1] * to, f[3] * to);
+            if constexpr (R8) qf[c][1] = qf[c][3] = 0;
+          }
         }
       }
     }
@@ -302,8 +341,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
-    lsum[0] = lsum[1] = 0.f;
-    m[0] = m[1] = mv[0] = mv[1] = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) lsum[e] = 0.f, m[e] = mv[e] = -INFINITY;
 
     for (; u < stop; ++u, ++cc.tile) {
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][st], parity))) {
@@ -324,51 +363,63 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         for (int q = 0; q < KSTEPS / 4; ++q) {
           uint32_t r[4];
           ldsm_x4(r, kaddr + row * DIM + (((4 * q + lane / 8) ^ ((row >> kRowShift) & kRowMask)) << 4));
+          if constexpr (F8) {
+            mma_e4m3(s[j], qf[2 * q], r[0], r[1]);
+            mma_e4m3(s[j], qf[2 * q + 1], r[2], r[3]);
+            if constexpr (!R8) {
+              mma_e4m3(s[j], qf[DIM / 32 + 2 * q], r[0], r[1]);
+              mma_e4m3(s[j], qf[DIM / 32 + 2 * q + 1], r[2], r[3]);
+            }
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            kv8_half2<MODE>(r[i], b0, b1);
-            mma_f16(s[j], qf[4 * q + i], b0, b1);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              kv8_half2<MODE>(r[i], b0, b1);
+              mma_f16(s[j], qf[4 * q + i], b0, b1);
+            }
           }
         }
+        if constexpr (F8 && R8) s[j][0] += s[j][2], s[j][1] += s[j][3];
       }
       const int j0 = cc.tile * kTile;
       const bool mask = have != 3 || j0 < in0 || j0 + kTile > in1;
-      float half[2][2];  // row, half tile: largest score
+      constexpr int H = TWO ? 2 : 1;  // blocks of the tile that have scales of their own
+      float top[NE][H];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < NE; ++e) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < H; ++f) {
           const float fac = rowfac[e] * (f ? sc.z : sc.x);
-          float top = -INFINITY;
+          float x = -INFINITY;
 #pragma unroll
-          for (int j = 2 * f; j < 2 * f + 2; ++j)
+          for (int j = 4 / H * f; j < 4 / H * (f + 1); ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float x = s[j][2 * e + i] * fac;
+              float y = s[j][2 * e + i] * fac;
               if (mask) {
                 const int at = j0 + 8 * j + 2 * t + i;
-                if (at < beg[e] || at >= end[e] || !(have >> f & 1)) x = -INFINITY;
+                if (at < beg[e] || at >= end[e] || !(have >> f & 1)) y = -INFINITY;
               }
-              s[j][2 * e + i] = x;
-              top = fmaxf(top, x);
+              s[j][2 * e + i] = y;
+              x = fmaxf(x, y);
             }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          half[e][f] = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          top[e][f] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
         }
       }
-      float f_half[2][2], scale_o[2];
+      float scale_o[NE];
       bool moved = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float nm = fmaxf(m[e], fmaxf(half[e][0], half[e][1]));
-        const float nv = fmaxf(mv[e], fmaxf(half[e][0] + sc.y, half[e][1] + sc.w));
+      for (int e = 0; e < NE; ++e) {
+        float nm = fmaxf(m[e], top[e][0]), nv = fmaxf(mv[e], top[e][0] + sc.y);
+        if (TWO) nm = fmaxf(nm, top[e][H - 1]), nv = fmaxf(nv, top[e][H - 1] + sc.w);
         const float um = nm == -INFINITY ? 0.f : nm, uv = nv == -INFINITY ? 0.f : nv;
         lsum[e] *= ex2_approx_f(m[e] - um);
         scale_o[e] = ex2_approx_f(mv[e] - uv);
         moved |= nv != mv[e];
-        f_half[e][0] = ex2_approx_f(fminf(um + sc.y - uv, 126.f));
-        f_half[e][1] = ex2_approx_f(fminf(um + sc.w - uv, 126.f));
+        float f_half[H];
+        f_half[0] = ex2_approx_f(fminf(um + sc.y - uv, 126.f));
+        if (TWO) f_half[H - 1] = ex2_approx_f(fminf(um + sc.w - uv, 126.f));
         m[e] = nm, mv[e] = nv;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -376,14 +427,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           for (int i = 0; i < 2; ++i) {
             const float w = ex2_approx_f(s[j][2 * e + i] - um);
             lsum[e] += w;
-            s[j][2 * e + i] = w * f_half[e][j / 2];
+            s[j][2 * e + i] = w * f_half[TWO ? j / 2 : 0];
           }
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           oacc[i][0] *= scale_o[0], oacc[i][1] *= scale_o[0];
-          oacc[i][2] *= scale_o[1], oacc[i][3] *= scale_o[1];
+          if constexpr (!R8) oacc[i][2] *= scale_o[NE - 1], oacc[i][3] *= scale_o[NE - 1];
         }
       }
       // ---- output: 16 keys per step; a 16-byte chunk of V gives two n tiles ----
@@ -391,9 +442,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int k = 0; k < 2; ++k) {
         uint32_t pf[4];
         pf[0] = pack_f16(s[2 * k][0], s[2 * k][1]);
-        pf[1] = pack_f16(s[2 * k][2], s[2 * k][3]);
+        pf[1] = R8 ? 0 : pack_f16(s[2 * k][2], s[2 * k][3]);
         pf[2] = pack_f16(s[2 * k + 1][0], s[2 * k + 1][1]);
-        pf[3] = pack_f16(s[2 * k + 1][2], s[2 * k + 1][3]);
+        pf[3] = R8 ? 0 : pack_f16(s[2 * k + 1][2], s[2 * k + 1][3]);
         const int row = 16 * k + (lane / 8 & 1) * 8 + lane % 8;
 #pragma unroll
         for (int c = 0; c < KSTEPS; c += 2) {
@@ -421,9 +472,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (bad) break;
 
     // ---- the segment's output over this warp's keys ----
-    float lse2[2];
+    float lse2[NE];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < NE; ++e) {
       float l = lsum[e];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -437,7 +488,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const bool whole = lo <= u0 && u1 <= hi;
     if (whole || u1 < hi) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < NE; ++e) {
         const int i = g + 8 * e;
         if (i >= rows) continue;
         if (whole) {
@@ -462,7 +513,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     } else {
       part = u0;
-      if (t == 0) s_lse[warp][g] = lse2[0], s_lse[warp][g + 8] = lse2[1];
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        if (t == 0) s_lse[warp][g + 8 * e] = lse2[e];
     }
     if (u < hi) {
       // the next segment; cc.tile stands at its end
@@ -481,12 +534,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 
   // ---- parts of one CTA ----
+  grid_dep_launch();  // the join may be scheduled (it waits for the whole of this launch)
   if (lane == 0) s_u0[warp] = part;
   __syncthreads();  // every ring is done with
   float* parts = reinterpret_cast<float*>(smem);  // [warp][16][DIM]
   if (part >= 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < NE; ++e) {
       float* o = parts + (warp * 16 + g + 8 * e) * DIM + 4 * t;
 #pragma unroll
       for (int c = 0; c < KSTEPS; ++c)
@@ -552,30 +606,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-// Joins the parts of a segment that several CTAs hold: one CTA per (segment,
-// output row), its warps over the parts, their sums in warp order.
+// Joins the parts of a segment that several CTAs hold, in order of the shares.  A
+// CTA does some output rows of one segment; with few parts a warp does a whole
+// row, with many the warps take parts and their sums are added in warp order.
 template <int DIM>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ DecodeArgs a, int grid) {
-  constexpr int kList = 1024;
-  __shared__ float s_w[kList];
+  constexpr int kList = 256, kFew = 12;
   __shared__ int s_at[kList];
+  __shared__ float s_w[kList];
   __shared__ float red[8];
   __shared__ __align__(16) float s_o[8][DIM];
   const Kv8Params& p = a.p;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int64_t r = blockIdx.x / p.heads;
-  const int h = blockIdx.x % p.heads, i = blockIdx.y;
+  const int h = blockIdx.x % p.heads;
   const Kv8Span sp = kv8_span(p, r);
-  const int n = tiles_of(sp);
-  if (n == 0 || i >= sp.n * p.group) return;
-  __shared__ int64_t s_all, s_before;
-  if (warp == 0) {
-    const int64_t all = tiles_before(p, p.rows, lane), before = tiles_before(p, r, lane);
-    if (lane == 0) s_all = all * p.heads, s_before = before * p.heads;
-  }
-  __syncthreads();
-  const int64_t all = s_all, ctas = ctas_for(all, grid);
-  const int64_t u0 = s_before + (int64_t)h * n, u1 = u0 + n;
+  const int n = tiles_of(sp), rows = sp.n * p.group;
+  if (n == 0) return;
+  grid_dep_wait();
+  const int64_t all = a.before[p.rows] * p.heads, ctas = ctas_for(all, grid);
+  const int64_t u0 = a.before[r] * p.heads + (int64_t)h * n, u1 = u0 + n;
   // CTAs whose shares meet the segment: c with start(c) < u1 and start(c + 1) > u0
   int64_t c0 = u0 * ctas / all, c1;
   while (c0 > 0 && cta_start(all, c0, ctas) > u0) --c0;
@@ -586,11 +636,10 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   // one entry per CTA for what its warps left of the segment, and one for a warp
   // that goes on after the segment's end
   const int entries = (int)(c1 - c0 + 1) + 1;
-  if (entries > kList) return;
-  float top = -INFINITY;
   bool direct = false;
-  for (int k = tid; k < entries; k += 256) {
-    const int64_t c = k < entries - 1 ? c0 + k : c1;
+  if (tid < entries) {
+    const bool after = tid == entries - 1;
+    const int64_t c = after ? c1 : c0 + tid;
     const int64_t lo = cta_start(all, c, ctas), hi = cta_start(all, c + 1, ctas);
     int at = -1;
     int64_t first = -1, last_hi = 0;
@@ -600,52 +649,102 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
       if (s <= u0 && e >= u1) {
         direct = true;
       } else if (e <= u1) {
-        if (first < 0) first = s, at = k < entries - 1 ? (int)((c * kWarps + w) * 2 + 1) : at;
+        if (first < 0) {
+          first = s;
+          if (!after) at = (int)((c * kWarps + w) * 2 + 1);
+        }
         last_hi = e;
-      } else if (k == entries - 1) {
+      } else if (after) {
         at = (int)((c * kWarps + w) * 2);
       }
     }
     if (first >= 0 && first <= u0 && last_hi >= u1) direct = true;
-    s_at[k] = at;
-    const float x = at >= 0 && !direct ? a.ws[(int64_t)at * kSlot<DIM> + 16 * DIM + i] : -INFINITY;
-    s_w[k] = x;
-    top = fmaxf(top, x);
+    s_at[tid] = at;
   }
-  // (the workspace was written by the launch before, which has completed)
   if (__syncthreads_or(direct)) return;  // written already
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (top > -INFINITY) {
-    for (int k = warp; k < entries; k += 8) {
-      if (s_at[k] < 0) continue;
-      const float c = ex2_approx_f(s_w[k] - top);
-      l += c;
-      if (lane < DIM / 4) {
-        const float4 x = *reinterpret_cast<const float4*>(a.ws + (int64_t)s_at[k] * kSlot<DIM> + i * DIM + 4 * lane);
-        o.x = fmaf(c, x.x, o.x), o.y = fmaf(c, x.y, o.y);
-        o.z = fmaf(c, x.z, o.z), o.w = fmaf(c, x.w, o.w);
+  auto lse_of = [&](int k, int i) {
+    return s_at[k] >= 0 ? a.ws[(int64_t)s_at[k] * kSlot<DIM> + 16 * DIM + i] : -INFINITY;
+  };
+  auto add = [&](int k, int i, float c, float4& o) {
+    if (lane < DIM / 4) {
+      const float4 x = *reinterpret_cast<const float4*>(a.ws + (int64_t)s_at[k] * kSlot<DIM> + i * DIM + 4 * lane);
+      o.x = fmaf(c, x.x, o.x), o.y = fmaf(c, x.y, o.y), o.z = fmaf(c, x.z, o.z), o.w = fmaf(c, x.w, o.w);
+    }
+  };
+  auto finish = [&](int i, float4 o, float top, float l) {
+    const int64_t to = out_row<DIM>(p, sp, h, i);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (lane < DIM / 4)
+      *reinterpret_cast<uint2*>(p.o + to * DIM + 4 * lane) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[to] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  };
+  if (entries <= kFew) {
+    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+      const float mine = lane < entries ? lse_of(lane, i) : -INFINITY;
+      float top = mine;
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+      if (top > -INFINITY)
+        for (int k = 0; k < entries; ++k) {
+          if (s_at[k] < 0) continue;
+          const float c = ex2_approx_f(__shfl_sync(0xffffffffu, mine, k) - top);
+          l += c;
+          add(k, i, c, o);
+        }
+      finish(i, o, top, l);
+    }
+    return;
+  }
+  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
+    float top = tid < entries ? lse_of(tid, i) : -INFINITY;
+    const float mine = top;
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    __syncthreads();
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    __syncthreads();
+    if (tid < entries) s_w[tid] = s_at[tid] >= 0 && top > -INFINITY ? ex2_approx_f(mine - top) : 0.f;
+    __syncthreads();
+    // four parts at a time, so that their loads are in flight together
+    for (int k0 = warp; k0 < entries; k0 += 32) {
+      float c[4];
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = k0 + 8 * j;
+        c[j] = e < entries ? s_w[e] : 0.f;
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c[j] > 0.f && lane < DIM / 4)
+          x[j] = *reinterpret_cast<const float4*>(a.ws + (int64_t)s_at[e] * kSlot<DIM> + i * DIM + 4 * lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        l += c[j];
+        o.x = fmaf(c[j], x[j].x, o.x), o.y = fmaf(c[j], x[j].y, o.y);
+        o.z = fmaf(c[j], x[j].z, o.z), o.w = fmaf(c[j], x[j].w, o.w);
       }
     }
+    __syncthreads();
+    if (lane < DIM / 4) *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
+    if (lane == 0) red[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+      l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < 8; ++w) {
+        l += red[w];
+        if (lane < DIM / 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_o[w][4 * lane]);
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
+      }
+      finish(i, o, top, l);
+    }
   }
-  __syncthreads();
-  if (lane < DIM / 4) *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
-  if (lane == 0) red[warp] = l;
-  __syncthreads();
-  l = 0.f;
-  for (int w = 0; w < 8; ++w) l += red[w];
-  const int64_t to = out_row<DIM>(p, sp, h, i);
-  if (tid < DIM / 2) {
-    float x = 0.f, y = 0.f;
-    for (int w = 0; w < 8; ++w) x += s_o[w][2 * tid], y += s_o[w][2 * tid + 1];
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    *reinterpret_cast<uint32_t*>(p.o + to * DIM + 2 * tid) = pack_bf16(x * inv, y * inv);
-  }
-  if (p.lse && tid == 0) p.lse[to] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Most tiles that a row can have, by its table and window.
@@ -676,28 +775,48 @@ gdn_status run(DecodeArgs& a, cudaStream_t st) {
     return GDN_ERR_CUDA;
   a.whole = by_segment(p);
   const int64_t grid = a.whole ? p.rows * p.heads : grid_of(p);
-  auto kern = kv8_decode_kernel<MODE, DIM, S>;
+  // up to eight query rows: half of the softmax's work, and q's two parts in one fragment
+  const bool r8 = (int64_t)p.tokens * p.group <= 8;
+  auto kern = p.page < kTile
+                  ? (r8 ? kv8_decode_kernel<MODE, DIM, S, true, true> : kv8_decode_kernel<MODE, DIM, S, true, false>)
+                  : (r8 ? kv8_decode_kernel<MODE, DIM, S, false, true> : kv8_decode_kernel<MODE, DIM, S, false, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
   kern<<<(unsigned)grid, kWarps * 32, bytes, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (a.whole) return GDN_OK;
-  kv8_join_kernel<DIM><<<dim3((unsigned)(p.rows * p.heads), (unsigned)(p.tokens * p.group)), 256, 0, st>>>(a, (int)grid);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  // rows of a segment in one CTA, unless the segments leave SMs idle
+  const int64_t segments = p.rows * p.heads, rows = (int64_t)p.tokens * p.group;
+  int64_t y = 304 / segments;
+  y = y < 1 ? 1 : y < rows ? y : rows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)segments, (unsigned)y);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<DIM>, a, (int)grid) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
+
+// Workspace: tiles before each row, then the parts.
+size_t before_bytes(const Kv8Params& p) { return ((size_t)(p.rows + 1) * 8 + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t kv8_decode_workspace(const Kv8Params& p, int dim) {
   if (by_segment(p)) return 0;
-  return (size_t)grid_of(p) * kWarps * 2 * (16 * dim + 16) * sizeof(float);
+  return before_bytes(p) + (size_t)grid_of(p) * kWarps * 2 * (16 * dim + 16) * sizeof(float);
 }
 
 gdn_status launch_kv8_decode(const Kv8Params& p, int mode, int dim, void* workspace,
                              cudaStream_t st) {
   DecodeArgs a;
   a.p = p;
-  a.ws = static_cast<float*>(workspace);
+  a.before = static_cast<int64_t*>(workspace);
+  a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + before_bytes(p));
   if (mode == GDN_QDQ_E4M3)
     return dim == 128 ? run<GDN_QDQ_E4M3, 128>(a, st) : run<GDN_QDQ_E4M3, 64>(a, st);
   return dim == 128 ? run<GDN_QDQ_INT8, 128>(a, st) : run<GDN_QDQ_INT8, 64>(a, st);

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
     }
     float up, back;
-    kv8_q_factor(most, up, back);
+    kv8_q_factor<8>(most, up, back);
     rowfac = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
     if (p.scale < 0.f) up = -up;
 #pragma unroll
