@@ -7,9 +7,8 @@
 //     P = 2^(s - reference)  (one thread per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
 // Warp 13 brings the codes of 128 keys by TMA (a box per page); warps 8-11 turn them
-// into fp16 (exact), as swizzled operand tiles; one lane of warp 12 issues the
-// products, those of one tile while the rows of the other compute; warps 0-3 and
-// 4-7 are the rows of the two tiles.
+// into fp16 (exact), as swizzled operand tiles; one lane each of warps 12
+// and 14 issues a tile's products; warps 0-3 and 4-7 are the rows of the two tiles.
 //
 // Products of fp16 codes bound it together with shared memory: per 128 keys the
 // two tiles' operands are read at the rate of the products, and the converted
@@ -34,7 +33,7 @@ __device__ int g_kv8_prefill_error;
 
 constexpr int kKeys = 128, kRows = 256;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 512;  // four warpgroups; of the last, warp 12 issues and warp 13 loads
+constexpr int kThreads = 512;  // four warpgroups; of the last, warps 12 and 14 issue and warp 13 loads
 // registers per thread of the warpgroups: together what the launch gave (4 x 128)
 constexpr int kSoftRegs = 200, kConvRegs = 64, kIssueRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs == 4 * 128, "register shares");
@@ -153,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   constexpr int BK = kKeys / CH;   // keys of a block
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone;
-  __shared__ __align__(8) uint64_t cfull[2], cfree[2];  // codes of K, of V
+  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone[2];
+  __shared__ __align__(8) uint64_t cfull[2][2];  // codes of K, of V
   __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
   __shared__ int valid[4];        // bit c: the block has a page
   __shared__ uint32_t tmem_slot;
@@ -163,8 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid % 32;
   const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);  // uniform
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  unsigned char *sQ = smem, *sK = smem + 2 * kTileBytes, *sV = smem + 4 * kTileBytes;
-  unsigned char* sC = smem + 6 * kTileBytes;  // codes: K, V
+  unsigned char *sQ = smem, *sK = smem + 2 * kTileBytes;  // sK: K 0, K 1, V 0, V 1
+  // Codes arrive where their fp16 tile will be: 128 codes of a row on its second
+  // panel, so that a row is read and written over by the same eight lanes.  (Rows
+  // of 64 codes have a place of their own.)
+  auto codes_at = [&](int kv, int b) {
+    return DIM == 128 ? sK + (2 * kv + b) * kTileBytes + kKeys * 128 : smem + 6 * kTileBytes + (2 * kv + b) * kKeys * DIM;
+  };
 
   // ---- which rows and keys (long blocks of rows first) ----
   const int64_t rh = p.rows * p.heads;
@@ -196,11 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
-      mbar_init(&kfree[i], 1), mbar_init(&vfree[i], 1);
+      mbar_init(&kfree[i], two ? 2 : 1), mbar_init(&vfree[i], two ? 2 : 1);
+      mbar_init(&odone[i], 1);
       mbar_init(&sfull[i], 1), mbar_init(&pready[i], 128);
-      mbar_init(&cfull[i], 1), mbar_init(&cfree[i], kConvWarps * 32);
+      mbar_init(&cfull[i][0], 1), mbar_init(&cfull[i][1], 1);
     }
-    mbar_init(&odone, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     // ---- outputs ----
     const bool any = nt > 0 && run && ok;
     if (any) {
-      ok = __all_sync(0xffffffffu, wait(&odone, 0));
+      ok = __all_sync(0xffffffffu, wait(&odone[t], 0));
       tc_fence_after();
     }
     const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
@@ -411,8 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     // 128-byte rows: (0 5) (1 4) (2 7) (3 6), the even warps the first of each two pairs
     const int row0c = DIM == 128 ? (cw / 2) * 8 + (((r8 + (cw & 1)) ^ ((lane >> 2 & 1) ? 5 : 0)))
                                  : cw * 8 + r8;
-    auto convert = [&](const unsigned char* from, unsigned char* to) {
-#pragma unroll
+#pragma unroll 1
+    for (int x = 0; x < 2 * nt; ++x) {  // K 0, V 0, K 1, V 1, ...
+      const int kv = x & 1, i = x >> 1, b = i & 1;
+      if (!wait(&cfull[kv][b], (i >> 1) & 1)) break;
+      unsigned char* to = sK + (2 * kv + b) * kTileBytes;
+      const unsigned char* from = codes_at(kv, b);
+#pragma unroll 4
       for (int e = 0; e < kPer; ++e) {
         const int row = row0c + e * kStep;
         const int at = DIM == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
@@ -423,22 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         kv8_half2<MODE>(u.y, lo.z, lo.w);
         kv8_half2<MODE>(u.z, hi.x, hi.y);
         kv8_half2<MODE>(u.w, hi.z, hi.w);
+        __syncwarp();  // the row's eight lanes have read it: half of it is written over
         *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
         *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
       }
       fence_proxy_async();
-    };
-    for (int i = 0; i < nt; ++i) {
-      const int b = i & 1;
-      const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-      if (!wait(&cfull[0], i & 1) || !wait(&kfree[b], free_parity)) break;
-      convert(sC, sK + b * kTileBytes);
-      mbar_arrive(&kfull[b]);
-      mbar_arrive(&cfree[0]);
-      if (!wait(&cfull[1], i & 1) || !wait(&vfree[b], free_parity)) break;
-      convert(sC + kKeys * DIM, sV + b * kTileBytes);
-      mbar_arrive(&vfull[b]);
-      mbar_arrive(&cfree[1]);
+      mbar_arrive(kv ? &vfull[b] : &kfull[b]);
     }
   } else {
     set_regs_down<kIssueRegs>();
@@ -472,19 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       bool ok = true;
       #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        ok = __all_sync(0xffffffffu, wait(&cfree[kv], (i & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, wait(kv ? &vfree[i & 1] : &kfree[i & 1], ((i >> 1) & 1) ^ 1));
         if (!ok) break;
         if (kv == 0) {
           if (lane < CH) meta[i & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
           if (lane == 0) valid[i & 3] = (int)bits;
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(&cfull[kv], bytes);
+        if (lane == 0) mbar_expect_tx(&cfull[kv][i & 1], bytes);
         __syncwarp();
         issued[kv] = i + 1;
         if (have)
-          tma_load_3d(sC + kv * kKeys * DIM + (lane << p.shift) * DIM, &a.map, 0, 0,
-                      (int)((kv * p.pages + id) * p.heads + h), &cfull[kv]);
+          tma_load_3d(codes_at(kv, i & 1) + (lane << p.shift) * DIM, &a.map, 0, 0,
+                      (int)((kv * p.pages + id) * p.heads + h), &cfull[kv][i & 1]);
       }
       if (!ok) break;
       id = id1;
@@ -492,42 +491,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       id1 = i + 2 < nt ? page_of(ka + i + 2) : -1;
     }
     // no copy is in flight when the CTA ends, whatever ended the loop
-    if (issued[0] > 0) mbar_wait(&cfull[0], (issued[0] - 1) & 1);
-    if (issued[1] > 0) mbar_wait(&cfull[1], (issued[1] - 1) & 1);
-  } else if (warp == kSoftWarps + kConvWarps && nt > 0) {
-    // ======================= products =======================
-    // The whole warp goes through this, so that descriptors stay in uniform
-    // registers; one elected lane issues.
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      for (int i = max(issued[kv] - 2, 0); i < issued[kv]; ++i) mbar_wait(&cfull[kv][i & 1], (i >> 1) & 1);
+  } else if ((warp == kSoftWarps + kConvWarps || (warp == kSoftWarps + kConvWarps + 2 && two)) && nt > 0) {
+    // ======================= products of tile t =======================
+    // One warp per tile, so that the waits of one do not hold up the other.  The
+    // whole warp goes through this, so that descriptors stay in uniform registers;
+    // one elected lane issues.
+    const int t = warp == kSoftWarps + kConvWarps ? 0 : 1;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-    const uint32_t dq = desc_lo(base, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
+    const uint32_t dq = desc_lo(base + t * kTileBytes, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
     const uint32_t dv = desc_lo(base + 4 * kTileBytes, kKeys * 128);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
+    const uint32_t s_at = tm + t * kKeys, o_at = tm + 256 + t * 128;
     const bool lead = elect_one();
-    auto qk = [&](int t, int i) {
-      const uint32_t q = dq + t * kTileStep, k = dk + (i & 1) * kTileStep;
+    auto qk = [&](int i) {
+      const uint32_t k = dk + (i & 1) * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
           const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
-          umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
+          umma_ss(s_at, dq + off, k + off, kIdQK, s > 0);
         }
         umma_commit(&sfull[t]);
+        umma_commit(&kfree[i & 1]);
       }
       __syncwarp();
     };
-    auto pv = [&](int t, int i) {
+    auto pv = [&](int i) {
       const uint32_t v = dv + (i & 1) * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-          umma_ts(tm + 256 + t * 128, tm + t * kKeys + 8 * s, v + s * (2048 >> 4), kIdPV,
-                  i > 0 || s > 0);
+          umma_ts(o_at, s_at + 8 * s, v + s * (2048 >> 4), kIdPV, i > 0 || s > 0);
+        umma_commit(&vfree[i & 1]);
       }
-      __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (lead) umma_commit(bar);
       __syncwarp();
     };
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -536,35 +536,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     bool ok = all_wait(&kfull[0], 0);
     if (ok) {
       tc_fence_after();
-      qk(0, 0);
-      if (two) qk(1, 0);
-      commit(&kfree[0]);
+      qk(0);
     }
     for (int i = 0; i < nt && ok; ++i) {
-      const int b = i & 1, nb = (i + 1) & 1;
-      const uint32_t par = (i >> 1) & 1;
-      ok = all_wait(&vfull[b], par) && all_wait(&pready[0], i & 1);
+      ok = all_wait(&vfull[i & 1], (i >> 1) & 1);
+      // the next keys as well, while the rows still compute
+      if (i + 1 < nt) ok = ok && all_wait(&kfull[(i + 1) & 1], ((i + 1) >> 1) & 1);
+      ok = ok && all_wait(&pready[t], i & 1);
       if (!ok) break;
       tc_fence_after();
-      pv(0, i);
-      if (i + 1 < nt) {
-        ok = all_wait(&kfull[nb], ((i + 1) >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        qk(0, i + 1);
-      }
-      if (two) {
-        ok = all_wait(&pready[1], i & 1);
-        if (!ok) break;
-        tc_fence_after();
-        pv(1, i);
-        if (i + 1 < nt) qk(1, i + 1);
-      }
-      commit(&vfree[b]);
-      if (i + 1 < nt) commit(&kfree[nb]);
+      pv(i);
+      if (i + 1 < nt) qk(i + 1);
     }
-    commit(&odone);  // completes with every product issued
-    wait(&odone, 0);
+    if (lead) umma_commit(&odone[t]);  // completes with every product issued here
+    __syncwarp();
+    wait(&odone[t], 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -632,7 +618,7 @@ gdn_status run(PrefillArgs& a, cudaStream_t st) {
     return GDN_ERR_CUDA;
   const int64_t blocks = (int64_t)a.blocks * p.rows * p.heads;
   if (blocks * a.splits > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  constexpr int bytes = (6 * 2 + 2) * kKeys * DIM + 1024;
+  constexpr int bytes = 6 * kKeys * DIM * 2 + (DIM == 128 ? 0 : 4 * kKeys * DIM) + 1024;
   auto kern = kv8_prefill_kernel<MODE, DIM, CH>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
