@@ -147,7 +147,7 @@ gdn_status validate_kv8(const gdn_kv8_problem* p) {
   if ((int64_t)p->cols * p->page > 0x7fffffffLL || p->pages > 0x7fffffffLL ||
       p->rows > 0x7fffffffLL || p->total > 0x7fffffffLL ||
       2 * p->pages * p->heads > 0x7fffffffLL || p->rows * p->heads > 0x7fffffffLL ||
-      (int64_t)p->heads * p->group > 65535)
+      (int64_t)p->tokens * p->group > 0x7ffffeffLL || (int64_t)p->heads * p->group > 65535)
     return GDN_ERR_UNSUPPORTED_SHAPE;
   if (!isfinite(p->scale)) return GDN_ERR_INVALID_ARG;
   for (const int64_t s : {p->x_row, p->x_token, p->x_head, p->v_row, p->v_token, p->v_head})

@@ -4,11 +4,11 @@
 // share the head, query-major; a CTA takes 256 of them, as two tiles of 128, so
 // that one conversion of a block of keys serves both.  Per 128 keys and tile:
 //     S = Q K^T   (tcgen05, fp16 x fp16 -> fp32 in TMEM)
-//     P = 2^(s - reference)  (one thread per query row; written over S as fp16)
+//     P = 2^(s - reference)  (two threads per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
-// Warp 13 brings the codes of 128 keys by TMA (a box per page); warps 8-11 turn them
-// into fp16 (exact), as swizzled operand tiles; one lane each of warps 12
-// and 14 issues a tile's products; warps 0-3 and 4-7 are the rows of the two tiles.
+// One warp brings the codes of 128 keys by TMA (a box per page); four turn them into
+// fp16 (exact), as swizzled operand tiles; one lane each of two warps issues a tile's
+// products; and eight warps per tile are its rows, two threads to a row.
 //
 // Products of fp16 codes bound it together with shared memory: per 128 keys the
 // two tiles' operands are read at the rate of the products, and the converted
@@ -32,11 +32,12 @@ namespace {
 __device__ int g_kv8_prefill_error;
 
 constexpr int kKeys = 128, kRows = 256;
-constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 512;  // four warpgroups; of the last, warps 12 and 14 issue and warp 13 loads
-// registers per thread of the warpgroups: together what the launch gave (4 x 128)
-constexpr int kSoftRegs = 200, kConvRegs = 64, kIssueRegs = 48;
-static_assert(2 * kSoftRegs + kConvRegs + kIssueRegs == 4 * 128, "register shares");
+constexpr int kSoftWarps = 16, kConvWarps = 4;
+constexpr int kIssuer = kSoftWarps + kConvWarps;  // warps 20 and 22 issue, warp 21 loads
+constexpr int kThreads = 768;
+// registers per thread of the warpgroups: together what the launch gave (6 x 80)
+constexpr int kSoftRegs = 96, kConvRegs = 48, kIssueRegs = 48;
+static_assert(4 * kSoftRegs + kConvRegs + kIssueRegs == 6 * 80, "register shares");
 
 struct PrefillArgs {
   Kv8Params p;
@@ -144,6 +145,18 @@ __device__ __forceinline__ uint32_t unit_at(int row, int u) {
   return (uint32_t)((u >> 3) * (kKeys * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4));
 }
 
+// 32 bytes, a whole sector at once where the address allows
+__device__ __forceinline__ void store32(__nv_bfloat16* to, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // CH: blocks of a tile of keys that have scales of their own (two at least)
 template <int MODE, int DIM, int CH>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
@@ -156,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   __shared__ __align__(8) uint64_t cfull[2][2];  // codes of K, of V
   __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
   __shared__ int valid[4];        // bit c: the block has a page
+  __shared__ float row_factor[kRows];
+  __shared__ float2 other[2][2][kRows];  // [parity of the tile][half of the keys][row]: maxima
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -171,22 +186,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   };
 
   // ---- which rows and keys (long blocks of rows first) ----
-  const int64_t rh = p.rows * p.heads;
+  const unsigned rh = (unsigned)(p.rows * p.heads);
   const int split = blockIdx.x % a.splits;
-  const int64_t x = blockIdx.x / a.splits;
+  const unsigned x = blockIdx.x / a.splits;
   const int block = a.blocks - 1 - (int)(x / rh);
-  const int64_t r = x % rh / p.heads;
-  const int h = (int)(x % rh % p.heads);
+  const int r = (int)(x % rh / (unsigned)p.heads), h = (int)(x % rh % (unsigned)p.heads);
   const Kv8Span sp = kv8_span(p, r);
-  const int64_t rows = (int64_t)sp.n * p.group, row0 = (int64_t)block * kRows;
+  const int rows = sp.n * p.group, row0 = block * kRows;
   if (row0 >= rows) return;
-  const int here = (int)(rows - row0 < kRows ? rows - row0 : kRows);
+  const int here = min(rows - row0, kRows);
   const bool two = here > 128;
   int ka, kb;  // tiles of keys
   {
     int b0, e0, b1, e1;
-    kv8_seen(p, sp, (int)(row0 / p.group), b0, e0);
-    kv8_seen(p, sp, (int)((row0 + here - 1) / p.group), b1, e1);
+    kv8_seen(p, sp, row0 / p.group, b0, e0);
+    kv8_seen(p, sp, (row0 + here - 1) / p.group, b1, e1);
     // begins and ends both grow along the rows
     ka = b0 / kKeys;
     kb = e1 > b0 ? (e1 + kKeys - 1) / kKeys : ka;
@@ -202,50 +216,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
       mbar_init(&kfree[i], two ? 2 : 1), mbar_init(&vfree[i], two ? 2 : 1);
       mbar_init(&odone[i], 1);
-      mbar_init(&sfull[i], 1), mbar_init(&pready[i], 128);
+      mbar_init(&sfull[i], 1), mbar_init(&pready[i], 256);
       mbar_init(&cfull[i][0], 1), mbar_init(&cfull[i][1], 1);
     }
     abort_flag = 0;
     fence_mbar_init();
   }
 
-  // ---- queries: one thread per row; what it keeps for the softmax ----
-  const int i_row = warp < kSoftWarps ? tid : 0;  // row of the block
-  float rowfac = 0.f;
-  int beg = 0, end = 0;
-  const int qi = (int)((row0 + i_row) / p.group), hg = (int)((row0 + i_row) % p.group);
-  const bool mine = warp < kSoftWarps && i_row < here;
+  // ---- queries, 16 rows per warp, two at a time: 16 (or 8) lanes read a row ----
   if (warp < kSoftWarps) {
-    unsigned char* to = sQ + (i_row / 128) * kTileBytes;
-    const int row = i_row % 128;
-    const __nv_bfloat16* x8 = p.x + kv8_at(p, r, sp.base, qi, p.x_row, p.x_token) +
-                              (h * p.group + hg) * p.x_head;
-    if (mine) kv8_seen(p, sp, qi, beg, end);
-    uint4 q[DIM / 8];
+    constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;  // lanes of a row, rows at a time
+    const int u = lane % kLanes;
+    uint4 q[16 / kAt];
 #pragma unroll
-    for (int u = 0; u < DIM / 8; ++u)
-      q[u] = mine ? *reinterpret_cast<const uint4*>(x8 + 8 * u) : make_uint4(0, 0, 0, 0);
-    float most = 0.f;
+    for (int k = 0; k < 16 / kAt; ++k) {
+      const int i = warp * 16 + k * kAt + lane / kLanes, qi = (row0 + i) / p.group;
+      q[k] = make_uint4(0, 0, 0, 0);
+      if (i < here)
+        q[k] = *reinterpret_cast<const uint4*>(
+            p.x + kv8_at(p, r, sp.base, qi, p.x_row, p.x_token) +
+            (int64_t)(h * p.group + (row0 + i) % p.group) * p.x_head + 8 * u);
+    }
 #pragma unroll
-    for (int u = 0; u < DIM / 8; ++u) {
-      float f[8];
-      bf16x8(q[u], f);
+    for (int k = 0; k < 16 / kAt; ++k) {
+      const int i = warp * 16 + k * kAt + lane / kLanes;
+      float f[8], most = 0.f;
+      bf16x8(q[k], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
-    }
-    float up, back;
-    kv8_q_factor<8>(most, up, back);
-    rowfac = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
-    if (p.scale < 0.f) up = -up;
 #pragma unroll
-    for (int u = 0; u < DIM / 8; ++u) {
-      float f[8];
-      bf16x8(q[u], f);
-      *reinterpret_cast<uint4*>(to + unit_at(row, u)) =
+      for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      float up, back;
+      kv8_q_factor<8>(most, up, back);
+      if (u == 0) row_factor[i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
+      if (p.scale < 0.f) up = -up;
+      *reinterpret_cast<uint4*>(sQ + (i / 128) * kTileBytes + unit_at(i % 128, u)) =
           make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
                      pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
     }
     fence_proxy_async();
+  }
+  // meanwhile, the loader's page ids and scales of its first tiles
+  const int boxes = kKeys >> p.shift;
+  auto page_of = [&](int tile) {
+    const int j = tile * kKeys + (lane << p.shift);
+    return lane < boxes && j < sp.end ? p.table[(int64_t)r * p.cols + (j >> p.shift)] : -1;
+  };
+  auto scale_of = [&](int id) {
+    if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
+    const int64_t tile = (int64_t)id * p.heads + h;
+    return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
+  };
+  int id = -1, id1 = -1;
+  float2 sc0 = make_float2(0.f, 0.f);
+  if (warp == kIssuer + 1) {
+    if (nt > 0) id = page_of(ka), sc0 = scale_of(id);
+    if (nt > 1) id1 = page_of(ka + 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -258,50 +284,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     return false;
   };
 
-  float l = 0.f, m = -INFINITY, mv = -INFINITY;
-
   if (warp < kSoftWarps) {
     set_regs_up<kSoftRegs>();
     // ======================= softmax =======================
-    const int t = warp / 4;
+    // Two threads per query row, each with half of a tile's keys; they agree on the
+    // row's maxima through shared memory.
+    const int t = warp / 8, half = (warp / 4) & 1, row = (warp & 3) * 32 + lane, i_row = t * 128 + row;
+    constexpr int HK = kKeys / 2, HC = CH / 2;  // a thread's keys, and blocks of them
+    float l = 0.f, m = -INFINITY, mv = -INFINITY;
+    const float rowfac = row_factor[i_row];
+    const bool mine = i_row < here;
+    const int qi = (row0 + i_row) / p.group;
+    int beg = 0, end = 0;
+    if (mine) kv8_seen(p, sp, qi, beg, end);
+    __syncwarp();
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_col = lane_base + t * kKeys, o_col = lane_base + 256 + t * 128;
+    const uint32_t s_col = lane_base + t * kKeys, o_col = lane_base + 256 + t * 128 + half * (DIM / 2);
     // keys that every row of this tile sees
     int in0 = 0, in1 = 0;
     {
-      const int64_t last = row0 + (t * 128 + 127 < here ? t * 128 + 127 : here - 1);
+      const int last = row0 + min(t * 128 + 127, here - 1);
       int b0, e0, b1, e1;
-      kv8_seen(p, sp, (int)((row0 + t * 128) / p.group), b0, e0);
-      kv8_seen(p, sp, (int)(last / p.group), b1, e1);
+      kv8_seen(p, sp, (row0 + t * 128) / p.group, b0, e0);
+      kv8_seen(p, sp, last / p.group, b1, e1);
       in0 = b1, in1 = e0;
     }
     const bool run = t == 0 || two;  // the tile has rows
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 256;\n" ::"r"(1 + t) : "memory"); };
     bool ok = true;
     for (int i = 0; i < nt && run; ++i) {
-      if (!__all_sync(0xffffffffu, wait(&sfull[t], i & 1))) {
-        ok = false;
-        break;
+      ok = ok && __all_sync(0xffffffffu, wait(&sfull[t], i & 1));
+      if (!ok) {  // a wait gave up: only the barriers that others may stand at
+        pair_sync();
+        continue;
       }
       tc_fence_after();
-      const int j0 = (ka + i) * kKeys;
-      const int have = valid[i & 3];
-      float v[4][32];
+      const int j0 = (ka + i) * kKeys + half * HK;
+      const int have = valid[i & 3] >> (half * HC);
+      float v[2][32];
+      tmem_ld32(s_col + half * HK, v[0]);
+      tmem_ld32(s_col + half * HK + 32, v[1]);
+      tmem_wait_ld(v[0]);
+      tmem_wait_ld(v[1]);
+      if ((have & ((1 << HC) - 1)) != (1 << HC) - 1 || j0 < in0 || j0 + HK > in1) {
+        const int first = beg - j0;
+        const unsigned n = (unsigned)max(end - beg, 0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld(v[c]);
-      if (have != (1 << CH) - 1 || j0 < in0 || j0 + kKeys > in1) {
-#pragma unroll
-        for (int e = 0; e < kKeys; ++e) {
-          const int j = j0 + e;
-          if (j < beg || j >= end || !(have >> (e / BK) & 1)) v[e / 32][e % 32] = -INFINITY;
-        }
+        for (int e = 0; e < HK; ++e)
+          if ((unsigned)(e - first) >= n || !(have >> (e / BK) & 1)) v[e / 32][e % 32] = -INFINITY;
       }
       // largest product of each block
-      float fac[CH], off[CH];
-      float nm = m, nv = -INFINITY;
+      float fac[HC], off[HC];
+      float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
+      for (int c = 0; c < HC; ++c) {
         float top[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -309,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
 #pragma unroll
           for (int e = q + 4; e < BK; e += 4) top[q] = fmaxf(top[q], v[(c * BK + e) / 32][(c * BK + e) % 32]);
         }
-        const float2 sc = meta[i & 3][c];
+        const float2 sc = meta[i & 3][half * HC + c];
         // (a factor of 0 would make -inf of a masked key a NaN)
         fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
         off[c] = sc.y;
@@ -317,6 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         nm = fmaxf(nm, x);
         nv = fmaxf(nv, x + sc.y);
       }
+      // (the other thread has its half of S in registers before it comes here, so P
+      // may be written over S after this)
+      other[i & 1][half][i_row] = make_float2(nm, nv);
+      pair_sync();
+      const float2 o2 = other[i & 1][half ^ 1][i_row];
+      nm = fmaxf(fmaxf(nm, o2.x), m), nv = fmaxf(nv, o2.y);
       const float um = nm == -INFINITY ? 0.f : nm;
       l *= ex2_approx_f(m - um);
       m = nm;
@@ -325,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         mv = to;
         if (i > 0) {  // the products into O so far have completed with S
 #pragma unroll 1
-          for (int c = 0; c < DIM / 16; ++c) {
+          for (int c = 0; c < DIM / 32; ++c) {
             float w[16];
             tmem_ld16(o_col + 16 * c, w);
             uint32_t u[16];
@@ -337,10 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       }
       const float uv = mv == -INFINITY ? 0.f : mv;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
-      float2 sum[CH];
+      for (int c = 0; c < HC; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+      float2 sum[HC];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -351,16 +393,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           sum[b] = (32 * c + e) % BK == 0 ? w : add2(sum[b], w);
           pk[e / 2] = pack_f16(w.x, w.y);
         }
-        tmem_st16(s_col + 16 * c, pk);
+        tmem_st16(s_col + half * (HK / 2) + 16 * c, pk);
       }
 #pragma unroll
-      for (int c = 0; c < CH; ++c) l = fmaf(sum[c].x + sum[c].y, ex2_approx_f(-off[c] - um), l);
+      for (int c = 0; c < HC; ++c) l = fmaf(sum[c].x + sum[c].y, ex2_approx_f(-off[c] - um), l);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&pready[t]);
     }
 
-    // ---- outputs ----
+    // ---- outputs: each thread half of its row's dims ----
+    // the row's sum, in the order of the keys
+    pair_sync();
+    other[0][half][i_row].x = l;
+    pair_sync();
+    l = other[0][0][i_row].x + other[0][1][i_row].x;
     const bool any = nt > 0 && run && ok;
     if (any) {
       ok = __all_sync(0xffffffffu, wait(&odone[t], 0));
@@ -368,13 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     }
     const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
     const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + hg;
+    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + (row0 + i_row) % p.group;
     float* part = a.ws + ((int64_t)blockIdx.x * kRows + i_row) * (DIM + 4);
+    const bool wide = ((uintptr_t)p.o & 31) == 0;
     if ((nt == 0 || run) && ok) {
 #pragma unroll
-      for (int c = 0; c < DIM / 32; ++c) {
+      for (int c = 0; c < DIM / 64; ++c) {
         float v[32];
         if (any) {
+          __syncwarp();
           tmem_ld32(o_col + 32 * c, v);
           tmem_wait_ld(v);
         } else {
@@ -382,23 +431,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
         if (mine) {
-          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3)
+          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3); where nothing was seen the
+          // factor is 0 and O holds finite sums or zeros
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            // where nothing was seen the factor is 0 and O holds finite sums or zeros
-            const float f0 = v[e] * fac, f1 = v[e + 2] * fac, f2 = v[e + 1] * fac, f3 = v[e + 3] * fac;
-            const float f4 = v[e + 4] * fac, f5 = v[e + 6] * fac, f6 = v[e + 5] * fac, f7 = v[e + 7] * fac;
+          for (int e = 0; e < 32; e += 16) {
+            const int d = half * (DIM / 2) + 32 * c + e;
             if (a.splits == 1) {
-              *reinterpret_cast<uint4*>(p.o + at * DIM + 32 * c + e) =
-                  make_uint4(pack_bf16(f0, f1), pack_bf16(f2, f3), pack_bf16(f4, f5), pack_bf16(f6, f7));
+              uint32_t w[8];
+#pragma unroll
+              for (int f = 0; f < 16; f += 4)
+                w[f / 2] = pack_bf16(v[e + f] * fac, v[e + f + 2] * fac),
+                w[f / 2 + 1] = pack_bf16(v[e + f + 1] * fac, v[e + f + 3] * fac);
+              store32(p.o + at * DIM + d, w, wide);
             } else {
-              *reinterpret_cast<float4*>(part + 32 * c + e) = make_float4(f0, f1, f2, f3);
-              *reinterpret_cast<float4*>(part + 32 * c + e + 4) = make_float4(f4, f5, f6, f7);
+#pragma unroll
+              for (int f = 0; f < 16; f += 4)
+                *reinterpret_cast<float4*>(part + d + f) =
+                    make_float4(v[e + f] * fac, v[e + f + 2] * fac, v[e + f + 1] * fac, v[e + f + 3] * fac);
             }
           }
         }
       }
-      if (mine) {
+      if (mine && half == 0) {
         if (a.splits > 1) part[DIM] = lse2;
         else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
       }
@@ -442,23 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   } else {
     set_regs_down<kIssueRegs>();
   }
-  if (warp == kSoftWarps + kConvWarps + 1) {
+  if (warp == kIssuer + 1) {
     // ======================= codes by TMA =======================
-    // page ids and scales were asked for a tile before
-    const int boxes = kKeys >> p.shift;
-    auto page_of = [&](int tile) {
-      const int j = tile * kKeys + (lane << p.shift);
-      return lane < boxes && j < sp.end ? p.table[(int64_t)r * p.cols + (j >> p.shift)] : -1;
-    };
-    auto scale_of = [&](int id) {
-      if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
-      const int64_t tile = (int64_t)id * p.heads + h;
-      return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
-    };
-    int id = -1, id1 = -1, issued[2] = {0, 0};
-    float2 sc = make_float2(0.f, 0.f);
-    if (nt > 0) id = page_of(ka), sc = scale_of(id);
-    if (nt > 1) id1 = page_of(ka + 1);
+    // page ids and scales are asked for a tile before
+    int issued[2] = {0, 0};
+    float2 sc = sc0;
     for (int i = 0; i < nt; ++i) {
       const bool have = id >= 0 && id < p.pages;
       // block c of the scales lies in page c >> (log2 of blocks per page)
@@ -494,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
       for (int i = max(issued[kv] - 2, 0); i < issued[kv]; ++i) mbar_wait(&cfull[kv][i & 1], (i >> 1) & 1);
-  } else if ((warp == kSoftWarps + kConvWarps || (warp == kSoftWarps + kConvWarps + 2 && two)) && nt > 0) {
+  } else if ((warp == kIssuer || (warp == kIssuer + 2 && two)) && nt > 0) {
     // ======================= products of tile t =======================
     // One warp per tile, so that the waits of one do not hold up the other.  The
     // whole warp goes through this, so that descriptors stay in uniform registers;
     // one elected lane issues.
-    const int t = warp == kSoftWarps + kConvWarps ? 0 : 1;
+    const int t = warp == kIssuer ? 0 : 1;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
     const uint32_t dq = desc_lo(base + t * kTileBytes, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
