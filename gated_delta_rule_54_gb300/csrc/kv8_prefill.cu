@@ -43,8 +43,9 @@ struct PrefillArgs {
   Kv8Params p;
   CUtensorMap map;  // codes, a page of a head per box
   float* ws;   // splits > 1: parts [block][split][256][DIM + 1 ...]
-  int blocks;  // 256-row blocks of a row's queries
-  int splits;  // CTAs that share the keys of a block
+  int blocks;      // 256-row blocks of a row's queries
+  int splits;      // items that share the keys of a block
+  unsigned items;  // rows * heads * blocks * splits
 };
 
 // fp16 x fp16 -> fp32
@@ -157,7 +158,43 @@ __device__ __forceinline__ void store32(__nv_bfloat16* to, const uint32_t (&w)[8
   }
 }
 
-// CH: blocks of a tile of keys that have scales of their own (two at least)
+// One piece of work: up to 256 query rows of a (row, K/V head), and the tiles of
+// keys that they see (of which a split has its share).  Items with the most keys
+// come first, so that the CTAs, which take every gridDim.x-th, end together.
+struct Item {
+  Kv8Span sp;
+  int r, h, row0, here;  // here == 0: nothing
+  int ka, nt;
+  bool two;
+};
+__device__ __forceinline__ Item item_of(const PrefillArgs& a, unsigned at) {
+  const Kv8Params& p = a.p;
+  const unsigned rh = (unsigned)(p.rows * p.heads);
+  const int split = at % a.splits;
+  const unsigned x = at / a.splits;
+  Item m;
+  m.row0 = (a.blocks - 1 - (int)(x / rh)) * kRows;
+  m.r = (int)(x % rh / (unsigned)p.heads), m.h = (int)(x % rh % (unsigned)p.heads);
+  m.sp = kv8_span(p, m.r);
+  m.here = max(min(m.sp.n * p.group - m.row0, kRows), 0);
+  m.two = m.here > 128;
+  m.ka = m.nt = 0;
+  if (m.here > 0) {
+    int b0, e0, b1, e1;
+    kv8_seen(p, m.sp, m.row0 / p.group, b0, e0);
+    kv8_seen(p, m.sp, (m.row0 + m.here - 1) / p.group, b1, e1);
+    // begins and ends both grow along the rows
+    const int ka = b0 / kKeys;
+    const int64_t n = e1 > b0 ? (e1 + kKeys - 1) / kKeys - ka : 0;
+    m.ka = ka + (int)(n * split / a.splits);
+    m.nt = ka + (int)(n * (split + 1) / a.splits) - m.ka;
+  }
+  return m;
+}
+
+// CH: blocks of a tile of keys that have scales of their own (two at least).
+// The CTA stays for all its items: the loader and the converters run ahead into the
+// next one while the rows of this one finish.
 template <int MODE, int DIM, int CH>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int kTileBytes = kKeys * DIM * 2;
@@ -165,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   constexpr int BK = kKeys / CH;   // keys of a block
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], odone[2];
-  __shared__ __align__(8) uint64_t cfull[2][2];  // codes of K, of V
+  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2];  // by buffer
+  __shared__ __align__(8) uint64_t cfull[2][2];                             // codes of K, of V
+  __shared__ __align__(8) uint64_t qready[2], sfull[2], pready[2], odone[2];  // by tile of rows
   __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
   __shared__ int valid[4];        // bit c: the block has a page
   __shared__ float row_factor[kRows];
@@ -185,93 +223,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     return DIM == 128 ? sK + (2 * kv + b) * kTileBytes + kKeys * 128 : smem + 6 * kTileBytes + (2 * kv + b) * kKeys * DIM;
   };
 
-  // ---- which rows and keys (long blocks of rows first) ----
-  const unsigned rh = (unsigned)(p.rows * p.heads);
-  const int split = blockIdx.x % a.splits;
-  const unsigned x = blockIdx.x / a.splits;
-  const int block = a.blocks - 1 - (int)(x / rh);
-  const int r = (int)(x % rh / (unsigned)p.heads), h = (int)(x % rh % (unsigned)p.heads);
-  const Kv8Span sp = kv8_span(p, r);
-  const int rows = sp.n * p.group, row0 = block * kRows;
-  if (row0 >= rows) return;
-  const int here = min(rows - row0, kRows);
-  const bool two = here > 128;
-  int ka, kb;  // tiles of keys
-  {
-    int b0, e0, b1, e1;
-    kv8_seen(p, sp, row0 / p.group, b0, e0);
-    kv8_seen(p, sp, (row0 + here - 1) / p.group, b1, e1);
-    // begins and ends both grow along the rows
-    ka = b0 / kKeys;
-    kb = e1 > b0 ? (e1 + kKeys - 1) / kKeys : ka;
-    const int64_t n = kb - ka;
-    kb = ka + (int)(n * (split + 1) / a.splits);
-    ka = ka + (int)(n * split / a.splits);
-  }
-  const int nt = kb - ka;
-
   if (warp == 0) tmem_alloc(&tmem_slot, kCols);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
-      mbar_init(&kfree[i], two ? 2 : 1), mbar_init(&vfree[i], two ? 2 : 1);
-      mbar_init(&odone[i], 1);
-      mbar_init(&sfull[i], 1), mbar_init(&pready[i], 256);
+      mbar_init(&kfree[i], 2), mbar_init(&vfree[i], 2);  // both issuers
       mbar_init(&cfull[i][0], 1), mbar_init(&cfull[i][1], 1);
+      mbar_init(&qready[i], 256), mbar_init(&sfull[i], 1), mbar_init(&pready[i], 256);
+      mbar_init(&odone[i], 1);
     }
     abort_flag = 0;
     fence_mbar_init();
-  }
-
-  // ---- queries, 16 rows per warp, two at a time: 16 (or 8) lanes read a row ----
-  if (warp < kSoftWarps) {
-    constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;  // lanes of a row, rows at a time
-    const int u = lane % kLanes;
-    uint4 q[16 / kAt];
-#pragma unroll
-    for (int k = 0; k < 16 / kAt; ++k) {
-      const int i = warp * 16 + k * kAt + lane / kLanes, qi = (row0 + i) / p.group;
-      q[k] = make_uint4(0, 0, 0, 0);
-      if (i < here)
-        q[k] = *reinterpret_cast<const uint4*>(
-            p.x + kv8_at(p, r, sp.base, qi, p.x_row, p.x_token) +
-            (int64_t)(h * p.group + (row0 + i) % p.group) * p.x_head + 8 * u);
-    }
-#pragma unroll
-    for (int k = 0; k < 16 / kAt; ++k) {
-      const int i = warp * 16 + k * kAt + lane / kLanes;
-      float f[8], most = 0.f;
-      bf16x8(q[k], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      float up, back;
-      kv8_q_factor<8>(most, up, back);
-      if (u == 0) row_factor[i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
-      if (p.scale < 0.f) up = -up;
-      *reinterpret_cast<uint4*>(sQ + (i / 128) * kTileBytes + unit_at(i % 128, u)) =
-          make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
-                     pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
-    }
-    fence_proxy_async();
-  }
-  // meanwhile, the loader's page ids and scales of its first tiles
-  const int boxes = kKeys >> p.shift;
-  auto page_of = [&](int tile) {
-    const int j = tile * kKeys + (lane << p.shift);
-    return lane < boxes && j < sp.end ? p.table[(int64_t)r * p.cols + (j >> p.shift)] : -1;
-  };
-  auto scale_of = [&](int id) {
-    if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
-    const int64_t tile = (int64_t)id * p.heads + h;
-    return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
-  };
-  int id = -1, id1 = -1;
-  float2 sc0 = make_float2(0.f, 0.f);
-  if (warp == kIssuer + 1) {
-    if (nt > 0) id = page_of(ka), sc0 = scale_of(id);
-    if (nt > 1) id1 = page_of(ka + 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -286,261 +248,338 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
 
   if (warp < kSoftWarps) {
     set_regs_up<kSoftRegs>();
-    // ======================= softmax =======================
+    // ======================= rows =======================
     // Two threads per query row, each with half of a tile's keys; they agree on the
     // row's maxima through shared memory.
     const int t = warp / 8, half = (warp / 4) & 1, row = (warp & 3) * 32 + lane, i_row = t * 128 + row;
     constexpr int HK = kKeys / 2, HC = CH / 2;  // a thread's keys, and blocks of them
-    float l = 0.f, m = -INFINITY, mv = -INFINITY;
-    const float rowfac = row_factor[i_row];
-    const bool mine = i_row < here;
-    const int qi = (row0 + i_row) / p.group;
-    int beg = 0, end = 0;
-    if (mine) kv8_seen(p, sp, qi, beg, end);
-    __syncwarp();
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 256;\n" ::"r"(1 + t) : "memory"); };
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lane_base + t * kKeys, o_col = lane_base + 256 + t * 128 + half * (DIM / 2);
-    // keys that every row of this tile sees
-    int in0 = 0, in1 = 0;
-    {
-      const int last = row0 + min(t * 128 + 127, here - 1);
-      int b0, e0, b1, e1;
-      kv8_seen(p, sp, (row0 + t * 128) / p.group, b0, e0);
-      kv8_seen(p, sp, last / p.group, b1, e1);
-      in0 = b1, in1 = e0;
-    }
-    const bool run = t == 0 || two;  // the tile has rows
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 256;\n" ::"r"(1 + t) : "memory"); };
-    bool ok = true;
-    for (int i = 0; i < nt && run; ++i) {
-      ok = ok && __all_sync(0xffffffffu, wait(&sfull[t], i & 1));
-      if (!ok) {  // a wait gave up: only the barriers that others may stand at
-        pair_sync();
-        continue;
-      }
-      tc_fence_after();
-      const int j0 = (ka + i) * kKeys + half * HK;
-      const int have = valid[i & 3] >> (half * HC);
-      float v[2][32];
-      tmem_ld32(s_col + half * HK, v[0]);
-      tmem_ld32(s_col + half * HK + 32, v[1]);
-      tmem_wait_ld(v[0]);
-      tmem_wait_ld(v[1]);
-      if ((have & ((1 << HC) - 1)) != (1 << HC) - 1 || j0 < in0 || j0 + HK > in1) {
-        const int first = beg - j0;
-        const unsigned n = (unsigned)max(end - beg, 0);
-#pragma unroll
-        for (int e = 0; e < HK; ++e)
-          if ((unsigned)(e - first) >= n || !(have >> (e / BK) & 1)) v[e / 32][e % 32] = -INFINITY;
-      }
-      // largest product of each block
-      float fac[HC], off[HC];
-      float nm = -INFINITY, nv = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < HC; ++c) {
-        float top[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          top[q] = v[(c * BK + q) / 32][(c * BK + q) % 32];
-#pragma unroll
-          for (int e = q + 4; e < BK; e += 4) top[q] = fmaxf(top[q], v[(c * BK + e) / 32][(c * BK + e) % 32]);
-        }
-        const float2 sc = meta[i & 3][half * HC + c];
-        // (a factor of 0 would make -inf of a masked key a NaN)
-        fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
-        off[c] = sc.y;
-        const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac[c];
-        nm = fmaxf(nm, x);
-        nv = fmaxf(nv, x + sc.y);
-      }
-      // (the other thread has its half of S in registers before it comes here, so P
-      // may be written over S after this)
-      other[i & 1][half][i_row] = make_float2(nm, nv);
-      pair_sync();
-      const float2 o2 = other[i & 1][half ^ 1][i_row];
-      nm = fmaxf(fmaxf(nm, o2.x), m), nv = fmaxf(nv, o2.y);
-      const float um = nm == -INFINITY ? 0.f : nm;
-      l *= ex2_approx_f(m - um);
-      m = nm;
-      if (__any_sync(0xffffffffu, nv > mv + 8.f)) {
-        const float to = fmaxf(mv, nv), f = ex2_approx_f(mv - (to == -INFINITY ? 0.f : to));
-        mv = to;
-        if (i > 0) {  // the products into O so far have completed with S
-#pragma unroll 1
-          for (int c = 0; c < DIM / 32; ++c) {
-            float w[16];
-            tmem_ld16(o_col + 16 * c, w);
-            uint32_t u[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(w[e] * f);
-            tmem_st16(o_col + 16 * c, u);
-          }
-        }
-      }
-      const float uv = mv == -INFINITY ? 0.f : mv;
-#pragma unroll
-      for (int c = 0; c < HC; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
-      float2 sum[HC];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int b = (32 * c + e) / BK;
-          const float2 x = fma2(make_float2(v[c][e], v[c][e + 1]), make_float2(fac[b], fac[b]),
-                                make_float2(off[b], off[b]));
-          const float2 w = make_float2(ex2_approx_f(x.x), ex2_approx_f(x.y));
-          sum[b] = (32 * c + e) % BK == 0 ? w : add2(sum[b], w);
-          pk[e / 2] = pack_f16(w.x, w.y);
-        }
-        tmem_st16(s_col + half * (HK / 2) + 16 * c, pk);
-      }
-#pragma unroll
-      for (int c = 0; c < HC; ++c) l = fmaf(sum[c].x + sum[c].y, ex2_approx_f(-off[c] - um), l);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&pready[t]);
-    }
-
-    // ---- outputs: each thread half of its row's dims ----
-    // the row's sum, in the order of the keys
-    pair_sync();
-    other[0][half][i_row].x = l;
-    pair_sync();
-    l = other[0][0][i_row].x + other[0][1][i_row].x;
-    const bool any = nt > 0 && run && ok;
-    if (any) {
-      ok = __all_sync(0xffffffffu, wait(&odone[t], 0));
-      tc_fence_after();
-    }
-    const float fac = any && l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - m + kKv8Shift<MODE>) / l : 0.f;
-    const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-    const int64_t at = (sp.base + qi) * (p.heads * p.group) + h * p.group + (row0 + i_row) % p.group;
-    float* part = a.ws + ((int64_t)blockIdx.x * kRows + i_row) * (DIM + 4);
     const bool wide = ((uintptr_t)p.o & 31) == 0;
-    if ((nt == 0 || run) && ok) {
+    // Queries: a warp brings 16 rows of its tile, 16 (or 8) lanes to a row.
+    constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;  // lanes of a row, rows at a time
+    uint4 q[16 / kAt];
+    auto load_q = [&](const Item& m) {
+      const int i0 = t * 128 + (warp & 7) * 16 + lane / kLanes;
+      int qi = (m.row0 + i0) / p.group, hg = (m.row0 + i0) % p.group;
 #pragma unroll
-      for (int c = 0; c < DIM / 64; ++c) {
-        float v[32];
-        if (any) {
-          __syncwarp();
-          tmem_ld32(o_col + 32 * c, v);
-          tmem_wait_ld(v);
-        } else {
+      for (int k = 0; k < 16 / kAt; ++k) {
+        q[k] = make_uint4(0, 0, 0, 0);
+        if (i0 + k * kAt < m.here)
+          q[k] = *reinterpret_cast<const uint4*>(p.x + kv8_at(p, m.r, m.sp.base, qi, p.x_row, p.x_token) +
+                                                 (int64_t)(m.h * p.group + hg) * p.x_head + 8 * (lane % kLanes));
+        for (hg += kAt; hg >= p.group; hg -= p.group) ++qi;
+      }
+    };
+    auto store_q = [&]() {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+      for (int k = 0; k < 16 / kAt; ++k) {
+        const int i = (warp & 7) * 16 + k * kAt + lane / kLanes, u = lane % kLanes;
+        float f[8], most = 0.f;
+        bf16x8(q[k], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(f[e]));
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        float up, back;
+        kv8_q_factor<8>(most, up, back);
+        if (u == 0) row_factor[t * 128 + i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
+        if (p.scale < 0.f) up = -up;
+        *reinterpret_cast<uint4*>(sQ + t * kTileBytes + unit_at(i, u)) =
+            make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
+                       pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
+      }
+      fence_proxy_async();
+    };
+    bool ok = true;
+    // tiles of keys that the tile of rows went through, all of the CTA's, and items with any
+    uint32_t n = 0, kv_tiles = 0, outs = 0;
+    for (unsigned it = blockIdx.x; it < a.items; it += gridDim.x) {
+      const Item m = item_of(a, it);
+      const bool run = m.here > 0 && (t == 0 || m.two);  // the tile has rows
+      if (run) {
+        load_q(m);
+        store_q();  // (the products that read the item before have completed)
+        pair_sync();
+        if (m.nt > 0 && ok) mbar_arrive(&qready[t]);
+      }
+      float l = 0.f, mx = -INFINITY, mv = -INFINITY;
+      const float rowfac = row_factor[i_row];
+      const bool mine = i_row < m.here;
+      const int qi = (m.row0 + i_row) / p.group;
+      int beg = 0, end = 0, in0, in1;  // keys of this row, and those that every row of this tile sees
+      if (mine) kv8_seen(p, m.sp, qi, beg, end);
+      {
+        const int last = m.row0 + max(min(t * 128 + 127, m.here - 1), 0);
+        int b0, e0, b1, e1;
+        kv8_seen(p, m.sp, (m.row0 + t * 128) / p.group, b0, e0);
+        kv8_seen(p, m.sp, last / p.group, b1, e1);
+        in0 = b1, in1 = e0;
+      }
+      __syncwarp();
+      for (int i = 0; i < m.nt && run; ++i) {
+        const uint32_t tile = n + i;
+        ok = ok && __all_sync(0xffffffffu, wait(&sfull[t], tile & 1));
+        if (!ok) {  // a wait gave up: only the barriers that others may stand at
+          pair_sync();
+          continue;
         }
-        if (mine) {
-          // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3); where nothing was seen the
-          // factor is 0 and O holds finite sums or zeros
+        tc_fence_after();
+        const int j0 = (m.ka + i) * kKeys + half * HK;
+        const uint32_t slot = (kv_tiles + i) & 3;
+        const int have = valid[slot] >> (half * HC);
+        float v[2][32];
+        tmem_ld32(s_col + half * HK, v[0]);
+        tmem_ld32(s_col + half * HK + 32, v[1]);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        if ((have & ((1 << HC) - 1)) != (1 << HC) - 1 || j0 < in0 || j0 + HK > in1) {
+          const int first = beg - j0;
+          const unsigned len = (unsigned)max(end - beg, 0);
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            const int d = half * (DIM / 2) + 32 * c + e;
-            if (a.splits == 1) {
-              uint32_t w[8];
+          for (int e = 0; e < HK; ++e)
+            if ((unsigned)(e - first) >= len || !(have >> (e / BK) & 1)) v[e / 32][e % 32] = -INFINITY;
+        }
+        // largest product of each block
+        float fac[HC], off[HC];
+        float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
-              for (int f = 0; f < 16; f += 4)
-                w[f / 2] = pack_bf16(v[e + f] * fac, v[e + f + 2] * fac),
-                w[f / 2 + 1] = pack_bf16(v[e + f + 1] * fac, v[e + f + 3] * fac);
-              store32(p.o + at * DIM + d, w, wide);
-            } else {
+        for (int c = 0; c < HC; ++c) {
+          float top[4];
 #pragma unroll
-              for (int f = 0; f < 16; f += 4)
-                *reinterpret_cast<float4*>(part + d + f) =
-                    make_float4(v[e + f] * fac, v[e + f + 2] * fac, v[e + f + 1] * fac, v[e + f + 3] * fac);
+          for (int q4 = 0; q4 < 4; ++q4) {
+            top[q4] = v[(c * BK + q4) / 32][(c * BK + q4) % 32];
+#pragma unroll
+            for (int e = q4 + 4; e < BK; e += 4) top[q4] = fmaxf(top[q4], v[(c * BK + e) / 32][(c * BK + e) % 32]);
+          }
+          const float2 sc = meta[slot][half * HC + c];
+          // (a factor of 0 would make -inf of a masked key a NaN)
+          fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
+          off[c] = sc.y;
+          const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac[c];
+          nm = fmaxf(nm, x);
+          nv = fmaxf(nv, x + sc.y);
+        }
+        // (the other thread has its half of S in registers before it comes here, so P
+        // may be written over S after this)
+        other[i & 1][half][i_row] = make_float2(nm, nv);
+        pair_sync();
+        const float2 o2 = other[i & 1][half ^ 1][i_row];
+        nm = fmaxf(fmaxf(nm, o2.x), mx), nv = fmaxf(nv, o2.y);
+        const float um = nm == -INFINITY ? 0.f : nm;
+        l *= ex2_approx_f(mx - um);
+        mx = nm;
+        if (__any_sync(0xffffffffu, nv > mv + 8.f)) {
+          const float to = fmaxf(mv, nv), f = ex2_approx_f(mv - (to == -INFINITY ? 0.f : to));
+          mv = to;
+          if (i > 0) {  // the products into O so far have completed with S
+#pragma unroll 1
+            for (int c = 0; c < DIM / 32; ++c) {
+              float w[16];
+              tmem_ld16(o_col + 16 * c, w);
+              uint32_t u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(w[e] * f);
+              tmem_st16(o_col + 16 * c, u);
             }
           }
         }
+        const float uv = mv == -INFINITY ? 0.f : mv;
+#pragma unroll
+        for (int c = 0; c < HC; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+        float2 sum[HC];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int b = (32 * c + e) / BK;
+            const float2 x = fma2(make_float2(v[c][e], v[c][e + 1]), make_float2(fac[b], fac[b]),
+                                  make_float2(off[b], off[b]));
+            const float2 w = make_float2(ex2_approx_f(x.x), ex2_approx_f(x.y));
+            sum[b] = (32 * c + e) % BK == 0 ? w : add2(sum[b], w);
+            pk[e / 2] = pack_f16(w.x, w.y);
+          }
+          tmem_st16(s_col + half * (HK / 2) + 16 * c, pk);
+        }
+#pragma unroll
+        for (int c = 0; c < HC; ++c) l = fmaf(sum[c].x + sum[c].y, ex2_approx_f(-off[c] - um), l);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pready[t]);
       }
-      if (mine && half == 0) {
-        if (a.splits > 1) part[DIM] = lse2;
-        else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
+
+      if (run) {
+        // ---- outputs: each thread half of its row's dims ----
+        // the row's sum, in the order of the keys
+        pair_sync();
+        other[0][half][i_row].x = l;
+        pair_sync();
+        l = other[0][0][i_row].x + other[0][1][i_row].x;
+        const bool any = m.nt > 0;
+        if (any) {
+          ok = ok && __all_sync(0xffffffffu, wait(&odone[t], outs & 1));
+          tc_fence_after();
+        }
+        const float fac = l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - mx + kKv8Shift<MODE>) / l : 0.f;
+        const float lse2 = l > 0.f ? mx + log2f(l) : -INFINITY;
+        const int64_t at = (m.sp.base + qi) * (p.heads * p.group) + m.h * p.group + (m.row0 + i_row) % p.group;
+        float* part = a.ws + ((int64_t)it * kRows + i_row) * (DIM + 4);
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < DIM / 64; ++c) {
+            float v[32];
+            if (any) {
+              __syncwarp();
+              tmem_ld32(o_col + 32 * c, v);
+              tmem_wait_ld(v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = 0.f;
+            }
+            if (mine) {
+              // columns 4 i .. 4 i + 3 are dims 4 i + (0 2 1 3); where nothing was seen the
+              // factor is 0 and O holds finite sums or zeros
+#pragma unroll
+              for (int e = 0; e < 32; e += 16) {
+                const int d = half * (DIM / 2) + 32 * c + e;
+                if (a.splits == 1) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int f = 0; f < 16; f += 4)
+                    w[f / 2] = pack_bf16(v[e + f] * fac, v[e + f + 2] * fac),
+                    w[f / 2 + 1] = pack_bf16(v[e + f + 1] * fac, v[e + f + 3] * fac);
+                  store32(p.o + at * DIM + d, w, wide);
+                } else {
+#pragma unroll
+                  for (int f = 0; f < 16; f += 4)
+                    *reinterpret_cast<float4*>(part + d + f) =
+                        make_float4(v[e + f] * fac, v[e + f + 2] * fac, v[e + f + 1] * fac, v[e + f + 3] * fac);
+                }
+              }
+            }
+          }
+          if (mine && half == 0) {
+            if (a.splits > 1) part[DIM] = lse2;
+            else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
+          }
+        }
+        tc_fence_before();  // O has been read: the next item's products may write it (after P's signal)
+        if (any) ++outs;
+        n += m.nt;
       }
+      kv_tiles += m.nt;
     }
-  } else if (warp < kSoftWarps + kConvWarps) {
+  } else if (warp < kIssuer) {
     set_regs_down<kConvRegs>();
     // ======================= codes to fp16 =======================
     // a lane takes 16 codes at a time; the two rows of eight neighbouring lanes are
     // chosen so that their loads and their stores each fall on different banks
-    const int ct = tid - kSoftWarps * 32, cw = ct / 32;
+    const int cw = warp - kSoftWarps;
     constexpr int kPer = DIM / 16, kStep = 2048 / DIM;
     const int unit = DIM == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const int r8 = DIM == 128 ? (lane >> 4 & 1) * 2 : lane >> 2;
     // 128-byte rows: (0 5) (1 4) (2 7) (3 6), the even warps the first of each two pairs
     const int row0c = DIM == 128 ? (cw / 2) * 8 + (((r8 + (cw & 1)) ^ ((lane >> 2 & 1) ? 5 : 0)))
                                  : cw * 8 + r8;
+    uint32_t n = 0;  // tiles so far
+    bool ok = true;
+    for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+      const int nt = item_of(a, it).nt;
 #pragma unroll 1
-    for (int x = 0; x < 2 * nt; ++x) {  // K 0, V 0, K 1, V 1, ...
-      const int kv = x & 1, i = x >> 1, b = i & 1;
-      if (!wait(&cfull[kv][b], (i >> 1) & 1)) break;
-      unsigned char* to = sK + (2 * kv + b) * kTileBytes;
-      const unsigned char* from = codes_at(kv, b);
+      for (int x = 0; x < 2 * nt && ok; ++x) {  // K, V, K, V, ...
+        const int kv = x & 1;
+        const uint32_t tile = n + (x >> 1), b = tile & 1;
+        ok = wait(&cfull[kv][b], (tile >> 1) & 1);
+        if (!ok) break;
+        unsigned char* to = sK + (2 * kv + b) * kTileBytes;
+        const unsigned char* from = codes_at(kv, b);
 #pragma unroll 4
-      for (int e = 0; e < kPer; ++e) {
-        const int row = row0c + e * kStep;
-        const int at = DIM == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
-                                  : row * 64 + ((unit ^ (row >> 1 & 3)) << 4);
-        const uint4 u = *reinterpret_cast<const uint4*>(from + at);
-        uint4 lo, hi;
-        kv8_half2<MODE>(u.x, lo.x, lo.y);
-        kv8_half2<MODE>(u.y, lo.z, lo.w);
-        kv8_half2<MODE>(u.z, hi.x, hi.y);
-        kv8_half2<MODE>(u.w, hi.z, hi.w);
-        __syncwarp();  // the row's eight lanes have read it: half of it is written over
-        *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
-        *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
+        for (int e = 0; e < kPer; ++e) {
+          const int row = row0c + e * kStep;
+          const int at = DIM == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
+                                    : row * 64 + ((unit ^ (row >> 1 & 3)) << 4);
+          const uint4 u = *reinterpret_cast<const uint4*>(from + at);
+          uint4 lo, hi;
+          kv8_half2<MODE>(u.x, lo.x, lo.y);
+          kv8_half2<MODE>(u.y, lo.z, lo.w);
+          kv8_half2<MODE>(u.z, hi.x, hi.y);
+          kv8_half2<MODE>(u.w, hi.z, hi.w);
+          __syncwarp();  // the row's eight lanes have read it: half of it is written over
+          *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
+          *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
+        }
+        fence_proxy_async();
+        mbar_arrive(kv ? &vfull[b] : &kfull[b]);
       }
-      fence_proxy_async();
-      mbar_arrive(kv ? &vfull[b] : &kfull[b]);
+      n += nt;
     }
   } else {
     set_regs_down<kIssueRegs>();
   }
   if (warp == kIssuer + 1) {
     // ======================= codes by TMA =======================
-    // page ids and scales are asked for a tile before
+    const int boxes = kKeys >> p.shift;
+    uint32_t n = 0;  // tiles so far
     int issued[2] = {0, 0};
-    float2 sc = sc0;
-    for (int i = 0; i < nt; ++i) {
-      const bool have = id >= 0 && id < p.pages;
-      // block c of the scales lies in page c >> (log2 of blocks per page)
-      const int from = (lane * BK) >> p.shift;
-      const float ks = __shfl_sync(0xffffffffu, sc.x, from & 31);
-      const float vs = __shfl_sync(0xffffffffu, sc.y, from & 31);
-      const bool there = __shfl_sync(0xffffffffu, (int)have, from & 31);
-      const unsigned bits = __ballot_sync(0xffffffffu, there && lane < CH);
-      const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have)) * (DIM << p.shift);
-      bool ok = true;
-      #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        ok = __all_sync(0xffffffffu, wait(kv ? &vfree[i & 1] : &kfree[i & 1], ((i >> 1) & 1) ^ 1));
-        if (!ok) break;
-        if (kv == 0) {
-          if (lane < CH) meta[i & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
-          if (lane == 0) valid[i & 3] = (int)bits;
+    bool ok = true;
+    for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+      const Item m = item_of(a, it);
+      // page ids and scales are asked for a tile before
+      auto page_of = [&](int i) {
+        const int j = (m.ka + i) * kKeys + (lane << p.shift);
+        return lane < boxes && i < m.nt && j < m.sp.end ? p.table[(int64_t)m.r * p.cols + (j >> p.shift)] : -1;
+      };
+      auto scale_of = [&](int id) {
+        if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
+        const int64_t tile = (int64_t)id * p.heads + m.h;
+        return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
+      };
+      int id = page_of(0), id1 = page_of(1);
+      float2 sc = scale_of(id);
+      for (int i = 0; i < m.nt; ++i) {
+        const uint32_t tile = n + i, b = tile & 1;
+        const bool have = id >= 0 && id < p.pages;
+        // block c of the scales lies in page c >> (log2 of blocks per page)
+        const int from = (lane * BK) >> p.shift;
+        const float ks = __shfl_sync(0xffffffffu, sc.x, from & 31);
+        const float vs = __shfl_sync(0xffffffffu, sc.y, from & 31);
+        const bool there = __shfl_sync(0xffffffffu, (int)have, from & 31);
+        const unsigned bits = __ballot_sync(0xffffffffu, there && lane < CH);
+        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have)) * (DIM << p.shift);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && __all_sync(0xffffffffu, wait(kv ? &vfree[b] : &kfree[b], ((tile >> 1) & 1) ^ 1));
+          if (!ok) break;
+          if (kv == 0) {
+            if (lane < CH) meta[tile & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
+            if (lane == 0) valid[tile & 3] = (int)bits;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(&cfull[kv][b], bytes);
+          __syncwarp();
+          issued[kv] = (int)tile + 1;
+          if (have)
+            tma_load_3d(codes_at(kv, b) + (lane << p.shift) * DIM, &a.map, 0, 0,
+                        (int)((kv * p.pages + id) * p.heads + m.h), &cfull[kv][b]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(&cfull[kv][i & 1], bytes);
-        __syncwarp();
-        issued[kv] = i + 1;
-        if (have)
-          tma_load_3d(codes_at(kv, i & 1) + (lane << p.shift) * DIM, &a.map, 0, 0,
-                      (int)((kv * p.pages + id) * p.heads + h), &cfull[kv][i & 1]);
+        if (!ok) break;
+        id = id1;
+        sc = scale_of(id);
+        id1 = page_of(i + 2);
       }
-      if (!ok) break;
-      id = id1;
-      sc = i + 1 < nt ? scale_of(id) : sc;
-      id1 = i + 2 < nt ? page_of(ka + i + 2) : -1;
+      n += m.nt;
     }
     // no copy is in flight when the CTA ends, whatever ended the loop
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
       for (int i = max(issued[kv] - 2, 0); i < issued[kv]; ++i) mbar_wait(&cfull[kv][i & 1], (i >> 1) & 1);
-  } else if ((warp == kIssuer || (warp == kIssuer + 2 && two)) && nt > 0) {
+  } else if (warp == kIssuer || warp == kIssuer + 2) {
     // ======================= products of tile t =======================
-    // One warp per tile, so that the waits of one do not hold up the other.  The
-    // whole warp goes through this, so that descriptors stay in uniform registers;
-    // one elected lane issues.
+    // One warp per tile of rows, so that the waits of one do not hold up the other.
+    // The whole warp goes through this, so that descriptors stay in uniform
+    // registers; one elected lane issues.
     const int t = warp == kIssuer ? 0 : 1;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
@@ -549,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     constexpr uint32_t kTileStep = kTileBytes >> 4;
     const uint32_t s_at = tm + t * kKeys, o_at = tm + 256 + t * 128;
     const bool lead = elect_one();
-    auto qk = [&](int i) {
-      const uint32_t k = dk + (i & 1) * kTileStep;
+    auto qk = [&](uint32_t b) {
+      const uint32_t k = dk + b * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
@@ -558,41 +597,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           umma_ss(s_at, dq + off, k + off, kIdQK, s > 0);
         }
         umma_commit(&sfull[t]);
-        umma_commit(&kfree[i & 1]);
+        umma_commit(&kfree[b]);
       }
       __syncwarp();
     };
-    auto pv = [&](int i) {
-      const uint32_t v = dv + (i & 1) * kTileStep;
+    auto pv = [&](uint32_t b, bool add) {
+      const uint32_t v = dv + b * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-          umma_ts(o_at, s_at + 8 * s, v + s * (2048 >> 4), kIdPV, i > 0 || s > 0);
-        umma_commit(&vfree[i & 1]);
+          umma_ts(o_at, s_at + 8 * s, v + s * (2048 >> 4), kIdPV, add || s > 0);
+        umma_commit(&vfree[b]);
       }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (lead) umma_commit(bar);
       __syncwarp();
     };
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wait(bar, parity));
     };
-    bool ok = all_wait(&kfull[0], 0);
-    if (ok) {
-      tc_fence_after();
-      qk(0);
+    uint32_t n = 0, mine = 0, outs = 0;  // tiles, tiles of this warp's, items of this warp's so far
+    bool ok = true;
+    for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
+      const Item m = item_of(a, it);
+      if (m.nt == 0) continue;
+      if (t == 0 || m.two) {
+        ok = all_wait(&qready[t], outs & 1) && all_wait(&kfull[n & 1], (n >> 1) & 1);
+        if (ok) {
+          tc_fence_after();
+          qk(n & 1);
+        }
+        for (int i = 0; i < m.nt && ok; ++i) {
+          const uint32_t tile = n + i;
+          ok = all_wait(&vfull[tile & 1], (tile >> 1) & 1);
+          // the next keys as well, while the rows still compute
+          if (i + 1 < m.nt) ok = ok && all_wait(&kfull[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
+          ok = ok && all_wait(&pready[t], (mine + i) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          pv(tile & 1, i > 0);
+          if (i + 1 < m.nt) qk((tile + 1) & 1);
+        }
+        mine += m.nt;
+        commit(&odone[t]);  // completes with every product issued so far
+        ++outs;
+      } else {
+        // no rows in this tile: the buffers are free as far as it goes
+        for (uint32_t tile = n; tile < n + m.nt && ok; ++tile) {
+          ok = all_wait(&kfull[tile & 1], (tile >> 1) & 1);
+          commit(&kfree[tile & 1]);
+          ok = ok && all_wait(&vfull[tile & 1], (tile >> 1) & 1);
+          commit(&vfree[tile & 1]);
+        }
+      }
+      n += m.nt;
     }
-    for (int i = 0; i < nt && ok; ++i) {
-      ok = all_wait(&vfull[i & 1], (i >> 1) & 1);
-      // the next keys as well, while the rows still compute
-      if (i + 1 < nt) ok = ok && all_wait(&kfull[(i + 1) & 1], ((i + 1) >> 1) & 1);
-      ok = ok && all_wait(&pready[t], i & 1);
-      if (!ok) break;
-      tc_fence_after();
-      pv(i);
-      if (i + 1 < nt) qk(i + 1);
-    }
-    if (lead) umma_commit(&odone[t]);  // completes with every product issued here
-    __syncwarp();
-    wait(&odone[t], 0);
+    if (outs > 0) wait(&odone[t], (outs - 1) & 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -664,7 +726,8 @@ gdn_status run(PrefillArgs& a, cudaStream_t st) {
   auto kern = kv8_prefill_kernel<MODE, DIM, CH>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return GDN_ERR_CUDA;
-  kern<<<(unsigned)(blocks * a.splits), kThreads, bytes, st>>>(a);
+  a.items = (unsigned)(blocks * a.splits);
+  kern<<<a.items < 152 ? a.items : 152, kThreads, bytes, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (a.splits == 1) return GDN_OK;
   kv8_prefill_join_kernel<DIM><<<dim3((unsigned)blocks, kRows / 8), 256, 0, st>>>(a);
