@@ -7,7 +7,7 @@
 //     P = 2^(s - reference)  (two threads per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
 // One warp brings the codes of 128 keys by TMA (a box per page); four turn them into
-// fp16 (exact), as swizzled operand tiles; one lane each of two warps issues a tile's
+// fp16 (exact), as swizzled operand tiles; one lane of a warp issues the
 // products; and eight warps per tile are its rows, two threads to a row.
 //
 // Products of fp16 codes bound it together with shared memory: per 128 keys the
@@ -33,7 +33,7 @@ __device__ int g_kv8_prefill_error;
 
 constexpr int kKeys = 128, kRows = 256;
 constexpr int kSoftWarps = 16, kConvWarps = 4;
-constexpr int kIssuer = kSoftWarps + kConvWarps;  // warps 20 and 22 issue, warp 21 loads
+constexpr int kIssuer = kSoftWarps + kConvWarps;  // warp 20 issues, warp 21 loads
 constexpr int kThreads = 768;
 // registers per thread of the warpgroups: together what the launch gave (6 x 80)
 constexpr int kSoftRegs = 96, kConvRegs = 48, kIssueRegs = 48;
@@ -158,6 +158,23 @@ __device__ __forceinline__ void store32(__nv_bfloat16* to, const uint32_t (&w)[8
   }
 }
 
+// 16 bytes, or zeros; a predicate rather than a branch, so that several of these are
+// in flight together
+__device__ __forceinline__ uint4 load_if(const __nv_bfloat16* from, bool there) {
+  uint4 u;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n"
+      " mov.b32 %3, 0;\n @p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+      : "l"(from), "r"((int)there));
+  return u;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // One piece of work: up to 256 query rows of a (row, K/V head), and the tiles of
 // keys that they see (of which a split has its share).  Items with the most keys
 // come first, so that the CTAs, which take every gridDim.x-th, end together.
@@ -227,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
-      mbar_init(&kfree[i], 2), mbar_init(&vfree[i], 2);  // both issuers
+      mbar_init(&kfree[i], 1), mbar_init(&vfree[i], 1);
       mbar_init(&cfull[i][0], 1), mbar_init(&cfull[i][1], 1);
       mbar_init(&qready[i], 256), mbar_init(&sfull[i], 1), mbar_init(&pready[i], 256);
       mbar_init(&odone[i], 1);
@@ -265,10 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       int qi = (m.row0 + i0) / p.group, hg = (m.row0 + i0) % p.group;
 #pragma unroll
       for (int k = 0; k < 16 / kAt; ++k) {
-        q[k] = make_uint4(0, 0, 0, 0);
-        if (i0 + k * kAt < m.here)
-          q[k] = *reinterpret_cast<const uint4*>(p.x + kv8_at(p, m.r, m.sp.base, qi, p.x_row, p.x_token) +
-                                                 (int64_t)(m.h * p.group + hg) * p.x_head + 8 * (lane % kLanes));
+        q[k] = load_if(p.x + kv8_at(p, m.r, m.sp.base, qi, p.x_row, p.x_token) +
+                           (int64_t)(m.h * p.group + hg) * p.x_head + 8 * (lane % kLanes),
+                       i0 + k * kAt < m.here);
         for (hg += kAt; hg >= p.group; hg -= p.group) ++qi;
       }
     };
@@ -346,18 +362,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
-          float top[4];
+          float top[2];
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
+          for (int q4 = 0; q4 < 2; ++q4) {
             top[q4] = v[(c * BK + q4) / 32][(c * BK + q4) % 32];
 #pragma unroll
-            for (int e = q4 + 4; e < BK; e += 4) top[q4] = fmaxf(top[q4], v[(c * BK + e) / 32][(c * BK + e) % 32]);
+            for (int e = q4 + 2; e + 2 < BK; e += 4)
+              top[q4] = max3(top[q4], v[(c * BK + e) / 32][(c * BK + e) % 32], v[(c * BK + e + 2) / 32][(c * BK + e + 2) % 32]);
           }
+          // (the chains took all but the last two)
+          top[0] = max3(top[0], v[(c * BK + BK - 2) / 32][(c * BK + BK - 2) % 32], v[(c * BK + BK - 1) / 32][(c * BK + BK - 1) % 32]);
           const float2 sc = meta[slot][half * HC + c];
           // (a factor of 0 would make -inf of a masked key a NaN)
           fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
           off[c] = sc.y;
-          const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac[c];
+          const float x = fmaxf(top[0], top[1]) * fac[c];
           nm = fmaxf(nm, x);
           nv = fmaxf(nv, x + sc.y);
         }
@@ -483,6 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     // 128-byte rows: (0 5) (1 4) (2 7) (3 6), the even warps the first of each two pairs
     const int row0c = DIM == 128 ? (cw / 2) * 8 + (((r8 + (cw & 1)) ^ ((lane >> 2 & 1) ? 5 : 0)))
                                  : cw * 8 + r8;
+    const int from0 = DIM == 128 ? row0c * 128 + ((unit ^ (row0c & 7)) << 4)
+                                 : row0c * 64 + ((unit ^ (row0c >> 1 & 3)) << 4);
+    const uint32_t to0 = unit_at(row0c, 2 * unit), to1 = unit_at(row0c, 2 * unit + 1);
     uint32_t n = 0;  // tiles so far
     bool ok = true;
     for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
@@ -495,20 +517,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         if (!ok) break;
         unsigned char* to = sK + (2 * kv + b) * kTileBytes;
         const unsigned char* from = codes_at(kv, b);
-#pragma unroll 4
-        for (int e = 0; e < kPer; ++e) {
-          const int row = row0c + e * kStep;
-          const int at = DIM == 128 ? row * 128 + ((unit ^ (row & 7)) << 4)
-                                    : row * 64 + ((unit ^ (row >> 1 & 3)) << 4);
-          const uint4 u = *reinterpret_cast<const uint4*>(from + at);
-          uint4 lo, hi;
-          kv8_half2<MODE>(u.x, lo.x, lo.y);
-          kv8_half2<MODE>(u.y, lo.z, lo.w);
-          kv8_half2<MODE>(u.z, hi.x, hi.y);
-          kv8_half2<MODE>(u.w, hi.z, hi.w);
-          __syncwarp();  // the row's eight lanes have read it: half of it is written over
-          *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit)) = lo;
-          *reinterpret_cast<uint4*>(to + unit_at(row, 2 * unit + 1)) = hi;
+        // four rows' codes at a time (rows kStep apart: the swizzle is the same)
+#pragma unroll
+        for (int e0 = 0; e0 < kPer; e0 += 4) {
+          uint4 u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = *reinterpret_cast<const uint4*>(from + from0 + (e0 + e) * kStep * DIM);
+          __syncwarp();  // the rows' lanes have read them: half of a row is written over
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 lo, hi;
+            kv8_half2<MODE>(u[e].x, lo.x, lo.y);
+            kv8_half2<MODE>(u[e].y, lo.z, lo.w);
+            kv8_half2<MODE>(u[e].z, hi.x, hi.y);
+            kv8_half2<MODE>(u[e].w, hi.z, hi.w);
+            *reinterpret_cast<uint4*>(to + to0 + (e0 + e) * kStep * 128) = lo;
+            *reinterpret_cast<uint4*>(to + to1 + (e0 + e) * kStep * 128) = hi;
+          }
         }
         fence_proxy_async();
         mbar_arrive(kv ? &vfull[b] : &kfull[b]);
@@ -575,39 +601,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
       for (int i = max(issued[kv] - 2, 0); i < issued[kv]; ++i) mbar_wait(&cfull[kv][i & 1], (i >> 1) & 1);
-  } else if (warp == kIssuer || warp == kIssuer + 2) {
-    // ======================= products of tile t =======================
-    // One warp per tile of rows, so that the waits of one do not hold up the other.
-    // The whole warp goes through this, so that descriptors stay in uniform
-    // registers; one elected lane issues.
-    const int t = warp == kIssuer ? 0 : 1;
+  } else if (warp == kIssuer) {
+    // ======================= products =======================
+    // The tiles of rows in turn: P V of one block of keys, then Q K^T of the next; so
+    // one tile's products run while the other's rows compute.  (With a warp for each
+    // tile they fall into step, and the tensor cores wait for both.)  The whole warp
+    // goes through this, so that descriptors stay in uniform registers; one elected
+    // lane issues.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-    const uint32_t dq = desc_lo(base + t * kTileBytes, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
+    const uint32_t dq = desc_lo(base, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
     const uint32_t dv = desc_lo(base + 4 * kTileBytes, kKeys * 128);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
-    const uint32_t s_at = tm + t * kKeys, o_at = tm + 256 + t * 128;
     const bool lead = elect_one();
-    auto qk = [&](uint32_t b) {
-      const uint32_t k = dk + b * kTileStep;
+    auto qk = [&](int t, uint32_t b) {
+      const uint32_t k = dk + b * kTileStep, q = dq + t * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
           const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
-          umma_ss(s_at, dq + off, k + off, kIdQK, s > 0);
+          umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
         }
         umma_commit(&sfull[t]);
-        umma_commit(&kfree[b]);
       }
       __syncwarp();
     };
-    auto pv = [&](uint32_t b, bool add) {
+    auto pv = [&](int t, uint32_t b, bool add) {
       const uint32_t v = dv + b * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-          umma_ts(o_at, s_at + 8 * s, v + s * (2048 >> 4), kIdPV, add || s > 0);
-        umma_commit(&vfree[b]);
+          umma_ts(tm + 256 + t * 128, tm + t * kKeys + 8 * s, v + s * (2048 >> 4), kIdPV, add || s > 0);
       }
       __syncwarp();
     };
@@ -618,43 +642,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wait(bar, parity));
     };
-    uint32_t n = 0, mine = 0, outs = 0;  // tiles, tiles of this warp's, items of this warp's so far
+    uint32_t n = 0, done[2] = {0, 0}, outs[2] = {0, 0};  // tiles of keys; by tile of rows: those, and items
     bool ok = true;
     for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item m = item_of(a, it);
       if (m.nt == 0) continue;
-      if (t == 0 || m.two) {
-        ok = all_wait(&qready[t], outs & 1) && all_wait(&kfull[n & 1], (n >> 1) & 1);
-        if (ok) {
-          tc_fence_after();
-          qk(n & 1);
-        }
-        for (int i = 0; i < m.nt && ok; ++i) {
-          const uint32_t tile = n + i;
-          ok = all_wait(&vfull[tile & 1], (tile >> 1) & 1);
-          // the next keys as well, while the rows still compute
-          if (i + 1 < m.nt) ok = ok && all_wait(&kfull[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
-          ok = ok && all_wait(&pready[t], (mine + i) & 1);
+      ok = all_wait(&kfull[n & 1], (n >> 1) & 1) && all_wait(&qready[0], outs[0] & 1);
+      tc_fence_after();
+      if (ok) qk(0, n & 1);
+      if (m.two) {
+        ok = ok && all_wait(&qready[1], outs[1] & 1);
+        tc_fence_after();
+        if (ok) qk(1, n & 1);
+      }
+      if (ok) commit(&kfree[n & 1]);
+      for (int i = 0; i < m.nt && ok; ++i) {
+        const uint32_t tile = n + i, b = tile & 1;
+        const bool more = i + 1 < m.nt;
+        ok = all_wait(&vfull[b], (tile >> 1) & 1);
+        if (more) ok = ok && all_wait(&kfull[b ^ 1], ((tile + 1) >> 1) & 1);
+        ok = ok && all_wait(&pready[0], (done[0] + i) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        pv(0, b, i > 0);
+        if (more) qk(0, b ^ 1);
+        if (m.two) {
+          ok = all_wait(&pready[1], (done[1] + i) & 1);
           if (!ok) break;
           tc_fence_after();
-          pv(tile & 1, i > 0);
-          if (i + 1 < m.nt) qk((tile + 1) & 1);
+          pv(1, b, i > 0);
+          if (more) qk(1, b ^ 1);
         }
-        mine += m.nt;
-        commit(&odone[t]);  // completes with every product issued so far
-        ++outs;
-      } else {
-        // no rows in this tile: the buffers are free as far as it goes
-        for (uint32_t tile = n; tile < n + m.nt && ok; ++tile) {
-          ok = all_wait(&kfull[tile & 1], (tile >> 1) & 1);
-          commit(&kfree[tile & 1]);
-          ok = ok && all_wait(&vfull[tile & 1], (tile >> 1) & 1);
-          commit(&vfree[tile & 1]);
-        }
+        commit(&vfree[b]);
+        if (more) commit(&kfree[b ^ 1]);
+      }
+      commit(&odone[0]);  // completes with every product issued so far
+      done[0] += m.nt, ++outs[0];
+      if (m.two) {
+        commit(&odone[1]);
+        done[1] += m.nt, ++outs[1];
       }
       n += m.nt;
     }
-    if (outs > 0) wait(&odone[t], (outs - 1) & 1);
+    if (outs[0] > 0) wait(&odone[0], (outs[0] - 1) & 1);
+    if (outs[1] > 0) wait(&odone[1], (outs[1] - 1) & 1);
   }
   tc_fence_before();
   __syncthreads();
