@@ -552,6 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     bool ok = true;
     for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item m = item_of(a, it);
+      // (this warp is two tiles of keys ahead of the rows: their queries may come near)
+      for (int i = lane; i < m.here && it != blockIdx.x; i += 32) {
+        const int qi = (m.row0 + i) / p.group;
+        const __nv_bfloat16* x = p.x + kv8_at(p, m.r, m.sp.base, qi, p.x_row, p.x_token) +
+                                 (int64_t)(m.h * p.group + (m.row0 + i) - qi * p.group) * p.x_head;
+#pragma unroll
+        for (int d = 0; d < DIM; d += 64) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x + d));
+      }
       // page ids and scales are asked for a tile before
       auto page_of = [&](int i) {
         const int j = (m.ka + i) * kKeys + (lane << p.shift);
