@@ -124,9 +124,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
     kv8_plan_kernel(const PlanParams p) {
   cg::cluster_group cl = cg::this_cluster();
   __shared__ int cnt[32];
-  // s_a: fork's children of a row, then the pages wanted by the rows before a
-  // row; s_b: fork's first child of a row
-  __shared__ int s_a[kMaxRows], s_b[kMaxRows];
+  // small arrays of all rows, in every CTA.  s_a: fork's children of a row, then the
+  // pages wanted by the rows before a row; s_b: fork's first child of a row; and the
+  // lengths, the parents (fork) or the extra tokens (reserve).
+  extern __shared__ int s_rows[];
+  int *s_a = s_rows, *s_b = s_a + p.rows, *s_len = s_b + p.rows, *s_par = s_len + p.rows;
   __shared__ int s_total, s_over;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int gtid = (int)cl.block_rank() * kPlanThreads + tid, gwarp = gtid / 32;
@@ -138,21 +140,25 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
 
   // ---- fork, reserve: reference counts of what stays --------------------
   for (int64_t i = gtid; i < P; i += kCtas * kPlanThreads) p.refs_out[i] = p.refs[i];
-  auto parent = [&](int r) {
-    if (p.drop) return p.drop[r] ? -1 : r;
-    const int q = p.parents[r];
-    return q >= 0 && q < rows ? q : -1;
-  };
+  for (int r = tid; r < rows; r += kPlanThreads) {
+    s_len[r] = max(p.lengths[r], 0);
+    if constexpr (OP == kFork) {
+      const int q = p.drop ? (p.drop[r] ? -1 : r) : p.parents[r];
+      s_par[r] = q >= 0 && q < rows ? q : -1;
+      s_a[r] = 0, s_b[r] = rows;
+    } else {
+      s_par[r] = max(p.extra[r], 0);
+    }
+  }
+  __syncthreads();
   if constexpr (OP == kFork) {
-    for (int r = tid; r < rows; r += kPlanThreads) s_a[r] = 0, s_b[r] = rows;
-    __syncthreads();
     for (int r = tid; r < rows; r += kPlanThreads) {
-      const int q = parent(r);
+      const int q = s_par[r];
       if (q >= 0) atomicAdd(&s_a[q], 1), atomicMin(&s_b[q], r);
     }
     cl.sync();  // counts copied, children known
     for (int r = gwarp; r < rows; r += kPlanWarps) {
-      const int len = p.lengths[r], own = min(pages_of(len, p.page), p.cols), kids = s_a[r];
+      const int len = s_len[r], own = min(pages_of(len, p.page), p.cols), kids = s_a[r];
       for (int c = lane; c < own; c += 32) {
         const bool whole = (int64_t)(c + 1) * p.page <= len;
         const int more = (whole ? kids : min(kids, 1)) - 1;
@@ -163,19 +169,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   }
   // reserve: pages of a row's longer sequence
   auto need = [&](int r) {
-    const int64_t len = (int64_t)max(p.lengths[r], 0) + max(p.extra[r], 0);
-    return (int)((len + p.page - 1) / p.page);
+    return (int)(((int64_t)s_len[r] + s_par[r] + p.page - 1) / p.page);
   };
   // fresh pages wanted by a row
   auto wanted = [&](int r) {
     if constexpr (OP == kFork) {
-      const int q = parent(r);
-      return q >= 0 && p.lengths[q] > 0 && p.lengths[q] % p.page != 0 && s_b[q] != r &&
-                     pages_of(p.lengths[q], p.page) <= p.cols
-                 ? 1
-                 : 0;
+      const int q = s_par[r];
+      return q >= 0 && s_len[q] % p.page != 0 && s_b[q] != r && pages_of(s_len[q], p.page) <= p.cols ? 1 : 0;
     } else {
-      return min(need(r), p.cols) - min(pages_of(p.lengths[r], p.page), p.cols);
+      return min(need(r), p.cols) - min(pages_of(s_len[r], p.page), p.cols);
     }
   };
   // a scan by one warp of each CTA; sums stop at 2^30, above any number of pages
@@ -193,7 +195,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
       if (r < rows) s_a[r] = min(run + x - w, 1 << 30);
       run = min(run + __shfl_sync(0xffffffffu, x, 31), 1 << 30);
       if constexpr (OP == kReserve) {
-        const int fit = max(p.cols, r < rows ? pages_of(p.lengths[r], p.page) : 0);
+        const int fit = max(p.cols, r < rows ? pages_of(s_len[r], p.page) : 0);
         const int o = r < rows ? min(max(need(r) - fit, 0), 1 << 25) : 0;
         over = min(over + warp_sum(o), 1 << 30);
       }
@@ -222,7 +224,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   if (gtid == 0) *p.count_out = total - have + s_over, *p.n_moves = OP == kFork ? have : 0;
   for (int r = gwarp; r < rows; r += kPlanWarps) {
     if constexpr (OP == kFork) {
-      const int q = parent(r), len = q >= 0 ? max(p.lengths[q], 0) : 0;
+      const int q = s_par[r], len = q >= 0 ? s_len[q] : 0;
       const int own = min(pages_of(len, p.page), p.cols), k = s_a[r];
       const bool fresh = wanted(r) > 0;
       for (int c = lane; c < p.cols; c += 32) {
@@ -242,7 +244,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
       }
       if (lane == 0) p.lengths_out[r] = len;
     } else {
-      const int64_t len = max(p.lengths[r], 0), ex = max(p.extra[r], 0);
+      const int64_t len = s_len[r], ex = s_par[r];
       const int own = min(pages_of((int)len, p.page), p.cols), k = s_a[r], w = wanted(r);
       for (int c = lane; c < p.cols; c += 32) {
         int pg = c < own ? p.table[(int64_t)r * p.cols + c] : -1;
@@ -350,9 +352,16 @@ gdn_status run_plan(int op, const gdn_kv8_pool& pool, PlanParams p, void* worksp
   p.dst = p.src + move_ints(pool);
   p.list = p.dst + move_ints(pool);
   p.pages = pool.pages, p.rows = pool.rows, p.cols = pool.cols, p.page = pool.page;
-  if (op == kFork) kv8_plan_kernel<kFork><<<kCtas, kPlanThreads, 0, st>>>(p);
-  else if (op == kReserve) kv8_plan_kernel<kReserve><<<kCtas, kPlanThreads, 0, st>>>(p);
-  else kv8_compact_kernel<<<kCtas, kPlanThreads, 0, st>>>(p);
+  if (op == kCompact) {
+    kv8_compact_kernel<<<kCtas, kPlanThreads, 0, st>>>(p);
+  } else {
+    auto kern = op == kFork ? kv8_plan_kernel<kFork> : kv8_plan_kernel<kReserve>;
+    const int bytes = 16 * (int)pool.rows;  // at most 64 KiB
+    if (bytes > 47 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return GDN_ERR_CUDA;
+    kern<<<kCtas, kPlanThreads, bytes, st>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -63,54 +63,72 @@ def kv8_pool(layers, pages, heads, dim, page=64, device="cuda"):
 def _strides(x, shape):
     """(row, token, head) strides in elements of [rows, tokens, heads, dim] or [total, heads, dim]."""
     s = x.stride()
-    _need(s[-1] == 1 or shape[-1] == 1, "the last dim must be contiguous")
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError("the last dim must be contiguous")
     if len(shape) == 4:
         a, b, c = s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0
         return a, b, c
     return 0, s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0
 
 
+def _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode):
+    """Says what _problem does not take."""
+    dev = codes.get_device()
+    _need(dev >= 0, "codes must be a CUDA tensor")
+    _say(dev, ("codes", codes, _u8), ("scales", scales, _f32), ("table", table, _i32),
+         ("lengths", lengths, _i32))
+    _need(codes.dim() == 5 and codes.shape[0] == 2, "codes must be [2, pages, heads, page, dim]")
+    _need(scales.shape == codes.shape[:3], "scales must be [2, pages, heads]")
+    _need(table.dim() == 2 and lengths.shape == table.shape[:1],
+          "table must be [rows, columns] and lengths [rows]")
+    _need(x.get_device() == dev, "q, k, v must be on cuda:%d" % dev)
+    _need(mode in _MODES, "mode must be one of %s, got %r" % (sorted(_MODES), mode))
+    rows, heads, dim = table.shape[0], codes.shape[2], codes.shape[4]
+    if cu_seqlens is None:
+        _need(x.dim() == 4 and x.shape[0] == rows, "expected [rows, tokens, heads, dim]")
+    else:
+        _say(dev, ("cu_seqlens", cu_seqlens, _i32))
+        _need(x.dim() == 3, "expected packed [total, heads, dim]")
+        _need(cu_seqlens.shape == (rows + 1,), "cu_seqlens must be [rows + 1]")
+    _need(x.shape[-1] == dim, "head dim %d is not the cache's %d" % (x.shape[-1], dim))
+    _need(heads > 0 and x.shape[-2] > 0 and x.shape[-2] % heads == 0,
+          "%d heads cannot share %d K/V heads" % (x.shape[-2], heads))
+    if v is not None:
+        _need(v.get_device() == dev and v.dtype is x.dtype and v.shape == x.shape,
+              "k and v must have the same shape, type and device")
+        _need(x.shape[-2] == heads, "k and v must have the cache's heads")
+    raise ValueError("arguments do not fit together")
+
+
 def _problem(x, v, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, scale, causal,
              window):
-    """The packed gdn_kv8_problem."""
+    """The packed gdn_kv8_problem.  (Texts are made only for what is refused: this is on the
+    way of every token.)"""
     dev = codes.get_device()
-    if not (_plain(codes, _u8, dev) and _plain(scales, _f32, dev) and _plain(table, _i32, dev)
-            and _plain(lengths, _i32, dev) and dev >= 0):
-        _need(dev >= 0, "codes must be a CUDA tensor")
-        _say(dev, ("codes", codes, _u8), ("scales", scales, _f32), ("table", table, _i32),
-             ("lengths", lengths, _i32))
-    cs, shape = codes.shape, x.shape
-    _need(len(cs) == 5 and cs[0] == 2, "codes must be [2, pages, heads, page, dim]")
+    cs, shape, m = codes.shape, x.shape, _MODES.get(mode)
+    if not (dev >= 0 and codes.dtype is _u8 and codes.is_contiguous() and _plain(scales, _f32, dev)
+            and _plain(table, _i32, dev) and _plain(lengths, _i32, dev) and x.get_device() == dev
+            and len(cs) == 5 and cs[0] == 2 and scales.shape == cs[:3] and table.dim() == 2
+            and lengths.shape == table.shape[:1] and m is not None):
+        _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode)
     _, pages, heads, page, dim = cs
-    rows, cols = table.shape if table.dim() == 2 else (-1, -1)
-    _need(scales.shape == cs[:3], "scales must be [2, pages, heads]")
-    _need(rows >= 0 and lengths.shape == (rows,), "table must be [rows, columns] and lengths [rows]")
-    _need(x.get_device() == dev, "q, k, v must be on cuda:%d" % dev)
-    m = _MODES.get(mode)
-    _need(m is not None, "mode must be one of %s, got %r" % (sorted(_MODES), mode))
+    rows, cols = table.shape
     if cu_seqlens is None:
-        _need(len(shape) == 4 and shape[0] == rows, "expected [rows, tokens, heads, dim]")
+        fits = len(shape) == 4 and shape[0] == rows
         tokens, cu = shape[1], 0
         total = rows * tokens
     else:
-        _say(dev, ("cu_seqlens", cu_seqlens, _i32))
-        _need(len(shape) == 3, "expected packed [total, heads, dim]")
-        _need(cu_seqlens.shape == (rows + 1,), "cu_seqlens must be [rows + 1]")
+        fits = len(shape) == 3 and _plain(cu_seqlens, _i32, dev) and cu_seqlens.shape == (rows + 1,)
         total = tokens = shape[0]
         if max_seqlen is not None and max_seqlen < tokens:
             tokens = int(max_seqlen)
         cu = cu_seqlens.data_ptr()
     xh = shape[-2]
-    _need(shape[-1] == dim, "head dim %d is not the cache's %d" % (shape[-1], dim))
-    _need(heads > 0 and xh > 0 and xh % heads == 0,
-          "%d heads cannot share %d K/V heads" % (xh, heads))
+    if not (fits and shape[-1] == dim and heads > 0 and xh > 0 and xh % heads == 0 and (
+            v is None or (xh == heads and v.shape == shape and v.dtype is x.dtype and v.get_device() == dev))):
+        _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode)
     strides = _strides(x, shape)
-    more = strides
-    if v is not None:
-        _need(v.get_device() == dev and v.dtype is x.dtype and v.shape == shape,
-              "k and v must have the same shape, type and device")
-        _need(xh == heads, "k and v must have the cache's heads")
-        more = _strides(v, shape)
+    more = strides if v is None else _strides(v, shape)
     return _KV8(pages, rows, total, tokens, cols, heads, xh // heads, dim, page, m,
                 _XTYPES.get(x.dtype, 99), causal, window, scale, cu, *strides, *more)
 
