@@ -13,7 +13,9 @@ namespace {
 // chunks of eight bf16 per thread, the next block's while this one is worked on),
 // their maximum is the block's, and their codes go out as 8-byte stores.  The
 // bytes are the bf16 tokens in and the codes out; the old codes of the page are
-// read and written only when the new tokens raise its scale.
+// read and written only when the new tokens raise its scale.  Eight uneven prompts of
+// up to 4096 tokens, 8 heads of 128, pages of 32, INT8, 121 MB: 22.5 us, 5.4 TB/s
+// (a CTA per block, without the next one in flight: 28 us).
 template <int MODE, int DIM, int NT, int CH>
 __global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int blocks, int per) {
   constexpr int C8 = DIM / 8;

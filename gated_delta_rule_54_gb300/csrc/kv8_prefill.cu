@@ -10,9 +10,14 @@
 // fp16 (exact), as swizzled operand tiles; one lane of a warp issues the
 // products; and eight warps per tile are its rows, two threads to a row.
 //
-// Products of fp16 codes bound it together with shared memory: per 128 keys the
-// two tiles' operands are read at the rate of the products, and the converted
-// tiles are written besides.
+// Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
+// PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
+// heads, E4M3: 221 us, 1.00 PFLOP/s (tensor pipe active 47 and 55 %).  Instruction
+// issue bounds it: a pair of tiles takes about 9600 warp instructions per 128 keys
+// (the rows' softmax two thirds, the conversion a quarter), 56 % of the issue slots;
+// without the exponentials it is 3 % faster, and moving an eighth of them to the FMA
+// pipe made it 3 % slower.  One thread per row (8 warps) took 15 % longer, a CTA per
+// item 5 %, and an issuing warp for each tile 12 %.
 //
 // Scales.  s_j = q . code_j * (scale * ks(block of j)), and V's scale joins the
 // exponent: P_j = 2^(s_j + log2 vs - mv), so that fp16 holds it for any scales;
