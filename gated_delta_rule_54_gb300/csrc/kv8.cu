@@ -15,7 +15,7 @@ namespace {
 // bytes are the bf16 tokens in and the codes out; the old codes of the page are
 // read and written only when the new tokens raise its scale.  Eight uneven prompts of
 // up to 4096 tokens, 8 heads of 128, pages of 32, INT8, 121 MB: 22.5 us, 5.4 TB/s
-// (a CTA per block, without the next one in flight: 28 us).
+// (28 us before the next block's loads were in flight).
 template <int MODE, int DIM, int NT, int CH>
 __global__ void __launch_bounds__(NT) kv8_append_kernel(const Kv8Params p, int blocks, int per) {
   constexpr int C8 = DIM / 8;
@@ -113,7 +113,9 @@ gdn_status run_append(const Kv8Params& p, cudaStream_t st) {
   // pages that n consecutive positions can touch
   const int blocks = (p.tokens + p.page - 2) / p.page + 1;
   if (p.rows * blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  // blocks per CTA: up to 8 while 152 SMs still get eight CTAs each
+  // blocks per CTA, whose loads overlap: up to 8 while 152 SMs still get eight CTAs
+  // each (8 prompts to 4096 tokens 23.4 us, with one block each 28.8; one such
+  // prompt, which gives less CTAs, 6.4 and 6.2)
   int per = 1;
   while (per < 8 && per < 2 * p.heads && p.rows * blocks * 2 * p.heads / (2 * per) >= 152 * 8) per *= 2;
   const dim3 grid((unsigned)(p.rows * blocks), (unsigned)((2 * p.heads + per - 1) / per));
@@ -169,7 +171,11 @@ Kv8Params params_of(const gdn_kv8_problem& p) {
   return k;
 }
 
-// one 16-row tile holds a row's queries of a K/V head
+// One 16-row tile holds a row's queries of a K/V head: the kernel that streams the
+// codes, else the one that converts them for tiles of 128 rows.  Measured with
+// 16 query rows, stream / tiles in us: 64 rows x 8 heads x 8192 keys 247/395 (four
+// query rows 179/394); the tiles are a little faster where the calls are small
+// (1 x 8 x 700 keys 13.8/12.6).
 bool few_rows(const gdn_kv8_problem& p) { return (int64_t)p.tokens * p.group <= 16; }
 
 bool off16(std::initializer_list<const void*> ptrs) {

@@ -9,8 +9,8 @@
 // A warp that holds a whole segment writes its output; otherwise it has a part
 // (its output normalised over its own keys, and their log-sum-exp), the parts of
 // one CTA are joined in shared memory, and what is left goes to the workspace,
-// where a second launch joins the parts of a segment in order.  Short tables
-// give one CTA per segment instead, and then nothing is left to join.
+// where a second launch joins the parts of a segment in order.  Where it is faster
+// (by_segment) a CTA has one segment instead, and nothing is left to join.
 //
 // A warp runs by itself: a ring of S tiles (K and V, by TMA, 128- or 64-byte
 // swizzle) that its lane 0 refills, warp products with fp32 sums, and an online
@@ -22,11 +22,12 @@
 //
 // Measured on a GB300 (kernel alone): 64 rows of 2192 .. 8192 keys, 8 K/V heads of
 // 128, E4M3, 676 MB: 117 us, 5.8 TB/s (copying: 6.8); with nothing but its loads 108
-// us.  2 rows of 101072 and 131071 keys, 4 heads, INT8, 260 MB: 54 us.  What is left
-// is instruction issue: two warps per scheduler, half of whose slots are taken.
-// Scores from E4M3 codes as they are took 16 % off the time against fp16
-// conversion of K, and so did leaving out rows 8-15 where there are none; 12 warps
-// with two tiles each (168 registers) came out as 8 warps with three.
+// us (an earlier build, 136 us with its products).  2 rows of 101072 and 131071 keys,
+// 4 heads, INT8, 260 MB: 55 us.  DRAM is at 73 and 59 %, instruction issue at half of
+// its slots from two warps per scheduler; the join takes 9 and 8 us.
+// With both launches the first case takes 127 us; with 12 warps of two tiles (168
+// registers) it took 155 where 8 warps of three took 146, and scores from E4M3
+// codes as they are together with the leaving out of rows 8-15 made 126 of that.
 #include <cuda.h>
 
 #include "kv8.cuh"
@@ -39,10 +40,6 @@ namespace {
 __device__ int g_kv8_device_error;
 
 constexpr int kTile = 32, kWarps = 8;
-// Tables of up to this many tiles: one CTA per segment.  A segment of 64 tiles is
-// eight per warp, about 9 us, which is what the second launch and the search for
-// the shares cost otherwise.
-constexpr int kSegmentTiles = 64;
 
 struct DecodeArgs {
   Kv8Params p;
@@ -764,8 +761,22 @@ int64_t most_tiles(const Kv8Params& p) {
   if (p.window > 0 && (int64_t)p.window + p.tokens < keys) keys = (int64_t)p.window + p.tokens;
   return (keys + kTile - 1) / kTile + 1;
 }
+// One CTA per segment, or the line of all tiles?  A CTA alone takes 6 us + 0.18 us per
+// tile; the line takes 11 to 20 us more than its bytes (shares, a second launch), but
+// leaves no SM idle and no wave half full.  Measured, line / segment in us, 128-wide
+// E4M3 heads:
+//     segments     256 keys   1024 keys   2048 keys   4096 keys
+//           8     10.9/6.8   12.9/11.5   14.5/17.4   12.9/29.1
+//          64     11.7/7.4   19.1/11.7   21.6/17.6   26.3/29.5
+//         152     13.3/7.4   18.1/12.3   24.2/18.3   39.1/33.5
+//         256     18.8/13.3  26.3/22.8   40.5/39.4   59.6/62.9
+//         512     22.8/24.9  41.2/50.1   60.3/74.9   99.7/121
+//        8192      162/355     401/615
+// So: one wave up to a length that grows with the SMs it fills, two waves of
+// short segments, and the line for the rest.
 bool by_segment(const Kv8Params& p) {
-  return most_tiles(p) <= kSegmentTiles && p.rows * p.heads <= 0x7fffffffLL;
+  const int64_t segments = p.rows * p.heads, tiles = most_tiles(p);
+  return segments <= 152 ? tiles <= 36 + segments : segments <= 304 && tiles <= 40;
 }
 int64_t grid_of(const Kv8Params& p) {
   const int64_t tiles = most_tiles(p) * p.rows * p.heads;
@@ -786,7 +797,9 @@ gdn_status run(DecodeArgs& a, cudaStream_t st) {
     return GDN_ERR_CUDA;
   a.whole = by_segment(p);
   const int64_t grid = a.whole ? p.rows * p.heads : grid_of(p);
-  // up to eight query rows: half of the softmax's work, and q's two parts in one fragment
+  // up to eight query rows: half of the softmax's work, and q's two parts in one
+  // fragment (eight rows, 64 x 8192 keys with both launches: E4M3 122 us, with the
+  // code for sixteen 162; INT8 130 and 139)
   const bool r8 = (int64_t)p.tokens * p.group <= 8;
   auto kern = p.page < kTile
                   ? (r8 ? kv8_decode_kernel<MODE, DIM, S, true, true> : kv8_decode_kernel<MODE, DIM, S, true, false>)

@@ -7,6 +7,11 @@
 // further launches and no word from the host.  The mover copies whole pages in
 // all planes from the list that the plan left in the workspace; it is bound by
 // HBM (each byte read once and written once).
+//
+// Measured on a GB300, 128 rows, 8000 pages, 4 layers of 4 heads: plan 12 us, mover 7
+// us; compacting 500 pages 9 and 5 us.  Latency bounds both: the plan is a chain of
+// cluster barriers and trips to L2 (the rows' small arrays in shared memory took
+// 15 us to 12), and there are few pages to move.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -13,11 +13,11 @@
 // Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
 // PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
 // heads, E4M3: 221 us, 1.00 PFLOP/s (tensor pipe active 47 and 55 %).  Instruction
-// issue bounds it: a pair of tiles takes about 9600 warp instructions per 128 keys
-// (the rows' softmax two thirds, the conversion a quarter), 56 % of the issue slots;
-// without the exponentials it is 3 % faster, and moving an eighth of them to the FMA
-// pipe made it 3 % slower.  One thread per row (8 warps) took 15 % longer, a CTA per
-// item 5 %, and an issuing warp for each tile 12 %.
+// issue bounds it, 2.2 a clock of the four schedulers: in the steps' order, one thread per row
+// (8 warps) took 345 and 258 us, two 331 and 240, a CTA per SM for all its items 328
+// and 249, and one issuing warp for both tiles with a shorter conversion 290 and 221.
+// Without the exponentials it is 3 to 4 % faster, and with some of them moved to the
+// FMA pipe slower.
 //
 // Scales.  s_j = q . code_j * (scale * ks(block of j)), and V's scale joins the
 // exponent: P_j = 2^(s_j + log2 vs - mv), so that fp16 holds it for any scales;
@@ -745,7 +745,8 @@ int64_t blocks_of(const Kv8Params& p) {
   return ((int64_t)p.tokens * p.group + kRows - 1) / kRows;
 }
 // CTAs per block of rows: where the blocks do not fill 152 SMs, the keys are
-// split, down to two tiles each
+// split, down to two tiles each (in us, split / whole: 256 tokens x 4 heads of one K/V head
+// on 8192 keys 26/114; 512 x 4 of four on 4096 32/62; 64 x 4 of two on 700 19/20)
 int splits_of(const Kv8Params& p) {
   int64_t keys = (int64_t)p.cols * p.page;
   if (p.window > 0 && (int64_t)p.window + p.tokens < keys) keys = (int64_t)p.window + p.tokens;
@@ -793,8 +794,8 @@ gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* works
   a.ws = static_cast<float*>(workspace);
   a.blocks = (int)blocks_of(p);
   a.splits = splits_of(p);
-  // pages of 64 and 128 tokens: two scales per tile of keys (their per-row work is
-  // four times that of one per 16 keys otherwise)
+  // pages of 64 and 128 tokens: two scales per tile of keys instead of eight (4 x 4096
+  // tokens, pages of 64: 277 us, with eight 286)
   auto pick = [&](auto two, auto eight) { return p.page >= 64 ? two(a, st) : eight(a, st); };
   if (mode == GDN_QDQ_E4M3)
     return dim == 128 ? pick(run<GDN_QDQ_E4M3, 128, 2>, run<GDN_QDQ_E4M3, 128, 8>)

@@ -114,6 +114,22 @@ def test_few_rows(case):
     _run(np.random.default_rng(case), lengths, tokens, heads, group, dim, page, mode, window=window)
 
 
+@pytest.mark.parametrize("rows,heads,most,page,dim,mode", [
+    (16, 8, 2000, 64, 128, "e4m3"),    # a CTA per (row, head), long
+    (45, 5, 1200, 32, 64, "int8"),     # two waves of them
+    (45, 5, 1300, 32, 64, "int8"),     # one column more
+    (48, 8, 90, 16, 128, "e4m3"),      # many short ones: a warp's share has several
+    (200, 16, 40, 16, 64, "int8"),
+    (330, 1, 1, 16, 128, "int8"),
+])
+def test_many_short_rows(rows, heads, most, page, dim, mode):
+    rng = np.random.default_rng(rows + most)
+    lengths = rng.integers(0, most + 1, rows)
+    lengths[rng.integers(rows)] = most
+    for group, tokens in ((2, 1), (3, 4)):
+        _run(rng, [int(n) for n in lengths], tokens, heads, group, dim, page, mode)
+
+
 MANY = [
     # lengths, tokens, heads, group, dim, page, mode, window, packed
     ([17], 17, 1, 1, 128, 64, "e4m3", 0, False),
