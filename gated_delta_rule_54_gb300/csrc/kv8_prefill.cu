@@ -3,19 +3,24 @@
 // The query rows of a (row, K/V head) are its queries times the query heads that
 // share the head, query-major; a CTA takes 256 of them, as two tiles of 128, so
 // that one conversion of a block of keys serves both.  Per 128 keys and tile:
-//     S = Q K^T   (tcgen05, fp16 x fp16 -> fp32 in TMEM)
+//     S = Q K^T   (tcgen05, fp16 x fp16 or E4M3 x E4M3 -> fp32 in TMEM)
 //     P = 2^(s - reference)  (two threads per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
 // One warp brings the codes of 128 keys by TMA (a box per page); four turn them into
 // fp16 (exact), as swizzled operand tiles; one lane of a warp issues the
 // products; and eight warps per tile are its rows, two threads to a row.
+// E4M3 codes of K, 128 to a row, are an operand as they arrive; q is then the sum of
+// two E4M3 numbers, which is exact for elements down to 2^-10 of the row's largest (8
+// bits = 4 + 4) and off by 2^-18 of that below.  Two products at twice the rate
+// take the time of the one with fp16, and K is not converted: 197 us for 221 in the
+// second case below, 267 for 286 (INT8) in the first.
 //
 // Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
 // PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
-// heads, E4M3: 221 us, 1.00 PFLOP/s (tensor pipe active 47 and 55 %).  Instruction
-// issue bounds it, 2.2 a clock of the four schedulers: in the steps' order, one thread per row
+// heads, E4M3: 197 us, 1.12 PFLOP/s.  Instruction issue bounds it, 2.2 a clock of the
+// four schedulers with the tensor pipe active 47 % of the time in the first: in the steps' order, one thread per row
 // (8 warps) took 345 and 258 us, two 331 and 240, a CTA per SM for all its items 328
-// and 249, and one issuing warp for both tiles with a shorter conversion 290 and 221.
+// and 249, and one issuing warp for both tiles with a shorter conversion 290 and 221 (fp16 products).
 // Without the exponentials it is 3 to 4 % faster, and with some of them moved to the
 // FMA pipe slower.
 //
@@ -75,6 +80,15 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint
       "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
       " setp.ne.b32 p, %5, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
+}
+// the same with E4M3 operands, 32 bytes (elements) of a row per product; of the
+// instruction descriptor, whose two formats are 0 for E4M3 as for fp16, nothing differs
+__device__ __forceinline__ void umma_ss_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
 }
 // A in TMEM: row i in lane i, two fp16 per column
@@ -220,12 +234,13 @@ __device__ __forceinline__ Item item_of(const PrefillArgs& a, unsigned at) {
 template <int MODE, int DIM, int CH>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int kTileBytes = kKeys * DIM * 2;
+  constexpr bool F8 = MODE == GDN_QDQ_E4M3 && DIM == 128;  // scores from the codes as they are
   constexpr uint32_t kCols = 512;  // S0 S1 O0 O1
   constexpr int BK = kKeys / CH;   // keys of a block
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2];  // by buffer
-  __shared__ __align__(8) uint64_t cfull[2][2];                             // codes of K, of V
+  __shared__ __align__(8) uint64_t cfull[2][2];                             // codes of K, of V; by buffer
   __shared__ __align__(8) uint64_t qready[2], sfull[2], pready[2], odone[2];  // by tile of rows
   __shared__ float2 meta[4][CH];  // per block of a tile: K scale, log2 of V scale
   __shared__ int valid[4];        // bit c: the block has a page
@@ -304,10 +319,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
         float up, back;
-        kv8_q_factor<8>(most, up, back);
-        if (u == 0) row_factor[t * 128 + i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 ? 256.f : 1.f);
+        kv8_q_factor<F8 ? 7 : 8>(most, up, back);
+        // (fp16 holds an E4M3 code's value times 2^-8)
+        if (u == 0) row_factor[t * 128 + i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 && !F8 ? 256.f : 1.f);
         if (p.scale < 0.f) up = -up;
-        *reinterpret_cast<uint4*>(sQ + t * kTileBytes + unit_at(i, u)) =
+        if constexpr (F8) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2 h0, h1, l0, l1;
+            hi[e] = e4m3_code2(f[4 * e], f[4 * e + 1], up, h0) | (uint32_t)e4m3_code2(f[4 * e + 2], f[4 * e + 3], up, h1) << 16;
+            lo[e] = e4m3_code2(f[4 * e] * up - h0.x, f[4 * e + 1] * up - h0.y, 1.f, l0) |
+                    (uint32_t)e4m3_code2(f[4 * e + 2] * up - h1.x, f[4 * e + 3] * up - h1.y, 1.f, l1) << 16;
+          }
+          unsigned char* to = sQ + t * kTileBytes + unit_at(i, u >> 1) + (u & 1) * 8;
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + kKeys * 128) = make_uint2(lo[0], lo[1]);
+        } else *reinterpret_cast<uint4*>(sQ + t * kTileBytes + unit_at(i, u)) =
             make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
                        pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
       }
@@ -515,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const int nt = item_of(a, it).nt;
 #pragma unroll 1
-      for (int x = 0; x < 2 * nt && ok; ++x) {  // K, V, K, V, ...
-        const int kv = x & 1;
+      for (int x = F8; x < 2 * nt && ok; x += 1 + F8) {  // K, V, K, V, ...; or V alone
+        const int kv = F8 ? 1 : x & 1;
         const uint32_t tile = n + (x >> 1), b = tile & 1;
         ok = wait(&cfull[kv][b], (tile >> 1) & 1);
         if (!ok) break;
@@ -623,7 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     // lane issues.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-    const uint32_t dq = desc_lo(base, 16), dk = desc_lo(base + 2 * kTileBytes, 16);
+    const uint32_t dq = desc_lo(base, 16);
+    const uint32_t dk = desc_lo(base + 2 * kTileBytes + (F8 ? kKeys * 128 : 0), 16);
+    uint64_t* kthere = F8 ? &cfull[0][0] : &kfull[0];  // K's operand of a buffer
     const uint32_t dv = desc_lo(base + 4 * kTileBytes, kKeys * 128);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
     const bool lead = elect_one();
@@ -632,8 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
       if (lead) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
-          const uint32_t off = ((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4;
-          umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
+          const uint32_t at = (s & 3) * 32 >> 4, off = ((s >> 2) * (kKeys * 128) >> 4) + at;
+          if constexpr (F8)  // q's first parts, then its second ones, with the same codes
+            umma_ss_e4m3(tm + t * kKeys, q + off, k + at, kIdQK, s > 0);
+          else
+            umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
         }
         umma_commit(&sfull[t]);
       }
@@ -660,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     for (unsigned it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item m = item_of(a, it);
       if (m.nt == 0) continue;
-      ok = all_wait(&kfull[n & 1], (n >> 1) & 1) && all_wait(&qready[0], outs[0] & 1);
+      ok = all_wait(&kthere[n & 1], (n >> 1) & 1) && all_wait(&qready[0], outs[0] & 1);
       tc_fence_after();
       if (ok) qk(0, n & 1);
       if (m.two) {
@@ -673,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         const uint32_t tile = n + i, b = tile & 1;
         const bool more = i + 1 < m.nt;
         ok = all_wait(&vfull[b], (tile >> 1) & 1);
-        if (more) ok = ok && all_wait(&kfull[b ^ 1], ((tile + 1) >> 1) & 1);
+        if (more) ok = ok && all_wait(&kthere[b ^ 1], ((tile + 1) >> 1) & 1);
         ok = ok && all_wait(&pready[0], (done[0] + i) & 1);
         if (!ok) break;
         tc_fence_after();
