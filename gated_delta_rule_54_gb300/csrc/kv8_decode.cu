@@ -21,11 +21,12 @@
 // any scales.
 //
 // Measured on a GB300 (kernel alone): 64 rows of 2192 .. 8192 keys, 8 K/V heads of
-// 128, E4M3, 676 MB: 117 us, 5.8 TB/s (copying: 6.8); with nothing but its loads 108
+// 128, E4M3, 676 MB: 115 us, 5.9 TB/s (copying: 6.8); with nothing but its loads 108
 // us (an earlier build, 136 us with its products).  2 rows of 101072 and 131071 keys,
-// 4 heads, INT8, 260 MB: 55 us.  DRAM is at 73 and 59 %, instruction issue at half of
-// its slots from two warps per scheduler; the join takes 9 and 8 us.
-// With both launches the first case takes 127 us; with 12 warps of two tiles (168
+// 4 heads, INT8, 260 MB: 54 us.  DRAM is at 73 and 59 %, instruction issue at half of
+// its slots from two warps per scheduler; the join takes 8 us.
+// With both launches the first case takes 125 us (127 with 64-bit divisions for the
+// shares; 1024 rows of 16 keys 81 and 69); with 12 warps of two tiles (168
 // registers) it took 155 where 8 warps of three took 146, and scores from E4M3
 // codes as they are together with the leaving out of rows 8-15 made 126 of that.
 #include <cuda.h>
@@ -56,10 +57,19 @@ __device__ __forceinline__ int tiles_of(const Kv8Span& s) {
   return s.end > s.begin ? (s.end + kTile - 1) / kTile - s.begin / kTile : 0;
 }
 
-// Shares of the line of tiles: CTA c of n, warp w of it.
-__device__ __forceinline__ int64_t cta_start(int64_t all, int64_t c, int64_t n) {
-  return all / n * c + all % n * c / n;
+// a / b of numbers >= 0; nearly always both have 32 bits, whose division is far shorter
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
+// Shares of the line of tiles: CTA c of n (at most 152), warp w of it.
+struct Shares {
+  int64_t each;
+  uint32_t rest, n;
+  __device__ __forceinline__ Shares(int64_t all, int64_t ctas) {
+    each = quotient(all, ctas), n = (uint32_t)ctas, rest = (uint32_t)(all - each * ctas);
+  }
+  __device__ __forceinline__ int64_t start(int64_t c) const { return each * c + rest * (uint32_t)c / n; }
+};
 __device__ __forceinline__ int64_t warp_start(int64_t lo, int64_t hi, int w) {
   return lo + (hi - lo) * w / kWarps;
 }
@@ -114,9 +124,9 @@ __device__ __forceinline__ Cursor locate(const Kv8Params& p, int64_t u, int lane
   c.t0 = s.begin / kTile;
   c.t1 = c.t0 + tiles_of(s);
   const int64_t n = c.t1 - c.t0, off = u - c.u0;
-  c.h = n > 0 ? (int)(off / n) : 0;
+  c.h = n > 0 ? (int)quotient(off, n) : 0;
   c.u0 += c.h * n;
-  c.tile = c.t0 + (n > 0 ? (int)(off % n) : 0);
+  c.tile = c.t0 + (int)(off - c.h * n);
   return c;
 }
 
@@ -186,7 +196,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int64_t n = ctas_for(all, gridDim.x);
     lo = hi = 0;
     if (blockIdx.x < n && all > 0) {
-      const int64_t c0 = cta_start(all, blockIdx.x, n), c1 = cta_start(all, blockIdx.x + 1, n);
+      const Shares shares(all, n);
+      const int64_t c0 = shares.start(blockIdx.x), c1 = shares.start(blockIdx.x + 1);
       lo = warp_start(c0, c1, warp), hi = warp_start(c0, c1, warp + 1);
       if (lo < hi) pc = locate(p, lo, lane);
     }
@@ -635,12 +646,15 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   const int64_t all = a.before[p.rows] * p.heads, ctas = ctas_for(all, grid);
   const int64_t u0 = a.before[r] * p.heads + (int64_t)h * n, u1 = u0 + n;
   // CTAs whose shares meet the segment: c with start(c) < u1 and start(c + 1) > u0
-  int64_t c0 = u0 * ctas / all, c1;
-  while (c0 > 0 && cta_start(all, c0, ctas) > u0) --c0;
-  while (cta_start(all, c0 + 1, ctas) <= u0) ++c0;
-  c1 = (u1 - 1) * ctas / all;
-  while (c1 > 0 && cta_start(all, c1, ctas) > u1 - 1) --c1;
-  while (cta_start(all, c1 + 1, ctas) <= u1 - 1) ++c1;
+  const Shares shares(all, ctas);
+  auto cta_of = [&](int64_t u) {
+    const float near = (float)u * ((float)ctas / (float)all);
+    int c = min((int)near, (int)ctas - 1);
+    while (c > 0 && shares.start(c) > u) --c;
+    while (shares.start(c + 1) <= u) ++c;
+    return c;
+  };
+  const int64_t c0 = cta_of(u0), c1 = cta_of(u1 - 1);
   // one entry per CTA for what its warps left of the segment, and one for a warp
   // that goes on after the segment's end
   const int entries = (int)(c1 - c0 + 1) + 1;
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   if (tid < entries) {
     const bool after = tid == entries - 1;
     const int64_t c = after ? c1 : c0 + tid;
-    const int64_t lo = cta_start(all, c, ctas), hi = cta_start(all, c + 1, ctas);
+    const int64_t lo = shares.start(c), hi = shares.start(c + 1);
     int at = -1;
     int64_t first = -1, last_hi = 0;
     for (int w = 0; w < kWarps; ++w) {

@@ -11,16 +11,16 @@
 // products; and eight warps per tile are its rows, two threads to a row.
 // E4M3 codes of K, 128 to a row, are an operand as they arrive; q is then the sum of
 // two E4M3 numbers, which is exact for elements down to 2^-10 of the row's largest (8
-// bits = 4 + 4) and off by 2^-18 of that below.  Two products at twice the rate
-// take the time of the one with fp16, and K is not converted: 197 us for 221 in the
-// second case below, 267 for 286 (INT8) in the first.
+// bits = 4 + 4) and off by 2^-18 of that below.  K is not converted, which took the
+// second case below from 221 us to 197; the first takes 267 with E4M3 codes.
 //
 // Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
 // PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
 // heads, E4M3: 197 us, 1.12 PFLOP/s.  Instruction issue bounds it, 2.2 a clock of the
-// four schedulers with the tensor pipe active 47 % of the time in the first: in the steps' order, one thread per row
-// (8 warps) took 345 and 258 us, two 331 and 240, a CTA per SM for all its items 328
-// and 249, and one issuing warp for both tiles with a shorter conversion 290 and 221 (fp16 products).
+// four schedulers with the tensor pipe active 47 % of the time in the first.  In the
+// steps' order (fp16 products), one thread per row (8 warps) took 345 and 258 us, two
+// 331 and 240, a CTA per SM for all its items 328 and 249, and one issuing warp for
+// both tiles with a shorter conversion 290 and 221.
 // Without the exponentials it is 3 to 4 % faster, and with some of them moved to the
 // FMA pipe slower.
 //
