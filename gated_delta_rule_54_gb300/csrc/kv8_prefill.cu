@@ -9,7 +9,7 @@
 // One warp brings the codes of 128 keys by TMA (a box per page); four turn them into
 // fp16 (exact), as swizzled operand tiles; one lane of a warp issues the
 // products; and eight warps per tile are its rows, two threads to a row.
-// E4M3 codes of K, 128 to a row, are an operand as they arrive; q is then the sum of
+// E4M3 codes of K are an operand as they arrive; q is then the sum of
 // two E4M3 numbers, which is exact for elements down to 2^-10 of the row's largest (8
 // bits = 4 + 4) and off by 2^-18 of that below.  K is not converted, which took the
 // second case below from 221 us to 197; the first takes 267 with E4M3 codes.
@@ -83,13 +83,15 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
 }
 // the same with E4M3 operands, 32 bytes (elements) of a row per product; of the
-// instruction descriptor, whose two formats are 0 for E4M3 as for fp16, nothing differs
+// instruction descriptor, whose two formats are 0 for E4M3 as for fp16, nothing differs.
+// Rows of 64 bytes: SBO 512, 64-byte swizzle.
+template <int DIM>
 __device__ __forceinline__ void umma_ss_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
       " setp.ne.b32 p, %5, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
+      "r"(a), "r"(b), "r"(id), "r"(DIM == 128 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29), "r"((uint32_t)acc));
 }
 // A in TMEM: row i in lane i, two fp16 per column
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
@@ -234,7 +236,7 @@ __device__ __forceinline__ Item item_of(const PrefillArgs& a, unsigned at) {
 template <int MODE, int DIM, int CH>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int kTileBytes = kKeys * DIM * 2;
-  constexpr bool F8 = MODE == GDN_QDQ_E4M3 && DIM == 128;  // scores from the codes as they are
+  constexpr bool F8 = MODE == GDN_QDQ_E4M3;  // scores from the codes as they are
   constexpr uint32_t kCols = 512;  // S0 S1 O0 O1
   constexpr int BK = kKeys / CH;   // keys of a block
   constexpr uint32_t kIdQK = idesc_f16(128, kKeys, 0, 0), kIdPV = idesc_f16(128, DIM, 0, 1);
@@ -320,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
         float up, back;
         kv8_q_factor<F8 ? 7 : 8>(most, up, back);
-        // (fp16 holds an E4M3 code's value times 2^-8)
-        if (u == 0) row_factor[t * 128 + i] = back * fabsf(p.scale) * kLog2eF * (MODE == GDN_QDQ_E4M3 && !F8 ? 256.f : 1.f);
+        if (u == 0) row_factor[t * 128 + i] = back * fabsf(p.scale) * kLog2eF;
         if (p.scale < 0.f) up = -up;
         if constexpr (F8) {
           uint32_t hi[2], lo[2];
@@ -332,9 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
             lo[e] = e4m3_code2(f[4 * e] * up - h0.x, f[4 * e + 1] * up - h0.y, 1.f, l0) |
                     (uint32_t)e4m3_code2(f[4 * e + 2] * up - h1.x, f[4 * e + 3] * up - h1.y, 1.f, l1) << 16;
           }
-          unsigned char* to = sQ + t * kTileBytes + unit_at(i, u >> 1) + (u & 1) * 8;
+          unsigned char* to = sQ + t * kTileBytes + (u & 1) * 8 +
+                              (DIM == 128 ? unit_at(i, u >> 1) : i * 64 + (((u >> 1) ^ (i >> 1 & 3)) << 4));
           *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(to + kKeys * 128) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(to + kKeys * DIM) = make_uint2(lo[0], lo[1]);
         } else *reinterpret_cast<uint4*>(sQ + t * kTileBytes + unit_at(i, u)) =
             make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
                        pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
@@ -652,19 +654,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
     const uint32_t dq = desc_lo(base, 16);
-    const uint32_t dk = desc_lo(base + 2 * kTileBytes + (F8 ? kKeys * 128 : 0), 16);
+    const uint32_t dk = desc_lo(base + (uint32_t)((F8 ? codes_at(0, 0) : sK) - smem), 16);
+    constexpr uint32_t kKStep = (F8 && DIM == 64 ? kKeys * DIM : kTileBytes) >> 4;
     uint64_t* kthere = F8 ? &cfull[0][0] : &kfull[0];  // K's operand of a buffer
     const uint32_t dv = desc_lo(base + 4 * kTileBytes, kKeys * 128);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
     const bool lead = elect_one();
     auto qk = [&](int t, uint32_t b) {
-      const uint32_t k = dk + b * kTileStep, q = dq + t * kTileStep;
+      const uint32_t k = dk + b * kKStep, q = dq + t * kTileStep;
       if (lead) {
 #pragma unroll
         for (int s = 0; s < DIM / 16; ++s) {
-          const uint32_t at = (s & 3) * 32 >> 4, off = ((s >> 2) * (kKeys * 128) >> 4) + at;
+          constexpr int kRow = F8 ? DIM / 32 : 4;  // products along a row of an operand's panel
+          const uint32_t at = s % kRow * 32 >> 4, off = (s / kRow * (kKeys * (F8 ? DIM : 128)) >> 4) + at;
           if constexpr (F8)  // q's first parts, then its second ones, with the same codes
-            umma_ss_e4m3(tm + t * kKeys, q + off, k + at, kIdQK, s > 0);
+            umma_ss_e4m3<DIM>(tm + t * kKeys, q + off, k + at, kIdQK, s > 0);
           else
             umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
         }
