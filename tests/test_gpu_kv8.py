@@ -130,6 +130,21 @@ def test_many_short_rows(rows, heads, most, page, dim, mode):
         _run(rng, [int(n) for n in lengths], tokens, heads, group, dim, page, mode)
 
 
+@pytest.mark.parametrize("rows", [3, 200, 400])
+@pytest.mark.parametrize("cols", [0, 2])
+def test_rows_without_keys(rows, cols):
+    """Nothing in the cache for any row, and tables without columns."""
+    codes, scales = kv8_pool(1, 4, 1, 64, page=16)
+    table = torch.full((rows, cols), -1, dtype=torch.int32, device="cuda")
+    q = torch.randn(rows, 2, 2, 64, device="cuda").to(torch.bfloat16)
+    for n in (0, 5):
+        lengths = torch.full((rows,), n, dtype=torch.int32, device="cuda")
+        o, lse = kv8_attention(q, codes[0], scales[0], table, lengths, need_lse=True)
+        assert torch.all(o == 0)
+        assert torch.all(torch.isneginf(lse))
+    assert load().gdn_device_error(0) == 0
+
+
 MANY = [
     # lengths, tokens, heads, group, dim, page, mode, window, packed
     ([17], 17, 1, 1, 128, 64, "e4m3", 0, False),
