@@ -21,14 +21,13 @@
 // any scales.
 //
 // Measured on a GB300 (kernel alone): 64 rows of 2192 .. 8192 keys, 8 K/V heads of
-// 128, E4M3, 676 MB: 115 us, 5.9 TB/s (copying: 6.8); with nothing but its loads 108
-// us (an earlier build, 136 us with its products).  2 rows of 101072 and 131071 keys,
-// 4 heads, INT8, 260 MB: 54 us.  DRAM is at 73 and 59 %, instruction issue at half of
-// its slots from two warps per scheduler; the join takes 8 us.
-// With both launches the first case takes 125 us (127 with 64-bit divisions for the
-// shares; 1024 rows of 16 keys 81 and 69); with 12 warps of two tiles (168
-// registers) it took 155 where 8 warps of three took 146, and scores from E4M3
-// codes as they are together with the leaving out of rows 8-15 made 126 of that.
+// 128, E4M3, 676 MB: 115 us, 5.9 TB/s (copying: 6.8).  2 rows of 101072 and 131071
+// keys, 4 heads, INT8, 260 MB: 54 us.  DRAM is at 73 and 59 %, instruction issue at
+// half of its slots from two warps per scheduler; the join takes 8 us.
+// The first case with both launches: 12 warps of two tiles (168 registers) took 155 us,
+// 8 warps of three 146 (117 without their products), scores from E4M3 codes as they
+// are and the leaving out of rows 8-15 made it 126, 32-bit divisions for the shares
+// 125 (1024 rows of 16 keys: 81 to 69).
 #include <cuda.h>
 
 #include "kv8.cuh"
@@ -776,16 +775,16 @@ int64_t most_tiles(const Kv8Params& p) {
   return (keys + kTile - 1) / kTile + 1;
 }
 // One CTA per segment, or the line of all tiles?  A CTA alone takes 6 us + 0.18 us per
-// tile; the line takes 11 to 20 us more than its bytes (shares, a second launch), but
+// tile; the line pays for its shares and a second launch, but
 // leaves no SM idle and no wave half full.  Measured, line / segment in us, 128-wide
 // E4M3 heads:
 //     segments     256 keys   1024 keys   2048 keys   4096 keys
-//           8     10.9/6.8   12.9/11.5   14.5/17.4   12.9/29.1
-//          64     11.7/7.4   19.1/11.7   21.6/17.6   26.3/29.5
-//         152     13.3/7.4   18.1/12.3   24.2/18.3   39.1/33.5
-//         256     18.8/13.3  26.3/22.8   40.5/39.4   59.6/62.9
-//         512     22.8/24.9  41.2/50.1   60.3/74.9   99.7/121
-//        8192      162/355     401/615
+//           8     10.1/7.0   12.3/11.4   13.4/17.2   12.1/29.1
+//          64     10.9/7.5   18.2/11.7   20.7/17.8   25.4/29.5
+//         152     12.3/7.4   17.2/12.3   23.4/18.6   38.3/33.7
+//         256     17.7/13.4  25.2/22.8   39.7/39.6   59.0/63.4
+//         512     21.8/25.0  40.4/49.7   59.5/76.3   98.9/122
+//        8192      151/357     390/617
 // So: one wave up to a length that grows with the SMs it fills, two waves of
 // short segments, and the line for the rest.
 bool by_segment(const Kv8Params& p) {

@@ -16,8 +16,9 @@
 //
 // Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
 // PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
-// heads, E4M3: 197 us, 1.12 PFLOP/s.  Instruction issue bounds it, 2.2 a clock of the
-// four schedulers with the tensor pipe active 47 % of the time in the first.  In the
+// heads, E4M3: 197 us, 1.12 PFLOP/s.  The tensor pipe is active 47 and 61 % of the
+// time; instruction issue, 2.2 a clock of the four schedulers, bounds it with the
+// chain from S by its maxima to P of each tile of rows.  In the
 // steps' order (fp16 products), one thread per row (8 warps) took 345 and 258 us, two
 // 331 and 240, a CTA per SM for all its items 328 and 249, and one issuing warp for
 // both tiles with a shorter conversion 290 and 221.
