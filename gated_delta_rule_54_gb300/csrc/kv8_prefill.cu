@@ -27,7 +27,9 @@
 //
 // Scales.  s_j = q . code_j * (scale * ks(block of j)), and V's scale joins the
 // exponent: P_j = 2^(s_j + log2 vs - mv), so that fp16 holds it for any scales;
-// the denominator takes a block's sum times 2^(mv - log2 vs - m).  mv follows the
+// the denominator takes a block's sum times 2^(mv - log2 vs - m).  That exponent is held
+// to 40: a block below it (a V scale that small, or 0) has P below 2^-40, which is 0 in
+// fp16, while its sum and the factor stay numbers.  mv follows the
 // maximum of s_j + log2 vs only when that grows by more than 2^8 (fp16 has the
 // room), and then O is rescaled in TMEM.
 #include <cuda.h>
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         }
         const float uv = mv == -INFINITY ? 0.f : mv;
 #pragma unroll
-        for (int c = 0; c < HC; ++c) off[c] = off[c] > -INFINITY ? off[c] - uv : -um;
+        for (int c = 0; c < HC; ++c) off[c] = fmaxf(off[c] - uv, -um - 40.f);
         float2 sum[HC];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
