@@ -640,8 +640,8 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   const int h = blockIdx.x % p.heads;
   const Kv8Span sp = kv8_span(p, r);
   const int n = tiles_of(sp), rows = sp.n * p.group;
+  grid_dep_wait();  // by every CTA: the launches after this one are ordered behind it alone
   if (n == 0) return;
-  grid_dep_wait();
   const int64_t all = a.before[p.rows] * p.heads, ctas = ctas_for(all, grid);
   const int64_t u0 = a.before[r] * p.heads + (int64_t)h * n, u1 = u0 + n;
   // CTAs whose shares meet the segment: c with start(c) < u1 and start(c + 1) > u0

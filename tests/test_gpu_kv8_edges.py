@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import kv8_attention
+from gated_delta_rule_54_gb300 import kv8_attention, kv8_pool
 from oracle import serve as ref
 from test_gpu_kv8 import _check, _cuda, _pool, _table
 
@@ -49,3 +49,19 @@ def test_codes_under_a_scale_of_zero(mode, dim, page, tokens):
     got = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), mode=mode, need_lse=True)
     _check(got, q.float().cpu().numpy(), codes, scales, table, lengths, mode, dim ** -0.5)
     assert torch.all(got[0][1] == 0)
+
+
+# ---- what follows a call in the stream sees its outputs -------------------
+def test_next_kernel_sees_rows_without_keys():
+    """No row has a key, so nothing is left to join: a copy right behind the call has the zeros."""
+    rows, heads = 3000, 8
+    codes, scales = kv8_pool(1, 4, heads, 128, page=16)
+    table = torch.full((rows, 64), -1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    q = torch.randn(rows, 2, heads * 8, 128, device="cuda").to(torch.bfloat16)
+    out, seen = torch.empty_like(q), torch.empty_like(q)
+    for _ in range(20):
+        out.fill_(7.0)
+        kv8_attention(q, codes[0], scales[0], table, lengths, out=out)
+        seen.copy_(out)
+        assert int(torch.count_nonzero(seen)) == 0

@@ -1,0 +1,21 @@
+"""Host side of the serving operators' corners: what is refused, and what the sources have to keep."""
+import os
+import re
+
+import pytest
+
+from gated_delta_rule_54_gb300 import _lib
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(_lib.__file__)), "csrc")
+
+
+@pytest.mark.parametrize("name", ["kv8_decode.cu", "kv8_pages.cu", "beam.cu"])
+def test_dependent_launches_wait_before_any_return(name):
+    """A kernel that may start before its predecessor ends orders the rest of the stream behind it
+    only by its own wait, so no thread leaves before that."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    kernels = [k for k in re.split(r"__global__", text)[1:] if "grid_dep_wait()" in k]
+    assert kernels
+    for k in kernels:
+        assert not re.search(r"\breturn\b", k[:k.index("grid_dep_wait()")])
