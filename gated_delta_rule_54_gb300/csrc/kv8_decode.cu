@@ -554,7 +554,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   // ---- parts of one CTA ----
   grid_dep_launch();  // the join may be scheduled (it waits for the whole of this launch)
   if (lane == 0) s_u0[warp] = part;
-  __syncthreads();  // every ring is done with
+  // every ring is done with; where a wait gave up the parts are not all there, and with a
+  // CTA per segment, whose parts make a whole otherwise, there is no workspace for them
+  if (__syncthreads_or(bad)) return;
   float* parts = reinterpret_cast<float*>(smem);  // [warp][16][DIM]
   if (part >= 0) {
 #pragma unroll

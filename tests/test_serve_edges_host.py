@@ -19,3 +19,13 @@ def test_dependent_launches_wait_before_any_return(name):
     assert kernels
     for k in kernels:
         assert not re.search(r"\breturn\b", k[:k.index("grid_dep_wait()")])
+
+
+def test_parts_stay_in_the_cta_where_a_wait_gave_up():
+    """With a CTA per segment the call has no workspace, and a part that is not whole would be
+    stored through a null pointer: the CTA has to leave before it looks for a place for one."""
+    with open(os.path.join(CSRC, "kv8_decode.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    body = text[text.index("kv8_decode_kernel("):text.index("kv8_join_kernel(")]
+    gone = body.index("if (__syncthreads_or(bad)) return;")
+    assert body.index("s_u0[warp] = part;") < gone < body.index("slot = a.ws")
