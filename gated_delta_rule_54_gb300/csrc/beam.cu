@@ -17,6 +17,10 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -358,6 +362,40 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const __g
   }
 }
 
+// The states go through one launch in no order, so no buffer that is written may meet
+// another one, but for a state's own in place.  Buffers in the order of their addresses:
+// a written one must lie past all before it, a read one past all written ones (the same
+// buffer may be read for several states).
+bool apart(int n, const void* const* src, void* const* dst, const int64_t* row_bytes,
+           const int32_t* parents, int64_t rows) {
+  struct Range {
+    uintptr_t from, to;
+    bool written;
+  };
+  Range few[128], *r = few;
+  std::unique_ptr<Range[]> many;
+  if (2 * (int64_t)n + 1 > 128) {
+    many.reset(new (std::nothrow) Range[2 * (size_t)n + 1]);
+    if (!(r = many.get())) return false;
+  }
+  int64_t m = 0;
+  r[m++] = {(uintptr_t)parents, (uintptr_t)(parents + rows), false};
+  for (int i = 0; i < n; ++i) {
+    if (row_bytes[i] == 0) continue;
+    const uintptr_t a = (uintptr_t)src[i], c = (uintptr_t)dst[i], bytes = (uintptr_t)(rows * row_bytes[i]);
+    r[m++] = {c, c + bytes, true};
+    if (a != c) r[m++] = {a, a + bytes, false};
+  }
+  std::sort(r, r + m, [](const Range& x, const Range& y) { return x.from < y.from; });
+  uintptr_t any = 0, written = 0;
+  for (int64_t i = 0; i < m; ++i) {
+    if (r[i].from < (r[i].written ? any : written)) return false;
+    any = std::max(any, r[i].to);
+    if (r[i].written) written = std::max(written, r[i].to);
+  }
+  return true;
+}
+
 }  // namespace
 
 }  // namespace gdn
@@ -428,9 +466,8 @@ gdn_status gdn_beam_reorder(int32_t n, const void* const* src, void* const* dst,
     if (row_bytes[i] == 0) continue;
     if (!src[i] || !dst[i]) return GDN_ERR_INVALID_ARG;
     if (((uintptr_t)src[i] | (uintptr_t)dst[i]) & 15) return GDN_ERR_MISALIGNED;
-    const uintptr_t a = (uintptr_t)src[i], c = (uintptr_t)dst[i], bytes = (uintptr_t)(rows * row_bytes[i]);
-    if (a != c && a < c + bytes && c < a + bytes) return GDN_ERR_INVALID_ARG;
   }
+  if (!apart(n, src, dst, row_bytes, parents, rows)) return GDN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t groups = (rows + beams - 1) / beams;
   for (int i = 0; i < n;) {

@@ -354,7 +354,8 @@ def beam_reorder(states: Sequence[torch.Tensor], parents, beams: int, out=None):
     """Row r of every state [rows, ...] becomes row parents[r] (int32, any shape of rows
     elements; -1: zeros).  In place by default: parents then stay within groups of ``beams``
     consecutive rows, and a row that keeps itself is not touched.  ``out`` gives other buffers
-    of the same shapes, one per state (any parents).  Rows are a multiple of 16 bytes.
+    of the same shapes, one per state (any parents); a buffer that is written may not overlap
+    any other state or buffer.  Rows are a multiple of 16 bytes.
     Returns the states that were written."""
     dst = list(states if out is None else out)
     if not states:

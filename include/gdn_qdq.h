@@ -603,7 +603,9 @@ gdn_status gdn_beam_select(const gdn_beam_problem* p, const void* logits, const 
  * of row_bytes[i] bytes a row (a multiple of 16).  dst[i] may be src[i] (in
  * place: rows that keep themselves are not touched); then parents stay within
  * groups of `beams` consecutive rows (others are not followed: the row stays).
- * Any other overlap is an error.  src, dst and row_bytes are host arrays.
+ * Any other overlap of a dst with a src or dst, of the same state or of another,
+ * or with parents is an error: the states are moved in no order.  src, dst and row_bytes are host
+ * arrays.
  */
 gdn_status gdn_beam_reorder(int32_t n, const void* const* src, void* const* dst,
                             const int64_t* row_bytes, const int32_t* parents, int64_t rows,

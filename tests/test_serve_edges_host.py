@@ -29,3 +29,28 @@ def test_parts_stay_in_the_cta_where_a_wait_gave_up():
     body = text[text.index("kv8_decode_kernel("):text.index("kv8_join_kernel(")]
     gone = body.index("if (__syncthreads_or(bad)) return;")
     assert body.index("s_u0[warp] = part;") < gone < body.index("slot = a.ws")
+
+
+def test_reorder_refuses_buffers_that_meet():
+    """All states move in one launch without order, so what one writes no other may read or write."""
+    import struct
+    lib, A, row, rows = _lib.load(), 1 << 20, 64, 4
+    q = lambda v: struct.pack("%dQ" % len(v), *v)
+
+    def call(src, dst, sizes=None):
+        return lib.gdn_beam_reorder(len(src), q(src), q(dst), q(sizes or [row] * len(src)), 4096, rows, 2, None)
+
+    a, b, c, d = (A + i * row * rows for i in range(4))
+    bad = -1
+    assert call([a, b], [b, a]) == bad                       # swapped
+    assert call([a, b], [c, c]) == bad                       # one buffer for two
+    assert call([a, a], [a, a]) == bad                       # one state twice, in place
+    assert call([a, b], [b, b]) == bad
+    assert call([a, b], [a + row, d]) == bad                 # a shifted overlap of its own
+    assert call([a, b, d], [c, b + row, d]) == bad           # and of another's
+    assert call([a, c], [b, a + 3 * row], [row, row]) == bad
+    many = [A + i * row * rows for i in range(200)]
+    assert call(many, many[1:] + [many[0]]) == bad
+    assert call([a], [4096]) == bad                          # the parents
+    # (no device here, or an address that is not one: what is apart comes as far as the launch, and is not tried)
+    assert call([a, b], [c, d], [24, 24]) == -3
