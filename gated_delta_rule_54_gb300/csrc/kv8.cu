@@ -234,7 +234,8 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
   if (s != GDN_OK) return s;
   if (p->total == 0) return GDN_OK;
   if (!q || !o || !lengths) return GDN_ERR_INVALID_ARG;
-  if (p->pages > 0 && p->cols > 0 && (!codes || !scales || !table)) return GDN_ERR_INVALID_ARG;
+  // (the kernels look up a row's pages whether or not the cache has any)
+  if (p->cols > 0 && (!table || (p->pages > 0 && (!codes || !scales)))) return GDN_ERR_INVALID_ARG;
   if (off16({q, codes, o}) || off4({scales, table, lengths, lse, p->cu_seqlens}) ||
       ((uintptr_t)workspace & 255))
     return GDN_ERR_MISALIGNED;

@@ -1,4 +1,5 @@
 """Host side of the serving operators' corners: what is refused, and what the sources have to keep."""
+import ctypes
 import os
 import re
 
@@ -54,3 +55,19 @@ def test_reorder_refuses_buffers_that_meet():
     assert call([a], [4096]) == bad                          # the parents
     # (no device here, or an address that is not one: what is apart comes as far as the launch, and is not tried)
     assert call([a, b], [c, d], [24, 24]) == -3
+
+
+def _kv8(**kw):
+    p = _lib.GdnKv8Problem(pages=10, rows=2, total=2, tokens=1, cols=4, heads=2, group=4, dim=128, page=64, mode=1, dtype=0,
+                           causal=1, window=0, scale=0.1, cu_seqlens=None, x_row=1024, x_token=1024, x_head=128)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_attention_needs_a_table_of_columns(tokens):
+    """A table with columns is read even where the cache has no pages."""
+    lib, A = _lib.load(), 4096
+    p = ctypes.byref(_kv8(pages=0, tokens=tokens, total=2 * tokens))
+    assert lib.gdn_kv8_attention(p, A, None, None, None, A, A, None, A, 1 << 40, None) == -1
