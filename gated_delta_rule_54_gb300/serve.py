@@ -4,7 +4,8 @@ Argument marshalling only (``include/gdn_qdq.h`` has the definitions).  A layer'
 ``codes`` uint8 [2, pages, heads, page, dim] (0: K, 1: V) and ``scales`` f32 [2, pages, heads],
 one scale per page of tokens and head; a pool over layers has a leading [layers].  Rows find
 their pages in ``table`` int32 [rows, columns]; ``refs`` int32 [pages] counts the holders of a
-page.  Everything runs on the current stream and nothing waits for the host.
+page.  Everything runs on the current stream and nothing waits for the host.  A ``workspace`` is any
+contiguous tensor with enough bytes, on the same device.
 """
 from __future__ import annotations
 
@@ -52,6 +53,13 @@ def _say(dev, *named):
               "%s must be a CUDA tensor on cuda:%d" % (name, dev))
         _need(t.dtype == dtype, "%s must be %s" % (name, dtype))
         _need(t.is_contiguous(), "%s must be contiguous" % name)
+
+
+def _room(workspace, dev):
+    """Address and bytes of a workspace."""
+    _need(isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous(),
+          "workspace must be a contiguous tensor on cuda:%d" % dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kv8_pool(layers, pages, heads, dim, page=64, device="cuda"):
@@ -175,8 +183,7 @@ def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=
         return lib.gdn_kv8_attention(
             p, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), table.data_ptr(),
             lengths.data_ptr(), out.data_ptr(), lse.data_ptr() if need_lse else None,
-            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-            _raw_stream(dev))
+            *((None, 0) if ws is None else _room(ws, dev)), _raw_stream(dev))
 
     st = call(workspace)
     if st == _TOO_SMALL and workspace is None:
@@ -246,7 +253,7 @@ def _fork(codes, scales, table, lengths, parents, drop, refs, workspace):
         p, codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
         refs.data_ptr(), parents.data_ptr() if drop is None else None,
         None if drop is None else drop.data_ptr(), t.data_ptr(), n.data_ptr(), r.data_ptr(),
-        missing.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        missing.data_ptr(), *_room(ws, dev), _raw_stream(dev))
     if st:
         _raise("gdn_kv8_fork", st)
     return t, n, r, missing
@@ -281,7 +288,7 @@ def kv8_reserve(codes, scales, table, lengths, extra, refs, workspace=None):
     missing = torch.empty(1, dtype=_i32, device=codes.device)
     st = _fns().gdn_kv8_reserve(
         p, table.data_ptr(), lengths.data_ptr(), refs.data_ptr(), extra.data_ptr(), t.data_ptr(),
-        n.data_ptr(), r.data_ptr(), missing.data_ptr(), ws.data_ptr(), ws.numel(),
+        n.data_ptr(), r.data_ptr(), missing.data_ptr(), *_room(ws, dev),
         _raw_stream(dev))
     if st:
         _raise("gdn_kv8_reserve", st)
@@ -293,13 +300,14 @@ def kv8_compact(codes, scales, table, lengths, refs, workspace=None):
     lowest at or above n goes to the i-th lowest free page below n.  Returns new
     (table, refs, live) with live int32 [1] = n.  Page ids held elsewhere become stale."""
     p = _pool_problem(codes, scales, table, lengths, refs)
+    dev = codes.get_device()
     ws = _pool_workspace(p, workspace, codes.device)
     t, r = torch.empty_like(table), torch.empty_like(refs)
     live = torch.empty(1, dtype=_i32, device=codes.device)
     st = _fns().gdn_kv8_compact(
         p, codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        refs.data_ptr(), t.data_ptr(), r.data_ptr(), live.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(codes.get_device()))
+        refs.data_ptr(), t.data_ptr(), r.data_ptr(), live.data_ptr(), *_room(ws, dev),
+        _raw_stream(dev))
     if st:
         _raise("gdn_kv8_compact", st)
     return t, r, live
@@ -343,7 +351,7 @@ def beam_select(logits, scores, finished=None, k: Optional[int] = None, eos=-1, 
     st = lib.gdn_beam_select(
         p, logits.data_ptr(), scores.data_ptr(),
         None if finished is None else finished.data_ptr(), best.data_ptr(), parents.data_ptr(),
-        tokens.data_ptr(), done.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        tokens.data_ptr(), done.data_ptr(), *_room(workspace, dev),
         _raw_stream(dev))
     if st:
         _raise("gdn_beam_select", st)
