@@ -121,12 +121,14 @@ def _problem(x, v, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, 
         _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode)
     _, pages, heads, page, dim = cs
     rows, cols = table.shape
+    if len(shape) != (4 if cu_seqlens is None else 3):
+        _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode)
     if cu_seqlens is None:
-        fits = len(shape) == 4 and shape[0] == rows
+        fits = shape[0] == rows
         tokens, cu = shape[1], 0
         total = rows * tokens
     else:
-        fits = len(shape) == 3 and _plain(cu_seqlens, _i32, dev) and cu_seqlens.shape == (rows + 1,)
+        fits = _plain(cu_seqlens, _i32, dev) and cu_seqlens.shape == (rows + 1,)
         total = tokens = shape[0]
         if max_seqlen is not None and max_seqlen < tokens:
             tokens = int(max_seqlen)
@@ -368,6 +370,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parents, beams: int, out=None):
     dst = list(states if out is None else out)
     if not states:
         return dst
+    _need(states[0].dim() > 0, "states must be [rows, ...]")
     dev, rows = states[0].get_device(), states[0].shape[0]
     if not _plain(parents, _i32, dev):
         _say(dev, ("parents", parents, _i32))
@@ -375,7 +378,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parents, beams: int, out=None):
     _need(len(dst) == len(states), "out must have one buffer per state")
     n, src, to, size = len(dst), [], [], []
     for x, y in zip(states, dst):
-        _need(x.get_device() == dev and dev >= 0 and x.is_contiguous() and x.shape[0] == rows,
+        _need(x.get_device() == dev and dev >= 0 and x.is_contiguous() and x.dim() > 0 and x.shape[0] == rows,
               "states must be contiguous [rows, ...] on one CUDA device")
         _need(y is x or (y.shape == x.shape and y.dtype is x.dtype and y.get_device() == dev
                          and y.is_contiguous()), "out must match the states")

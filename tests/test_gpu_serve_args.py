@@ -2,8 +2,8 @@
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import (beam_select, kv8_attention, kv8_compact, kv8_fork, kv8_free, kv8_pool, kv8_reserve,
-                                       kv8_workspace_bytes)
+from gated_delta_rule_54_gb300 import (beam_reorder, beam_select, kv8_append, kv8_attention, kv8_compact, kv8_fork,
+                                       kv8_free, kv8_pool, kv8_reserve, kv8_workspace_bytes)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,22 @@ def test_workspaces():
     for call in calls:
         call(room.view(torch.float32))
     torch.cuda.synchronize()
+
+
+def test_tensors_of_too_few_dims():
+    """Tensors with dims missing are refused in words."""
+    codes, scales = kv8_pool(1, 8, 2, 64, page=16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, n, cu = torch.full((2, 4), -1, **i32), torch.zeros(2, **i32), torch.zeros(3, **i32)
+    for shape in ((), (64,), (4, 64), (2, 4, 64), (1, 2, 1, 4, 64)):
+        q = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+        for offsets in (None, cu):
+            if offsets is not None and len(shape) == 3:
+                continue
+            with pytest.raises(ValueError):
+                kv8_attention(q, codes[0], scales[0], table, n, cu_seqlens=offsets)
+            with pytest.raises(ValueError):
+                kv8_append(q, q, codes[0], scales[0], table, n, cu_seqlens=offsets)
+    parents = torch.zeros(1, **i32)
+    with pytest.raises(ValueError):
+        beam_reorder([torch.zeros((), device="cuda")], parents, 1)
