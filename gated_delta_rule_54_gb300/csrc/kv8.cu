@@ -147,8 +147,9 @@ gdn_status validate_kv8(const gdn_kv8_problem* p) {
     return GDN_ERR_UNSUPPORTED_SHAPE;
   if (!p->cu_seqlens && p->total != p->rows * p->tokens) return GDN_ERR_INVALID_ARG;
   if (p->rows == 0 && p->total > 0) return GDN_ERR_INVALID_ARG;
-  // positions are 32-bit; heads are a grid dimension; page ids are 32-bit
-  if ((int64_t)p->cols * p->page > 0x7fffffffLL || p->pages > 0x7fffffffLL ||
+  // positions are 32-bit, with room to round one up to a tile of keys and to look some
+  // tiles ahead; heads are a grid dimension; page ids are 32-bit
+  if ((int64_t)p->cols * p->page > 0x7fff0000LL || p->pages > 0x7fffffffLL ||
       p->rows > 0x7fffffffLL || p->total > 0x7fffffffLL ||
       2 * p->pages * p->heads > 0x7fffffffLL || p->rows * p->heads > 0x7fffffffLL ||
       (int64_t)p->tokens * p->group > 0x7ffffeffLL || (int64_t)p->heads * p->group > 65535)

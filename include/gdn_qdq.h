@@ -454,7 +454,7 @@ typedef struct {
   int64_t rows;               /* sequences                                       */
   int64_t total;              /* tokens of q (k, v) over all rows                */
   int32_t tokens;             /* a row's tokens (packed: an upper bound)         */
-  int32_t cols;               /* columns of the table                            */
+  int32_t cols;               /* columns of the table (cols * page <= 2^31 - 2^16) */
   int32_t heads;              /* K/V heads                                       */
   int32_t group;              /* query heads per K/V head (attention)            */
   int32_t dim;                /* head dim: 64 or 128                             */

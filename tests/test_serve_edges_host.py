@@ -71,3 +71,11 @@ def test_attention_needs_a_table_of_columns(tokens):
     lib, A = _lib.load(), 4096
     p = ctypes.byref(_kv8(pages=0, tokens=tokens, total=2 * tokens))
     assert lib.gdn_kv8_attention(p, A, None, None, None, A, A, None, A, 1 << 40, None) == -1
+
+
+@pytest.mark.parametrize("cols,page,code", [((1 << 27) - 1, 16, -3), ((1 << 24) - 1, 128, -3), ((1 << 27) - 4095, 16, -3),
+                                            ((1 << 27) - 4096, 16, 0), ((1 << 24) - 512, 128, 0)])
+def test_positions_leave_room_to_round_up(cols, page, code):
+    """Positions are 32-bit and the kernels round them up to tiles of keys: a table whose last
+    positions would pass 2^31 there is refused."""
+    assert _lib.load().gdn_kv8_validate(ctypes.byref(_kv8(cols=cols, page=page))) == code
