@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
         // (the other thread has its half of S in registers before it comes here, so P
         // may be written over S after this)
         other[i & 1][half][i_row] = make_float2(nm, nv);
+        tc_fence_before();
         pair_sync();
+        tc_fence_after();
         const float2 o2 = other[i & 1][half ^ 1][i_row];
         nm = fmaxf(fmaxf(nm, o2.x), mx), nv = fmaxf(nv, o2.y);
         const float um = nm == -INFINITY ? 0.f : nm;

@@ -79,3 +79,12 @@ def test_positions_leave_room_to_round_up(cols, page, code):
     """Positions are 32-bit and the kernels round them up to tiles of keys: a table whose last
     positions would pass 2^31 there is refused."""
     assert _lib.load().gdn_kv8_validate(ctypes.byref(_kv8(cols=cols, page=page))) == code
+
+
+def test_scores_are_read_before_they_are_written_over():
+    """Two threads read the halves of a row of S, and both write P over its first half: the
+    barrier between these orders TMEM accesses of different threads only with its fences."""
+    with open(os.path.join(CSRC, "kv8_prefill.cu")) as f:
+        text = re.sub(r"\s+", " ", re.sub(r"//[^\n]*", "", f.read()))
+    read, write = text.index("tmem_ld32(s_col + half * HK, v[0]);"), text.index("tmem_st16(s_col + half * (HK / 2)")
+    assert "tc_fence_before(); pair_sync(); tc_fence_after();" in text[read:write]
