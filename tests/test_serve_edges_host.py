@@ -88,3 +88,14 @@ def test_scores_are_read_before_they_are_written_over():
         text = re.sub(r"\s+", " ", re.sub(r"//[^\n]*", "", f.read()))
     read, write = text.index("tmem_ld32(s_col + half * HK, v[0]);"), text.index("tmem_st16(s_col + half * (HK / 2)")
     assert "tc_fence_before(); pair_sync(); tc_fence_after();" in text[read:write]
+
+
+def test_tmem_loads_are_waited_for_in_one_piece():
+    """What a tcgen05.ld gives may be used after its wait only.  A wait in a statement of its own
+    does not say so to the compiler, unless the values pass through it."""
+    for name in ("tc.cuh", "kv8_prefill.cu"):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        for piece in re.findall(r"asm volatile\((.*?)\);\n", text, re.S):
+            if "tcgen05.wait::ld" in piece:
+                assert "tcgen05.ld" in piece or '"+f"' in piece
