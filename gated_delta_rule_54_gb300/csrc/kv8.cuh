@@ -119,6 +119,33 @@ __device__ __forceinline__ void kv8_q_factor(float most, float& to, float& back)
   back = __uint_as_float((uint32_t)(e - E + 127) << 23);
 }
 
+// q beside E4M3 codes.  A row with its largest element in [2^7, 2^8) is the sum of an E4M3
+// number (four bits) and what that leaves (at most 2^-4 of an element's binade, so three of
+// bf16's eight bits) as an E5M2 number: exact for elements down to 2^-13 of the largest.
+// Below 2^-6 the first is off by at most 2^-10, of which three bits leave 2^-14, i.e. such
+// elements are off by at most 2^-21 of the row's largest.  (INT8 codes meet q in fp16,
+// which is exact down to 2^-25 of it.)  Four codes at a time, little-endian.
+__device__ __forceinline__ uint32_t kv8_q_first(const float* f, float to, float (&rest)[4]) {
+  float2 a, b;
+  const uint32_t w = e4m3_code2(f[0], f[1], to, a) | (uint32_t)e4m3_code2(f[2], f[3], to, b) << 16;
+  rest[0] = f[0] * to - a.x, rest[1] = f[1] * to - a.y;
+  rest[2] = f[2] * to - b.x, rest[3] = f[3] * to - b.y;
+  return w;
+}
+__device__ __forceinline__ uint32_t kv8_e5m2x4(const float (&x)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E5M2);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E5M2);
+  return lo | hi << 16;
+}
+__device__ __forceinline__ void mma_e5m2_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e5m2.e4m3.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));

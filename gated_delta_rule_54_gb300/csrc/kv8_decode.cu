@@ -15,7 +15,7 @@
 // A warp runs by itself: a ring of S tiles (K and V, by TMA, 128- or 64-byte
 // swizzle) that its lane 0 refills, warp products with fp32 sums, and an online
 // softmax.  E4M3 scores come from the codes as they are, with q as a sum of two
-// E4M3 numbers; INT8 codes, and those of V, are exact in fp16 (q keeps its bits by
+// 8-bit numbers; INT8 codes, and those of V, are exact in fp16 (q keeps its bits by
 // a power of two per row).  A block's V scale multiplies the probabilities, so these run
 // against a second maximum, of score + log2(scale), and stay within [0, 1] for
 // any scales.
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   constexpr int KSTEPS = DIM / 16, NT = DIM / 8;      // 16-byte chunks of a row; n tiles of V
   constexpr int NE = R8 ? 1 : 2;                      // query rows of a thread: g, g + 8
   constexpr bool F8 = MODE == GDN_QDQ_E4M3;           // scores from the codes as they are
+  constexpr float kRest = 32.f;                       // R8: of q's second part
   constexpr int kBytes = kTile * DIM;                 // K or V of a tile
   constexpr int kRowMask = DIM == 128 ? 7 : 3, kRowShift = DIM == 128 ? 0 : 1;
   extern __shared__ unsigned char smem_raw[];
@@ -293,10 +294,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     sp = kv8_span(p, cc.r);
     const int rows = sp.n * p.group;
     // q fragments.  INT8: fp16, element pairs in the order kv8_half2 gives K's.  E4M3:
-    // q as the sum of two E4M3 numbers, which is exact for elements down to 2^-10
-    // of the row's largest (8 bits = 4 + 4) and off by 2^-18 of it below; the second
-    // ones are rows 8-15 of the same fragment where these are free (R8), else one
-    // of their own.
+    // the two parts of q (kv8.cuh).  Up to eight rows (R8) the second ones are rows 8-15
+    // of the same fragment, so E4M3 as well; with 2^5 of their own, which their sums give
+    // back, that leaves 2^-15 where E5M2 leaves 2^-14.  Else they are E5M2 in a fragment of
+    // their own.
     constexpr int QF = F8 ? (R8 ? DIM / 32 : DIM / 16) : KSTEPS;
     uint32_t qf[QF][4];
     float rowfac[NE];
@@ -331,15 +332,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           bf16x4(raw[e][c], f);
           if constexpr (F8) {
             // k 16 c + 4 t ..: register 2 (c & 1) of row g, 2 (c & 1) + 1 of row g + 8
-            float2 h0, h1;
-            const uint32_t hi = e4m3_code2(f[0], f[1], to, h0) | (uint32_t)e4m3_code2(f[2], f[3], to, h1) << 16;
-            float2 l0, l1;
-            const uint32_t lo = e4m3_code2(f[0] * to - h0.x, f[1] * to - h0.y, 1.f, l0) |
-                                (uint32_t)e4m3_code2(f[2] * to - h1.x, f[3] * to - h1.y, 1.f, l1) << 16;
+            float rest[4];
+            const uint32_t hi = kv8_q_first(f, to, rest);
             if constexpr (R8) {
-              qf[c / 2][2 * (c & 1)] = hi, qf[c / 2][2 * (c & 1) + 1] = lo;
+              float2 l0, l1;
+              qf[c / 2][2 * (c & 1)] = hi;
+              qf[c / 2][2 * (c & 1) + 1] = e4m3_code2(rest[0], rest[1], kRest, l0) |
+                                           (uint32_t)e4m3_code2(rest[2], rest[3], kRest, l1) << 16;
             } else {
-              qf[c / 2][2 * (c & 1) + e] = hi, qf[DIM / 32 + c / 2][2 * (c & 1) + e] = lo;
+              qf[c / 2][2 * (c & 1) + e] = hi, qf[DIM / 32 + c / 2][2 * (c & 1) + e] = kv8_e5m2x4(rest);
             }
           } else {
             qf[c][e] = pack_f16(f[0] * to, f[2] * to);
@@ -385,8 +386,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mma_e4m3(s[j], qf[2 * q], r[0], r[1]);
             mma_e4m3(s[j], qf[2 * q + 1], r[2], r[3]);
             if constexpr (!R8) {
-              mma_e4m3(s[j], qf[DIM / 32 + 2 * q], r[0], r[1]);
-              mma_e4m3(s[j], qf[DIM / 32 + 2 * q + 1], r[2], r[3]);
+              mma_e5m2_e4m3(s[j], qf[DIM / 32 + 2 * q], r[0], r[1]);
+              mma_e5m2_e4m3(s[j], qf[DIM / 32 + 2 * q + 1], r[2], r[3]);
             }
           } else {
 #pragma unroll
@@ -397,7 +398,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
           }
         }
-        if constexpr (F8 && R8) s[j][0] += s[j][2], s[j][1] += s[j][3];
+        if constexpr (F8 && R8)
+          s[j][0] = fmaf(s[j][2], 1.f / kRest, s[j][0]), s[j][1] = fmaf(s[j][3], 1.f / kRest, s[j][1]);
       }
       const int j0 = cc.tile * kTile;
       const bool mask = have != 3 || j0 < in0 || j0 + kTile > in1;

@@ -3,15 +3,15 @@
 // The query rows of a (row, K/V head) are its queries times the query heads that
 // share the head, query-major; a CTA takes 256 of them, as two tiles of 128, so
 // that one conversion of a block of keys serves both.  Per 128 keys and tile:
-//     S = Q K^T   (tcgen05, fp16 x fp16 or E4M3 x E4M3 -> fp32 in TMEM)
+//     S = Q K^T   (tcgen05, fp16 x fp16 or 8-bit x E4M3 -> fp32 in TMEM)
 //     P = 2^(s - reference)  (two threads per query row; written over S as fp16)
 //     O += P V    (tcgen05 with P from TMEM)
 // One warp brings the codes of 128 keys by TMA (a box per page); four turn them into
 // fp16 (exact), as swizzled operand tiles; one lane of a warp issues the
 // products; and eight warps per tile are its rows, two threads to a row.
-// E4M3 codes of K are an operand as they arrive; q is then the sum of
-// two E4M3 numbers, which is exact for elements down to 2^-10 of the row's largest (8
-// bits = 4 + 4) and off by 2^-18 of that below.  K is not converted, which took the
+// E4M3 codes of K are an operand as they arrive; q is then the sum of an E4M3 and an
+// E5M2 number, exact for elements down to 2^-13 of the row's largest and off by at most
+// 2^-21 of that below (kv8.cuh).  K is not converted, which took the
 // second case below from 221 us to 197; the first takes 267 with E4M3 codes.
 //
 // Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
@@ -85,11 +85,12 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint
       " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
 }
-// the same with E4M3 operands, 32 bytes (elements) of a row per product; of the
-// instruction descriptor, whose two formats are 0 for E4M3 as for fp16, nothing differs.
+// the same with 8-bit operands, 32 bytes (elements) of a row per product.  In the
+// instruction descriptor E4M3 is format 0, as fp16 is there, and E5M2 format 1 (A's: bit 7).
 // Rows of 64 bytes: SBO 512, 64-byte swizzle.
+constexpr uint32_t kAE5M2 = 1u << 7;
 template <int DIM>
-__device__ __forceinline__ void umma_ss_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
+__device__ __forceinline__ void umma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
       " setp.ne.b32 p, %5, 0;\n"
@@ -331,10 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float2 h0, h1, l0, l1;
-            hi[e] = e4m3_code2(f[4 * e], f[4 * e + 1], up, h0) | (uint32_t)e4m3_code2(f[4 * e + 2], f[4 * e + 3], up, h1) << 16;
-            lo[e] = e4m3_code2(f[4 * e] * up - h0.x, f[4 * e + 1] * up - h0.y, 1.f, l0) |
-                    (uint32_t)e4m3_code2(f[4 * e + 2] * up - h1.x, f[4 * e + 3] * up - h1.y, 1.f, l1) << 16;
+            float rest[4];
+            hi[e] = kv8_q_first(f + 4 * e, up, rest);
+            lo[e] = kv8_e5m2x4(rest);
           }
           unsigned char* to = sQ + t * kTileBytes + (u & 1) * 8 +
                               (DIM == 128 ? unit_at(i, u >> 1) : i * 64 + (((u >> 1) ^ (i >> 1 & 3)) << 4));
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           constexpr int kRow = F8 ? DIM / 32 : 4;  // products along a row of an operand's panel
           const uint32_t at = s % kRow * 32 >> 4, off = (s / kRow * (kKeys * (F8 ? DIM : 128)) >> 4) + at;
           if constexpr (F8)  // q's first parts, then its second ones, with the same codes
-            umma_ss_e4m3<DIM>(tm + t * kKeys, q + off, k + at, kIdQK, s > 0);
+            umma_ss_f8<DIM>(tm + t * kKeys, q + off, k + at, kIdQK | (s < kRow ? 0 : kAE5M2), s > 0);
           else
             umma_ss(tm + t * kKeys, q + off, k + off, kIdQK, s > 0);
         }

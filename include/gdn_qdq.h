@@ -502,7 +502,11 @@ gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v
  *   o   = sum_j softmax_j(scale q . K_j) V_j        bf16
  *   lse = log sum_j exp(scale q . K_j)              f32 (or NULL)
  * A query that sees no key (also: t < 0) has o = 0 and lse = -inf.  Sums and
- * softmax statistics are fp32; probabilities enter the V product in fp16.
+ * softmax statistics are fp32.  Fewer bits: probabilities enter the V product in
+ * fp16 (11 bits, and 2^-25 of a query's largest below 2^-14 of it).  q enters exactly but
+ * for elements far below the largest |element| of their (query, head): with E4M3 codes
+ * those below 2^-13 of it are off by at most 2^-21 of it, with INT8 codes those below
+ * 2^-25 by at most 2^-33.
  *   q   bf16 [rows, tokens, heads * group, dim] or packed [total, ...], strided
  *   o   bf16 [total, heads * group, dim] contiguous,  lse f32 [total, heads * group]
  *   workspace  gdn_kv8_workspace_bytes(p) bytes, 256-byte aligned

@@ -65,3 +65,46 @@ def test_next_kernel_sees_rows_without_keys():
         kv8_attention(q, codes[0], scales[0], table, lengths, out=out)
         seen.copy_(out)
         assert int(torch.count_nonzero(seen)) == 0
+
+
+# ---- q with one channel far above the others ------------------------------
+@pytest.mark.parametrize("mode", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("tokens,group", [(1, 4), (4, 4), (20, 1), (150, 2)])
+def test_q_with_a_large_channel(mode, dim, page, tokens, group):
+    """A channel of q 2^10 to 2^14 times the others, where K is nothing or the same for all keys.
+
+    q of an E4M3 cache is the sum of an E4M3 and an E5M2 number (or two E4M3 numbers): with
+    the row's largest in [2^7, 2^8) the first is off by 2^-4 of an element's binade, which
+    leaves at most three bits, down to elements of 2^-6; below, the first is off by at most
+    2^-10 and three bits of that leave 2^-14: 2^-21 of the row's largest for elements below
+    2^-13 of it.  INT8 caches take q in fp16, exact here."""
+    rng = np.random.default_rng(33)
+    lengths = [1, 2, 5, 40, 300]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, 1, page, dim, mode)
+    codes[0, ..., 5] = 0
+    codes[0, ..., 9] = 0x78 if mode == "e4m3" else 90      # 256 or 90 of the scale
+    scales[0] = scales[0, 0]                               # the channel is the same for all keys
+    table = _table(rng, lengths, page, pages)
+    args = _cuda(codes, scales, table, np.array(lengths, np.int32))
+    for channel in (5, 9):
+        for e in (10, 12, 14):
+            q = _q(rng, len(lengths), tokens, group, dim)
+            q[..., channel] *= 2.0 ** e
+            o, lse = (x.float().cpu().numpy().astype(np.float64) for x in kv8_attention(q, *args, mode=mode, need_lse=True))
+            x = q.float().cpu().numpy().astype(np.float64)
+            for r, n in enumerate(lengths):
+                ro, rl, absum, top, dots = ref.attention(x[r], codes, scales, table[r], n, mode, dim ** -0.5)
+                score = 2.0 ** -20 * (dots + 1)
+                if mode == "e4m3":
+                    keys = codes[0][table[r, :-(-n // page)], 0].reshape(-1, dim)[:n]
+                    k = np.abs(ref.decode_codes(keys, mode)) * float(scales[0, 0, 0])
+                    most = np.abs(x[r]).max(-1, keepdims=True)
+                    small = np.abs(x[r]) < 2.0 ** -13 * most
+                    score = score + dim ** -0.5 * 2.0 ** -21 * most[..., 0] * (small @ k.T).max(-1)
+                seen = np.isfinite(rl)
+                assert np.all(np.abs(lse[r][seen] - rl[seen]) <= 2.0 ** -16 + score[seen]), (channel, e, r)
+                tol = (1.01 * 2.0 ** -8 * np.abs(ro) + (2.0 ** -11 + 2.0 ** -15 + 2 * np.expm1(score)[..., None]) * absum
+                       + 2.0 ** -25 * n * top[..., None] + 1e-37)
+                assert np.all(np.abs(o[r] - ro) <= tol), (channel, e, r)
