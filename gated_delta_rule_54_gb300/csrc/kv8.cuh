@@ -108,14 +108,22 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// maximum that is NaN where an operand is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
 // A power of two that brings a row of q with this largest magnitude to [2^E, 2^(E+1)),
-// and its inverse.  (In fp16 with E = 8 a row's small elements keep at least 33 bits
-// below its largest.)
+// and its inverse.  Where that is an infinity the power is 0, which makes a NaN of it, and
+// of every score of the row (8 bits hold no infinity).  (In fp16 with E = 8 a row's
+// small elements keep at least 33 bits below its largest.)
 template <int E>
 __device__ __forceinline__ void kv8_q_factor(float most, float& to, float& back) {
   int e = (int)(__float_as_uint(most) >> 23) - 127;
   e = e < -100 ? -100 : e > 120 ? 120 : e;
-  to = __uint_as_float((uint32_t)(E - e + 127) << 23);
+  to = most <= 3.402823466e38f ? __uint_as_float((uint32_t)(E - e + 127) << 23) : 0.f;
   back = __uint_as_float((uint32_t)(e - E + 127) << 23);
 }
 
@@ -150,6 +158,15 @@ __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The scales of a block as the kernels take them: K's, and log2 of V's.  Where one of the
+// two is no number in [0, inf) K's is NaN, so that the scores, and what comes of them, are
+// NaN for the queries that see a key of the block, and for no others.
+__device__ __forceinline__ float2 kv8_scales(float ks, float vs) {
+  const float top = 3.402823466e38f;
+  if (!(ks >= 0.f && ks <= top && vs >= 0.f && vs <= top)) return make_float2(__int_as_float(0x7fffffff), -INFINITY);
+  return make_float2(ks, lg2_approx(vs));
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,

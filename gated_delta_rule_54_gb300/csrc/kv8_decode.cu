@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         w_id = -1;
       } else {
         const int64_t tile = (int64_t)w_id * p.heads + w_h;
-        w_ks = p.scales[tile];
-        w_lv = lg2_approx(p.scales[tile + p.pages * p.heads]);
+        const float2 sc = kv8_scales(p.scales[tile], p.scales[tile + p.pages * p.heads]);
+        w_ks = sc.x, w_lv = sc.y;
       }
     }
     const int from = first - w_base;
@@ -498,10 +498,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       float l = lsum[e];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      lse2[e] = l > 0.f ? m[e] + log2f(l) : -INFINITY;
+      // l is 0 where no key is seen, and NaN where a score is
+      lse2[e] = l == 0.f ? -INFINITY : m[e] + log2f(l);
       // mv is -inf where every V scale seen is 0
-      const float fac = l > 0.f && mv[e] > -INFINITY
-                            ? ex2_approx_f(mv[e] - m[e] + kKv8Shift<MODE>) / l : 0.f;
+      const float fac = l == 0.f ? 0.f
+                        : mv[e] > -INFINITY ? ex2_approx_f(mv[e] - m[e] + kKv8Shift<MODE>) / l : 0.f * l;
 #pragma unroll
       for (int i = 0; i < NT; ++i) oacc[i][2 * e] *= fac, oacc[i][2 * e + 1] *= fac;
     }
@@ -599,10 +600,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const int i = at / (DIM / 4), d = at % (DIM / 4) * 4;
       float top = -INFINITY;
       for (int w = w0; w <= last; ++w)
-        if (s_u0[w] == u0) top = fmaxf(top, s_lse[w][i]);
+        if (s_u0[w] == u0) top = max_nan(top, s_lse[w][i]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-      if (top > -INFINITY) {
+      if (top != -INFINITY) {
         for (int w = w0; w <= last; ++w) {
           if (s_u0[w] != u0) continue;
           const float c = ex2_approx_f(s_lse[w][i] - top);
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const float inv = 1.f / l;
         o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
       }
-      const float lse2 = top > -INFINITY ? top + log2f(l) : -INFINITY;
+      const float lse2 = top != -INFINITY ? top + log2f(l) : -INFINITY;
       if (whole) {
         const int64_t to = out_row<DIM>(p, f, s_h[w0], i);
         *reinterpret_cast<uint2*>(p.o + to * DIM + d) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
@@ -629,7 +630,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 // Joins the parts of a segment that several CTAs hold, in order of the shares.  A
-// CTA does some output rows of one segment; with few parts a warp does a whole
+// CTA does some output rows of one segment (a part whose log-sum-exp is NaN makes the
+// output NaN); with few parts a warp does a whole
 // row, with many the warps take parts and their sums are added in warp order.
 template <int DIM>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ DecodeArgs a, int grid) {
@@ -698,20 +700,20 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   };
   auto finish = [&](int i, float4 o, float top, float l) {
     const int64_t to = out_row<DIM>(p, sp, h, i);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane < DIM / 4)
       *reinterpret_cast<uint2*>(p.o + to * DIM + 4 * lane) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[to] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && lane == 0) p.lse[to] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
   };
   if (entries <= kFew) {
     for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
       const float mine = lane < entries ? lse_of(lane, i) : -INFINITY;
       float top = mine;
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-      if (top > -INFINITY)
+      if (top != -INFINITY)
         for (int k = 0; k < entries; ++k) {
           if (s_at[k] < 0) continue;
           const float c = ex2_approx_f(__shfl_sync(0xffffffffu, mine, k) - top);
@@ -725,15 +727,15 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ D
   for (int i = blockIdx.y; i < rows; i += gridDim.y) {
     float top = tid < entries ? lse_of(tid, i) : -INFINITY;
     const float mine = top;
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
     __syncthreads();
     if (lane == 0) red[warp] = top;
     __syncthreads();
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+    for (int w = 0; w < 8; ++w) top = max_nan(top, red[w]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     __syncthreads();
-    if (tid < entries) s_w[tid] = s_at[tid] >= 0 && top > -INFINITY ? ex2_approx_f(mine - top) : 0.f;
+    if (tid < entries) s_w[tid] = s_at[tid] >= 0 && top != -INFINITY ? ex2_approx_f(mine - top) : 0.f;
     __syncthreads();
     // four parts at a time, so that their loads are in flight together
     for (int k0 = warp; k0 < entries; k0 += 32) {

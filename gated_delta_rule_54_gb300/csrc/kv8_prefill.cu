@@ -411,10 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           // (the chains took all but the last two)
           top[0] = max3(top[0], v[(c * BK + BK - 2) / 32][(c * BK + BK - 2) % 32], v[(c * BK + BK - 1) / 32][(c * BK + BK - 1) % 32]);
           const float2 sc = meta[slot][half * HC + c];
-          // (a factor of 0 would make -inf of a masked key a NaN)
-          fac[c] = fmaxf(rowfac * sc.x, 1e-30f);
+          const float most = fmaxf(top[0], top[1]);
+          fac[c] = rowfac * sc.x;
+          fac[c] = fac[c] < 1e-30f ? 1e-30f : fac[c];
           off[c] = sc.y;
-          const float x = fmaxf(top[0], top[1]) * fac[c];
+          const float x = most * fac[c];
+          // (a factor of 0, or of NaN where the row sees nothing of the block, would make
+          // -inf of a masked key a NaN)
+          if (most == -INFINITY) fac[c] = 1e-30f;
           nm = fmaxf(nm, x);
           nv = fmaxf(nv, x + sc.y);
         }
@@ -481,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           ok = ok && __all_sync(0xffffffffu, wait(&odone[t], outs & 1));
           tc_fence_after();
         }
-        const float fac = l > 0.f && mv > -INFINITY ? ex2_approx_f(mv - mx + kKv8Shift<MODE>) / l : 0.f;
-        const float lse2 = l > 0.f ? mx + log2f(l) : -INFINITY;
+        // l is 0 where no key is seen, and NaN where a score is
+        const float fac = l == 0.f ? 0.f : mv > -INFINITY ? ex2_approx_f(mv - mx + kKv8Shift<MODE>) / l : 0.f * l;
+        const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
         const int64_t at = (m.sp.base + qi) * (p.heads * p.group) + m.h * p.group + (m.row0 + i_row) % p.group;
         float* part = a.ws + ((int64_t)it * kRows + i_row) * (DIM + 4);
         if (ok) {
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           ok = ok && __all_sync(0xffffffffu, wait(kv ? &vfree[b] : &kfree[b], ((tile >> 1) & 1) ^ 1));
           if (!ok) break;
           if (kv == 0) {
-            if (lane < CH) meta[tile & 3][lane] = make_float2(ks, there ? lg2_approx(vs) : -INFINITY);
+            if (lane < CH) meta[tile & 3][lane] = there ? kv8_scales(ks, vs) : make_float2(0.f, -INFINITY);
             if (lane == 0) valid[tile & 3] = (int)bits;
           }
           __syncwarp();
@@ -764,10 +769,10 @@ __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const __grid_cons
   const float* part = a.ws + (x * a.splits * kRows + i) * (DIM + 4);
   constexpr int64_t step = (int64_t)kRows * (DIM + 4);
   float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, part[s * step + DIM]);
+  for (int s = 0; s < a.splits; ++s) top = max_nan(top, part[s * step + DIM]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  for (int s = 0; s < a.splits && top > -INFINITY; ++s) {
+  for (int s = 0; s < a.splits && top != -INFINITY; ++s) {
     const float c = ex2_approx_f(part[s * step + DIM] - top);
     l += c;
     if (lane < DIM / 4) {
@@ -775,12 +780,12 @@ __global__ void __launch_bounds__(256) kv8_prefill_join_kernel(const __grid_cons
       o.x = fmaf(c, v.x, o.x), o.y = fmaf(c, v.y, o.y), o.z = fmaf(c, v.z, o.z), o.w = fmaf(c, v.w, o.w);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t at = (sp.base + row / p.group) * (p.heads * p.group) + h * p.group + row % p.group;
   if (lane < DIM / 4)
     *reinterpret_cast<uint2*>(p.o + at * DIM + 4 * lane) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (p.lse && lane == 0) p.lse[at] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 int64_t blocks_of(const Kv8Params& p) {

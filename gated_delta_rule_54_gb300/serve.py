@@ -150,7 +150,7 @@ def kv8_append(k, v, codes, scales, table, start, cu_seqlens=None, max_seqlen=No
     int32 [rows + 1] (``max_seqlen``: an upper bound of a row's tokens); any strides that are
     multiples of 8, last dim contiguous.  codes, scales: one layer's cache.  A page's scale is
     max |x| / 448 (E4M3) or / 127 (INT8) over its tokens so far; where a new token raises it,
-    the page's older codes are rounded again."""
+    the page's older codes are rounded again.  A NaN or an infinity in a token makes the scale one."""
     p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, 1, 0)
     st = _fns().gdn_kv8_append(p, k.data_ptr(), v.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                table.data_ptr(), start.data_ptr(), _raw_stream(codes.get_device()))
@@ -169,7 +169,8 @@ def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=
     the last of its lengths[r] tokens, which are all in the cache; a query sees the keys up to
     its own position (``causal``), and with ``window`` > 0 only the last ``window`` of them.
     scale defaults to dim ** -0.5.  Returns o bf16 like q and, with ``need_lse``, the log of
-    the sum of exponentials f32 [..., query heads]; a query that sees nothing gets 0 and -inf."""
+    the sum of exponentials f32 [..., query heads]; a query that sees nothing gets 0 and -inf, and
+    one that is not finite or sees a key of a block whose scale is not gets NaN in both."""
     p = _problem(q, None, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode,
                  codes.shape[-1] ** -0.5 if scale is None else scale, 1 if causal else 0, window)
     dev = codes.get_device()

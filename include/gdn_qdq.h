@@ -480,12 +480,13 @@ gdn_status gdn_kv8_validate(const gdn_kv8_problem* p);
  * Append: row r's new tokens take positions start[r] .. start[r] + n_r - 1
  * (n_r = tokens, or cu[r + 1] - cu[r]).  Per touched (page, head), x the new
  * tokens in it and the slots before them old:
- *   s_old = scale if there are old slots, else 0;   a = max |x|
+ *   s_old = scale if there are old slots, else 0;   a = max |x|, NaN if one is
  *   s = max(s_old, fl(a / M));  r = fl(1 / s)   (r infinite: s = r = 0)
  *   code(new) = rne(fl(x r));  if s > s_old: code(old) = rne(fl(fl(code s_old) r))
  * so a block keeps one scale while it fills; the old codes are rounded again
- * only when a larger token arrives.  A page written here must belong to one
- * row only (gdn_kv8_fork keeps it so).
+ * only when a larger token arrives.  A NaN or an infinity makes the block's scale
+ * NaN or infinite while the page fills, and its codes mean nothing.  A page
+ * written here must belong to one row only (gdn_kv8_fork keeps it so).
  *   k, v  bf16 [rows, tokens, heads, dim] or packed [total, heads, dim], strided
  *   start i32 [rows]    table i32 [rows, cols]    codes, scales: one layer's
  */
@@ -501,12 +502,15 @@ gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v
  * head h / group.
  *   o   = sum_j softmax_j(scale q . K_j) V_j        bf16
  *   lse = log sum_j exp(scale q . K_j)              f32 (or NULL)
- * A query that sees no key (also: t < 0) has o = 0 and lse = -inf.  Sums and
- * softmax statistics are fp32.  Fewer bits: probabilities enter the V product in
- * fp16 (11 bits, and 2^-25 of a query's largest below 2^-14 of it).  q enters exactly but
- * for elements far below the largest |element| of their (query, head): with E4M3 codes
- * those below 2^-13 of it are off by at most 2^-21 of it, with INT8 codes those below
- * 2^-25 by at most 2^-33.
+ * A query that sees no key (also: t < 0) has o = 0 and lse = -inf.  One that has
+ * an element that is not finite and sees a key, or that sees a key of a block
+ * whose K or V scale is no number in [0, inf), has o = NaN and lse = NaN; the
+ * others are not affected.  Sums and softmax statistics are fp32.  Fewer bits:
+ * probabilities enter the V product in fp16 (11 bits, and 2^-25 of a query's
+ * largest below 2^-14 of it).  q enters exactly but for elements far below the
+ * largest |element| of their (query, head): with E4M3 codes those below 2^-13 of
+ * it are off by at most 2^-21 of it, with INT8 codes those below 2^-25 by at
+ * most 2^-33.
  *   q   bf16 [rows, tokens, heads * group, dim] or packed [total, ...], strided
  *   o   bf16 [total, heads * group, dim] contiguous,  lse f32 [total, heads * group]
  *   workspace  gdn_kv8_workspace_bytes(p) bytes, 256-byte aligned

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import kv8_attention, kv8_pool
+from gated_delta_rule_54_gb300 import kv8_append, kv8_attention, kv8_pool, load
 from oracle import serve as ref
 from test_gpu_kv8 import _check, _cuda, _pool, _table
 
@@ -108,3 +108,118 @@ def test_q_with_a_large_channel(mode, dim, page, tokens, group):
                 tol = (1.01 * 2.0 ** -8 * np.abs(ro) + (2.0 ** -11 + 2.0 ** -15 + 2 * np.expm1(score)[..., None]) * absum
                        + 2.0 ** -25 * n * top[..., None] + 1e-37)
                 assert np.all(np.abs(o[r] - ro) <= tol), (channel, e, r)
+
+
+# ---- numbers that are none ------------------------------------------------
+def _positions(length, tokens, window):
+    """[tokens, length]: which key each query sees."""
+    pos = length - tokens + np.arange(tokens)[:, None]
+    j = np.arange(length)[None]
+    return (j <= pos) & ((j > pos - window) if window else True)
+
+
+BAD = [
+    # lengths, tokens, heads, group, dim, page, mode, window
+    ([100, 64, 130], 1, 2, 2, 128, 64, "e4m3", 0),
+    ([100, 64, 130], 1, 2, 2, 64, 16, "int8", 40),
+    ([150, 70], 6, 2, 2, 128, 16, "e4m3", 30),
+    ([150, 70], 6, 2, 2, 64, 32, "int8", 0),
+    ([9000, 6000], 1, 2, 4, 128, 64, "int8", 0),      # a line of tiles: parts are joined
+    ([9000, 6000], 1, 2, 16, 64, 128, "e4m3", 3000),
+    ([200, 130], 130, 2, 1, 128, 16, "e4m3", 0),
+    ([200, 130], 130, 2, 1, 64, 64, "int8", 50),
+    ([3000, 2500], 20, 2, 2, 128, 128, "int8", 0),    # few blocks: the keys are split
+    ([3000, 2500], 20, 2, 2, 64, 32, "e4m3", 700),
+]
+
+
+@pytest.mark.parametrize("case", range(len(BAD)))
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_blocks_that_are_no_numbers(case, what):
+    """A query that sees a key of a block whose K or V scale is not finite gets NaN; nobody else does."""
+    lengths, tokens, heads, group, dim, page, mode, window = BAD[case]
+    rng = np.random.default_rng(40 + case)
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, heads, page, dim, mode)
+    table = _table(rng, lengths, page, pages)
+    poisoned, hit = scales.copy(), []
+    for r, n in enumerate(lengths):                    # a block near the end of head r % heads
+        c = max(0, -(-n // page) - 2)
+        poisoned[(r + case) % 2, table[r, c], r % heads] = what
+        hit.append((c * page, (c + 1) * page))
+    q = _q(rng, len(lengths), tokens, heads * group, dim)
+    args = dict(mode=mode, window=window, need_lse=True)
+    o, lse = kv8_attention(q, *_cuda(codes, poisoned, table, np.array(lengths, np.int32)), **args)
+    clean = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), **args)
+    for r, n in enumerate(lengths):
+        sees = torch.from_numpy(_positions(n, tokens, window)[:, hit[r][0]:hit[r][1]].any(1)).cuda()
+        of = slice(r % heads * group, (r % heads + 1) * group)
+        for x, y in zip((o[r], lse[r]), (clean[0][r], clean[1][r])):
+            assert torch.all(torch.isnan(x[sees][:, of]))
+            y = y.clone()
+            bad = torch.zeros_like(y, dtype=torch.bool)
+            bad[:, of] = sees.view(-1, 1, *[1] * (y.dim() - 2))
+            assert torch.allclose(x[~bad].float(), y[~bad].float(), rtol=2.0 ** -7, atol=1e-3)
+            assert not torch.any(torch.isnan(x[~bad]))
+    assert load().gdn_device_error(0) == 0
+
+
+@pytest.mark.parametrize("case", range(len(BAD)))
+def test_queries_that_are_no_numbers(case):
+    lengths, tokens, heads, group, dim, page, mode, window = BAD[case]
+    rng = np.random.default_rng(60 + case)
+    lengths = lengths + [0]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, heads, page, dim, mode)
+    table = _table(rng, lengths, page, pages)
+    q = _q(rng, len(lengths), tokens, heads * group, dim)
+    args = (*_cuda(codes, scales, table, np.array(lengths, np.int32)),)
+    clean = kv8_attention(q, *args, mode=mode, window=window, need_lse=True)
+    bad = torch.zeros(q.shape[:-1], dtype=torch.bool, device="cuda")
+    for r in range(len(lengths)):
+        for i, what in enumerate((float("nan"), float("inf"), float("-inf"))):
+            t, h = (7 * r + 3 * i) % tokens, (r + i) % (heads * group)
+            q[r, t, h, (11 * r + i) % dim] = what
+            bad[r, t, h] = True
+    o, lse = kv8_attention(q, *args, mode=mode, window=window, need_lse=True)
+    none = torch.isneginf(clean[1])
+    assert torch.all(torch.isnan(o[bad & ~none])) and torch.all(torch.isnan(lse[bad & ~none]))
+    assert torch.all(o[none] == 0) and torch.all(torch.isneginf(lse[none]))
+    assert torch.equal(o[~bad], clean[0][~bad]) and torch.equal(lse[~bad], clean[1][~bad])
+
+
+@pytest.mark.parametrize("mode", ["e4m3", "int8"])
+@pytest.mark.parametrize("tokens", [1, 50])
+def test_append_of_what_is_no_number(mode, tokens):
+    """A NaN among a block's tokens makes its scale NaN, an infinity makes it infinite, for good; other blocks are
+    as ever."""
+    rng = np.random.default_rng(70)
+    heads, dim, page, rows = 3, 64, 16, 2
+    codes, scales = np.zeros((2, 16, heads, page, dim), np.uint8), np.zeros((2, 16, heads), np.float32)
+    table = np.arange(16, dtype=np.int32).reshape(2, 8)
+    c, s, t = _cuda(codes, scales, table)
+    bad = np.zeros(scales.shape, bool)
+    for step in range(3):
+        x = rng.standard_normal((2, rows, tokens, heads, dim)).astype(np.float32)
+        x = torch.from_numpy(x).to(torch.bfloat16)
+        clean = x.float().numpy()
+        if step == 1:                                  # position 3 or so of the first, or a whole block
+            x[0, 0, 0, 1, 7], x[1, 1, tokens // 2, 2, 0], x[0, 1, 0, 0, 3] = float("nan"), float("inf"), float("-inf")
+        start = np.full(rows, step * tokens, np.int32)
+        kv8_append(x[0].cuda(), x[1].cuda(), c, s, t, _cuda(start)[0], mode=mode)
+        ref.append(clean[0], clean[1], codes, scales, table, start, [tokens] * rows, mode)
+        if step == 0:
+            continue
+        got = s.cpu().numpy()
+        b0, b1 = (tokens * 1) // page, (tokens + tokens // 2) // page
+        want = {(0, table[0, b0], 1): np.nan, (1, table[1, b1], 2): np.inf, (0, table[1, b0], 0): np.inf}
+        for at, v in want.items():
+            assert np.isnan(got[at]) if np.isnan(v) else got[at] == v
+            bad[at] = True
+        assert np.array_equal(got[~bad], scales[~bad])
+        assert np.array_equal(c.cpu().numpy()[~bad], codes[~bad])
+    n = np.full(rows, 3 * tokens, np.int32)
+    q = _q(rng, rows, 1, heads, dim)
+    o, lse = kv8_attention(q, c, s, t, _cuda(n)[0], mode=mode, need_lse=True)
+    lost = torch.tensor([[False, True, False], [True, False, True]], device="cuda")
+    assert torch.equal(torch.isnan(lse[:, 0]), lost) and torch.equal(torch.isnan(o[:, 0]).all(-1), lost)
