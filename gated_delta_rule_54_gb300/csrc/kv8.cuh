@@ -33,17 +33,19 @@ __device__ __forceinline__ int kv8_clamp(int64_t x, int64_t lo, int64_t hi) {
 }
 
 // First packed token and token count of row r (at most p.tokens; offsets that
-// run backwards count as none).
-__device__ __forceinline__ void kv8_row(const Kv8Params& p, int64_t r, int64_t& base, int& n) {
+// run backwards count as none).  False where a packed row has more tokens than that, or
+// lies outside of the call's.
+__device__ __forceinline__ bool kv8_row(const Kv8Params& p, int64_t r, int64_t& base, int& n) {
   if (p.cu) {
     base = p.cu[r];
     const int64_t end = p.cu[r + 1];
     n = kv8_clamp(end - base, 0, p.tokens);
     if (base < 0 || base + n > p.total) n = 0;
-  } else {
-    base = r * p.tokens;
-    n = p.tokens;
+    return end - base <= n;
   }
+  base = r * p.tokens;
+  n = p.tokens;
+  return true;
 }
 
 // Element offset of token i (of its row's n) of row r, head h in x or v.
@@ -54,7 +56,7 @@ __device__ __forceinline__ int64_t kv8_at(const Kv8Params& p, int64_t r, int64_t
 
 __device__ __forceinline__ Kv8Span kv8_span(const Kv8Params& p, int64_t r) {
   Kv8Span s;
-  kv8_row(p, r, s.base, s.n);
+  if (!kv8_row(p, r, s.base, s.n)) s.n = 0;
   s.len = p.lengths[r];
   const int64_t first = (int64_t)s.len - s.n;  // position of the first query
   s.end = kv8_clamp(s.len, 0, (int64_t)p.cols * p.page);
@@ -69,6 +71,32 @@ __device__ __forceinline__ void kv8_seen(const Kv8Params& p, const Kv8Span& s, i
   const int64_t pos = (int64_t)s.len - s.n + i;
   end = p.causal ? kv8_clamp(pos + 1, 0, s.end) : pos < 0 ? 0 : s.end;
   begin = p.window > 0 ? kv8_clamp(pos - p.window + 1, 0, s.end) : 0;
+}
+
+// Packed calls: outputs that no row computes, written by warp w of all.  Tokens before the
+// first row and after the last one belong to no query: 0 and -inf.  A row that breaks the
+// call's bound (kv8_row) gets NaN.
+template <int DIM>
+__device__ __forceinline__ void kv8_fill(const Kv8Params& p, int64_t w, int64_t all, int lane) {
+  const int64_t width = p.heads * p.group;
+  auto fill = [&](int64_t t0, int64_t t1, uint32_t pair, float lse) {
+    t0 = t0 < 0 ? 0 : t0, t1 = t1 > p.total ? p.total : t1;
+    for (int64_t i = t0 * width + w; i < t1 * width; i += all) {
+      if (lane < DIM / 8) reinterpret_cast<uint4*>(p.o + i * DIM)[lane] = make_uint4(pair, pair, pair, pair);
+      if (p.lse && lane == 0) p.lse[i] = lse;
+    }
+  };
+  fill(0, p.cu[0], 0u, -INFINITY);
+  fill(p.cu[p.rows], p.total, 0u, -INFINITY);
+  for (int64_t r0 = 0; r0 < p.rows; r0 += 32) {
+    int64_t base;
+    int n;
+    unsigned over = __ballot_sync(0xffffffffu, r0 + lane < p.rows && !kv8_row(p, r0 + lane, base, n));
+    for (; over; over &= over - 1) {
+      const int64_t r = r0 + __ffs(over) - 1;
+      fill(p.cu[r], p.cu[r + 1], 0x7fff7fffu, __int_as_float(0x7fffffff));
+    }
+  }
 }
 
 // Code bytes to fp16 pairs: of the bytes b0 b1 b2 b3 of w, even = (b0, b2) and

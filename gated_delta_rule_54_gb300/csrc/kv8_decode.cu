@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   int64_t issued = lo;
   Cursor cc = pc;  // the consumer's place
   for (int i = 0; i < S && issued < hi; ++i, ++issued) issue(i);
+  if (p.cu) kv8_fill<DIM>(p, (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps, lane);
 
   // ---- segments ----
   bool bad = false;
@@ -831,7 +832,8 @@ gdn_status run(DecodeArgs& a, cudaStream_t st) {
   // rows of a segment in one CTA, unless the segments leave SMs idle
   const int64_t segments = p.rows * p.heads, rows = (int64_t)p.tokens * p.group;
   int64_t y = 304 / segments;
-  y = y < 1 ? 1 : y < rows ? y : rows;
+  y = y < rows ? y : rows;
+  y = y < 1 ? 1 : y;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)segments, (unsigned)y);
   cfg.blockDim = dim3(256);

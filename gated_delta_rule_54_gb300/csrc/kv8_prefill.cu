@@ -746,6 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
     }
     if (outs[0] > 0) wait(&odone[0], (outs[0] - 1) & 1);
     if (outs[1] > 0) wait(&odone[1], (outs[1] - 1) & 1);
+  } else if (warp > kIssuer + 1 && p.cu) {
+    constexpr int kIdle = kThreads / 32 - kIssuer - 2;  // warps without another role
+    kv8_fill<DIM>(p, (int64_t)blockIdx.x * kIdle + warp - kIssuer - 2, (int64_t)gridDim.x * kIdle, lane);
   }
   tc_fence_before();
   __syncthreads();

@@ -147,7 +147,8 @@ def kv8_append(k, v, codes, scales, table, start, cu_seqlens=None, max_seqlen=No
     """New tokens go to the cache, in place: row r's at positions start[r] onwards.
 
     k, v bf16 [rows, tokens, heads, dim], or packed [total, heads, dim] with ``cu_seqlens``
-    int32 [rows + 1] (``max_seqlen``: an upper bound of a row's tokens); any strides that are
+    int32 [rows + 1] (``max_seqlen``: an upper bound of a row's tokens, further ones are not
+    written; without it the call is laid out for one row with all of them); any strides that are
     multiples of 8, last dim contiguous.  codes, scales: one layer's cache.  A page's scale is
     max |x| / 448 (E4M3) or / 127 (INT8) over its tokens so far; where a new token raises it,
     the page's older codes are rounded again.  A NaN or an infinity in a token makes the scale one."""
@@ -165,7 +166,9 @@ def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=
     h // (query heads / heads).
 
     q bf16 [rows, tokens, query heads, dim], or packed [total, query heads, dim] with
-    ``cu_seqlens`` (``max_seqlen``: an upper bound of a row's tokens).  Row r's queries are
+    ``cu_seqlens`` (``max_seqlen``: an upper bound of a row's tokens, which a row with more gets
+    NaN for; without it the call is laid out for one row with all of them, which costs time, most
+    where rows have few).  Tokens of no row get 0 and -inf.  Row r's queries are
     the last of its lengths[r] tokens, which are all in the cache; a query sees the keys up to
     its own position (``causal``), and with ``window`` > 0 only the last ``window`` of them.
     scale defaults to dim ** -0.5.  Returns o bf16 like q and, with ``need_lse``, the log of

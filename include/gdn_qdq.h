@@ -486,7 +486,8 @@ gdn_status gdn_kv8_validate(const gdn_kv8_problem* p);
  * so a block keeps one scale while it fills; the old codes are rounded again
  * only when a larger token arrives.  A NaN or an infinity makes the block's scale
  * NaN or infinite while the page fills, and its codes mean nothing.  A page
- * written here must belong to one row only (gdn_kv8_fork keeps it so).
+ * written here must belong to one row only (gdn_kv8_fork keeps it so).  Of a packed
+ * row with more than `tokens` tokens only the first `tokens` are taken.
  *   k, v  bf16 [rows, tokens, heads, dim] or packed [total, heads, dim], strided
  *   start i32 [rows]    table i32 [rows, cols]    codes, scales: one layer's
  */
@@ -505,7 +506,9 @@ gdn_status gdn_kv8_append(const gdn_kv8_problem* p, const void* k, const void* v
  * A query that sees no key (also: t < 0) has o = 0 and lse = -inf.  One that has
  * an element that is not finite and sees a key, or that sees a key of a block
  * whose K or V scale is no number in [0, inf), has o = NaN and lse = NaN; the
- * others are not affected.  Sums and softmax statistics are fp32.  Fewer bits:
+ * others are not affected.  In a packed call tokens of no row (before cu[0], from
+ * cu[rows] on) have o = 0 and lse = -inf, and a row with more than `tokens` tokens
+ * has NaN in both.  Sums and softmax statistics are fp32.  Fewer bits:
  * probabilities enter the V product in fp16 (11 bits, and 2^-25 of a query's
  * largest below 2^-14 of it).  q enters exactly but for elements far below the
  * largest |element| of their (query, head): with E4M3 codes those below 2^-13 of

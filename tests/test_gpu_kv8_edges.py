@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import kv8_append, kv8_attention, kv8_pool, load
+from gated_delta_rule_54_gb300 import GdnError, kv8_append, kv8_attention, kv8_pool, load
 from oracle import serve as ref
 from test_gpu_kv8 import _check, _cuda, _pool, _table
 
@@ -223,3 +223,65 @@ def test_append_of_what_is_no_number(mode, tokens):
     o, lse = kv8_attention(q, c, s, t, _cuda(n)[0], mode=mode, need_lse=True)
     lost = torch.tensor([[False, True, False], [True, False, True]], device="cuda")
     assert torch.equal(torch.isnan(lse[:, 0]), lost) and torch.equal(torch.isnan(o[:, 0]).all(-1), lost)
+
+
+# ---- packed calls: tokens of no row, and rows above the bound -------------
+@pytest.mark.parametrize("most,group", [(3, 2), (60, 2)])
+def test_packed_tokens_of_no_row(most, group):
+    rng = np.random.default_rng(80)
+    heads, dim, page, mode = 2, 64, 16, "e4m3"
+    counts, lengths = [most, 0, 1, most], [90, 20, 0, 75]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, heads, page, dim, mode)
+    table = _table(rng, lengths, page, pages)
+    starts = 5 + np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    total = int(starts[-1]) + 40
+    q = torch.from_numpy(rng.standard_normal((total, heads * group, dim))).to(torch.bfloat16).cuda()
+    out = torch.full_like(q, 7.0)
+    filler = torch.full((total, heads * group), 9.0, device="cuda")
+    del filler                                         # (the next tensor of this size finds the 9s)
+    o, lse = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), mode=mode, need_lse=True, out=out,
+                           cu_seqlens=torch.from_numpy(starts).cuda(), max_seqlen=most)
+    _check((o, lse), q.float().cpu().numpy(), codes, scales, table, lengths, mode, dim ** -0.5, starts)
+    for part in (slice(0, 5), slice(int(starts[-1]), total)):
+        assert torch.all(o[part] == 0) and torch.all(torch.isneginf(lse[part]))
+
+
+@pytest.mark.parametrize("most,group", [(3, 2), (60, 2)])
+def test_packed_rows_above_the_bound(most, group):
+    """max_seqlen is a promise; a row that breaks it gets NaN, not an uninitialised rest."""
+    rng = np.random.default_rng(81)
+    heads, dim, page, mode = 2, 64, 16, "int8"
+    counts, lengths = [most, most + 2, 1], [90, 100, 30]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, heads, page, dim, mode)
+    table = _table(rng, lengths, page, pages)
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((int(starts[-1]), heads * group, dim))).to(torch.bfloat16).cuda()
+    out = torch.full_like(q, 7.0)
+    o, lse = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), mode=mode, need_lse=True, out=out,
+                           cu_seqlens=torch.from_numpy(starts).cuda(), max_seqlen=most)
+    over = slice(int(starts[1]), int(starts[2]))
+    assert torch.all(torch.isnan(o[over])) and torch.all(torch.isnan(lse[over]))
+    for r in (0, 2):
+        sl = slice(int(starts[r]), int(starts[r + 1]))
+        _check((o[sl], lse[sl]), q[sl].float().cpu().numpy(), codes, scales, table[r:r + 1], [lengths[r]], mode, dim ** -0.5,
+               np.array([0, counts[r]]))
+
+
+@pytest.mark.parametrize("most,length", [(0, 40), (0, 40000), (-1, 40)])
+def test_packed_bounds_without_a_token(most, length):
+    """A bound of 0 leaves rows with tokens above it; below 0 it is none."""
+    codes, scales = kv8_pool(1, 4, 1, 64, page=16)
+    table = torch.zeros(2, -(-length // 16), dtype=torch.int32, device="cuda")
+    lengths = torch.full((2,), length, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    q = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    call = lambda: kv8_attention(q, codes[0], scales[0], table, lengths, cu_seqlens=cu, max_seqlen=most, need_lse=True)
+    if most < 0:
+        with pytest.raises(GdnError):
+            call()
+        return
+    o, lse = call()
+    assert torch.all(torch.isnan(o[:3])) and torch.all(torch.isnan(lse[:3]))
+    assert torch.all(o[3:] == 0) and torch.all(torch.isneginf(lse[3:]))
