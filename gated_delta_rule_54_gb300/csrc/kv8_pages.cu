@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
   // lengths, the parents (fork) or the extra tokens (reserve).
   extern __shared__ int s_rows[];
   int *s_a = s_rows, *s_b = s_a + p.rows, *s_len = s_b + p.rows, *s_par = s_len + p.rows;
-  __shared__ int s_total, s_over;
+  __shared__ int64_t s_total, s_over;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int gtid = (int)cl.block_rank() * kPlanThreads + tid, gwarp = gtid / 32;
   const int rows = (int)p.rows;
@@ -185,30 +185,30 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
       return min(need(r), p.cols) - min(pages_of(s_len[r], p.page), p.cols);
     }
   };
-  // a scan by one warp of each CTA; sums stop at 2^30, above any number of pages
+  // a scan by one warp of each CTA, in 64 bits: 4096 rows may want up to 2^27 pages each.  A
+  // row's place in it stops at 2^30, as many as a pool can have
   __syncthreads();  // the children have been read
   if (warp == 0) {
-    int run = 0, over = 0;
+    int64_t run = 0, over = 0;
     for (int r0 = 0; r0 < rows; r0 += 32) {
       const int r = r0 + lane;
-      const int w = r < rows ? min(wanted(r), 1 << 25) : 0;
-      int x = w;
+      const int64_t w = r < rows ? wanted(r) : 0;
+      int64_t x = w;
       for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
       }
-      if (r < rows) s_a[r] = min(run + x - w, 1 << 30);
-      run = min(run + __shfl_sync(0xffffffffu, x, 31), 1 << 30);
-      if constexpr (OP == kReserve) {
-        const int fit = max(p.cols, r < rows ? pages_of(s_len[r], p.page) : 0);
-        const int o = r < rows ? min(max(need(r) - fit, 0), 1 << 25) : 0;
-        over = min(over + warp_sum(o), 1 << 30);
-      }
+      if (r < rows) s_a[r] = (int)min(run + x - w, (int64_t)1 << 30);
+      run += __shfl_sync(0xffffffffu, x, 31);
+      if constexpr (OP == kReserve)
+        if (r < rows) over += max(need(r) - max(p.cols, pages_of(s_len[r], p.page)), 0);
     }
+    if constexpr (OP == kReserve)
+      for (int d = 16; d; d >>= 1) over += __shfl_xor_sync(0xffffffffu, over, d);
     if (lane == 0) s_total = run, s_over = over;
   }
   cl.sync();  // counts settled, wanted pages known
-  const int total = s_total;
+  const int64_t total = s_total;
   // ---- the lowest free pages --------------------------------------------
   int free_ = 0;
   if (total > 0)
@@ -224,9 +224,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPlanThreads)
       rank += __popc(mask);
     }
   cl.sync();
-  const int have = all < total ? all : total;
+  const int have = all < total ? all : (int)total;
   for (int i = gtid; i < have; i += kCtas * kPlanThreads) p.refs_out[p.list[i]] = 1;
-  if (gtid == 0) *p.count_out = total - have + s_over, *p.n_moves = OP == kFork ? have : 0;
+  if (gtid == 0) *p.count_out = (int)min(total - have + s_over, (int64_t)0x7fffffff), *p.n_moves = OP == kFork ? have : 0;
   for (int r = gwarp; r < rows; r += kPlanWarps) {
     if constexpr (OP == kFork) {
       const int q = s_par[r], len = q >= 0 ? s_len[q] : 0;

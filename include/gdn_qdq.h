@@ -532,7 +532,7 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
  * arrays (no overlap with the inputs), table entries past a row's pages are -1,
  * and choices are fixed: fresh pages are the lowest free ones, given in row
  * order.  `missing` counts pages that were wanted and not there (their table
- * entries are -1).
+ * entries are -1), up to 2^31 - 1.
  */
 typedef struct {
   int64_t pages;        /* pages of the pool                                     */

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import GdnError, kv8_append, kv8_attention, kv8_pool, load
+from gated_delta_rule_54_gb300 import GdnError, kv8_append, kv8_attention, kv8_pool, kv8_reserve, load
 from oracle import serve as ref
 from test_gpu_kv8 import _check, _cuda, _pool, _table
 
@@ -285,3 +285,15 @@ def test_packed_bounds_without_a_token(most, length):
     o, lse = call()
     assert torch.all(torch.isnan(o[:3])) and torch.all(torch.isnan(lse[:3]))
     assert torch.all(o[3:] == 0) and torch.all(torch.isneginf(lse[3:]))
+
+
+# ---- pages ----------------------------------------------------------------
+def test_reserve_counts_all_that_is_missing():
+    """Rows that want more pages than any pool has are counted in full."""
+    codes, scales = kv8_pool(1, 6, 1, 64, page=16)
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    lengths, refs = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(6, dtype=torch.int32, device="cuda")
+    extra = torch.tensor([1 << 30, 16, 1 << 30], dtype=torch.int32, device="cuda")
+    t, n, r, missing = kv8_reserve(codes, scales, table, lengths, extra, refs)
+    assert t.tolist() == [[0, 1, 2, 3], [4, -1, -1, -1], [5, -1, -1, -1]] and n.tolist() == [64, 16, 64]
+    assert int(missing) == 2 * (1 << 26) + 1 - 6
