@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(1024) beam_join_kernel(const SelectParams p) {
   __shared__ int32_t token[32][32];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;  // one warp per beam
   const int64_t item = blockIdx.x, row = item * p.beams + w;
-  const float before = p.scores[row];
+  const float given = p.scores[row], before = given == given ? given : -INFINITY;
   const bool done = p.finished && p.finished[row];
   grid_dep_wait();
   float sc = -INFINITY;

@@ -584,8 +584,9 @@ gdn_status gdn_kv8_compact(const gdn_kv8_pool* p, uint8_t* codes, float* scales,
  * x its logits and m their maximum; a finished beam has one candidate, itself
  * with token `eos` and its score.  Order: score descending, then beam, then
  * logit descending, then token.  Where there are fewer than K candidates the
- * rest score -inf (token 0, or eos of a finished beam).  NaN logits count as
- * -inf, +inf as the largest finite number.
+ * rest score -inf (token 0, or eos of a finished beam).  NaN logits and scores
+ * count as -inf, +inf logits as the largest finite number.  Outputs do not overlap
+ * the inputs.
  *   logits   bf16 or f32 [batch, beams, vocab], row stride `stride` elements
  *   scores   f32 [batch, beams]      finished u8 [batch, beams] or NULL
  *   out      scores f32, parents i32 (batch * beams + beam: a row index),
