@@ -175,9 +175,10 @@ Kv8Params params_of(const gdn_kv8_problem& p) {
 
 // One 16-row tile holds a row's queries of a K/V head: the kernel that streams the
 // codes, else the one that converts them for tiles of 128 rows.  Measured with
-// 16 query rows, stream / tiles in us: 64 rows x 8 heads x 8192 keys 247/395 (four
-// query rows 179/394); the tiles are a little faster where the calls are small
-// (1 x 8 x 700 keys 13.8/12.6).
+// 16 query rows, stream / tiles in us: 64 rows x 8 heads, 8192 keys each, 128-wide E4M3
+// 245/358, INT8 209/401, 64-wide 164/288 and 155/310 (four query rows, 128-wide: 178/358
+// and 190/401); 1 x 8 x 700 keys 13.9/13.2, 12.7/13.2, 10.1/11.3 and 9.7/11.7.  A full
+// wave of short keys, 16 x 8 x 2048: 25/30, 22/31, 17/24 and 16/24.
 bool few_rows(const gdn_kv8_problem& p) { return (int64_t)p.tokens * p.group <= 16; }
 
 bool off16(std::initializer_list<const void*> ptrs) {

@@ -21,8 +21,8 @@
 // any scales.
 //
 // Measured on a GB300 (kernel alone): 64 rows of 2192 .. 8192 keys, 8 K/V heads of
-// 128, E4M3, 676 MB: 115 us, 5.9 TB/s (copying: 6.8).  2 rows of 101072 and 131071
-// keys, 4 heads, INT8, 260 MB: 54 us.  DRAM is at 73 and 59 %, instruction issue at
+// 128, E4M3, 676 MB: 116 us, 5.8 TB/s (copying: 6.8).  2 rows of 101072 and 131071
+// keys, 4 heads, INT8, 260 MB: 55 us.  DRAM is at 72 and 57 %, instruction issue at
 // half of its slots from two warps per scheduler; the join takes 8 us.
 // The first case with both launches: 12 warps of two tiles (168 registers) took 155 us,
 // 8 warps of three 146 (117 without their products), scores from E4M3 codes as they
@@ -784,16 +784,24 @@ int64_t most_tiles(const Kv8Params& p) {
 // One CTA per segment, or the line of all tiles?  A CTA alone takes 6 us + 0.18 us per
 // tile; the line pays for its shares and a second launch, but
 // leaves no SM idle and no wave half full.  Measured, line / segment in us, 128-wide
-// E4M3 heads:
+// E4M3 heads (INT8 within 8 % of these):
 //     segments     256 keys   1024 keys   2048 keys   4096 keys
+//           2     10.1/7.2   11.9/11.5   13.4/17.5   11.9/29.3
 //           8     10.1/7.0   12.3/11.4   13.4/17.2   12.1/29.1
 //          64     10.9/7.5   18.2/11.7   20.7/17.8   25.4/29.5
 //         152     12.3/7.4   17.2/12.3   23.4/18.6   38.3/33.7
 //         256     17.7/13.4  25.2/22.8   39.7/39.6   59.0/63.4
 //         512     21.8/25.0  40.4/49.7   59.5/76.3   98.9/122
 //        8192      151/357     390/617
+// and 64-wide E4M3 heads (INT8 within 8 %):
+//           2      9.1/6.4   11.3/9.5   12.1/13.5  10.9/21.6
+//          64     10.3/6.6   15.9/9.7   17.5/13.8  20.3/22.2
+//         152     10.9/6.6   14.3/9.7   18.3/13.8  26.8/22.5
+//         256     16.0/11.7  20.9/17.9  27.5/26.3  45.2/47.1
+//         512     18.9/21.8  29.1/34.1  46.0/57.9  73.7/90.9
 // So: one wave up to a length that grows with the SMs it fills, two waves of
-// short segments, and the line for the rest.
+// short segments, and the line for the rest (of the above it misses 5 % once: 64-wide,
+// 256 segments of 2048 keys).
 bool by_segment(const Kv8Params& p) {
   const int64_t segments = p.rows * p.heads, tiles = most_tiles(p);
   return segments <= 152 ? tiles <= 36 + segments : segments <= 304 && tiles <= 40;
@@ -818,8 +826,8 @@ gdn_status run(DecodeArgs& a, cudaStream_t st) {
   a.whole = by_segment(p);
   const int64_t grid = a.whole ? p.rows * p.heads : grid_of(p);
   // up to eight query rows: half of the softmax's work, and q's two parts in one
-  // fragment (eight rows, 64 x 8192 keys with both launches: E4M3 122 us, with the
-  // code for sixteen 162; INT8 130 and 139)
+  // fragment (eight rows, 64 rows of 2192 .. 8192 keys, 8 heads, both launches: E4M3 121 us,
+  // with the code for sixteen 162; INT8 129 and 139)
   const bool r8 = (int64_t)p.tokens * p.group <= 8;
   auto kern = p.page < kTile
                   ? (r8 ? kv8_decode_kernel<MODE, DIM, S, true, true> : kv8_decode_kernel<MODE, DIM, S, true, false>)

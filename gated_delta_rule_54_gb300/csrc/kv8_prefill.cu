@@ -12,13 +12,15 @@
 // E4M3 codes of K are an operand as they arrive; q is then the sum of an E4M3 and an
 // E5M2 number, exact for elements down to 2^-13 of the row's largest and off by at most
 // 2^-21 of that below (kv8.cuh).  K is not converted, which took the
-// second case below from 221 us to 197; the first takes 267 with E4M3 codes.
+// second case below from 221 us to 197; the first takes 265 with E4M3 codes.
 //
-// Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 283 us, 0.97
+// Measured on a GB300: 4 x 4096 tokens, causal, 16 heads of 128, INT8: 285 us, 0.97
 // PFLOP/s; three uneven prompts of up to 2048 tokens against up to 8200 keys, 16 on 4
-// heads, E4M3: 197 us, 1.12 PFLOP/s.  The tensor pipe is active 47 and 61 % of the
-// time; instruction issue, 2.2 a clock of the four schedulers, bounds it with the
-// chain from S by its maxima to P of each tile of rows.  In the
+// heads, E4M3: 197 us, 1.12 PFLOP/s.  Two things bound it.  While a CTA has work the tensor
+// pipe is active 46 and 61 % of the time; instruction issue, 2.2 a clock of the four
+// schedulers, holds it there with the chain from S by its maxima to P of each tile of rows.
+// And the CTAs do not end together: their active cycles are 91 and 77 % of the longest
+// one's on average (see Item).  In the
 // steps' order (fp16 products), one thread per row (8 warps) took 345 and 258 us, two
 // 331 and 240, a CTA per SM for all its items 328 and 249, and one issuing warp for
 // both tiles with a shorter conversion 290 and 221.
@@ -201,8 +203,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // One piece of work: up to 256 query rows of a (row, K/V head), and the tiles of
-// keys that they see (of which a split has its share).  Items with the most keys
-// come first, so that the CTAs, which take every gridDim.x-th, end together.
+// keys that they see (of which a split has its share).  Later blocks of rows, which see
+// more keys, come first, and a CTA takes every gridDim.x-th item.  That does not even the
+// CTAs out: it knows neither a row's context nor its tokens.  In units of 128 rows x 128
+// keys the file's first case gives a CTA 229 on average (196 to 260, of 6 or 7 items), the
+// second 176 (68 to 238, of 1 or 2).
 struct Item {
   Kv8Span sp;
   int r, h, row0, here;  // here == 0: nothing
@@ -796,7 +801,7 @@ int64_t blocks_of(const Kv8Params& p) {
 }
 // CTAs per block of rows: where the blocks do not fill 152 SMs, the keys are
 // split, down to two tiles each (in us, split / whole: 256 tokens x 4 heads of one K/V head
-// on 8192 keys 26/114; 512 x 4 of four on 4096 32/62; 64 x 4 of two on 700 19/20)
+// on 8192 keys 26/114; 512 x 4 of four on 4096 31/62; 64 x 4 of two on 700 19/20)
 int splits_of(const Kv8Params& p) {
   int64_t keys = (int64_t)p.cols * p.page;
   if (p.window > 0 && (int64_t)p.window + p.tokens < keys) keys = (int64_t)p.window + p.tokens;
@@ -845,7 +850,7 @@ gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* works
   a.blocks = (int)blocks_of(p);
   a.splits = splits_of(p);
   // pages of 64 and 128 tokens: two scales per tile of keys instead of eight (4 x 4096
-  // tokens, pages of 64: 277 us, with eight 286)
+  // tokens, pages of 64: 280 us, with eight 295)
   auto pick = [&](auto two, auto eight) { return p.page >= 64 ? two(a, st) : eight(a, st); };
   if (mode == GDN_QDQ_E4M3)
     return dim == 128 ? pick(run<GDN_QDQ_E4M3, 128, 2>, run<GDN_QDQ_E4M3, 128, 8>)
