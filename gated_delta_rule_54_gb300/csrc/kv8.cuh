@@ -150,7 +150,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 template <int E>
 __device__ __forceinline__ void kv8_q_factor(float most, float& to, float& back) {
   int e = (int)(__float_as_uint(most) >> 23) - 127;
-  e = e < -100 ? -100 : e > 120 ? 120 : e;
+  e = e < -118 ? -118 : e > 127 ? 127 : e;  // both powers are normal numbers
   to = most <= 3.402823466e38f ? __uint_as_float((uint32_t)(E - e + 127) << 23) : 0.f;
   back = __uint_as_float((uint32_t)(e - E + 127) << 23);
 }

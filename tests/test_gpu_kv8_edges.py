@@ -110,6 +110,22 @@ def test_q_with_a_large_channel(mode, dim, page, tokens, group):
                 assert np.all(np.abs(o[r] - ro) <= tol), (channel, e, r)
 
 
+@pytest.mark.parametrize("mode,dim,page", [("e4m3", 128, 64), ("int8", 64, 16), ("e4m3", 64, 32)])
+@pytest.mark.parametrize("tokens,group", [(1, 4), (4, 4), (40, 2)])
+@pytest.mark.parametrize("up", [122, 118, -104, -112])
+def test_q_of_any_size(mode, dim, page, tokens, group, up):
+    """Queries near the ends of their type's range against K that brings the scores back."""
+    rng = np.random.default_rng(34)
+    lengths = [3, 100, 333]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, 1, page, dim, mode)
+    scales[0] *= np.float32(2.0) ** -(up - (4 if up > 0 else 0))
+    table = _table(rng, lengths, page, pages)
+    q = (_q(rng, 3, tokens, group, dim).float() * 2.0 ** up).to(torch.bfloat16)
+    got = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), mode=mode, need_lse=True)
+    _check(got, q.float().cpu().numpy(), codes, scales, table, lengths, mode, dim ** -0.5)
+
+
 # ---- numbers that are none ------------------------------------------------
 def _positions(length, tokens, window):
     """[tokens, length]: which key each query sees."""
