@@ -197,6 +197,17 @@ __device__ __forceinline__ float2 kv8_scales(float ks, float vs) {
   return make_float2(ks, lg2_approx(vs));
 }
 
+// What turns a query's sum over P V into its output: 2^(mv - m) / l, in two steps, since the
+// power by itself may lie below the normal numbers.  0 where no key is seen (l is 0) or every V
+// scale seen is 0 (mv is -inf), NaN where a score is (l is NaN).
+template <int MODE>
+__device__ __forceinline__ float kv8_out_factor(float mv, float m, float l) {
+  if (l == 0.f) return 0.f;
+  if (mv == -INFINITY) return 0.f * l;
+  const float half = ex2_approx_f(0.5f * (mv - m + kKv8Shift<MODE>));
+  return half * (half / l);
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z,
                                             uint64_t* bar) {
   asm volatile(

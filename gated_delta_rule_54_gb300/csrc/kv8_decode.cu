@@ -501,9 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       // l is 0 where no key is seen, and NaN where a score is
       lse2[e] = l == 0.f ? -INFINITY : m[e] + log2f(l);
-      // mv is -inf where every V scale seen is 0
-      const float fac = l == 0.f ? 0.f
-                        : mv[e] > -INFINITY ? ex2_approx_f(mv[e] - m[e] + kKv8Shift<MODE>) / l : 0.f * l;
+      const float fac = kv8_out_factor<MODE>(mv[e], m[e], l);
 #pragma unroll
       for (int i = 0; i < NT; ++i) oacc[i][2 * e] *= fac, oacc[i][2 * e + 1] *= fac;
     }

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const __grid_c
           tc_fence_after();
         }
         // l is 0 where no key is seen, and NaN where a score is
-        const float fac = l == 0.f ? 0.f : mv > -INFINITY ? ex2_approx_f(mv - mx + kKv8Shift<MODE>) / l : 0.f * l;
+        const float fac = kv8_out_factor<MODE>(mv, mx, l);
         const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
         const int64_t at = (m.sp.base + qi) * (p.heads * p.group) + m.h * p.group + (m.row0 + i_row) % p.group;
         float* part = a.ws + ((int64_t)it * kRows + i_row) * (DIM + 4);

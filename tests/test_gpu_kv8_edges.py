@@ -51,6 +51,22 @@ def test_codes_under_a_scale_of_zero(mode, dim, page, tokens):
     assert torch.all(got[0][1] == 0)
 
 
+@pytest.mark.parametrize("tokens,group", [(1, 4), (8, 2), (40, 2)])
+@pytest.mark.parametrize("mode,dim,page", [("e4m3", 128, 64), ("int8", 64, 16), ("int8", 128, 128)])
+@pytest.mark.parametrize("power", [-127.5, -120, 110])
+def test_v_scales_of_any_size(mode, dim, page, tokens, group, power):
+    """V near the ends of its range: scales from 2^-128, the smallest that append writes."""
+    rng = np.random.default_rng(35)
+    lengths = [1, 60, 150]
+    pages = sum(-(-n // page) for n in lengths)
+    codes, scales = _pool(rng, pages, 1, page, dim, mode)
+    scales[1] = np.float32(2.0 ** power)
+    table = _table(rng, lengths, page, pages)
+    q = _q(rng, 3, tokens, group, dim)
+    got = kv8_attention(q, *_cuda(codes, scales, table, np.array(lengths, np.int32)), mode=mode, need_lse=True)
+    _check(got, q.float().cpu().numpy(), codes, scales, table, lengths, mode, dim ** -0.5)
+
+
 # ---- what follows a call in the stream sees its outputs -------------------
 def test_next_kernel_sees_rows_without_keys():
     """No row has a key, so nothing is left to join: a copy right behind the call has the zeros."""
