@@ -79,7 +79,7 @@ def draw(rng):
     heads, group = rng.choice([1, 2, 3, 4, 8]), rng.choice([1, 2, 3, 4, 5, 8])
     if kind == "rotary":
         rows, tokens, context = _log(rng, 1, 128), rng.choice([1, 1, _log(rng, 2, 4096)]), _log(rng, 1, 60000)
-        while rows * tokens * heads * (group + 2) * dim > 8 * 2700 * 8 * 6 * 128 or rows * (context + tokens) * heads * dim > 1 << 29:
+        while rows * tokens * heads * (group + 2) * dim > 8 * 2500 * 8 * 6 * 128 or rows * (context + tokens) * heads * dim > 1 << 29:
             rows, context = max(1, rows // 2), context * 2 // 3
         return dict(kind=kind, rows=rows, tokens=tokens, packed=rng.random() < 0.5, heads=heads, group=group, dim=dim,
                     rotary=16 * rng.randint(1, dim // 16), interleaved=rng.random() < 0.4, page=page, mode=mode, context=context,
