@@ -95,6 +95,21 @@ class GdnBeamProblem(ctypes.Structure):
     ]
 
 
+class GdnKv8Rotary(ctypes.Structure):
+    _fields_ = [
+        ("positions", ctypes.c_int64), ("q_row", ctypes.c_int64), ("q_token", ctypes.c_int64),
+        ("q_head", ctypes.c_int64), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+    ]
+
+
+class GdnLogitsProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("stride", ctypes.c_int64), ("bias_row", ctypes.c_int64),
+        ("mask_row", ctypes.c_int64), ("vocab", ctypes.c_int32), ("cols", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 # these take the structure (by reference) or its packed bytes
 _KP = _KL = _BP = _P
 SIGNATURES = {
@@ -126,6 +141,10 @@ SIGNATURES = {
     "gdn_kv8_append": (ctypes.c_int, [_KP, _P, _P, _P, _P, _P, _P, _P]),
     "gdn_kv8_workspace_bytes": (_SZ, [_KP]),
     "gdn_kv8_attention": (ctypes.c_int, [_KP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_kv8_append_rotary": (ctypes.c_int, [_KP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "gdn_kv8_shared_workspace_bytes": (_SZ, [_KP, ctypes.c_int32]),
+    "gdn_kv8_attention_shared": (ctypes.c_int, [_KP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                _P, _SZ, _P]),
     "gdn_kv8_pool_workspace_bytes": (_SZ, [_KL]),
     "gdn_kv8_copy_pages": (ctypes.c_int, [_KL, _P, _P, _P, _P, _I64, _P]),
     "gdn_kv8_fork": (ctypes.c_int, [_KL, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -134,6 +153,8 @@ SIGNATURES = {
     "gdn_beam_validate": (ctypes.c_int, [_BP]),
     "gdn_beam_workspace_bytes": (_SZ, [_BP]),
     "gdn_beam_select": (ctypes.c_int, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_beam_logits_validate": (ctypes.c_int, [_BP]),
+    "gdn_beam_logits": (ctypes.c_int, [_BP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "gdn_beam_reorder": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _P, _I64, ctypes.c_int32, _P]),
 }
 

@@ -21,7 +21,7 @@ OUT = os.path.join(PKG, "libgdn_qdq.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "qdq.cu", "fwd.cu", "fwd_fused.cu", "bwd.cu", "bwd_tc.cu", "bwd_scan_tc.cu", "bwd_noalloc.cu",
-           "decode.cu", "kv8.cu", "kv8_decode.cu", "kv8_prefill.cu", "kv8_pages.cu", "beam.cu", "kda.cu", "two_precision.cu", "two_precision_bwd.cu"]
+           "decode.cu", "kv8.cu", "kv8_decode.cu", "kv8_prefill.cu", "kv8_pages.cu", "kv8_rotary.cu", "kv8_shared.cu", "beam.cu", "beam_logits.cu", "kda.cu", "two_precision.cu", "two_precision_bwd.cu"]
 
 
 def _nvcc() -> str:

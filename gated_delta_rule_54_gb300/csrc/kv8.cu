@@ -161,6 +161,16 @@ gdn_status validate_kv8(const gdn_kv8_problem* p) {
   return GDN_OK;
 }
 
+// Rows in groups of `beams`, all with `tokens` queries; every key counts (no window).
+gdn_status validate_shared(const gdn_kv8_problem* p, int32_t beams) {
+  const gdn_status s = validate_kv8(p);
+  if (s != GDN_OK) return s;
+  if (beams < 1 || p->rows % beams != 0 || p->cu_seqlens) return GDN_ERR_INVALID_ARG;
+  if (p->window > 0) return GDN_ERR_UNSUPPORTED_MODE;
+  if ((int64_t)beams * p->tokens * p->group > 0x7ffffeffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
+  return GDN_OK;
+}
+
 Kv8Params params_of(const gdn_kv8_problem& p) {
   Kv8Params k = {};
   k.pages = p.pages, k.rows = p.rows, k.total = p.total;
@@ -252,6 +262,64 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows(*p)) return launch_kv8_decode(prm, p->mode, p->dim, workspace, st);
   return launch_kv8_prefill(prm, p->mode, p->dim, workspace, st);
+}
+
+gdn_status gdn_kv8_append_rotary(const gdn_kv8_problem* p, const gdn_kv8_rotary* w, const void* q,
+                                 const void* k, const void* v, const float* cos, const float* sin,
+                                 uint8_t* codes, float* scales, const int32_t* table,
+                                 const int32_t* start, void* q_out, void* stream) {
+  const gdn_status s = validate_kv8(p);
+  if (s != GDN_OK) return s;
+  if (!w || w->positions < 0 || (w->interleaved != 0 && w->interleaved != 1)) return GDN_ERR_INVALID_ARG;
+  if (w->dim <= 0 || w->dim > p->dim || w->dim % 16 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+  for (const int64_t x : {w->q_row, w->q_token, w->q_head})
+    if (x % 8 != 0) return GDN_ERR_MISALIGNED;
+  if (p->total == 0) return GDN_OK;
+  if (!q || !q_out || !k || !v || !start || (w->positions > 0 && (!cos || !sin))) return GDN_ERR_INVALID_ARG;
+  // (the rows' pages are looked up whether or not the cache has any)
+  if (p->cols > 0 && (!table || (p->pages > 0 && (!codes || !scales)))) return GDN_ERR_INVALID_ARG;
+  if (off16({q, q_out, k, v, codes, cos, sin}) || off4({scales, table, start, p->cu_seqlens}))
+    return GDN_ERR_MISALIGNED;
+  Kv8Params prm = params_of(*p);
+  prm.x = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  prm.codes = codes, prm.scales = scales, prm.table = table, prm.lengths = start;
+  prm.o = static_cast<__nv_bfloat16*>(q_out);
+  Kv8Rotary x = {};
+  x.q = static_cast<const __nv_bfloat16*>(q);
+  x.cos = cos, x.sin = sin, x.positions = w->positions;
+  x.q_row = w->q_row, x.q_token = w->q_token, x.q_head = w->q_head;
+  x.dim = w->dim, x.interleaved = w->interleaved;
+  return launch_kv8_rotary(prm, x, p->mode, p->dim, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_kv8_shared_workspace_bytes(const gdn_kv8_problem* p, int32_t beams) {
+  if (validate_shared(p, beams) != GDN_OK) return 0;
+  return kv8_shared_workspace(params_of(*p), beams, p->dim);
+}
+
+gdn_status gdn_kv8_attention_shared(const gdn_kv8_problem* p, int32_t beams, const void* q,
+                                    const uint8_t* codes, const float* scales, const int32_t* table,
+                                    const int32_t* lengths, const int32_t* shared, void* o,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  const gdn_status s = validate_shared(p, beams);
+  if (s != GDN_OK) return s;
+  if (p->total == 0) return GDN_OK;
+  if (!q || !o || !lengths || !shared) return GDN_ERR_INVALID_ARG;
+  if (p->cols > 0 && (!table || (p->pages > 0 && (!codes || !scales)))) return GDN_ERR_INVALID_ARG;
+  if (off16({q, codes, o}) || off4({scales, table, lengths, shared, lse}) || ((uintptr_t)workspace & 255))
+    return GDN_ERR_MISALIGNED;
+  const Kv8Params sized = params_of(*p);
+  const size_t need = kv8_shared_workspace(sized, beams, p->dim);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  Kv8Params prm = sized;
+  prm.x = static_cast<const __nv_bfloat16*>(q);
+  prm.codes = const_cast<uint8_t*>(codes), prm.scales = const_cast<float*>(scales);
+  prm.table = table, prm.lengths = lengths;
+  prm.o = static_cast<__nv_bfloat16*>(o), prm.lse = lse;
+  return launch_kv8_shared(prm, beams, shared, p->mode, p->dim, workspace,
+                           static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -245,7 +245,20 @@ __device__ __forceinline__ uint32_t kv8_code4(float a, float b, float c, float d
   }
 }
 
+// What an append with rotation has besides: the queries, and the angles of the positions.
+struct Kv8Rotary {
+  const __nv_bfloat16* q;
+  const float *cos, *sin;
+  int64_t positions, q_row, q_token, q_head;
+  int dim, interleaved;
+};
+
 // Launchers (arguments validated).
+gdn_status launch_kv8_rotary(const Kv8Params& p, const Kv8Rotary& w, int mode, int dim,
+                             cudaStream_t st);
+size_t kv8_shared_workspace(const Kv8Params& p, int beams, int dim);
+gdn_status launch_kv8_shared(const Kv8Params& p, int beams, const int32_t* shared, int mode, int dim,
+                             void* workspace, cudaStream_t st);
 size_t kv8_decode_workspace(const Kv8Params& p, int dim);
 gdn_status launch_kv8_decode(const Kv8Params& p, int mode, int dim, void* workspace,
                              cudaStream_t st);

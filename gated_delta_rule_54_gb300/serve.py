@@ -21,10 +21,12 @@ _i32, _u8, _f32, _bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _MODES = {k: v for k, v in QDQ_MODES.items() if v}
 _XTYPES = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"], torch.float32: DTYPES["fp32"]}
-# gdn_kv8_problem, gdn_kv8_pool and gdn_beam_problem as the C compiler lays them out
+# the problems' structures as the C compiler lays them out
 _KV8 = struct.Struct("@3q10ifP6q").pack
 _POOL = struct.Struct("@2q5i0q").pack
 _BEAM = struct.Struct("@2q5i0q").pack
+_ROTARY = struct.Struct("@4q2i").pack
+_LOGITS = struct.Struct("@4q3i0q").pack
 _TOO_SMALL = -5  # GDN_ERR_WORKSPACE_TOO_SMALL
 
 
@@ -34,6 +36,14 @@ def _fns():
 
 def _raise(fn, status):
     raise GdnError(fn, status)
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, the current stream of device dev), with that device current."""
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args, _raw_stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _raw_stream(dev))
 
 
 def _need(cond, text):
@@ -109,8 +119,8 @@ def _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode):
 
 
 def _problem(x, v, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, scale, causal,
-             window):
-    """The packed gdn_kv8_problem.  (Texts are made only for what is refused: this is on the
+             window, group=0):
+    """The packed gdn_kv8_problem (``group`` where x has the K/V heads).  (Texts are made only for what is refused: this is on the
     way of every token.)"""
     dev = codes.get_device()
     cs, shape, m = codes.shape, x.shape, _MODES.get(mode)
@@ -139,7 +149,7 @@ def _problem(x, v, codes, scales, table, lengths, cu_seqlens, max_seqlen, mode, 
         _bad_problem(x, v, codes, scales, table, lengths, cu_seqlens, mode)
     strides = _strides(x, shape)
     more = strides if v is None else _strides(v, shape)
-    return _KV8(pages, rows, total, tokens, cols, heads, xh // heads, dim, page, m,
+    return _KV8(pages, rows, total, tokens, cols, heads, group or xh // heads, dim, page, m,
                 _XTYPES.get(x.dtype, 99), causal, window, scale, cu, *strides, *more)
 
 
@@ -157,6 +167,47 @@ def kv8_append(k, v, codes, scales, table, start, cu_seqlens=None, max_seqlen=No
                                table.data_ptr(), start.data_ptr(), _raw_stream(codes.get_device()))
     if st:
         _raise("gdn_kv8_append", st)
+
+
+def _bad_rotary(q, k, cos, sin, dev):
+    """Says what kv8_append_rotary does not take of its queries and angles."""
+    _need(q.get_device() == dev and q.dtype is k.dtype, "q must have k's type and device")
+    _need(q.dim() == k.dim() and q.dim() >= 3 and q.shape[:-2] == k.shape[:-2] and q.shape[-1] == k.shape[-1],
+          "q must be like k but for the heads")
+    _need(q.shape[-2] > 0 and q.shape[-2] % k.shape[-2] == 0,
+          "%d heads cannot share %d K/V heads" % (q.shape[-2], k.shape[-2]))
+    _say(dev, ("cos", cos, _f32), ("sin", sin, _f32))
+    raise ValueError("cos and sin must be [positions, pairs]")
+
+
+def kv8_append_rotary(q, k, v, codes, scales, table, start, cos, sin, interleaved=False, cu_seqlens=None,
+                      max_seqlen=None, mode="e4m3"):
+    """New tokens go to the cache with their keys turned by position, in place; returns the queries,
+    turned as well, bf16 contiguous like q.
+
+    k, v and the cache as for kv8_append; q bf16 [rows, tokens, query heads, dim], or packed
+    [total, query heads, dim].  cos, sin f32 [positions, pairs]: the angles of row t are those of
+    position t, pairs a multiple of 8 and at most dim / 2.  The first 2 * pairs dims of a head
+    turn, dim j with dim pairs + j, or, ``interleaved``, dim 2 j with dim 2 j + 1.  The keys are
+    quantized from the fp32 numbers that this gives.  Queries are NaN at positions that cos does not
+    have, and so are the scales of key blocks written there; 0 for packed tokens of no row; and NaN
+    for a packed row with more than ``max_seqlen`` tokens."""
+    dev, qs, ks, cs = codes.get_device(), q.shape, k.shape, cos.shape
+    heads = ks[-2] if len(ks) >= 3 else 0
+    if not (heads > 0 and len(qs) == len(ks) and qs[:-2] == ks[:-2] and qs[-1] == ks[-1] and qs[-2] > 0
+            and qs[-2] % heads == 0 and q.get_device() == dev and q.dtype is k.dtype and _plain(cos, _f32, dev)
+            and _plain(sin, _f32, dev) and len(cs) == 2 and sin.shape == cs):
+        _need(len(ks) >= 3 and heads > 0, "expected k of [rows, tokens, heads, dim] or [total, heads, dim]")
+        _bad_rotary(q, k, cos, sin, dev)
+    p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, 1, 0, qs[-2] // heads)
+    w = _ROTARY(cs[0], *_strides(q, qs), 2 * cs[1], 1 if interleaved else 0)
+    out = torch.empty(qs, dtype=_bf16, device=codes.device)
+    st = _launch(
+        dev, _fns().gdn_kv8_append_rotary, p, w, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(), codes.data_ptr(),
+        scales.data_ptr(), table.data_ptr(), start.data_ptr(), out.data_ptr())
+    if st:
+        _raise("gdn_kv8_append_rotary", st)
+    return out
 
 
 def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=None, mode="e4m3",
@@ -197,6 +248,50 @@ def kv8_attention(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=
     if st:
         _raise("gdn_kv8_attention", st)
     return (out, lse) if need_lse else out
+
+
+def kv8_attention_shared(q, codes, scales, table, lengths, shared, beams, mode="e4m3",
+                         scale: Optional[float] = None, causal=True, need_lse=False, workspace=None,
+                         out=None):
+    """kv8_attention for rows that have their first tokens in common, which are read once.
+
+    Rows form groups of ``beams`` consecutive ones; shared int32 [rows / beams] counts the tokens
+    that a group has in common (the prompt of its beams: with kv8_fork its whole pages; all rows'
+    system prompt with beams = rows).  Positions below it are looked up in the table row of the
+    group's first row, the others in the row's own, so the result is kv8_attention's where the rows
+    hold the same tokens there.  q bf16 [rows, tokens, query heads, dim], for a few tokens each:
+    whole prompts gain nothing from sharing.  The rest as for kv8_attention."""
+    p = _problem(q, None, codes, scales, table, lengths, None, None, mode,
+                 codes.shape[-1] ** -0.5 if scale is None else scale, 1 if causal else 0, 0)
+    dev, beams = codes.get_device(), int(beams)
+    if not _plain(shared, _i32, dev):
+        _say(dev, ("shared", shared, _i32))
+    _need(beams > 0 and q.shape[0] % beams == 0 and shared.shape == (q.shape[0] // beams,),
+          "rows must be a multiple of beams, and shared [rows / beams]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=_bf16, device=codes.device)
+    else:
+        _say(dev, ("out", out, _bf16))
+        _need(out.shape == q.shape, "out must have q's shape")
+    lse = torch.empty(q.shape[:-1], dtype=_f32, device=codes.device) if need_lse else None
+    lib = _fns()
+    if workspace is None:
+        need = lib.gdn_kv8_shared_workspace_bytes(p, beams)
+        if need:
+            workspace = torch.empty(need, dtype=_u8, device=codes.device)
+    st = _launch(
+        dev, lib.gdn_kv8_attention_shared, p, beams, q.data_ptr(), codes.data_ptr(), scales.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+        shared.data_ptr(), out.data_ptr(), lse.data_ptr() if need_lse else None,
+        *((None, 0) if workspace is None else _room(workspace, dev)))
+    if st:
+        _raise("gdn_kv8_attention_shared", st)
+    return (out, lse) if need_lse else out
+
+
+def kv8_shared_workspace_bytes(q, codes, scales, table, lengths, beams, mode="e4m3") -> int:
+    """Bytes of the workspace that kv8_attention_shared takes for these arguments."""
+    return int(_fns().gdn_kv8_shared_workspace_bytes(
+        _problem(q, None, codes, scales, table, lengths, None, None, mode, 1.0, 1, 0), int(beams)))
 
 
 def kv8_workspace_bytes(q, codes, scales, table, lengths, cu_seqlens=None, max_seqlen=None,
@@ -319,6 +414,75 @@ def kv8_compact(codes, scales, table, lengths, refs, workspace=None):
     return t, r, live
 
 
+def _per_row(name, t, lead, width, dev, dtype):
+    """Address of t, and elements from one row's to the next (0: one for all): t is [width], or
+    [batch, beams, width] with rows evenly spaced or the same."""
+    if t is None:
+        return None, 0
+    _need(isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype,
+          "%s must be %s on cuda:%d" % (name, dtype, dev))
+    shape, st = t.shape, t.stride()
+    _need(t.dim() > 0 and shape[-1] >= width and (shape[-1] == 1 or st[-1] == 1) and (
+        t.dim() == 1 or shape[:-1] == lead),
+          "%s must be [%d] or [batch, beams, %d], the last dim contiguous" % (name, width, width))
+    if t.dim() == 1:
+        return t.data_ptr(), 0
+    row = st[1] if lead[1] > 1 else st[0] if lead[0] > 1 else 0
+    _need(lead[0] <= 1 or lead[1] <= 1 or st[0] == lead[1] * row, "rows of %s must be evenly spaced" % name)
+    return t.data_ptr(), row
+
+
+def beam_logits(logits, tokens=None, lengths=None, repetition=None, frequency=None, presence=None,
+                bias=None, mask=None, out=None):
+    """Logits as beam_select then takes them: penalties for repeated tokens, a bias, a grammar's mask.
+
+    logits bf16 or f32 [batch, beams, vocab] (last dim contiguous, rows evenly spaced).  tokens
+    int32 [batch, beams, columns] with lengths int32 [batch, beams] (or all columns): what each row
+    has said; ids outside the vocabulary (-1) count nowhere.  repetition, frequency, presence f32
+    [batch, beams]: a token that is there n > 0 times has its logit divided by ``repetition`` if
+    above 0, else multiplied by it, then less ``frequency`` * n and ``presence``.  bias f32
+    [vocab] or [batch, beams, vocab] is added.  mask int32 [words] or [batch, beams, words]: token
+    v is allowed where bit v % 32 of word v // 32 is set, the others get -inf.  All in fp32,
+    rounded once.  Returns logits like those given, contiguous; ``out`` may be the logits themselves."""
+    dev = logits.get_device()
+    _need(dev >= 0 and logits.dim() == 3, "logits must be [batch, beams, vocab] on CUDA")
+    b, w, v = lead = logits.shape
+    lead, s = lead[:2], logits.stride()
+    _need(v == 1 or s[2] == 1, "the vocabulary must be contiguous")
+    row = s[1] if w > 1 else s[0] if b > 1 else v
+    _need(w <= 1 or b <= 1 or s[0] == w * row, "rows of logits must be evenly spaced")
+    cols = 0
+    if tokens is None:
+        _need(repetition is None and frequency is None and presence is None and lengths is None,
+              "penalties need tokens")
+    else:
+        if not _plain(tokens, _i32, dev):
+            _say(dev, ("tokens", tokens, _i32))
+        _need(tokens.dim() == 3 and tokens.shape[:2] == lead, "tokens must be [batch, beams, columns]")
+        cols = tokens.shape[2]
+        for name, t, dtype in (("lengths", lengths, _i32), ("repetition", repetition, _f32),
+                               ("frequency", frequency, _f32), ("presence", presence, _f32)):
+            if t is not None:
+                if not _plain(t, dtype, dev):
+                    _say(dev, (name, t, dtype))
+                _need(t.shape == lead, "%s must be [batch, beams]" % name)
+    bias_at, bias_row = _per_row("bias", bias, lead, v, dev, _f32)
+    mask_at, mask_row = _per_row("mask", mask, lead, (v + 31) // 32, dev, _i32)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    else:
+        _say(dev, ("out", out, logits.dtype))
+        _need(out.shape == logits.shape, "out must have the logits' shape")
+    st = _launch(
+        dev, _fns().gdn_beam_logits, _LOGITS(b * w, row, bias_row, mask_row, v, cols, _XTYPES.get(logits.dtype, 99)), logits.data_ptr(),
+        None if tokens is None else tokens.data_ptr(), None if lengths is None else lengths.data_ptr(),
+        None if repetition is None else repetition.data_ptr(), None if frequency is None else frequency.data_ptr(),
+        None if presence is None else presence.data_ptr(), bias_at, mask_at, out.data_ptr())
+    if st:
+        _raise("gdn_beam_logits", st)
+    return out
+
+
 def beam_select(logits, scores, finished=None, k: Optional[int] = None, eos=-1, workspace=None):
     """The k best continuations of each batch item's beams (k defaults to the beams).
 
@@ -397,6 +561,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parents, beams: int, out=None):
     return dst
 
 
-__all__ = ["beam_reorder", "beam_select", "kv8_append", "kv8_attention", "kv8_compact",
-           "kv8_copy_pages", "kv8_fork", "kv8_free", "kv8_pool", "kv8_reserve",
+__all__ = ["beam_logits", "beam_reorder", "beam_select", "kv8_append", "kv8_append_rotary",
+           "kv8_attention", "kv8_attention_shared", "kv8_compact", "kv8_copy_pages", "kv8_fork",
+           "kv8_free", "kv8_pool", "kv8_reserve", "kv8_shared_workspace_bytes",
            "kv8_workspace_bytes", "GdnError"]

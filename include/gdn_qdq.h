@@ -526,6 +526,56 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
                              void* stream);
 
 /*
+ * Append with rotary positions: gdn_kv8_append of the turned keys, and the turned
+ * queries to an array of their own.  Token i of row r stands at position
+ * t = start[r] + i.  Pair j < dim / 2 of a head of q and k is (x_j, x_{j + dim/2}), or
+ * (x_2j, x_{2j+1}) where interleaved; with c = cos[t, j], s = sin[t, j]
+ *   a' = fl(fl(a c) - fl(b s))     b' = fl(fl(b c) + fl(a s))      in fp32
+ * and the other dims stay as they are.  Keys are quantized from these fp32 numbers;
+ * q' is rounded to bf16.  Where cos and sin have no row t, c = s = NaN: the queries are
+ * NaN there, and the scales of the key blocks that are written.  Which keys and values
+ * are written is as for gdn_kv8_append.  In a packed call queries of no row are 0,
+ * and all those of a row with more than `tokens` tokens are NaN.
+ *   q    bf16 [rows, tokens, heads * group, dim] or packed [total, ...], strided
+ *   cos, sin  f32 [positions, w->dim / 2], contiguous
+ *   q_out bf16 [total, heads * group, dim], overlaps nothing else
+ */
+typedef struct {
+  int64_t positions;             /* rows of cos and sin                           */
+  int64_t q_row, q_token, q_head; /* strides of q in elements, multiples of 8     */
+  int32_t dim;                   /* dims that turn: a multiple of 16, <= p->dim   */
+  int32_t interleaved;           /* 1: pairs are neighbours                       */
+} gdn_kv8_rotary;
+
+gdn_status gdn_kv8_append_rotary(const gdn_kv8_problem* p, const gdn_kv8_rotary* w, const void* q,
+                                 const void* k, const void* v, const float* cos, const float* sin,
+                                 uint8_t* codes, float* scales, const int32_t* table,
+                                 const int32_t* start, void* q_out, void* stream);
+
+/*
+ * Attention over the cache for rows that have their first tokens in common:
+ * gdn_kv8_attention, with these read once for a group of `beams` consecutive rows.
+ * Positions below shared[g] of every row of group g = row / beams are looked up in
+ * the table row of the group's first row, those from there on in the row's own.
+ * shared counts tokens (any number: what is below 0 or past the table is cut).
+ * What a query sees, NaNs and infinities, and the fewer bits of the probabilities
+ * are as for gdn_kv8_attention; q enters exactly but for elements below 2^-25 of
+ * the largest of their (query, head), which are off by at most 2^-33 of it.  A row's
+ * result does not depend on its group's other rows, but for the tokens of the first.
+ * Not packed (cu_seqlens NULL: GDN_ERR_INVALID_ARG), no window
+ * (GDN_ERR_UNSUPPORTED_MODE), rows a multiple of beams.
+ *   shared i32 [rows / beams]; the others as for gdn_kv8_attention
+ *   workspace  gdn_kv8_shared_workspace_bytes(p, beams) bytes, 256-byte aligned
+ */
+size_t gdn_kv8_shared_workspace_bytes(const gdn_kv8_problem* p, int32_t beams);
+
+gdn_status gdn_kv8_attention_shared(const gdn_kv8_problem* p, int32_t beams, const void* q,
+                                    const uint8_t* codes, const float* scales, const int32_t* table,
+                                    const int32_t* lengths, const int32_t* shared, void* o,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
  * Pages.  refs[p] counts the holders of page p (rows and whatever else the
  * caller counts); 0 = free.  A row holds the first ceil(lengths / page) pages
  * of its table row.  A partly filled page has one holder.  All outputs are new
@@ -609,6 +659,42 @@ gdn_status gdn_beam_select(const gdn_beam_problem* p, const void* logits, const 
                            const uint8_t* finished, float* scores_out, int32_t* parents,
                            int32_t* tokens, uint8_t* finished_out, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * Logits before the selection: penalties for the tokens of a row's history, a bias, and
+ * a mask.  With n the number of times that token v is among the row's first lengths[r]
+ * of `tokens` (ids outside the vocabulary count nowhere), x its logit, all steps
+ * in fp32:
+ *   n > 0:  x = x > 0 ? fl(x / repetition) : fl(x repetition)
+ *           x = fl(fl(x - fl(frequency n)) - presence)
+ *   x = fl(x + bias[v]);   x = -inf where the mask forbids v
+ * rounded to the logits' type.  Infinities and NaN go through these steps as they are.
+ * A penalty that is NULL is 1, 0, 0; bias and mask may be NULL.
+ *   logits  bf16 or f32 [rows, vocab], row stride `stride` elements
+ *   tokens  i32 [rows, cols]   lengths i32 [rows] or NULL: cols each (cut to 0 .. cols)
+ *   repetition, frequency, presence  f32 [rows]
+ *   bias    f32 [rows, vocab], rows bias_row elements apart (0: one for all)
+ *   mask    i32, rows mask_row words apart (0: one for all): token v is allowed where
+ *           bit v % 32 of word v / 32 is set
+ *   out     like logits, rows vocab elements apart; may be logits itself where those
+ *           are as well, and overlaps nothing else
+ */
+typedef struct {
+  int64_t rows;
+  int64_t stride;       /* elements from one row of logits to the next            */
+  int64_t bias_row;     /* 0 or >= vocab                                          */
+  int64_t mask_row;     /* 0 or >= ceil(vocab / 32)                               */
+  int32_t vocab;        /* >= 1                                                   */
+  int32_t cols;         /* columns of tokens                                      */
+  int32_t dtype;        /* GDN_DTYPE_BF16 or GDN_DTYPE_FP32                       */
+} gdn_logits_problem;
+
+gdn_status gdn_beam_logits_validate(const gdn_logits_problem* p);
+
+gdn_status gdn_beam_logits(const gdn_logits_problem* p, const void* logits, const int32_t* tokens,
+                           const int32_t* lengths, const float* repetition, const float* frequency,
+                           const float* presence, const float* bias, const int32_t* mask, void* out,
+                           void* stream);
 
 /*
  * Row r of every state becomes row parents[r] (-1: zeros).  n states, state i

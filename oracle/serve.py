@@ -105,6 +105,57 @@ def attention(q, codes, scales, table, length, mode, scale, causal=True, window=
     return o, lse, absum, top, dots
 
 
+def turn(x, positions, cos, sin, interleaved):
+    """x [n, heads, dim] fp32 turned by the angles of ``positions``; products and sums rounded to fp32."""
+    y, half = np.array(x, f32), cos.shape[1]
+    one, two = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    for i, t in enumerate(positions):
+        ok = 0 <= t < len(cos)
+        c, s = (cos[t], sin[t]) if ok else (f32(np.nan), f32(np.nan))
+        a, b = y[i][:, one].copy(), y[i][:, two].copy()
+        y[i][:, one] = (a * c).astype(f32) - (b * s).astype(f32)
+        y[i][:, two] = (b * c).astype(f32) + (a * s).astype(f32)
+    return y
+
+
+def attention_shared(q, codes, scales, first, own, shared, length, mode, scale, causal=True):
+    """One row whose positions below ``shared`` are in the pages ``first``, the others in ``own``."""
+    page = codes.shape[3]
+    end = max(0, min(length, len(own) * page))
+    j = np.arange(end)
+    ids = np.array([(first if t < shared else own)[t // page] for t in j], dtype=np.int64)
+    there = (ids >= 0) & (ids < codes.shape[1])
+    at = np.where(there, ids, 0)
+    # a cache with a page for each of the row's tokens
+    one = codes[:, at, :, j % page, :]                 # [keys, 2, heads, dim]
+    one = np.moveaxis(one, 0, 1)[:, :, :, None, :] if end else np.zeros((2, 0, codes.shape[2], 1, codes.shape[4]), np.uint8)
+    table = np.where(there, j, -1)
+    table = np.concatenate([table, np.full(max(len(own) * page - end, 0), -1, np.int64)])
+    return attention(q, one, scales[:, at], table, length, mode, scale, causal)
+
+
+def beam_logits(logits, tokens, lengths, repetition, frequency, presence, bias, mask):
+    """fp64, [rows, vocab]; tokens a list of lists, mask bool [rows, vocab] (True: allowed) or None."""
+    out = logits.astype(np.float64)
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        for r in range(len(out)):
+            count = {}
+            for t in tokens[r][:max(int(lengths[r]), 0)] if tokens is not None else ():
+                if 0 <= t < out.shape[1]:
+                    count[int(t)] = count.get(int(t), 0) + 1
+            for t, n in count.items():
+                x = out[r, t]
+                if repetition is not None:
+                    rep = np.float64(repetition[r])
+                    x = x / rep if x > 0 else x * rep
+                out[r, t] = x - (frequency[r] * n if frequency is not None else 0) - (presence[r] if presence is not None else 0)
+            if bias is not None:
+                out[r] += bias[r]
+            if mask is not None:
+                out[r][~mask[r]] = -np.inf
+    return out
+
+
 def _own(table, lengths, page):
     return [[int(table[r][c]) for c in range(min(-(-max(int(n), 0) // page), len(table[r])))]
             for r, n in enumerate(lengths)]
