@@ -266,5 +266,6 @@ size_t kv8_prefill_workspace(const Kv8Params& p, int dim);
 gdn_status launch_kv8_prefill(const Kv8Params& p, int mode, int dim, void* workspace,
                               cudaStream_t st);
 int kv8_prefill_device_error(bool reset);
+int kv8_shared_device_error(bool reset);
 
 }  // namespace gdn

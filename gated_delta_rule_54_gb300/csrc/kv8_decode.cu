@@ -880,8 +880,8 @@ int kv8_device_error(bool reset) {
     const int z = 0;
     if (cudaMemcpyToSymbol(g_kv8_device_error, &z, sizeof(int)) != cudaSuccess) return -1;
   }
-  const int u = kv8_prefill_device_error(reset);
-  return u < 0 ? -1 : v | u;
+  const int u = kv8_prefill_device_error(reset), w = kv8_shared_device_error(reset);
+  return u < 0 || w < 0 ? -1 : v | u | w;
 }
 
 }  // namespace gdn

@@ -36,9 +36,8 @@
 // room), and then O is rescaled in TMEM.
 #include <cuda.h>
 
-#include "kv8.cuh"
+#include "kv8_tc.cuh"
 #include "launch.h"
-#include "tc.cuh"
 
 namespace gdn {
 
@@ -62,109 +61,6 @@ struct PrefillArgs {
   int splits;      // items that share the keys of a block
   unsigned items;  // rows * heads * blocks * splits
 };
-
-// fp16 x fp16 -> fp32
-constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-// true in one lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t lead;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
-  return lead != 0;
-}
-// Products with descriptors given as the low word (start address and LBO) and the
-// common high word, so that stepping through a tile is one 32-bit add.
-constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // SBO 1024, 128-byte swizzle
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-  return (saddr >> 4) | (lbo >> 4) << 16;
-}
-__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
-      " setp.ne.b32 p, %5, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
-}
-// the same with 8-bit operands, 32 bytes (elements) of a row per product.  In the
-// instruction descriptor E4M3 is format 0, as fp16 is there, and E5M2 format 1 (A's: bit 7).
-// Rows of 64 bytes: SBO 512, 64-byte swizzle.
-constexpr uint32_t kAE5M2 = 1u << 7;
-template <int DIM>
-__device__ __forceinline__ void umma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
-      " setp.ne.b32 p, %5, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(DIM == 128 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29), "r"((uint32_t)acc));
-}
-// A in TMEM: row i in lane i, two fp16 per column
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %4};\n setp.ne.b32 p, %5, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(kDescHi), "r"((uint32_t)acc));
-}
-// 32 consecutive fp32 columns of this thread's lane; valid after tmem_wait_ld of them
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
-        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-// waits for this thread's loads; the values pass through so that no use moves before it
-__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
-                 "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
-                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
-                 "+f"(v[31])
-               :
-               : "memory");
-}
-// two fp32 operations at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
-        "l"(*reinterpret_cast<uint64_t*>(&c)));
-  return *reinterpret_cast<float2*>(&d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;\n"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-template <int N>
-__device__ __forceinline__ void set_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15};\n" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-}
 
 // Tile layout: panels of 64 columns, 128-byte rows, 16-byte units swizzled by
 // row & 7 (see tc.cuh).  Columns are stored in the order in which kv8_half2 gives
