@@ -92,11 +92,6 @@ __device__ __forceinline__ uint4 load_if(const __nv_bfloat16* from, bool there) 
       : "l"(from), "r"((int)there));
   return u;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 
 // One piece of work: up to 256 query rows of a (row, K/V head), and the tiles of
 // keys that they see (of which a split has its share).  Later blocks of rows, which see

@@ -40,11 +40,14 @@ __device__ int g_kv8_shared_error;
 
 constexpr int kTile = 32, kWarps = 4;  // own tokens: keys of a tile, warps of a CTA
 constexpr int kKeys = 128;             // the group's tokens: keys of a tile
-constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kIssuer = kSoftWarps + 2 * kConvWarps, kLoader = kIssuer + 1;
-constexpr int kThreads = 640;
+
+// Warps of the first kernel: two groups of four take the tiles in turn, so that one's exponentials
+// run in the other's latencies; eight turn codes into fp16 (E4M3: all V's, else half of them K's).
+constexpr int kGroups = 2, kSoft = 4 * kGroups, kConv = 8;
+constexpr int kIssueQK = kSoft + kConv, kIssuePV = kIssueQK + 1, kLoadK = kIssueQK + 2, kLoadV = kIssueQK + 3;
+constexpr int kThreads = (kSoft + kConv + 4) * 32;
 // registers per thread of the warpgroups: together no more than the launch gave (5 x 96)
-constexpr int kSoftRegs = 152, kConvRegs = 56, kRestRegs = 56;
+constexpr int kSoftRegs = 144, kConvRegs = 64, kRestRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * 96, "register shares");
 
 struct SharedArgs {
@@ -52,15 +55,10 @@ struct SharedArgs {
   CUtensorMap map;  // codes, a page of a head per box
   const int32_t* shared;
   float *parts, *lses;  // [slot][stride][DIM], [slot][stride]
-  int beams, nq, blocks;  // query rows of a block; blocks of a (group, head)
+  int beams, cw, blocks;  // query rows of a block; blocks of a (group, head)
   int stride;             // query rows of a part
   int grid;               // CTAs of the first launch
 };
-
-// What kv8_half2 leaves out of K goes half to the query's factor and half to K's scale, so that
-// neither leaves its range before the other.
-template <int MODE>
-constexpr float kRoot = MODE == GDN_QDQ_E4M3 ? 16.f : 1.f;
 
 // Keys of query i of a row (all of them, of the whole row): [0, end).
 __device__ __forceinline__ int seen_end(const Kv8Params& p, int64_t len, int i) {
@@ -70,18 +68,30 @@ __device__ __forceinline__ int seen_end(const Kv8Params& p, int64_t len, int i) 
   return p.causal ? kv8_clamp(pos + 1, 0, all) : pos < 0 ? 0 : all;
 }
 
-// Tokens that a group has in common, and their tiles.
+// Tokens that a group has in common (those that its first row has), and their tiles.
 __device__ __forceinline__ int common_of(const SharedArgs& a, int64_t g) {
-  return kv8_clamp(a.shared[g], 0, (int64_t)a.p.cols * a.p.page);
+  return kv8_clamp(min(a.shared[g], a.p.lengths[g * a.beams]), 0, (int64_t)a.p.cols * a.p.page);
 }
-__device__ __forceinline__ int tiles_of(int keys) { return (int)(((int64_t)keys + kKeys - 1) / kKeys); }
+__device__ __forceinline__ int tiles_of(int keys) { return (int)(((uint32_t)keys + kKeys - 1) / kKeys); }
 
-// Tiles of groups [0, g1), counted for one (head, block).
-__device__ __forceinline__ int64_t tiles_before(const SharedArgs& a, int64_t g1, int lane) {
-  int64_t n = 0;
-  for (int64_t g = lane; g < g1; g += 32) n += tiles_of(common_of(a, g));
-  for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-  return n;
+// Tiles of the groups before g1, and of all of them, counted for one (head, block).
+__device__ __forceinline__ void tiles_before(const SharedArgs& a, int64_t g1, int lane, int64_t& before, int64_t& all) {
+  const int64_t groups = a.p.rows / (uint32_t)a.beams;
+  before = all = 0;
+  for (int64_t g = lane; g < groups; g += 32) {
+    const int n = tiles_of(common_of(a, g));
+    all += n;
+    if (g < g1) before += n;
+  }
+  for (int d = 16; d; d >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+  }
+}
+
+// a / b of numbers >= 0; nearly always both have 32 bits, whose division is far shorter
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // Equal shares of the line of `all` tiles: the first `rest` of n CTAs have one tile more.
@@ -89,12 +99,12 @@ struct Shares {
   int64_t each, rest, n;
   __device__ __forceinline__ Shares(int64_t all, int grid) {
     n = all < grid ? all : grid;
-    each = n > 0 ? all / n : 0, rest = n > 0 ? all - each * n : 0;
+    each = n > 0 ? quotient(all, n) : 0, rest = all - each * n;
   }
   __device__ __forceinline__ int64_t start(int64_t c) const { return each * c + (c < rest ? c : rest); }
   __device__ __forceinline__ int64_t cta_of(int64_t u) const {
     const int64_t longer = rest * (each + 1);
-    return u < longer ? u / (each + 1) : rest + (u - longer) / each;
+    return u < longer ? quotient(u, each + 1) : rest + quotient(u - longer, each);
   }
 };
 
@@ -103,16 +113,25 @@ struct Walk {
   int64_t left, g;
   int common, tiles, hq, t;  // of the group; head * blocks + block; tile
   __device__ __forceinline__ Walk(const SharedArgs& a, int64_t cta, int lane) {
-    const int64_t groups = a.p.rows / a.beams, per = (int64_t)a.p.heads * a.blocks;
-    const Shares s(tiles_before(a, groups, lane) * per, a.grid);
+    const int64_t groups = a.p.rows / (uint32_t)a.beams, per = (int64_t)a.p.heads * a.blocks;
+    // (32 groups lie in the lanes: nearly always all)
+    const int mine = lane < groups ? common_of(a, lane) : 0;
+    int64_t before, all = tiles_of(mine);
+    if (groups <= 32) {
+      for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    } else {
+      tiles_before(a, 0, lane, before, all);
+    }
+    const Shares s(all * per, a.grid);
     left = 0, g = 0, common = tiles = hq = t = 0;
     if (cta >= s.n) return;
     const int64_t u = s.start(cta);
     left = s.start(cta + 1) - u;
-    int64_t before = 0;
+    before = 0;
     for (int64_t g0 = 0;; g0 += 32) {
-      const int64_t mine = g0 + lane < groups ? tiles_of(common_of(a, g0 + lane)) * per : 0;
-      int64_t x = mine;
+      const int have = g0 == 0 ? mine : g0 + lane < groups ? common_of(a, g0 + lane) : 0;
+      int64_t x = tiles_of(have) * per;
+      const int64_t here = x;
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
@@ -121,14 +140,15 @@ struct Walk {
       if (hit) {
         const int at = __ffs(hit) - 1;
         g = g0 + at;
-        before += __shfl_sync(0xffffffffu, x - mine, at);
+        before += __shfl_sync(0xffffffffu, x - here, at);
+        common = __shfl_sync(0xffffffffu, have, at);
         break;
       }
       before += __shfl_sync(0xffffffffu, x, 31);
     }
-    common = common_of(a, g), tiles = tiles_of(common);
+    tiles = tiles_of(common);
     const int64_t in = u - before;
-    hq = (int)(in / tiles), t = (int)(in - (int64_t)hq * tiles);
+    hq = (int)quotient(in, tiles), t = (int)(in - (int64_t)hq * tiles);
   }
   // tiles of the piece
   __device__ __forceinline__ int count() const { return left < tiles - t ? (int)left : tiles - t; }
@@ -170,50 +190,89 @@ __device__ __forceinline__ float half_reduce(float (&x)[16], int lane) {
   return x[0];
 }
 
-__device__ __forceinline__ void half_sync(int half) {
-  asm volatile("bar.sync %0, 128;\n" ::"r"(1 + half) : "memory");
+// Barriers of a group's four warps, and of all groups'.
+__device__ __forceinline__ void group_sync(int g) {
+  asm volatile("bar.sync %0, 128;\n" ::"r"(1 + g) : "memory");
 }
 // the same, and whether any of the threads says yes
-__device__ __forceinline__ bool half_any(int half, bool yes) {
+__device__ __forceinline__ bool group_any(int g, bool yes) {
   uint32_t any;
   asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                : "=r"(any)
-               : "r"((uint32_t)yes), "r"(1 + half)
+               : "r"((uint32_t)yes), "r"(1 + g)
                : "memory");
   return any;
 }
+template <int N>
+__device__ __forceinline__ void groups_sync() {
+  asm volatile("bar.sync 7, %0;\n" ::"n"(N) : "memory");
+}
 
-// Shared memory of the first kernel: fp16 tiles K 0, K 1, V 0, V 1; the codes of the next ones
-// arrive on their second panels, or, with 64 dims, behind.  V with 64 dims has a panel of zeros for
-// the other 64 lanes of O.
-template <int DIM, int NQ>
-struct Room {
-  static constexpr int tile = kKeys * DIM * 2, k = 0, v = 2 * tile, zero = 4 * tile;
-  static constexpr int codes = zero + (DIM == 64 ? kKeys * 128 : 0);
-  static constexpr int q = codes + (DIM == 64 ? 4 * kKeys * DIM : 0), pt = q + NQ * DIM * 2;
-  static constexpr int bytes = pt + NQ / 64 * kKeys * 128 + 1024;
-  static constexpr int codes_at(int kv, int b) {
-    return DIM == 128 ? (2 * kv + b) * tile + kKeys * 128 : codes + (2 * kv + b) * kKeys * DIM;
+// O += V^T P: V in rows of 128 bytes, P in rows of 2 CW bytes (64: 64-byte swizzle, SBO 512).
+template <int CW>
+__device__ __forceinline__ void umma_pv(uint32_t d, uint32_t v, uint32_t p, uint32_t id, bool acc) {
+  constexpr uint32_t hi = CW == 64 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %5};\n"
+      " setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(v), "r"(p), "r"(id), "r"(kDescHi), "r"(hi), "r"((uint32_t)acc));
+}
+
+// A place in a ring of N buffers, and the parity of its turn.
+template <int N>
+struct Ring {
+  uint32_t at = 0, turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) at = 0, turn ^= 1;
   }
 };
 
-template <int MODE, int DIM, int NQ>
+// Shared memory of the first kernel: codes of K and of V as they arrive, as many tiles of them as
+// there is room for, since what is on its way is what DRAM's latency leaves; fp16 tiles of V and
+// (INT8; E4M3 codes are an operand as they are) of K; the queries, and the groups' P.
+// V with 64 dims has a panel of zeros for the other 64 lanes of O.
+template <int MODE, int DIM, int CW>
+struct Room {
+  static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
+  static constexpr int raw = kKeys * DIM, tile = 2 * raw, ptile = kKeys * CW * 2;
+  static constexpr int raws = CW == 32 ? (f8 ? 4 : 3) : (f8 ? 3 : 2), vtiles = 2, ktiles = f8 ? 0 : 1;
+  static constexpr int k = 0, v = raws * raw, vt = v + raws * raw, zero = vt + vtiles * tile;
+  static constexpr int kt = zero + (DIM == 64 ? kKeys * 128 : 0), q = kt + ktiles * tile, pt = q + CW * DIM * 2;
+  static constexpr int bytes = pt + kGroups * ptile + 1024;
+  static_assert(bytes <= 227 * 1024 - (CW == 32 ? 10 : 18) * 1024, "shared memory (with what the kernel has besides)");
+};
+
+// Two E4M3 numbers (the low 16 bits) as fp16.
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+
+template <int MODE, int DIM, int CW>
 __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_constant__ SharedArgs a) {
-  using R = Room<DIM, NQ>;
-  constexpr uint32_t kCols = NQ == 64 ? 256 : 512;  // S 0, S 1, O
-  constexpr uint32_t kIdQK = idesc_f16(128, NQ, 0, 0), kIdPV = idesc_f16(128, NQ, 1, 1);
-  constexpr int kChunks = NQ / 32;  // of 16 columns, of a thread
+  using R = Room<MODE, DIM, CW>;
+  constexpr bool F8 = R::f8;
+  constexpr int G = kGroups;
+  constexpr uint32_t kCols = 2 * G * CW;  // S of each group, O of each group
+  constexpr uint32_t kIdQK = idesc_f16(128, CW, 0, 0), kIdPV = idesc_f16(128, CW, 1, 1);
+  constexpr uint32_t kBE5M2 = 1u << 10;
+  constexpr int kChunks = CW / 16;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t cfull[2][2];                       // codes of K, of V; by buffer
-  __shared__ __align__(8) uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  __shared__ __align__(8) uint64_t sfull[2], sfree[2], qready, pready, odone;
-  __shared__ float2 meta[4][8];  // per 16 keys of a tile: K scale, log2 of V scale
-  __shared__ int valid[4];       // bit c: they have a page
-  __shared__ int s_lim[NQ], s_min[2];  // keys that a column sees; the fewest of a half's columns
-  __shared__ __align__(16) float s_fac[NQ], s_m[NQ], s_out[NQ], s_by[2][NQ];
-  __shared__ float s_mv[NQ];
-  __shared__ __align__(16) float s_ratio[kSoftWarps][2][NQ / 2];  // 2^(log2 vs + m - mv), per half-warp
-  __shared__ float2 s_red[4][NQ];
+  // codes there, and free; fp16 tiles there, and free
+  __shared__ __align__(8) uint64_t kin[R::raws], kout[R::raws], vin[R::raws], vout[R::raws];
+  __shared__ __align__(8) uint64_t kfull, kfree, vfull[R::vtiles], vfree[R::vtiles];
+  __shared__ __align__(8) uint64_t sfull[G], sfree[G], pready[G], odone[G], qready;
+  __shared__ float2 meta[16][8];  // [tile]: per 16 keys K scale, log2 of V scale
+  __shared__ int valid[16];       // bit c: they have a page
+  __shared__ int2 vinfo[16];      // the same for those who have V, and the tile's tokens
+  __shared__ int s_lim[CW], s_min[G];  // keys that a column sees; the fewest of them
+  __shared__ __align__(16) float s_fac[CW];  // factor of a column's scores
+  // of a group's column: references of s and of s + log2 of V's scale; -m; sum; factor of its output; what a move makes of its sums, and of O
+  __shared__ __align__(16) float s_m[G][CW], s_mv[G][CW], s_neg[G][CW], s_sum[G][CW], s_out[G][CW], s_by[G][2][CW];
+  // for 16 keys of a tile: factor of the scores, 2^(log2 vs + m - mv)
+  __shared__ __align__(16) float s_by_k[kSoft][2][CW], s_ratio[kSoft][2][CW];
+  __shared__ float2 s_red[G][4][CW];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -224,13 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
   grid_dep_launch();  // the rows' own tokens need nothing of this launch until their join
   if (warp == 0) tmem_alloc(&tmem_slot, kCols);
   if (tid == 32) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&cfull[0][i], 1), mbar_init(&cfull[1][i], 1);
-      mbar_init(&kfull[i], kConvWarps * 32), mbar_init(&vfull[i], kConvWarps * 32);
-      mbar_init(&kfree[i], 1), mbar_init(&vfree[i], 1);
-      mbar_init(&sfull[i], 1), mbar_init(&sfree[i], kSoftWarps * 32);
+    for (int i = 0; i < R::raws; ++i) {
+      mbar_init(&kin[i], 1), mbar_init(&vin[i], 1);
+      mbar_init(&kout[i], F8 ? 1 : 4), mbar_init(&vout[i], F8 ? 8 : 4);
     }
-    mbar_init(&qready, kSoftWarps * 32), mbar_init(&pready, kSoftWarps * 32), mbar_init(&odone, 1);
+    for (int i = 0; i < R::vtiles; ++i) mbar_init(&vfull[i], F8 ? 8 : 4), mbar_init(&vfree[i], 1);
+    mbar_init(&kfull, 4), mbar_init(&kfree, 1);
+    for (int i = 0; i < G; ++i) mbar_init(&sfull[i], 1), mbar_init(&sfree[i], 4), mbar_init(&pready[i], 4), mbar_init(&odone[i], 1);
+    mbar_init(&qready, kSoft);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -250,30 +310,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     return false;
   };
   auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+  // one arrival for a warp, whose lanes have all come here
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
-  if (warp < kSoftWarps) {
+  if (warp < kSoft) {
     set_regs_up<kSoftRegs>();
     // ======================= keys =======================
-    const int half = warp / 4, quad = warp & 3, key = quad * 32 + lane, sub = lane >> 4;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    unsigned char *sQ = smem + R::q, *sP = smem + R::pt;
+    const int g = warp / 4, quad = warp & 3, key = quad * 32 + lane, sub = lane >> 4;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), s_col = lanes + g * CW, o_col = lanes + (G + g) * CW;
+    unsigned char *sQ = smem + R::q, *sP = smem + R::pt + g * R::ptile;
     const int per_row = p.tokens * p.group, all_q = a.beams * per_row;
+    float *ratio = s_ratio[warp][sub], *by_k = s_by_k[warp][sub], *fm = s_m[g], *fmv = s_mv[g], *neg = s_neg[g];
     bool ok = true;
-    uint32_t n = 0;  // tiles so far
+    uint32_t n = 0, mine = 0;  // tiles so far, and this group's
     for (; w.left > 0; w.next(a)) {
-      const int nt = w.count(), h = w.hq / a.blocks, q0 = w.hq % a.blocks * NQ;
-      const int here = min(all_q - q0, NQ);          // columns in use
-      const int hc = (here + 31) / 32 * 16, c0 = half * hc;  // a half's, in chunks of 16; the first of mine
+      const int nt = w.count(), h = w.hq / a.blocks, q0 = w.hq % a.blocks * CW;
+      const int here = min(all_q - q0, CW), hc = (here + 15) / 16 * 16;  // columns in use, in chunks of 16
       // ---- queries: DIM / 8 lanes to a row ----
       {
         constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;
-        for (int c = warp * kAt + lane / kLanes; c < 2 * hc; c += kSoftWarps * kAt) {
+        for (int c = warp * kAt + lane / kLanes; c < hc; c += kSoft * kAt) {
           const int i = q0 + c, r_in = i / per_row, x_in = i - r_in * per_row, u = lane % kLanes;
           const int64_t r = w.g * a.beams + r_in;
           uint4 raw = make_uint4(0, 0, 0, 0);
           if (c < here)
             raw = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_row + (x_in / p.group) * p.x_token +
                                                        (int64_t)(h * p.group + x_in % p.group) * p.x_head + 8 * u));
+          if (u == 0) s_lim[c] = c < here ? min(seen_end(p, p.lengths[r], x_in / p.group), w.common) : 0;
           float f[8], most = 0.f;
           bf16x8(raw, f);
 #pragma unroll
@@ -281,189 +347,248 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
 #pragma unroll
           for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
           float up, back;
-          kv8_q_factor<8>(most, up, back);
-          if (u == 0) {
-            s_fac[c] = back * fabsf(p.scale) * kLog2eF * kRoot<MODE>;
-            s_lim[c] = c < here ? min(seen_end(p, p.lengths[r], x_in / p.group), w.common) : 0;
-          }
+          kv8_q_factor<F8 ? 7 : 8>(most, up, back);
+          if (u == 0) s_fac[c] = back * fabsf(p.scale) * kLog2eF;
           if (p.scale < 0.f) up = -up;
-          *reinterpret_cast<uint4*>(sQ + unit_at(c, u, NQ)) =
-              make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
-                         pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
+          if constexpr (F8) {  // an E4M3 number and an E5M2 one (kv8.cuh)
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float rest[4];
+              hi[e] = kv8_q_first(f + 4 * e, up, rest);
+              lo[e] = kv8_e5m2x4(rest);
+            }
+            unsigned char* to = sQ + (u & 1) * 8 + (DIM == 128 ? unit_at(c, u >> 1, CW) : c * 64 + (((u >> 1) ^ (c >> 1 & 3)) << 4));
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + CW * DIM) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint4*>(sQ + unit_at(c, u, CW)) =
+                make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
+                           pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
+          }
         }
         fence_proxy_async();
-        if (ok) mbar_arrive(&qready);
+        if (ok) warp_arrive(&qready);
       }
-      asm volatile("bar.sync 3, 256;\n" ::: "memory");  // both halves: the columns' limits and factors
+      groups_sync<G * 128>();  // the columns' limits and factors
       if (quad == 0) {
         int least = 0x7fffffff;
-        for (int c = lane; c < hc; c += 32)
-          if (c0 + c < here) least = min(least, s_lim[c0 + c]);
+        for (int c = lane; c < hc; c += 32) {
+          if (c < here) least = min(least, s_lim[c]);
+          fm[c] = fmv[c] = -INFINITY, neg[c] = INFINITY;  // no score yet: any is too large
+        }
         least = __reduce_min_sync(0xffffffffu, least);
-        if (lane == 0) s_min[half] = least;
-        for (int c = lane; c < hc; c += 32) s_m[c0 + c] = s_mv[c0 + c] = -INFINITY;
+        if (lane == 0) s_min[g] = least;
       }
-      half_sync(half);
-      const int least = s_min[half];
+      group_sync(g);
+      const int least = s_min[g];
       float sum[kChunks][16];
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sum[c][e] = 0.f;
 
-      for (int i = 0; i < nt; ++i, ++n) {
-        ok = ok && all_wait(&sfull[n & 1], (n >> 1) & 1);
-        if (!ok) {  // a wait gave up: only the barriers that others may stand at
-          half_sync(half);
-          half_any(half, false);
+      const int first = (int)((g - n) & (G - 1));  // this group's first tile of the piece
+      for (int i = first; i < nt; i += G, ++mine) {
+        ok = ok && all_wait(&sfull[g], mine & 1);
+        if (!ok) {  // a wait gave up: only the barrier that others may stand at
+          if (i == first) group_sync(g), group_sync(g);
+          if (group_any(g, false)) group_sync(g), group_sync(g);
           continue;
         }
         tc_fence_after();
-        const uint32_t s_col = lanes + (n & 1) * NQ + c0;
-        const int j0 = (w.t + i) * kKeys, at = j0 + key;
-        const float2 sc = meta[n & 3][key >> 4];
-        const bool there = valid[n & 3] >> (key >> 4) & 1;
-        const bool mask = valid[n & 3] != 255 || j0 + kKeys > least;
-        // ---- maxima ----
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (16 * c >= hc) break;
-          float v[16];
-          tmem_ld16(s_col + 16 * c, v);
-          if (mask) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (!there || at >= s_lim[c0 + 16 * c + e]) v[e] = -INFINITY;
+        const int j0 = (w.t + i) * kKeys, at = j0 + key, slot = (n + i) & 15;
+        const float2 sc = meta[slot][key >> 4];
+        const bool there = valid[slot] >> (key >> 4) & 1;
+        const bool mask = valid[slot] != 255 || j0 + kKeys > least;
+        auto gone = [&](int col) { return !there || at >= s_lim[col]; };
+        auto tables = [&]() {
+          for (int c = lane & 15; c < hc; c += 16) {
+            const float mv = fmv[c];
+            by_k[c] = s_fac[c] * sc.x;
+            ratio[c] = ex2_approx_f(fminf(sc.y - neg[c] - (mv == -INFINITY ? 0.f : mv), 126.f));
           }
-          const float x = half_reduce<false>(v, lane);
-          const int col = c0 + 16 * c + (lane & 15);
-          // (a factor of 0 would make -inf a NaN)
-          float nm = x == -INFINITY ? x : x * (sc.x * s_fac[col]);
-          float nv = nm + sc.y;
-          nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 16));
-          nv = fmaxf(nv, __shfl_xor_sync(0xffffffffu, nv, 16));
-          if (lane < 16) s_red[quad][col] = make_float2(nm, nv);
-        }
-        half_sync(half);
-        bool moved = false;
-        for (int c = quad * 32 + lane; c < hc; c += 128) {
-          const int col = c0 + c;
-          float nm = -INFINITY, nv = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[q][col].x), nv = fmaxf(nv, s_red[q][col].y);
-          const float m = s_m[col], mv = s_mv[col];
-          float by = 1.f, by_o = 1.f;
-          if (nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[col] = nm, moved = true;
-          if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[col] = nv, moved = true;
-          s_by[0][col] = by, s_by[1][col] = by_o;
-        }
-        moved = half_any(half, moved);
-        // ---- what the references' change makes of the sums so far ----
-        if (n > 0 && i > 0) {
-          ok = all_wait(&odone, (n - 1) & 1);  // P and O are free
-          tc_fence_after();
-        }
-        if (moved && i > 0 && ok) {
+          __syncwarp();
+        };
+        // Probabilities against the references as they are; over: the largest number.  (Two forms,
+        // with a mask and without: predicates for it take half of the instructions.)
+        float over = 0.f;
+        auto probs = [&](auto masked, auto add) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             if (16 * c >= hc) break;
-            const uint32_t o_col = lanes + 2 * NQ + c0 + 16 * c;
             float v[16];
-            tmem_ld16(o_col, v);
-            uint32_t u[16];
+            tmem_ld16(s_col + 16 * c, v);
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              sum[c][e] *= s_by[0][c0 + 16 * c + e];
-              u[e] = __float_as_uint(v[e] * s_by[1][c0 + 16 * c + e]);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&by_k[16 * c + e]);
+              const float4 m = *reinterpret_cast<const float4*>(&neg[16 * c + e]);
+              const float4 r = *reinterpret_cast<const float4*>(&ratio[16 * c + e]);
+              float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
+              float2 y = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
+              if constexpr (decltype(masked)::value) {
+                if (gone(16 * c + e)) x.x = -INFINITY;
+                if (gone(16 * c + e + 1)) x.y = -INFINITY;
+                if (gone(16 * c + e + 2)) y.x = -INFINITY;
+                if (gone(16 * c + e + 3)) y.y = -INFINITY;
+              }
+              x = make_float2(ex2_approx_f(x.x), ex2_approx_f(x.y)), y = make_float2(ex2_approx_f(y.x), ex2_approx_f(y.y));
+              if constexpr (decltype(add)::value) {
+                const float2 s0 = add2(make_float2(sum[c][e], sum[c][e + 1]), x), s1 = add2(make_float2(sum[c][e + 2], sum[c][e + 3]), y);
+                sum[c][e] = s0.x, sum[c][e + 1] = s0.y, sum[c][e + 2] = s1.x, sum[c][e + 3] = s1.y;
+                over = max3(over, x.x, x.y), over = max3(over, y.x, y.y);
+              } else {
+                // what was too large for a sum stands alone in it
+                if (sum[c][e] == INFINITY) sum[c][e] = x.x;
+                if (sum[c][e + 1] == INFINITY) sum[c][e + 1] = x.y;
+                if (sum[c][e + 2] == INFINITY) sum[c][e + 2] = y.x;
+                if (sum[c][e + 3] == INFINITY) sum[c][e + 3] = y.y;
+              }
+              x = mul2(x, make_float2(r.x, r.y)), y = mul2(y, make_float2(r.z, r.w));
+              if constexpr (decltype(add)::value) over = max3(over, x.x, x.y), over = max3(over, y.x, y.y);
+              pk[e / 2] = pack_f16(x.x, x.y), pk[e / 2 + 1] = pack_f16(y.x, y.y);
             }
-            tmem_st16(o_col, u);
+            unsigned char* to = sP + key * (2 * CW);
+            const int swap = CW == 64 ? key & 7 : key >> 1 & 3;
+            *reinterpret_cast<uint4*>(to + (((2 * c) ^ swap) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ swap) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          }
+        };
+        // Maxima; columns that outgrew a reference by 2^8 get a new one.
+        auto references = [&]() {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (16 * c >= hc) break;
+            float v[16];
+            tmem_ld16(s_col + 16 * c, v);
+            if (mask) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (gone(16 * c + e)) v[e] = -INFINITY;
+            }
+            const float x = half_reduce<false>(v, lane);
+            const int col = 16 * c + (lane & 15);
+            // (a factor of 0 would make -inf a NaN)
+            float nm = x == -INFINITY ? x : x * (sc.x * s_fac[col]);
+            float nv = nm + sc.y;
+            nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 16));
+            nv = fmaxf(nv, __shfl_xor_sync(0xffffffffu, nv, 16));
+            if (lane < 16) s_red[g][quad][col] = make_float2(nm, nv);
+          }
+          group_sync(g);
+          for (int c = quad * 32 + lane; c < hc; c += 128) {
+            float nm = -INFINITY, nv = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[g][q][c].x), nv = fmaxf(nv, s_red[g][q][c].y);
+            const float m = fm[c], mv = fmv[c];
+            float by = 1.f, by_o = 1.f;
+            if (nm > m + 8.f) by = ex2_approx_f(m - nm), fm[c] = nm, neg[c] = -nm;
+            if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), fmv[c] = nv;
+            s_by[g][0][c] = by, s_by[g][1][c] = by_o;
+          }
+          group_sync(g);
+        };
+        if (i == first) {
+          references();
+        } else {
+          ok = all_wait(&odone[g], (mine - 1) & 1);  // P and O are free
+          tc_fence_after();
+        }
+        tables();
+        if (mask) probs(std::true_type(), std::true_type());
+        else probs(std::false_type(), std::true_type());
+        // a score that outgrew its column's references by 2^8: fp16 and the sums have the room for that
+        if (group_any(g, over > 256.f)) {
+          references();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (16 * c >= hc) break;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (sum[c][e] != INFINITY) sum[c][e] *= s_by[g][0][16 * c + e];
+            if (i > first && ok) {
+              float v[16];
+              tmem_ld16(o_col + 16 * c, v);
+              uint32_t u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * s_by[g][1][16 * c + e]);
+              tmem_st16(o_col + 16 * c, u);
+            }
           }
           tmem_wait_st();
-        }
-        // 2^(log2 vs + m - mv) of a column, for the keys of this half-warp
-        for (int c = lane & 15; c < hc; c += 16) {
-          const float m = s_m[c0 + c], mv = s_mv[c0 + c];
-          s_ratio[warp][sub][c] = ex2_approx_f(fminf((m == -INFINITY ? 0.f : m) + sc.y - (mv == -INFINITY ? 0.f : mv), 126.f));
-        }
-        __syncwarp();
-        // ---- probabilities ----
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (16 * c >= hc) break;
-          float v[16];
-          tmem_ld16(s_col + 16 * c, v);
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 fac = *reinterpret_cast<const float4*>(&s_fac[c0 + 16 * c + e]);
-            const float4 m = *reinterpret_cast<const float4*>(&s_m[c0 + 16 * c + e]);
-            const float4 ra = *reinterpret_cast<const float4*>(&s_ratio[warp][sub][16 * c + e]);
-            const float f4[4] = {fac.x, fac.y, fac.z, fac.w}, m4[4] = {m.x, m.y, m.z, m.w}, r4[4] = {ra.x, ra.y, ra.z, ra.w};
-            float pr[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x = v[e + k] * (sc.x * f4[k]) - (m4[k] == -INFINITY ? 0.f : m4[k]);
-              if (mask && (!there || at >= s_lim[c0 + 16 * c + e + k])) x = -INFINITY;
-              const float y = ex2_approx_f(x);
-              sum[c][e + k] += y;
-              pr[k] = y * r4[k];
-            }
-            pk[e / 2] = pack_f16(pr[0], pr[1]), pk[e / 2 + 1] = pack_f16(pr[2], pr[3]);
-          }
-          const int col = c0 + 16 * c, u = (col & 63) / 8;
-          unsigned char* to = sP + (col >> 6) * (kKeys * 128) + key * 128;
-          *reinterpret_cast<uint4*>(to + ((u ^ (key & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(to + (((u + 1) ^ (key & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          tables();
+          probs(std::true_type(), std::false_type());
         }
         fence_proxy_async();
         tc_fence_before();
-        if (ok) mbar_arrive(&sfree[n & 1]), mbar_arrive(&pready);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&pready[g]), mbar_arrive(&sfree[g]);
       }
 
-      // ---- the part: outputs over these keys, and log2 of the sums ----
-      half_sync(half);  // s_red has been read
+      // ---- the part: outputs over the piece's keys, and log2 of the sums ----
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (16 * c >= hc) break;
         float l = half_reduce<true>(sum[c], lane);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (lane < 16) s_red[quad][c0 + 16 * c + lane].x = l;
+        if (lane < 16) s_red[g][quad][16 * c + lane].x = l;
       }
-      half_sync(half);
-      const int64_t slot = w.slot(a, blockIdx.x);
-      for (int c = quad * 32 + lane; c < hc; c += 128) {
-        const int col = c0 + c;
-        const float l = (s_red[0][col].x + s_red[1][col].x) + (s_red[2][col].x + s_red[3][col].x);
-        // l is 0 where no key is seen, and NaN where a score is
-        s_out[col] = kv8_out_factor<MODE>(s_mv[col], s_m[col], l);
-        if (col < here) a.lses[slot * a.stride + col] = l == 0.f ? -INFINITY : s_m[col] + log2f(l);
+      if (first < nt) {
+        ok = ok && all_wait(&odone[g], (mine - 1) & 1);
+        tc_fence_after();
       }
-      half_sync(half);
-      ok = ok && all_wait(&odone, (n - 1) & 1);
+      group_sync(g);
+      for (int c = quad * 32 + lane; c < hc; c += 128)
+        s_sum[g][c] = (s_red[g][0][c].x + s_red[g][1][c].x) + (s_red[g][2][c].x + s_red[g][3][c].x);
+      tc_fence_before();
+      groups_sync<G * 128>();
       tc_fence_after();
-      // lane d of O is dim 4 (d / 4) + (0 2 1 3)[d % 4]
-      const int dim = (key & ~3) | (key & 1) << 1 | (key >> 1 & 1);
+      const int64_t slot = w.slot(a, blockIdx.x);
+      for (int c = warp * 32 + lane; c < hc; c += kSoft * 32) {
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (16 * c >= hc || !ok) break;
-        float v[16];
-        tmem_ld16(lanes + 2 * NQ + c0 + 16 * c, v);
+        for (int x = 0; x < G; ++x) m = fmaxf(m, s_m[x][c]);
+#pragma unroll
+        for (int x = 0; x < G; ++x) l += m == -INFINITY ? s_sum[x][c] : s_sum[x][c] * ex2_approx_f(s_m[x][c] - m);
+        // l is 0 where no key is seen, and NaN where a score is
+#pragma unroll
+        for (int x = 0; x < G; ++x) s_out[x][c] = kv8_out_factor<GDN_QDQ_INT8>(s_mv[x][c], m, l);  // (V as it is)
+        if (c < here) a.lses[slot * a.stride + c] = l == 0.f ? -INFINITY : m + log2f(l);
+      }
+      groups_sync<G * 128>();
+      // with INT8 codes lane d of O is dim 4 (d / 4) + (0 2 1 3)[d % 4]
+      const int dim = F8 ? key : (key & ~3) | (key & 1) << 1 | (key >> 1 & 1);
+      for (int c = 16 * g; c < hc && ok; c += 16 * G) {
+        float o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+          if ((int)((x - n) & (G - 1)) >= nt) continue;  // no tile of the piece was this group's
+          float v[16];
+          tmem_ld16(lanes + (G + x) * CW + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], s_out[x][c + e], o[e]);
+        }
         if (key < DIM) {
-          float* to = a.parts + (slot * a.stride + c0 + 16 * c) * DIM + dim;
+          float* to = a.parts + (slot * a.stride + c) * DIM + dim;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (c0 + 16 * c + e < here) to[e * DIM] = v[e] * s_out[c0 + 16 * c + e];
+            if (c + e < here) to[e * DIM] = o[e];
         }
       }
+      n += nt;
       tc_fence_before();  // O has been read: the next piece's products may write it (after P's signal)
-      asm volatile("bar.sync 3, 256;\n" ::: "memory");  // every column's values have been read
+      groups_sync<G * 128>();  // every column's values have been read
+      tc_fence_after();
     }
-  } else if (warp < kIssuer) {
+  } else if (warp < kIssueQK) {
     set_regs_down<kConvRegs>();
     // ======================= codes to fp16 =======================
     // a lane takes 16 codes at a time; the two rows of eight neighbouring lanes are
     // chosen so that their loads and their stores each fall on different banks
-    const int kv = (warp - kSoftWarps) / kConvWarps, cw = (warp - kSoftWarps) % kConvWarps;
+    const int cw = (warp - kSoft) % 4, second = (warp - kSoft) / 4;
     constexpr int kPer = DIM / 16, kStep = 2048 / DIM;
     const int unit = DIM == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const int r8 = DIM == 128 ? (lane >> 4 & 1) * 2 : lane >> 2;
@@ -473,147 +598,195 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     const int from0 = DIM == 128 ? row0c * 128 + ((unit ^ (row0c & 7)) << 4)
                                  : row0c * 64 + ((unit ^ (row0c >> 1 & 3)) << 4);
     const uint32_t to0 = unit_at(row0c, 2 * unit, kKeys), to1 = unit_at(row0c, 2 * unit + 1, kKeys);
-    bool ok = true;
-    const uint32_t all = (uint32_t)w.left;
-    for (uint32_t n = 0; n < all && ok; ++n) {
-      const uint32_t b = n & 1;
-      ok = wait(&cfull[kv][b], (n >> 1) & 1);
-      if (!ok) break;
-      unsigned char* to = smem + (2 * kv + b) * R::tile;
-      const unsigned char* from = smem + R::codes_at(kv, b);
-      // four rows' codes at a time (rows kStep apart: the swizzle is the same)
+    constexpr int kMine = F8 ? kPer / 2 : kPer;  // (rows kStep apart: the swizzle is the same)
+    const int e_first = F8 ? second * kMine : 0;
+    auto read = [&](uint4 (&u)[kMine], const unsigned char* from) {
 #pragma unroll
-      for (int e0 = 0; e0 < kPer; e0 += 4) {
-        uint4 u[4];
+      for (int e = 0; e < kMine; ++e) u[e] = *reinterpret_cast<const uint4*>(from + from0 + (e_first + e) * kStep * DIM);
+    };
+    auto write = [&](const uint4 (&u)[kMine], unsigned char* to) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          u[e] = *reinterpret_cast<const uint4*>(from + from0 + (e0 + e) * kStep * DIM);
-        __syncwarp();  // the rows' lanes have read them: half of a row is written over
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 lo, hi;
+      for (int e = 0; e < kMine; ++e) {
+        uint4 lo, hi;
+        if constexpr (F8) {
+          lo.x = half2_of(u[e].x), lo.y = half2_of(u[e].x >> 16), lo.z = half2_of(u[e].y), lo.w = half2_of(u[e].y >> 16);
+          hi.x = half2_of(u[e].z), hi.y = half2_of(u[e].z >> 16), hi.z = half2_of(u[e].w), hi.w = half2_of(u[e].w >> 16);
+        } else {
           kv8_half2<MODE>(u[e].x, lo.x, lo.y);
           kv8_half2<MODE>(u[e].y, lo.z, lo.w);
           kv8_half2<MODE>(u[e].z, hi.x, hi.y);
           kv8_half2<MODE>(u[e].w, hi.z, hi.w);
-          *reinterpret_cast<uint4*>(to + to0 + (e0 + e) * kStep * 128) = lo;
-          *reinterpret_cast<uint4*>(to + to1 + (e0 + e) * kStep * 128) = hi;
         }
+        *reinterpret_cast<uint4*>(to + to0 + (e_first + e) * kStep * 128) = lo;
+        *reinterpret_cast<uint4*>(to + to1 + (e_first + e) * kStep * 128) = hi;
       }
       fence_proxy_async();
-      mbar_arrive(kv ? &vfull[b] : &kfull[b]);
+    };
+    const uint32_t all = (uint32_t)w.left;
+    Ring<R::raws> in;
+    if (F8 || second) {
+      Ring<R::vtiles> out;
+      for (uint32_t n = 0; n < all; ++n, in.next(), out.next()) {
+        if (!all_wait(&vin[in.at], in.turn)) break;
+        uint4 u[kMine];
+        read(u, smem + R::v + in.at * R::raw);
+        const int2 what = vinfo[n & 15];
+        warp_arrive(&vout[in.at]);
+        if (F8 && (what.x < kKeys || what.y != 255)) {
+          // E4M3 bytes that are no number may stand where no token is
+#pragma unroll
+          for (int e = 0; e < kMine; ++e) {
+            const int row = row0c + (e_first + e) * kStep;
+            if (row >= what.x || !(what.y >> (row >> 4) & 1)) u[e] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        if (!all_wait(&vfree[out.at], out.turn ^ 1)) break;
+        write(u, smem + R::vt + out.at * R::tile);
+        warp_arrive(&vfull[out.at]);
+      }
+    } else {
+      for (uint32_t n = 0; n < all; ++n, in.next()) {
+        if (!all_wait(&kin[in.at], in.turn)) break;
+        uint4 u[kMine];
+        read(u, smem + R::k + in.at * R::raw);
+        warp_arrive(&kout[in.at]);
+        if (!all_wait(&kfree, (n & 1) ^ 1)) break;
+        write(u, smem + R::kt);
+        warp_arrive(&kfull);
+      }
     }
   } else {
     set_regs_down<kRestRegs>();
   }
-  if (warp == kLoader) {
+  if (warp == kLoadK || warp == kLoadV) {
     // ======================= codes by TMA =======================
-    const int boxes = kKeys >> p.shift;
-    uint32_t n = 0, issued[2] = {0, 0};
+    // A warp for K, which says what the tile has, and one for V.
+    // Lane l has page l of a window of 32, and its scales; those of the next window are asked for
+    // while this one's tiles are loaded.
+    const bool is_v = warp == kLoadV;
+    const int boxes = kKeys >> p.shift, shift = 31 - __clz(boxes), span = 32 >> shift;  // pages of a tile; tiles of a window
+    uint64_t *in = is_v ? vin : kin, *free = is_v ? vout : kout;
+    constexpr int bufs = R::raws;
+    uint32_t n = 0, issued = 0, b = 0, turn = 0;
     bool ok = true;
     for (; w.left > 0 && ok; w.next(a)) {
       const int nt = w.count(), h = w.hq / a.blocks;
       const int32_t* pages = p.table + w.g * a.beams * p.cols;
-      // page ids and scales are asked for a tile before
-      auto page_of = [&](int i) {
-        const int64_t j = (int64_t)(w.t + i) * kKeys + (lane << p.shift);
-        return lane < boxes && i < nt && j < w.common ? pages[j >> p.shift] : -1;
+      auto page_of = [&](int i) {  // of the window that begins with tile i
+        const int64_t j = ((int64_t)(w.t + i) * kKeys) + ((int64_t)lane << p.shift);
+        const int id = i + (lane >> shift) < nt && j < w.common ? pages[j >> p.shift] : -1;
+        return id < p.pages ? id : -1;
       };
       auto scale_of = [&](int id) {
-        if (id < 0 || id >= p.pages) return make_float2(0.f, 0.f);
+        if (is_v || id < 0) return make_float2(0.f, 0.f);
         const int64_t tile = (int64_t)id * p.heads + h;
         return make_float2(p.scales[tile], p.scales[tile + p.pages * p.heads]);
       };
-      int id = page_of(0), id1 = page_of(1);
-      float2 sc = scale_of(id);
+      int id = -1, later = page_of(0);
+      float2 sc = make_float2(0.f, 0.f), sc_later = scale_of(later);
       for (int i = 0; i < nt; ++i, ++n) {
-        const uint32_t b = n & 1;
-        const bool have = id >= 0 && id < p.pages;
-        // 16 keys c lie in page c >> (log2 of 16ths of a page)
-        const int from = (lane * 16) >> p.shift;
-        const float ks = __shfl_sync(0xffffffffu, sc.x, from & 31);
-        const float vs = __shfl_sync(0xffffffffu, sc.y, from & 31);
-        const bool there = __shfl_sync(0xffffffffu, (int)have, from & 31);
-        const unsigned bits = __ballot_sync(0xffffffffu, there && lane < 8);
-        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have)) * (DIM << p.shift);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && all_wait(kv ? &vfree[b] : &kfree[b], ((n >> 1) & 1) ^ 1);
-          if (!ok) break;
-          if (kv == 0) {
-            if (lane < 8) {
-              const float2 m = there ? kv8_scales(ks, vs) : make_float2(0.f, -INFINITY);
-              meta[n & 3][lane] = make_float2(m.x * kRoot<MODE>, m.y);
-            }
-            if (lane == 0) valid[n & 3] = (int)bits;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_expect_tx(&cfull[kv][b], bytes);
-          __syncwarp();
-          issued[kv] = n + 1;
-          if (have)
-            tma_load_3d(smem + R::codes_at(kv, b) + (lane << p.shift) * DIM, &a.map, 0, 0,
-                        (int)((kv * p.pages + id) * p.heads + h), &cfull[kv][b]);
-        }
+        const int at = i & (span - 1);  // in the window
+        if (at == 0) id = later, sc = sc_later, later = page_of(i + span);
+        if (at == 1) sc_later = scale_of(later);
+        ok = all_wait(&free[b], turn ^ 1);
         if (!ok) break;
-        id = id1;
-        sc = scale_of(id);
-        id1 = page_of(i + 2);
+        const bool have = id >= 0, now = lane >> shift == at;
+        if (have && now)
+          tma_load_3d(smem + (is_v ? R::v : R::k) + b * R::raw + ((lane & (boxes - 1)) << p.shift) * DIM, &a.map, 0, 0,
+                      (int)((is_v * p.pages + id) * p.heads + h), &in[b]);
+        issued = n + 1;
+        {
+          // 16 keys c lie in page c >> (log2 of 16ths of a page) of the tile
+          const int from = (at << shift) + ((lane * 16 >> p.shift) & (boxes - 1));
+          const float k1 = __shfl_sync(0xffffffffu, sc.x, from), v1 = __shfl_sync(0xffffffffu, sc.y, from);
+          const bool there = __shfl_sync(0xffffffffu, (int)have, from);
+          const unsigned bits = __ballot_sync(0xffffffffu, there && lane < 8);
+          // (this buffer of codes is free, so its last tile is multiplied, or its fp16 form waits for
+          // that of the tile before: tiles 16 back have been through everything)
+          if (lane < 8 && !is_v) meta[n & 15][lane] = there ? kv8_scales(k1, v1) : make_float2(0.f, -INFINITY);
+          if (lane == 0 && !is_v) valid[n & 15] = (int)bits;
+          if (lane == 0 && is_v) vinfo[n & 15] = make_int2((int)min((int64_t)kKeys, w.common - (int64_t)(w.t + i) * kKeys), (int)bits);
+        }
+        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have && now)) * (DIM << p.shift);
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(&in[b], bytes);
+        if (++b == bufs) b = 0, turn ^= 1;
       }
     }
     // no copy is in flight when the CTA ends, whatever ended the loop
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-      for (uint32_t i = issued[kv] > 2 ? issued[kv] - 2 : 0; i < issued[kv]; ++i) mbar_wait(&cfull[kv][i & 1], (i >> 1) & 1);
-  } else if (warp == kIssuer) {
+    for (uint32_t i = issued > bufs ? issued - bufs : 0; i < issued; ++i) mbar_wait(&in[i % bufs], (i / bufs) & 1);
+  } else if (warp == kIssueQK || warp == kIssuePV) {
     // ======================= products =======================
-    // Q K^T of a tile goes before P V of the one before it, so that the keys' threads have their
-    // next scores while the tensor cores do the outputs.  The whole warp goes through this; one
-    // elected lane issues.
+    // A warp for Q K^T, one for P V.  Each goes through this as a whole, and what it goes by comes
+    // from one lane, so that descriptors stay in uniform registers; one elected lane issues.  (One
+    // warp for both, on registers of its lanes, took 1500 cycles for a tile.)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-    const uint32_t dk = desc_lo(base + R::k, 16), dq = desc_lo(base + R::q, 16), dp = desc_lo(base + R::pt, kKeys * 128);
     const bool lead = elect_one();
+    uint32_t left = (uint32_t)__shfl_sync(0xffffffffu, (int)w.left, 0);
     bool ok = true;
-    auto qk = [&](uint32_t n) {
-      const uint32_t b = n & 1;
-      ok = ok && all_wait(&kfull[b], (n >> 1) & 1) && all_wait(&sfree[b], ((n >> 1) & 1) ^ 1);
-      if (!ok) return;
-      tc_fence_after();
-      if (lead) {
+    uint32_t n = 0;
+    if (warp == kIssueQK) {
+      const uint32_t dk = desc_lo(base + (F8 ? R::k : R::kt), 16), dq = desc_lo(base + R::q, 16);
+      Ring<R::raws> kb;
+      for (uint32_t pieces = 0; left > 0 && ok; w.next(a), ++pieces) {
+        const uint32_t nt = (uint32_t)__shfl_sync(0xffffffffu, w.count(), 0);
+        ok = all_wait(&qready, pieces & 1);
+        for (uint32_t i = 0; i < nt; ++i, ++n) {
+          const uint32_t g = n & (G - 1);
+          ok = ok && (F8 ? all_wait(&kin[kb.at], kb.turn) : all_wait(&kfull, n & 1)) && all_wait(&sfree[g], (n / G & 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            const uint32_t d = tm + g * CW, k = dk + (F8 ? kb.at * (R::raw >> 4) : 0);
+            if constexpr (F8) {
+              constexpr int kRow = DIM / 32;
 #pragma unroll
-        for (int s = 0; s < DIM / 16; ++s)
-          umma_ss(tm + b * NQ, dk + b * (R::tile >> 4) + (s / 4 * (kKeys * 128) >> 4) + (s % 4) * 2,
-                  dq + (s / 4 * (NQ * 128) >> 4) + (s % 4) * 2, kIdQK, s > 0);
-        umma_commit(&sfull[b]);
-        umma_commit(&kfree[b]);
-      }
-      __syncwarp();
-    };
-    uint32_t n = 0, pieces = 0;
-    for (; w.left > 0 && ok; w.next(a), ++pieces) {
-      const int nt = w.count();
-      ok = all_wait(&qready, pieces & 1);
-      qk(n);
-      for (int i = 0; i < nt && ok; ++i, ++n) {
-        if (i + 1 < nt) qk(n + 1);
-        const uint32_t b = n & 1;
-        ok = ok && all_wait(&pready, n & 1) && all_wait(&vfull[b], (n >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        // rows 64 and up of V^T: the other panel, or zeros
-        const uint32_t dv = desc_lo(base + R::v + b * R::tile, DIM == 128 ? kKeys * 128 : R::zero - R::v - b * R::tile);
-        if (lead) {
+              for (int s = 0; s < 2 * kRow; ++s)  // q's first parts, then its second ones, with the same codes
+                umma_ss_f8<DIM>(d, k + s % kRow * 2, dq + (s / kRow * (CW * DIM) >> 4) + s % kRow * 2, kIdQK | (s < kRow ? 0 : kBE5M2), s > 0);
+            } else {
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            umma_ss(tm + 2 * NQ, dv + s * (2048 >> 4), dp + s * (2048 >> 4), kIdPV, i > 0 || s > 0);
-          umma_commit(&odone);
-          umma_commit(&vfree[b]);
+              for (int s = 0; s < DIM / 16; ++s)
+                umma_ss(d, k + (s / 4 * (kKeys * 128) >> 4) + (s % 4) * 2, dq + (s / 4 * (CW * 128) >> 4) + (s % 4) * 2, kIdQK, s > 0);
+            }
+            umma_commit(F8 ? &kout[kb.at] : &kfree);
+            umma_commit(&sfull[g]);  // (the one that is waited for at the end)
+          }
+          __syncwarp();
+          kb.next();
         }
-        __syncwarp();
+        left -= nt;
+      }
+    } else {
+      const uint32_t dp = desc_lo(base + R::pt, 16);
+      Ring<R::vtiles> vb;
+      for (; left > 0 && ok; w.next(a)) {
+        const uint32_t nt = (uint32_t)__shfl_sync(0xffffffffu, w.count(), 0);
+        for (uint32_t i = 0; i < nt; ++i, ++n) {
+          const uint32_t g = n & (G - 1);
+          ok = ok && all_wait(&vfull[vb.at], vb.turn) && all_wait(&pready[g], n / G & 1);
+          if (!ok) break;
+          tc_fence_after();
+          // rows 64 and up of V^T: the other panel, or zeros
+          const uint32_t dv = desc_lo(base + R::vt + vb.at * R::tile, DIM == 128 ? kKeys * 128 : R::zero - R::vt - vb.at * R::tile);
+          if (lead) {
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              umma_pv<CW>(tm + (G + g) * CW, dv + s * (2048 >> 4), dp + g * (R::ptile >> 4) + s * (CW * 32 >> 4), kIdPV, i >= G || s > 0);
+            umma_commit(&vfree[vb.at]);
+            umma_commit(&odone[g]);
+          }
+          __syncwarp();
+          vb.next();
+        }
+        left -= nt;
       }
     }
-    if (n > 0) wait(&odone, (n - 1) & 1);
+    // every product issued has completed before the CTA ends
+    for (uint32_t g = 0; g < G; ++g) {
+      const uint32_t tiles = (n + G - 1 - g) / G;
+      if (tiles > 0) wait(warp == kIssueQK ? &sfull[g] : &odone[g], (tiles - 1) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -632,221 +805,298 @@ struct Codes<64> {
   using T = uint2;
 };
 
-// ROWS: 16 or 8 query rows of the CTA.
-template <int MODE, int DIM, int ROWS>
-__global__ void __launch_bounds__(kWarps * 32) kv8_own_kernel(const __grid_constant__ SharedArgs a) {
-  constexpr int NE = ROWS / 8, KC = DIM / 64, KSTEPS = DIM / 16, NT = DIM / 8;
+// Transposes 8 x 8 numbers of 16 bits, two of a row in a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Where a lane's codes of a key (step c, word w) lie in the key's dims; lane % 4 == t.
+template <int DIM>
+__device__ __forceinline__ int dim_of(int t, int c, int w) {
+  return (DIM == 128 ? 32 * t + 16 * c : 16 * t) + 4 * w;
+}
+
+// 8 NB query rows in a warp, the keys coming 16 at a time: S = K Q^T and O += V^T P as warp
+// products with the keys, then the dims, as the long side.  Lane (g, t): scores of keys g and
+// g + 8 for queries 2 t and 2 t + 1 of each eight; outputs of these at dims DIM / 8 g ...
+template <int MODE, int DIM, int NB>
+struct Rows {
+  static constexpr int KC = DIM / 64, KS = DIM / 16, MT = DIM / 16;
+  static constexpr bool F8 = MODE == GDN_QDQ_E4M3;
   using V = typename Codes<DIM>::T;
+  float o[MT][NB][4], l[NB][2], m[NB][2], mv[NB][2], fac[NB][2];
+  int lim[NB][2];  // keys that the query sees
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) o[j][b][0] = o[j][b][1] = o[j][b][2] = o[j][b][3] = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[b][e] = 0.f, m[b][e] = mv[b][e] = -INFINITY;
+  }
+  // Four codes of one key (two of each of two) as fp16.
+  static __device__ __forceinline__ void two(uint32_t w, uint32_t& first, uint32_t& second) {
+    if constexpr (F8) first = half2_of(w), second = half2_of(w >> 16);
+    else kv8_half2<MODE>(w, first, second);
+  }
+  // The products' other operand: eight queries, of which a lane has row g, by step.
+  static __device__ __forceinline__ uint2 query_of(uint2 raw, float to) {
+    float f[4];
+    bf16x4(raw, f);
+    return F8 ? make_uint2(pack_f16(f[0] * to, f[1] * to), pack_f16(f[2] * to, f[3] * to))
+              : make_uint2(pack_f16(f[0] * to, f[2] * to), pack_f16(f[1] * to, f[3] * to));
+  }
+
+  // 16 keys from position j0: K of keys g and g + 8, V of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9.
+  // part: not every query sees all of them, or they are not all of [from, to) or there.
+  template <class Q>
+  __device__ __forceinline__ void step(const uint4 (&kc)[2][KC], V (&vc)[4], const Q& query, float ks, float lv,
+                                       bool part, int j0, int from, int to, bool there, int g, int t) {
+    float s[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const uint32_t x[4] = {kc[0][c].x, kc[0][c].y, kc[0][c].z, kc[0][c].w};
+      const uint32_t y[4] = {kc[1][c].x, kc[1][c].y, kc[1][c].z, kc[1][c].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a[4];
+        two(x[w], a[0], a[2]);
+        two(y[w], a[1], a[3]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint2 q = query(4 * c + w, b);
+          mma_f16(s[b], a, q.x, q.y);
+        }
+      }
+    }
+    // ---- scores; does one outgrow its query's references by 2^8? ----
+    bool over = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = fac[b][e] * ks, most = fminf(m[b][e] + 8.f, mv[b][e] + 8.f - lv);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = s[b][2 * h + e] * f;
+          if (part) {
+            const int j = j0 + g + 8 * h;
+            if (j < from || j >= to || j >= lim[b][e] || !there) x = -INFINITY;
+          }
+          s[b][2 * h + e] = x;
+          over |= x > most;
+        }
+      }
+    if (F8 && part) {
+      // E4M3 bytes that are no number may stand where no token is
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + 2 * t + (x & 1) + 8 * (x >> 1);
+        if (j < from || j >= to || !there) vc[x] = V();
+      }
+    }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float nm = fmaxf(s[b][e], s[b][2 + e]);
+          nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 4));
+          nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 8));
+          nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 16));
+          const float nv = nm + lv;
+          if (nm > m[b][e] + 8.f) l[b][e] *= ex2_approx_f(m[b][e] - nm), m[b][e] = nm;
+          if (nv > mv[b][e] + 8.f) {
+            const float by = ex2_approx_f(mv[b][e] - nv);
+            mv[b][e] = nv;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) o[j][b][e] *= by, o[j][b][2 + e] *= by;
+          }
+        }
+    }
+    // ---- probabilities: from (key, queries) to (query, keys) ----
+    uint32_t pb[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float um = m[b][e] == -INFINITY ? 0.f : m[b][e], uv = mv[b][e] == -INFINITY ? 0.f : mv[b][e];
+        const float ratio = ex2_approx_f(fminf(um + lv - uv, 126.f));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float w = ex2_approx_f(s[b][2 * h + e] - um);
+          l[b][e] += w;
+          y[2 * h + e] = w * ratio;
+        }
+      }
+      pb[b][0] = transpose8(pack_f16(y[0], y[1]));
+      pb[b][1] = transpose8(pack_f16(y[2], y[3]));
+    }
+    // ---- outputs: rows g and g + 8 of product j are dims 2 j and 2 j + 1 of the lane's ----
+    const uint32_t* w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t*>(&vc[x]);
+#pragma unroll
+    for (int i = 0; i < DIM / 32; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        // of two neighbouring keys a, b: a0 b0 a1 b1 (E4M3), a0 a1 b0 b1 (INT8), then those of 2 and 3
+        const uint32_t sel = F8 ? (z ? 0x7362 : 0x5140) : (z ? 0x7632 : 0x5410);
+        uint32_t a[4];
+        two(__byte_perm(w[0][i], w[1][i], sel), a[0], a[1]);
+        two(__byte_perm(w[2][i], w[3][i], sel), a[2], a[3]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) mma_f16(o[2 * i + z][b], a, pb[b][0], pb[b][1]);
+      }
+  }
+
+  // Outputs over this warp's keys to to[query][DIM], and log2 of the sums to lse[query].
+  __device__ __forceinline__ void finish(float* to, float* lse, int g, int t) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[b][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const float f = kv8_out_factor<GDN_QDQ_INT8>(mv[b][e], m[b][e], x);  // (V as it is)
+        const int row = 8 * b + 2 * t + e;
+        if (g == 0) lse[row] = x == 0.f ? -INFINITY : m[b][e] + log2f(x);
+#pragma unroll
+        for (int j = 0; j < MT; j += 2)
+          *reinterpret_cast<float4*>(to + row * DIM + DIM / 8 * g + 2 * j) =
+              make_float4(o[j][b][e] * f, o[j][b][2 + e] * f, o[j + 1][b][e] * f, o[j + 1][b][2 + e] * f);
+      }
+  }
+};
+
+// The queries of eight rows as operand; row g of this lane is query row i (have: it exists).
+// Gives the row's factor of the scores.
+template <int MODE, int DIM, class Put>
+__device__ __forceinline__ float load_rows(const Kv8Params& p, const __nv_bfloat16* x, bool have, int t, const Put& put) {
+  constexpr int KS = DIM / 16;
+  uint2 raw[KS];
+  float most = 0.f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    raw[s] = have ? *reinterpret_cast<const uint2*>(x + dim_of<DIM>(t, s / 4, s % 4)) : make_uint2(0, 0);
+    float f[4];
+    bf16x4(raw[s], f);
+    most = fmaxf(most, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+  }
+  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  float to, back;
+  kv8_q_factor<8>(most, to, back);
+#pragma unroll
+  for (int s = 0; s < KS; ++s) put(s, Rows<MODE, DIM, 1>::query_of(raw[s], to));
+  return back * p.scale * kLog2eF;
+}
+
+// A row's own tokens, and the join.  ROWS = 8 NB query rows of the CTA.
+template <int MODE, int DIM, int NB>
+__global__ void __launch_bounds__(kWarps * 32) kv8_own_kernel(const __grid_constant__ SharedArgs a) {
+  using R = Rows<MODE, DIM, NB>;
+  constexpr int ROWS = 8 * NB;
   __shared__ __align__(16) float s_o[kWarps][ROWS][DIM];
   __shared__ float s_lse[kWarps][ROWS];
   const Kv8Params& p = a.p;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
   const int64_t r = blockIdx.x / p.heads;
-  const int h = blockIdx.x % p.heads, i0 = blockIdx.y * ROWS, rows = min(p.tokens * p.group - i0, ROWS);
+  const int h = blockIdx.x % p.heads, i0 = blockIdx.y * ROWS, rows_in = min(p.tokens * p.group - i0, ROWS);
   const int64_t len = p.lengths[r];
   const int most = kv8_clamp(len, 0, (int64_t)p.cols * p.page);
   const int64_t grp = r / a.beams;
   const int common = common_of(a, grp), from = min(common, most);
   const int32_t* pages = p.table + r * p.cols;
-  const int per = p.heads * a.blocks, tiles = tiles_of(common);  // of the group's tokens
-  const int64_t before = tiles_before(a, grp, lane) * per;
-  const Shares shares(tiles_before(a, p.rows / a.beams, lane) * per, a.grid);
-
-  // ---- queries: fp16 by a power of two per row, in the order of the codes ----
-  uint32_t qf[KSTEPS][4];
-  float rowfac[NE];
-  int end[NE];
+  R rows;
+  rows.clear();
+  uint2 q[R::KS][NB];
+  int least = 0x7fffffff;
 #pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    const int i = i0 + g + 8 * e;
-    const bool have = g + 8 * e < rows;
-    end[e] = have ? seen_end(p, len, i / p.group) : 0;
+  for (int b = 0; b < NB; ++b) {
+    const int i = i0 + 8 * b + g;
     const __nv_bfloat16* x = p.x + r * p.x_row + (i / p.group) * p.x_token + (int64_t)(h * p.group + i % p.group) * p.x_head;
-    uint2 raw[KSTEPS];
-    float mx = 0.f;
+    const float f = load_rows<MODE, DIM>(p, x, 8 * b + g < rows_in, t, [&](int s, uint2 y) { q[s][b] = y; });
 #pragma unroll
-    for (int s = 0; s < KSTEPS; ++s) {
-      // step s: the four dims from 64 (s / 4) + 16 t + 4 (s % 4) on
-      raw[s] = have ? *reinterpret_cast<const uint2*>(x + 64 * (s / 4) + 16 * t + 4 * (s % 4)) : make_uint2(0, 0);
-      float f[4];
-      bf16x4(raw[s], f);
-      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    float to, back;
-    kv8_q_factor<8>(mx, to, back);
-    rowfac[e] = back * p.scale * kLog2eF * kRoot<MODE>;
-#pragma unroll
-    for (int s = 0; s < KSTEPS; ++s) {
-      float f[4];
-      bf16x4(raw[s], f);
-      qf[s][e] = pack_f16(f[0] * to, f[2] * to);
-      qf[s][2 + e] = pack_f16(f[1] * to, f[3] * to);
+    for (int e = 0; e < 2; ++e) {
+      const int c = 8 * b + 2 * t + e;
+      rows.fac[b][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
+      rows.lim[b][e] = c < rows_in ? seen_end(p, len, (i0 + c) / p.group) : 0;
+      if (c < rows_in) least = min(least, rows.lim[b][e]);
     }
   }
-  if constexpr (NE == 1) {
-#pragma unroll
-    for (int s = 0; s < KSTEPS; ++s) qf[s][1] = qf[s][3] = 0;
-  }
+  least = __reduce_min_sync(0xffffffffu, least);
 
-  float oacc[NT][4], lsum[NE], m[NE], mv[NE];
+  // ---- keys, 16 at a time; the next ones are on their way ----
+  const int t0 = from / 16 + warp, t1 = most > from ? (most + 15) / 16 : 0;
+  uint4 kc[2][R::KC];
+  typename R::V vc[4];
+  float ks = 0.f, vs = 0.f;
+  bool there = false;
+  int id = -1;
+  auto page_of = [&](int tile) { return tile < t1 ? pages[(tile * 16) >> p.shift] : -1; };
+  auto load = [&](int tile) {
+    there = id >= 0 && id < p.pages;
+    const int64_t block = (int64_t)(there ? id : 0) * p.heads + h;
+    const int y = tile * 16 & (p.page - 1);
+    ks = vs = 0.f;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-  for (int e = 0; e < NE; ++e) lsum[e] = 0.f, m[e] = mv[e] = -INFINITY;
-
-  // ---- keys ----
-  const int t0 = from / kTile, t1 = most > from ? (most + kTile - 1) / kTile : t0;
-  for (int tile = t0 + warp; tile < t1; tile += kWarps) {
-    const int j0 = tile * kTile;
-    int64_t block[2];
-    bool have[2];
-    float ks[2], lv[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int j = j0 + 16 * f;
-      const int id = j < most && (j >> p.shift) < p.cols ? pages[j >> p.shift] : -1;
-      have[f] = id >= 0 && id < p.pages;
-      block[f] = (int64_t)(have[f] ? id : 0) * p.heads + h;
-      ks[f] = 0.f, lv[f] = -INFINITY;
-      if (have[f]) {
-        const float2 sc = kv8_scales(p.scales[block[f]], p.scales[block[f] + p.pages * p.heads]);
-        ks[f] = sc.x * kRoot<MODE>, lv[f] = sc.y;
+      for (int c = 0; c < R::KC; ++c) {
+        kc[x][c] = make_uint4(0, 0, 0, 0);
+        if (there) kc[x][c] = __ldg(reinterpret_cast<const uint4*>(p.codes + (block * p.page + y + g + 8 * x) * DIM + dim_of<DIM>(t, c, 0)));
       }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      vc[x] = typename R::V();
+      if (there)
+        vc[x] = __ldg(reinterpret_cast<const typename R::V*>(
+            p.codes + ((block + p.pages * p.heads) * p.page + y + 2 * t + (x & 1) + 8 * (x >> 1)) * DIM + DIM / 8 * g));
     }
-    uint4 kc[4][KC];
-    V vc[2][4];
+    if (there) ks = p.scales[block], vs = p.scales[block + p.pages * p.heads];
+  };
+  id = page_of(t0);
+  if (t0 < t1) load(t0);
+  id = page_of(t0 + kWarps);
+  for (int tile = t0; tile < t1; tile += kWarps) {
+    uint4 k[2][R::KC];
+    typename R::V v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        kc[j][c] = make_uint4(0, 0, 0, 0);
-        if (have[j / 2])
-          kc[j][c] = __ldg(reinterpret_cast<const uint4*>(
-              p.codes + (block[j / 2] * p.page + ((j0 + 8 * j + g) & (p.page - 1))) * DIM + 64 * c + 16 * t));
-      }
+      for (int c = 0; c < R::KC; ++c) k[x][c] = kc[x][c];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        vc[k][x] = V();
-        if (have[k])
-          vc[k][x] = __ldg(reinterpret_cast<const V*>(
-              p.codes + ((block[k] + p.pages * p.heads) * p.page +
-                         ((j0 + 16 * k + 2 * t + (x & 1) + 8 * (x >> 1)) & (p.page - 1))) * DIM + DIM / 8 * g));
-      }
-    // ---- scores: n tile j = keys 8 j .. 8 j + 7 ----
-    float s[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint32_t w[4] = {kc[j][c].x, kc[j][c].y, kc[j][c].z, kc[j][c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b0, b1;
-          kv8_half2<MODE>(w[i], b0, b1);
-          mma_f16(s[j], qf[4 * c + i], b0, b1);
-        }
-      }
-    }
-    float top[NE][2];
-#pragma unroll
-    for (int e = 0; e < NE; ++e)
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float fac = rowfac[e] * ks[f];
-        float x = -INFINITY;
-#pragma unroll
-        for (int j = 2 * f; j < 2 * f + 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int at = j0 + 8 * j + 2 * t + i;
-            float y = s[j][2 * e + i] * fac;
-            if (at < from || at >= most || at >= end[e] || !have[f]) y = -INFINITY;
-            s[j][2 * e + i] = y;
-            x = fmaxf(x, y);
-          }
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        top[e][f] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      }
-    // ---- softmax: m the largest score, mv the largest score + log2 of V's scale ----
-    float by[NE];
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const float nm = fmaxf(m[e], fmaxf(top[e][0], top[e][1]));
-      const float nv = fmaxf(mv[e], fmaxf(top[e][0] + lv[0], top[e][1] + lv[1]));
-      const float um = nm == -INFINITY ? 0.f : nm, uv = nv == -INFINITY ? 0.f : nv;
-      lsum[e] *= ex2_approx_f(m[e] - um);
-      by[e] = ex2_approx_f(mv[e] - uv);
-      m[e] = nm, mv[e] = nv;
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float half = ex2_approx_f(fminf(um + lv[f] - uv, 126.f));
-#pragma unroll
-        for (int j = 2 * f; j < 2 * f + 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float w = ex2_approx_f(s[j][2 * e + i] - um);
-            lsum[e] += w;
-            s[j][2 * e + i] = w * half;
-          }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      oacc[i][0] *= by[0], oacc[i][1] *= by[0];
-      if constexpr (NE == 2) oacc[i][2] *= by[1], oacc[i][3] *= by[1];
-    }
-    // ---- output: n tile j = dims j, j + DIM / 8, ... ----
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t pf[4];
-      pf[0] = pack_f16(s[2 * k][0], s[2 * k][1]);
-      pf[1] = NE == 2 ? pack_f16(s[2 * k][2], s[2 * k][3]) : 0;
-      pf[2] = pack_f16(s[2 * k + 1][0], s[2 * k + 1][1]);
-      pf[3] = NE == 2 ? pack_f16(s[2 * k + 1][2], s[2 * k + 1][3]) : 0;
-      const uint32_t* w[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t*>(&vc[k][x]);
-#pragma unroll
-      for (int i = 0; i < DIM / 32; ++i)
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          // bytes of two neighbouring keys: (a0 a1 b0 b1), then (a2 a3 b2 b3)
-          uint32_t e0, o0, e1, o1;
-          kv8_half2<MODE>(__byte_perm(w[0][i], w[1][i], z ? 0x7632 : 0x5410), e0, o0);
-          kv8_half2<MODE>(__byte_perm(w[2][i], w[3][i], z ? 0x7632 : 0x5410), e1, o1);
-          mma_f16(oacc[4 * i + 2 * z], pf, e0, e1);
-          mma_f16(oacc[4 * i + 2 * z + 1], pf, o0, o1);
-        }
-    }
+    for (int x = 0; x < 4; ++x) v[x] = vc[x];
+    const float2 sc = there ? kv8_scales(ks, vs) : make_float2(0.f, -INFINITY);
+    const bool have = there;
+    if (tile + kWarps < t1) load(tile + kWarps);
+    id = page_of(tile + 2 * kWarps);
+    rows.step(k, v, [&](int s, int b) { return q[s][b]; }, sc.x, sc.y, !have || tile * 16 < from || tile * 16 + 16 > least,
+              tile * 16, from, most, have, g, t);
   }
-
-  // ---- the warps' parts: outputs over their own keys, and log2 of the sums ----
-#pragma unroll
-  for (int e = 0; e < NE; ++e) {
-    float l = lsum[e];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const float fac = kv8_out_factor<MODE>(mv[e], m[e], l);
-    if (t == 0) s_lse[warp][g + 8 * e] = l == 0.f ? -INFINITY : m[e] + log2f(l);
-    // columns 2 t and 2 t + 1 of n tile j: dims DIM / 8 (2 t) + j and DIM / 8 (2 t + 1) + j
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int j = 0; j < NT; j += 4)
-        *reinterpret_cast<float4*>(&s_o[warp][g + 8 * e][DIM / 8 * (2 * t + c) + j]) =
-            make_float4(oacc[j][2 * e + c] * fac, oacc[j + 1][2 * e + c] * fac, oacc[j + 2][2 * e + c] * fac,
-                        oacc[j + 3][2 * e + c] * fac);
-  }
+  rows.finish(&s_o[warp][0][0], s_lse[warp], g, t);
+  // places of the group's parts
+  const int per = p.heads * a.blocks, tiles = tiles_of(common);
+  int64_t before, all;
+  tiles_before(a, grp, lane, before, all);
+  before *= per;
+  const Shares shares(all * per, a.grid);
   __syncthreads();
   grid_dep_wait();  // the parts of the group's tokens
-  for (int i = warp; i < rows; i += kWarps) {
+  for (int i = warp; i < rows_in; i += kWarps) {
     // this row's parts: those of the CTAs whose shares meet its (group, head, block)
-    const int qi = (int)(r - grp * a.beams) * (p.tokens * p.group) + i0 + i, hq = h * a.blocks + qi / a.nq, col = qi % a.nq;
+    const int qi = (int)(r - grp * a.beams) * (p.tokens * p.group) + i0 + i, hq = h * a.blocks + qi / a.cw, col = qi % a.cw;
     int64_t c0 = 0;
     int n = 0;
     if (tiles > 0) {
@@ -890,17 +1140,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_own_kernel(const __grid_const
   }
 }
 
-int blocks_of(int64_t rows, int nq) { return (int)((rows + nq - 1) / nq); }
-
 // Sizes that both launches go by.
 SharedArgs sized(const Kv8Params& p, int beams) {
   SharedArgs a = {};
   a.p = p;
   a.beams = beams;
   const int64_t rows = (int64_t)beams * p.tokens * p.group;
-  a.nq = rows <= 64 ? 64 : 128;
-  a.blocks = blocks_of(rows, a.nq);
-  a.stride = (int)(rows < a.nq ? rows : a.nq);
+  a.cw = rows <= 32 ? 32 : 64;
+  a.blocks = (int)((rows + a.cw - 1) / a.cw);
+  a.stride = (int)(rows < a.cw ? rows : a.cw);
   const int64_t tiles = ((int64_t)p.cols * p.page + kKeys - 1) / kKeys * (p.rows / beams) * p.heads * a.blocks;
   a.grid = (int)(tiles < 152 ? tiles : 152);
   return a;
@@ -908,15 +1156,11 @@ SharedArgs sized(const Kv8Params& p, int beams) {
 // Parts: one for each (group, head, block), and one more for each CTA.
 int64_t slots_of(const SharedArgs& a) { return a.p.rows / a.beams * a.p.heads * a.blocks + a.grid; }
 
-template <int MODE, int DIM, int NQ>
-gdn_status run_common(const SharedArgs& a, cudaStream_t st) {
-  auto kern = kv8_common_kernel<MODE, DIM, NQ>;
-  constexpr int bytes = Room<DIM, NQ>::bytes;
+gdn_status launch_common(void (*kern)(SharedArgs), int bytes, const SharedArgs& a, cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GDN_ERR_CUDA;
   kern<<<a.grid, kThreads, bytes, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
-
 template <int MODE, int DIM>
 gdn_status run(SharedArgs& a, cudaStream_t st) {
   const Kv8Params& p = a.p;
@@ -929,7 +1173,8 @@ gdn_status run(SharedArgs& a, cudaStream_t st) {
                                   DIM == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return GDN_ERR_CUDA;
   if (a.grid > 0) {
-    const gdn_status s = a.nq == 64 ? run_common<MODE, DIM, 64>(a, st) : run_common<MODE, DIM, 128>(a, st);
+    const gdn_status s = a.cw == 32 ? launch_common(kv8_common_kernel<MODE, DIM, 32>, Room<MODE, DIM, 32>::bytes, a, st)
+                                    : launch_common(kv8_common_kernel<MODE, DIM, 64>, Room<MODE, DIM, 64>::bytes, a, st);
     if (s != GDN_OK) return s;
   }
   cudaLaunchConfig_t cfg = {};
@@ -941,8 +1186,8 @@ gdn_status run(SharedArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = a.grid > 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, kv8_own_kernel<MODE, DIM, 8>, a)
-                            : cudaLaunchKernelEx(&cfg, kv8_own_kernel<MODE, DIM, 16>, a);
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, kv8_own_kernel<MODE, DIM, 1>, a)
+                            : cudaLaunchKernelEx(&cfg, kv8_own_kernel<MODE, DIM, 2>, a);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -557,11 +557,10 @@ gdn_status gdn_kv8_append_rotary(const gdn_kv8_problem* p, const gdn_kv8_rotary*
  * gdn_kv8_attention, with these read once for a group of `beams` consecutive rows.
  * Positions below shared[g] of every row of group g = row / beams are looked up in
  * the table row of the group's first row, those from there on in the row's own.
- * shared counts tokens (any number: what is below 0 or past the table is cut).
- * What a query sees, NaNs and infinities, and the fewer bits of the probabilities
- * are as for gdn_kv8_attention; q enters exactly but for elements below 2^-25 of
- * the largest of their (query, head), which are off by at most 2^-33 of it.  A row's
- * result does not depend on its group's other rows, but for the tokens of the first.
+ * shared counts tokens; it is cut to what the first row has (0 .. lengths, and the
+ * table's columns).  What a query sees, NaNs and infinities, and the fewer bits of
+ * the probabilities and of q are as for gdn_kv8_attention.  A row's result does not
+ * depend on its group's other rows, but for the tokens of the first.
  * Not packed (cu_seqlens NULL: GDN_ERR_INVALID_ARG), no window
  * (GDN_ERR_UNSUPPORTED_MODE), rows a multiple of beams.
  *   shared i32 [rows / beams]; the others as for gdn_kv8_attention

@@ -51,7 +51,8 @@ def _check(got, q, codes, scales, table, lens, shared, beams, mode, scale, causa
     o, lse = (x.float().cpu().numpy().astype(np.float64) for x in got)
     q = q.float().cpu().numpy().astype(np.float64)
     for r, n in enumerate(lens):
-        ro, rl, absum, top, dots = ref.attention_shared(q[r], codes, scales, table[r // beams * beams], table[r], int(shared[r // beams]),
+        first = r // beams * beams
+        ro, rl, absum, top, dots = ref.attention_shared(q[r], codes, scales, table[first], table[r], min(int(shared[r // beams]), int(lens[first])),
                                                         int(n), mode, scale, causal)
         seen = np.isfinite(rl)
         assert np.array_equal(np.isneginf(lse[r]), ~seen)
