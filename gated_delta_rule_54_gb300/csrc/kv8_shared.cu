@@ -38,8 +38,8 @@ namespace {
 
 __device__ int g_kv8_shared_error;
 
-constexpr int kTile = 32, kWarps = 4;  // own tokens: keys of a tile, warps of a CTA
-constexpr int kKeys = 128;             // the group's tokens: keys of a tile
+constexpr int kWarps = 4;   // own tokens: warps of a CTA
+constexpr int kKeys = 128;  // the group's tokens: keys of a tile
 
 // Warps of the first kernel: two groups of four take the tiles in turn, so that one's exponentials
 // run in the other's latencies; eight turn codes into fp16 (E4M3: all V's, else half of them K's).
@@ -236,7 +236,7 @@ template <int MODE, int DIM, int CW>
 struct Room {
   static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
   static constexpr int raw = kKeys * DIM, tile = 2 * raw, ptile = kKeys * CW * 2;
-  static constexpr int raws = CW == 32 ? (f8 ? 4 : 3) : (f8 ? 3 : 2), vtiles = 2, ktiles = f8 ? 0 : 1;
+  static constexpr int raws = CW == 32 ? (f8 ? 4 : 2) : (f8 ? 3 : 2), vtiles = 2, ktiles = f8 ? 0 : CW == 32 ? 2 : 1;
   static constexpr int k = 0, v = raws * raw, vt = v + raws * raw, zero = vt + vtiles * tile;
   static constexpr int kt = zero + (DIM == 64 ? kKeys * 128 : 0), q = kt + ktiles * tile, pt = q + CW * DIM * 2;
   static constexpr int bytes = pt + kGroups * ptile + 1024;
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
   extern __shared__ unsigned char smem_raw[];
   // codes there, and free; fp16 tiles there, and free
   __shared__ __align__(8) uint64_t kin[R::raws], kout[R::raws], vin[R::raws], vout[R::raws];
-  __shared__ __align__(8) uint64_t kfull, kfree, vfull[R::vtiles], vfree[R::vtiles];
+  constexpr int kKTiles = F8 ? 1 : R::ktiles;
+  __shared__ __align__(8) uint64_t kfull[kKTiles], kfree[kKTiles], vfull[R::vtiles], vfree[R::vtiles];
   __shared__ __align__(8) uint64_t sfull[G], sfree[G], pready[G], odone[G], qready;
   __shared__ float2 meta[16][8];  // [tile]: per 16 keys K scale, log2 of V scale
   __shared__ int valid[16];       // bit c: they have a page
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
       mbar_init(&kout[i], F8 ? 1 : 4), mbar_init(&vout[i], F8 ? 8 : 4);
     }
     for (int i = 0; i < R::vtiles; ++i) mbar_init(&vfull[i], F8 ? 8 : 4), mbar_init(&vfree[i], 1);
-    mbar_init(&kfull, 4), mbar_init(&kfree, 1);
+    for (int i = 0; i < kKTiles; ++i) mbar_init(&kfull[i], 4), mbar_init(&kfree[i], 1);
     for (int i = 0; i < G; ++i) mbar_init(&sfull[i], 1), mbar_init(&sfree[i], 4), mbar_init(&pready[i], 4), mbar_init(&odone[i], 1);
     mbar_init(&qready, kSoft);
     abort_flag = 0;
@@ -645,14 +646,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
         warp_arrive(&vfull[out.at]);
       }
     } else {
-      for (uint32_t n = 0; n < all; ++n, in.next()) {
+      Ring<kKTiles> out;
+      for (uint32_t n = 0; n < all; ++n, in.next(), out.next()) {
         if (!all_wait(&kin[in.at], in.turn)) break;
         uint4 u[kMine];
         read(u, smem + R::k + in.at * R::raw);
         warp_arrive(&kout[in.at]);
-        if (!all_wait(&kfree, (n & 1) ^ 1)) break;
-        write(u, smem + R::kt);
-        warp_arrive(&kfull);
+        if (!all_wait(&kfree[out.at], out.turn ^ 1)) break;
+        write(u, smem + R::kt + out.at * R::tile);
+        warp_arrive(&kfull[out.at]);
       }
     }
   } else {
@@ -728,17 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     uint32_t n = 0;
     if (warp == kIssueQK) {
       const uint32_t dk = desc_lo(base + (F8 ? R::k : R::kt), 16), dq = desc_lo(base + R::q, 16);
-      Ring<R::raws> kb;
+      Ring<F8 ? R::raws : kKTiles> kb;
+      uint64_t *there = F8 ? kin : kfull, *gone = F8 ? kout : kfree;
       for (uint32_t pieces = 0; left > 0 && ok; w.next(a), ++pieces) {
         const uint32_t nt = (uint32_t)__shfl_sync(0xffffffffu, w.count(), 0);
         ok = all_wait(&qready, pieces & 1);
         for (uint32_t i = 0; i < nt; ++i, ++n) {
           const uint32_t g = n & (G - 1);
-          ok = ok && (F8 ? all_wait(&kin[kb.at], kb.turn) : all_wait(&kfull, n & 1)) && all_wait(&sfree[g], (n / G & 1) ^ 1);
+          ok = ok && all_wait(&there[kb.at], kb.turn) && all_wait(&sfree[g], (n / G & 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
           if (lead) {
-            const uint32_t d = tm + g * CW, k = dk + (F8 ? kb.at * (R::raw >> 4) : 0);
+            const uint32_t d = tm + g * CW, k = dk + kb.at * ((F8 ? R::raw : R::tile) >> 4);
             if constexpr (F8) {
               constexpr int kRow = DIM / 32;
 #pragma unroll
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
               for (int s = 0; s < DIM / 16; ++s)
                 umma_ss(d, k + (s / 4 * (kKeys * 128) >> 4) + (s % 4) * 2, dq + (s / 4 * (CW * 128) >> 4) + (s % 4) * 2, kIdQK, s > 0);
             }
-            umma_commit(F8 ? &kout[kb.at] : &kfree);
+            umma_commit(&gone[kb.at]);
             umma_commit(&sfull[g]);  // (the one that is waited for at the end)
           }
           __syncwarp();
