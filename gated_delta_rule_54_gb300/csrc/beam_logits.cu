@@ -15,7 +15,8 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostSlice = 8192;  // tokens of a slice: their counts take 32 KB
+constexpr int kLoads = 4;                           // of eight logits, of a thread
+constexpr int kMostSlice = 8 * kThreads * kLoads;  // tokens of a slice: their counts take 32 KB
 
 struct LogitsParams {
   const void* logits;
@@ -33,26 +34,38 @@ __device__ __forceinline__ void store_one(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Eight neighbouring logits, aligned to 16 bytes.
-__device__ __forceinline__ void load_eight(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load_eight(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  float a[2];
-  bf16x2(u.x, a), x[0] = a[0], x[1] = a[1];
-  bf16x2(u.y, a), x[2] = a[0], x[3] = a[1];
-  bf16x2(u.z, a), x[4] = a[0], x[5] = a[1];
-  bf16x2(u.w, a), x[6] = a[0], x[7] = a[1];
-}
-__device__ __forceinline__ void store_eight(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store_eight(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    float a[2];
+    bf16x2(u.x, a), x[0] = a[0], x[1] = a[1];
+    bf16x2(u.y, a), x[2] = a[0], x[3] = a[1];
+    bf16x2(u.z, a), x[4] = a[0], x[5] = a[1];
+    bf16x2(u.w, a), x[6] = a[0], x[7] = a[1];
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
 
 // What a row's history does to the logit of a token that is in it n > 0 times; every step is
 // rounded to fp32.
@@ -68,50 +81,106 @@ struct Penalty {
 template <typename T, bool HISTORY, bool WIDE>
 __global__ void __launch_bounds__(kThreads) beam_logits_kernel(const __grid_constant__ LogitsParams p) {
   extern __shared__ uint32_t counts[];
-  const int64_t row = blockIdx.x / p.slices;
-  const int from = (int)(blockIdx.x % p.slices) * p.slice, n = min(p.slice, p.vocab - from), tid = threadIdx.x;
+  const int64_t row = blockIdx.x / (uint32_t)p.slices;
+  const int from = (int)(blockIdx.x % (uint32_t)p.slices) * p.slice, n = min(p.slice, p.vocab - from), tid = threadIdx.x;
   const T* in = static_cast<const T*>(p.logits) + row * p.stride + from;
   T* out = static_cast<T*>(p.out) + row * p.vocab + from;
   const float* bias = p.bias ? p.bias + row * p.bias_row + from : nullptr;
   const uint32_t* mask = p.mask ? p.mask + row * p.mask_row + from / 32 : nullptr;
+
+  // the slice's mask and logits are on their way while the history is counted
+  const int wide = WIDE ? n / 8 * 8 : 0;
+  uint32_t may[kLoads];
+  Eight<T> x8[kLoads];
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = 8 * (tid + j * kThreads);
+      may[j] = i < wide ? mask ? __ldg(mask + i / 32) >> (i % 32) & 0xffu : 0xffu : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (may[j]) x8[j].load(in + 8 * (tid + j * kThreads));
+  }
   Penalty penalty = {1.f, 0.f, 0.f};
   if constexpr (HISTORY) {
     if (p.repetition) penalty.repetition = p.repetition[row];
     if (p.frequency) penalty.frequency = p.frequency[row];
     if (p.presence) penalty.presence = p.presence[row];
+    const int len = p.lengths ? max(min(p.lengths[row], p.cols), 0) : p.cols;
     for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const int32_t* said = p.tokens + row * p.cols;
-    const int len = p.lengths ? max(min(p.lengths[row], p.cols), 0) : p.cols;
-    for (int i = tid; i < len; i += kThreads) {
-      const int64_t at = (int64_t)said[i] - from;
+    auto count = [&](int32_t t) {
+      const int64_t at = (int64_t)t - from;
       if (at >= 0 && at < n) atomicAdd(&counts[at], 1u);
+    };
+    // eight tokens of a thread in flight
+    for (int i0 = tid; i0 < len; i0 += 8 * kThreads) {
+      int32_t t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = i0 + j * kThreads < len ? __ldg(said + i0 + j * kThreads) : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) count(t[j]);
     }
     __syncthreads();
   }
   auto one = [&](float x, int i) {
     if constexpr (HISTORY)
       if (const uint32_t c = counts[i]) x = penalty(x, c);
-    if (bias) x = __fadd_rn(x, __ldg(bias + i));
-    return x;
+    return bias ? __fadd_rn(x, __ldg(bias + i)) : x;
   };
-  const int wide = WIDE ? n / 8 * 8 : 0;
   if constexpr (WIDE) {
-    for (int i = 8 * tid; i < wide; i += 8 * kThreads) {
-      const uint32_t may = mask ? __ldg(mask + i / 32) >> (i % 32) & 0xffu : 0xffu;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = 8 * (tid + j * kThreads);
+      if (i >= wide) break;
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = -INFINITY;
-      if (may) {
-        load_eight(in + i, x);
+      if (may[j]) {
+        x8[j].get(x);
+        if constexpr (HISTORY) {
+          const uint4 c0 = *reinterpret_cast<const uint4*>(counts + i), c1 = *reinterpret_cast<const uint4*>(counts + i + 4);
+          const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          if (c0.x | c0.y | c0.z | c0.w | c1.x | c1.y | c1.z | c1.w) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = may >> e & 1 ? one(x[e], i + e) : -INFINITY;
+            for (int e = 0; e < 8; ++e)
+              if (c[e]) x[e] = penalty(x[e], c[e]);
+          }
+        }
+        if (bias) {
+          Eight<float> b8;
+          float b[8];
+          b8.load(bias + i);
+          b8.get(b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(x[e], b[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!(may[j] >> e & 1)) x[e] = -INFINITY;
       }
-      store_eight(out + i, x);
+      Eight<T>::store(out + i, x);
     }
   }
-  for (int i = wide + tid; i < n; i += kThreads)
-    store_one(out + i, !mask || __ldg(mask + i / 32) >> (i % 32) & 1 ? one(load_one(in + i), i) : -INFINITY);
+  // what is left, or all where rows are not aligned: eight of a thread in flight
+  for (int i0 = wide + tid; i0 < n; i0 += 8 * kThreads) {
+    float x[8];
+    bool ok[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kThreads;
+      ok[j] = i < n && (!mask || (__ldg(mask + i / 32) >> (i % 32) & 1));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = ok[j] ? load_one(in + i0 + j * kThreads) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < n) store_one(out + i, ok[j] ? one(x[j], i) : -INFINITY);
+    }
+  }
 }
 
 gdn_status validate_logits(const gdn_logits_problem* p) {
@@ -176,7 +245,7 @@ gdn_status gdn_beam_logits(const gdn_logits_problem* p, const void* logits, cons
   q.slices = (p->vocab + q.slice - 1) / q.slice;
   const int64_t blocks = p->rows * q.slices;
   if (blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  const bool wide = ((a | b) & 15) == 0 && (p->rows == 1 || (stride * elem % 16 == 0 && p->vocab * elem % 16 == 0));
+  const bool wide = ((a | b | (uintptr_t)bias) & 15) == 0 && p->bias_row % 4 == 0 && (p->rows == 1 || (stride * elem % 16 == 0 && p->vocab * elem % 16 == 0));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool counts = history && p->cols > 0;
   if (p->dtype == GDN_DTYPE_BF16)
