@@ -79,7 +79,7 @@ struct Penalty {
 
 // HISTORY: there are penalties.  WIDE: rows are aligned to 16 bytes.
 template <typename T, bool HISTORY, bool WIDE>
-__global__ void __launch_bounds__(kThreads) beam_logits_kernel(const __grid_constant__ LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, 5) beam_logits_kernel(const __grid_constant__ LogitsParams p) {
   extern __shared__ uint32_t counts[];
   const int64_t row = blockIdx.x / (uint32_t)p.slices;
   const int from = (int)(blockIdx.x % (uint32_t)p.slices) * p.slice, n = min(p.slice, p.vocab - from), tid = threadIdx.x;
@@ -108,20 +108,23 @@ __global__ void __launch_bounds__(kThreads) beam_logits_kernel(const __grid_cons
     if (p.frequency) penalty.frequency = p.frequency[row];
     if (p.presence) penalty.presence = p.presence[row];
     const int len = p.lengths ? max(min(p.lengths[row], p.cols), 0) : p.cols;
+    // eight tokens of a thread in flight, the first ones before it is known how many count
+    const int32_t* said = p.tokens + row * p.cols;
+    int32_t t[8];
+    auto fetch = [&](int i0, int most) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = i0 + j * kThreads < most ? __ldg(said + i0 + j * kThreads) : -1;
+    };
+    fetch(tid, p.cols);
     for (int i = tid; i < (n + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const int32_t* said = p.tokens + row * p.cols;
-    auto count = [&](int32_t t) {
-      const int64_t at = (int64_t)t - from;
-      if (at >= 0 && at < n) atomicAdd(&counts[at], 1u);
-    };
-    // eight tokens of a thread in flight
     for (int i0 = tid; i0 < len; i0 += 8 * kThreads) {
-      int32_t t[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = i0 + j * kThreads < len ? __ldg(said + i0 + j * kThreads) : -1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) count(t[j]);
+      for (int j = 0; j < 8; ++j) {
+        const int64_t at = (int64_t)t[j] - from;
+        if (at >= 0 && at < n && i0 + j * kThreads < len) atomicAdd(&counts[at], 1u);
+      }
+      if (i0 + 8 * kThreads < len) fetch(i0 + 8 * kThreads, len);
     }
     __syncthreads();
   }
