@@ -28,6 +28,8 @@ _BEAM = struct.Struct("@2q5i0q").pack
 _ROTARY = struct.Struct("@4q2i").pack
 _LOGITS = struct.Struct("@4q3i0q").pack
 _TOO_SMALL = -5  # GDN_ERR_WORKSPACE_TOO_SMALL
+_contiguous = torch.contiguous_format
+_shared_bytes = {}  # of the workspace, by the problem's sizes
 
 
 def _fns():
@@ -193,18 +195,20 @@ def kv8_append_rotary(q, k, v, codes, scales, table, start, cos, sin, interleave
     have, and so are the scales of key blocks written there; 0 for packed tokens of no row; and NaN
     for a packed row with more than ``max_seqlen`` tokens."""
     dev, qs, ks, cs = codes.get_device(), q.shape, k.shape, cos.shape
-    heads = ks[-2] if len(ks) >= 3 else 0
-    if not (heads > 0 and len(qs) == len(ks) and qs[:-2] == ks[:-2] and qs[-1] == ks[-1] and qs[-2] > 0
-            and qs[-2] % heads == 0 and q.get_device() == dev and q.dtype is k.dtype and _plain(cos, _f32, dev)
-            and _plain(sin, _f32, dev) and len(cs) == 2 and sin.shape == cs):
-        _need(len(ks) >= 3 and heads > 0, "expected k of [rows, tokens, heads, dim] or [total, heads, dim]")
+    n = len(ks)
+    heads, xh = (ks[-2], qs[-2]) if n >= 3 and len(qs) == n else (0, 0)
+    if not (heads > 0 and xh > 0 and xh % heads == 0 and qs[0] == ks[0] and qs[-1] == ks[-1] and (n == 3 or qs[1] == ks[1])
+            and q.dtype is k.dtype and q.get_device() == dev and cos.dtype is _f32 and sin.dtype is _f32
+            and cos.get_device() == dev and sin.get_device() == dev and cos.is_contiguous() and sin.is_contiguous()
+            and len(cs) == 2 and sin.shape == cs):
+        _need(n >= 3 and ks[-2] > 0, "expected k of [rows, tokens, heads, dim] or [total, heads, dim]")
         _bad_rotary(q, k, cos, sin, dev)
-    p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, 1, 0, qs[-2] // heads)
+    p = _problem(k, v, codes, scales, table, start, cu_seqlens, max_seqlen, mode, 1.0, 1, 0, xh // heads)
     w = _ROTARY(cs[0], *_strides(q, qs), 2 * cs[1], 1 if interleaved else 0)
-    out = torch.empty(qs, dtype=_bf16, device=codes.device)
+    out = torch.empty_like(q, dtype=_bf16, memory_format=_contiguous)
     st = _launch(
-        dev, _fns().gdn_kv8_append_rotary, p, w, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(), codes.data_ptr(),
-        scales.data_ptr(), table.data_ptr(), start.data_ptr(), out.data_ptr())
+        dev, _fns().gdn_kv8_append_rotary, p, w, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos.data_ptr(), sin.data_ptr(),
+        codes.data_ptr(), scales.data_ptr(), table.data_ptr(), start.data_ptr(), out.data_ptr())
     if st:
         _raise("gdn_kv8_append_rotary", st)
     return out
@@ -269,14 +273,18 @@ def kv8_attention_shared(q, codes, scales, table, lengths, shared, beams, mode="
     _need(beams > 0 and q.shape[0] % beams == 0 and shared.shape == (q.shape[0] // beams,),
           "rows must be a multiple of beams, and shared [rows / beams]")
     if out is None:
-        out = torch.empty(q.shape, dtype=_bf16, device=codes.device)
+        out = torch.empty_like(q, dtype=_bf16, memory_format=_contiguous)
     else:
         _say(dev, ("out", out, _bf16))
         _need(out.shape == q.shape, "out must have q's shape")
-    lse = torch.empty(q.shape[:-1], dtype=_f32, device=codes.device) if need_lse else None
+    lse = torch.empty_like(q[..., 0], dtype=_f32, memory_format=_contiguous) if need_lse else None
     lib = _fns()
     if workspace is None:
-        need = lib.gdn_kv8_shared_workspace_bytes(p, beams)
+        need = _shared_bytes.get((p, beams))
+        if need is None:
+            if len(_shared_bytes) >= 256:
+                _shared_bytes.clear()
+            need = _shared_bytes[p, beams] = lib.gdn_kv8_shared_workspace_bytes(p, beams)
         if need:
             workspace = torch.empty(need, dtype=_u8, device=codes.device)
     st = _launch(
@@ -422,10 +430,10 @@ def _per_row(name, t, lead, width, dev, dtype):
     _need(isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype,
           "%s must be %s on cuda:%d" % (name, dtype, dev))
     shape, st = t.shape, t.stride()
-    _need(t.dim() > 0 and shape[-1] >= width and (shape[-1] == 1 or st[-1] == 1) and (
-        t.dim() == 1 or shape[:-1] == lead),
+    _need(len(shape) > 0 and shape[-1] >= width and (shape[-1] == 1 or st[-1] == 1) and (
+        len(shape) == 1 or tuple(shape[:-1]) == lead),
           "%s must be [%d] or [batch, beams, %d], the last dim contiguous" % (name, width, width))
-    if t.dim() == 1:
+    if len(shape) == 1:
         return t.data_ptr(), 0
     row = st[1] if lead[1] > 1 else st[0] if lead[0] > 1 else 0
     _need(lead[0] <= 1 or lead[1] <= 1 or st[0] == lead[1] * row, "rows of %s must be evenly spaced" % name)
@@ -446,8 +454,8 @@ def beam_logits(logits, tokens=None, lengths=None, repetition=None, frequency=No
     rounded once.  Returns logits like those given, contiguous; ``out`` may be the logits themselves."""
     dev = logits.get_device()
     _need(dev >= 0 and logits.dim() == 3, "logits must be [batch, beams, vocab] on CUDA")
-    b, w, v = lead = logits.shape
-    lead, s = lead[:2], logits.stride()
+    (b, w, v), s = logits.shape, logits.stride()
+    lead = (b, w)
     _need(v == 1 or s[2] == 1, "the vocabulary must be contiguous")
     row = s[1] if w > 1 else s[0] if b > 1 else v
     _need(w <= 1 or b <= 1 or s[0] == w * row, "rows of logits must be evenly spaced")
@@ -458,8 +466,9 @@ def beam_logits(logits, tokens=None, lengths=None, repetition=None, frequency=No
     else:
         if not _plain(tokens, _i32, dev):
             _say(dev, ("tokens", tokens, _i32))
-        _need(tokens.dim() == 3 and tokens.shape[:2] == lead, "tokens must be [batch, beams, columns]")
-        cols = tokens.shape[2]
+        ts = tokens.shape
+        _need(len(ts) == 3 and ts[0] == b and ts[1] == w, "tokens must be [batch, beams, columns]")
+        cols = ts[2]
         for name, t, dtype in (("lengths", lengths, _i32), ("repetition", repetition, _f32),
                                ("frequency", frequency, _f32), ("presence", presence, _f32)):
             if t is not None:
@@ -469,7 +478,7 @@ def beam_logits(logits, tokens=None, lengths=None, repetition=None, frequency=No
     bias_at, bias_row = _per_row("bias", bias, lead, v, dev, _f32)
     mask_at, mask_row = _per_row("mask", mask, lead, (v + 31) // 32, dev, _i32)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = torch.empty_like(logits, memory_format=_contiguous)
     else:
         _say(dev, ("out", out, logits.dtype))
         _need(out.shape == logits.shape, "out must have the logits' shape")
