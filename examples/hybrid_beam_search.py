@@ -2,12 +2,14 @@
 
 The model is small and its weights are random; what it shows is how the pieces meet:
 
-  prompt   gdn_chunk_fwd_qdq gives each GDN layer's state, kv8_append and kv8_attention take the
-           prompt through the attention layers
+  prompt   gdn_chunk_fwd_qdq gives each GDN layer's state, kv8_append_rotary and kv8_attention take
+           the prompt through the attention layers
   step     kv8_reserve makes room for one token per row, gdn_decode_qdq steps the states in
-           place, kv8_append and kv8_attention the caches
-  beams    beam_select picks the continuations; beam_reorder moves the states with them and
-           kv8_fork the pages (shared where they are full, copied where they are not)
+           place, kv8_append_rotary and kv8_attention the caches (kv8_attention_shared where the
+           beams' prompt is to be read once for all of them)
+  beams    beam_logits applies what is asked against repetitions, beam_select picks the
+           continuations; beam_reorder moves the states with them and kv8_fork the pages (shared
+           where they are full, copied where they are not)
   end      kv8_compact packs what is live
 
 Nothing in a step waits for the host.  Run: python examples/hybrid_beam_search.py
@@ -84,6 +86,10 @@ class Session:
     lengths: torch.Tensor
     refs: torch.Tensor
     missing: torch.Tensor = field(default=None)
+    cos: torch.Tensor = field(default=None)     # angles of the positions
+    sin: torch.Tensor = field(default=None)
+    shared: torch.Tensor = field(default=None)  # tokens that each prompt's beams have in common, if these are read once
+    beams: int = 1
 
 
 def start(model: HybridModel, rows: int, pages: int, columns: int) -> Session:
@@ -91,8 +97,10 @@ def start(model: HybridModel, rows: int, pages: int, columns: int) -> Session:
     codes, scales = gdn.kv8_pool(c.layers.count("a"), pages, c.heads, c.dim, page=c.page)
     i32 = dict(dtype=torch.int32, device="cuda")
     states = [torch.zeros(rows, c.heads * c.group, c.dim, c.dim, device="cuda") for k in c.layers if k == "g"]
+    angles = torch.arange(columns * c.page, dtype=torch.float64, device="cuda")[:, None] * (
+        10000.0 ** (-torch.arange(c.dim // 2, dtype=torch.float64, device="cuda") * 2 / c.dim))
     return Session(states, codes, scales, torch.full((rows, columns), -1, **i32), torch.zeros(rows, **i32),
-                   torch.zeros(pages, **i32), torch.zeros(1, **i32))
+                   torch.zeros(pages, **i32), torch.zeros(1, **i32), angles.cos().float(), angles.sin().float())
 
 
 def advance(model: HybridModel, s: Session, tokens: torch.Tensor) -> torch.Tensor:
@@ -116,26 +124,44 @@ def advance(model: HybridModel, s: Session, tokens: torch.Tensor) -> torch.Tenso
             o = o.to(torch.bfloat16)
             state += 1
         else:
-            gdn.kv8_append(k, v, s.codes[cache], s.scales[cache], s.table, first, mode=c.mode)
-            o = gdn.kv8_attention(q, s.codes[cache], s.scales[cache], s.table, s.lengths, mode=c.mode)
+            held = s.codes[cache], s.scales[cache], s.table
+            q = gdn.kv8_append_rotary(q, k, v, *held, first, s.cos, s.sin, mode=c.mode)
+            if s.shared is None or n > 1:
+                o = gdn.kv8_attention(q, *held, s.lengths, mode=c.mode)
+            else:
+                o = gdn.kv8_attention_shared(q, *held, s.lengths, s.shared, s.beams, mode=c.mode)
             cache += 1
         x = x + o.flatten(2) @ model.out[layer]
     return model.logits(x[:, -1])
 
 
-def search(model: HybridModel, prompts: torch.Tensor, beams: int, steps: int, eos: int = 1, pages: int = None):
-    """prompts [batch, n] -> (tokens [batch, beams, steps], scores [batch, beams], the session)."""
+def share(s: Session, batch: int, beams: int, tokens: int):
+    """From here on the first ``tokens`` of each prompt's beams are read once for all of them."""
+    s.shared, s.beams = torch.full((batch,), tokens, dtype=torch.int32, device="cuda"), beams
+
+
+def search(model: HybridModel, prompts: torch.Tensor, beams: int, steps: int, eos: int = 1, pages: int = None,
+           shared: bool = False, frequency: float = 0.0):
+    """prompts [batch, n] -> (tokens [batch, beams, steps], scores [batch, beams], the session).
+    shared: the whole pages of a prompt are read once for its beams; frequency: what each time that a
+    beam has said a token costs the next one."""
     batch, n = prompts.shape
     page, rows = model.cfg.page, batch * beams
     columns = -(-(n + steps) // page)
     s = start(model, rows, rows * columns + rows if pages is None else pages, columns)
     logits = advance(model, s, prompts.repeat_interleave(beams, 0))
+    if shared:
+        share(s, batch, beams, n // page * page)
+    cost = torch.full((batch, beams), frequency, device="cuda")
     scores = torch.full((batch, beams), float("-inf"), device="cuda")
     scores[:, 0] = 0.0                       # the beams are one and the same so far
     done = torch.zeros(batch, beams, dtype=torch.bool, device="cuda")
     history = torch.zeros(rows, 0, dtype=torch.int32, device="cuda")
     for step in range(steps):
-        scores, parents, tokens, done = gdn.beam_select(logits.view(batch, beams, -1), scores, done, eos=eos)
+        logits = logits.view(batch, beams, -1)
+        if frequency:
+            logits = gdn.beam_logits(logits, history.view(batch, beams, step), frequency=cost)
+        scores, parents, tokens, done = gdn.beam_select(logits, scores, done, eos=eos)
         parents = parents.flatten()
         gdn.beam_reorder(s.states, parents, beams)
         s.table, s.lengths, s.refs, missing = gdn.kv8_fork(s.codes, s.scales, s.table, s.lengths, parents, s.refs)
@@ -150,7 +176,7 @@ def search(model: HybridModel, prompts: torch.Tensor, beams: int, steps: int, eo
 def main():
     model = HybridModel(Config())
     prompts = torch.randint(2, model.cfg.vocab, (3, 75), generator=torch.Generator().manual_seed(1)).cuda()
-    tokens, scores, s = search(model, prompts, beams=4, steps=24)
+    tokens, scores, s = search(model, prompts, beams=4, steps=24, shared=True, frequency=0.5)
     live = int((s.refs > 0).sum())
     print("pages: %d live of %d (a copy per row would hold %d), %d missing" % (
         live, s.refs.numel(), int(((s.lengths + model.cfg.page - 1) // model.cfg.page).sum()), int(s.missing)))
