@@ -41,14 +41,27 @@ __device__ int g_kv8_shared_error;
 constexpr int kWarps = 4;   // own tokens: warps of a CTA
 constexpr int kKeys = 128;  // the group's tokens: keys of a tile
 
-// Warps of the first kernel: two groups of four take the tiles in turn, so that one's exponentials
-// run in the other's latencies; eight turn codes into fp16 (E4M3: all V's, else half of them K's).
-constexpr int kGroups = 2, kSoft = 4 * kGroups, kConv = 8;
-constexpr int kIssueQK = kSoft + kConv, kIssuePV = kIssueQK + 1, kLoadK = kIssueQK + 2, kLoadV = kIssueQK + 3;
-constexpr int kThreads = (kSoft + kConv + 4) * 32;
-// registers per thread of the warpgroups: together no more than the launch gave (5 x 96)
-constexpr int kSoftRegs = 144, kConvRegs = 64, kRestRegs = 64;
-static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * 96, "register shares");
+// The first kernel: CW query rows (columns) of a block, N of a product.  Units of four warps have 16
+// columns of a tile each, so that what they go through per tile is short (a unit with all
+// columns spent its time on fetching instructions); the units that this leaves take other
+// tiles: `sets` tiles are worked on at a time.  Warps turn codes into fp16: V's (E4M3), or K's
+// and V's, by the same four in turn or by four each.  More warps than these would leave a thread
+// fewer registers than it takes.
+template <int MODE, int CW>
+struct Plan {
+  static constexpr bool f8 = MODE == GDN_QDQ_E4M3, both = !f8 && CW == 64;
+  static constexpr int units = CW == 64 ? 4 : 2, soft = 4 * units, conv = CW == 64 || f8 ? 4 : 8;
+  static constexpr int issue_qk = soft + conv, issue_pv = issue_qk + 1, load_k = issue_qk + 2, load_v = issue_qk + 3;
+  static constexpr int threads = (soft + conv + 4) * 32;
+  // registers per thread of the warpgroups: together no more than the launch gave
+  static constexpr int launch_regs = units == 4 ? 80 : conv == 4 ? 120 : 96;
+  static constexpr int soft_regs = units == 4 ? 96 : 144, conv_regs = units == 4 ? 48 : 64, rest_regs = conv_regs;
+  static_assert(units * soft_regs + conv / 4 * conv_regs + rest_regs <= threads / 128 * launch_regs, "register shares");
+  static_assert(threads * launch_regs <= 65536, "registers");
+  static constexpr int per_tile = CW / 16, sets = units / per_tile, n = CW < 32 ? 32 : CW;
+  static constexpr int s_cols = 2 * sets * n;  // S: two of each set; then O, one of each
+  static constexpr uint32_t cols = s_cols + sets * n > 256 ? 512 : 256;
+};
 
 struct SharedArgs {
   Kv8Params p;
@@ -159,8 +172,9 @@ struct Walk {
     t = 0;
     if (++hq < a.p.heads * a.blocks) return;
     hq = 0;
-    do common = common_of(a, ++g), tiles = tiles_of(common);
-    while (tiles == 0);
+    const int64_t groups = a.p.rows / (uint32_t)a.beams;
+    for (tiles = 0; tiles == 0 && ++g < groups;) common = common_of(a, g), tiles = tiles_of(common);
+    if (tiles == 0) left = 0;
   }
   __device__ __forceinline__ int64_t slot(const SharedArgs& a, int64_t cta) const {
     return g * a.p.heads * a.blocks + hq + cta;
@@ -190,28 +204,28 @@ __device__ __forceinline__ float half_reduce(float (&x)[16], int lane) {
   return x[0];
 }
 
-// Barriers of a group's four warps, and of all groups'.
-__device__ __forceinline__ void group_sync(int g) {
-  asm volatile("bar.sync %0, 128;\n" ::"r"(1 + g) : "memory");
+// Barriers of a unit's four warps, and of all units'.
+__device__ __forceinline__ void unit_sync(int unit) {
+  asm volatile("bar.sync %0, 128;\n" ::"r"(1 + unit) : "memory");
 }
 // the same, and whether any of the threads says yes
-__device__ __forceinline__ bool group_any(int g, bool yes) {
+__device__ __forceinline__ bool unit_any(int unit, bool yes) {
   uint32_t any;
   asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                : "=r"(any)
-               : "r"((uint32_t)yes), "r"(1 + g)
+               : "r"((uint32_t)yes), "r"(1 + unit)
                : "memory");
   return any;
 }
-template <int N>
-__device__ __forceinline__ void groups_sync() {
-  asm volatile("bar.sync 7, %0;\n" ::"n"(N) : "memory");
+template <int THREADS>
+__device__ __forceinline__ void units_sync() {
+  asm volatile("bar.sync 7, %0;\n" ::"n"(THREADS) : "memory");
 }
 
-// O += V^T P: V in rows of 128 bytes, P in rows of 2 CW bytes (64: 64-byte swizzle, SBO 512).
-template <int CW>
+// O += V^T P: V in rows of 128 bytes, P in rows of 2 N bytes (64: 64-byte swizzle, SBO 512).
+template <int N>
 __device__ __forceinline__ void umma_pv(uint32_t d, uint32_t v, uint32_t p, uint32_t id, bool acc) {
-  constexpr uint32_t hi = CW == 64 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;
+  constexpr uint32_t hi = N == 64 ? kDescHi : (512u >> 4) | 1u << 14 | 4u << 29;
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %5};\n"
       " setp.ne.b32 p, %6, 0;\n"
@@ -234,15 +248,20 @@ struct Ring {
 // V with 64 dims has a panel of zeros for the other 64 lanes of O.
 template <int MODE, int DIM, int CW>
 struct Room {
+  using L = Plan<MODE, CW>;
   static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
-  static constexpr int raw = kKeys * DIM, tile = 2 * raw, ptile = kKeys * CW * 2;
-  static constexpr int raws = CW == 32 ? (f8 ? 4 : 2) : (f8 ? 3 : 2), vtiles = 2, ktiles = f8 ? 0 : CW == 32 ? 2 : 1;
+  static constexpr int raw = kKeys * DIM, tile = 2 * raw, ptile = kKeys * L::n * 2;
+  static constexpr int raws = f8 ? (CW == 32 ? 4 : 3) : 2, vtiles = 2, ktiles = f8 ? 0 : CW == 64 ? 1 : 2;
   static constexpr int k = 0, v = raws * raw, vt = v + raws * raw, zero = vt + vtiles * tile;
-  static constexpr int kt = zero + (DIM == 64 ? kKeys * 128 : 0), q = kt + ktiles * tile, pt = q + CW * DIM * 2;
-  static constexpr int bytes = pt + kGroups * ptile + 1024;
-  static_assert(bytes <= 227 * 1024 - (CW == 32 ? 10 : 18) * 1024, "shared memory (with what the kernel has besides)");
+  static constexpr int kt = zero + (DIM == 64 ? kKeys * 128 : 0), q = kt + ktiles * tile, pt = q + L::n * DIM * 2;
+  static constexpr int bytes = pt + L::sets * ptile + 1024;
+  static_assert(bytes <= 227 * 1024 - 10 * 1024, "shared memory (with what the kernel has besides)");
 };
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __half2 c = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&c);
+}
 // Two E4M3 numbers (the low 16 bits) as fp16.
 __device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
@@ -250,30 +269,31 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
 }
 
 template <int MODE, int DIM, int CW>
-__global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(const __grid_constant__ SharedArgs a) {
   using R = Room<MODE, DIM, CW>;
+  using L = Plan<MODE, CW>;
   constexpr bool F8 = R::f8;
-  constexpr int G = kGroups;
-  constexpr uint32_t kCols = 2 * G * CW;  // S of each group, O of each group
-  constexpr uint32_t kIdQK = idesc_f16(128, CW, 0, 0), kIdPV = idesc_f16(128, CW, 1, 1);
+  constexpr int G = L::sets, N = L::n;
+  constexpr uint32_t kIdQK = idesc_f16(128, N, 0, 0), kIdPV = idesc_f16(128, N, 1, 1);
   constexpr uint32_t kBE5M2 = 1u << 10;
-  constexpr int kChunks = CW / 16;
-  extern __shared__ unsigned char smem_raw[];
-  // codes there, and free; fp16 tiles there, and free
-  __shared__ __align__(8) uint64_t kin[R::raws], kout[R::raws], vin[R::raws], vout[R::raws];
   constexpr int kKTiles = F8 ? 1 : R::ktiles;
+  extern __shared__ unsigned char smem_raw[];
+  // codes there, and free; fp16 tiles there, and free; by buffer
+  __shared__ __align__(8) uint64_t kin[R::raws], kout[R::raws], vin[R::raws], vout[R::raws];
   __shared__ __align__(8) uint64_t kfull[kKTiles], kfree[kKTiles], vfull[R::vtiles], vfree[R::vtiles];
-  __shared__ __align__(8) uint64_t sfull[G], sfree[G], pready[G], odone[G], qready;
+  __shared__ __align__(8) uint64_t sfull[2 * G], sfree[2 * G], pready[G], odone[G], qready;  // of S by buffer, by set
   __shared__ float2 meta[16][8];  // [tile]: per 16 keys K scale, log2 of V scale
   __shared__ int valid[16];       // bit c: they have a page
-  __shared__ int2 vinfo[16];      // the same for those who have V, and the tile's tokens
-  __shared__ int s_lim[CW], s_min[G];  // keys that a column sees; the fewest of them
+  __shared__ int2 vinfo[16];      // the tile's tokens, and the same for those who have V
+  __shared__ __align__(16) int s_lim[CW];    // keys that a column sees
   __shared__ __align__(16) float s_fac[CW];  // factor of a column's scores
-  // of a group's column: references of s and of s + log2 of V's scale; -m; sum; factor of its output; what a move makes of its sums, and of O
-  __shared__ __align__(16) float s_m[G][CW], s_mv[G][CW], s_neg[G][CW], s_sum[G][CW], s_out[G][CW], s_by[G][2][CW];
+  // of a unit's column: references of s and of s + log2 of V's scale; -m; sum; factor of its
+  // output; what a move makes of its sums, and of O
+  __shared__ __align__(16) float s_m[L::units][16], s_mv[L::units][16], s_neg[L::units][16], s_sum[L::units][16], s_out[L::units][16];
+  __shared__ __align__(16) float s_by[L::units][2][16];
   // for 16 keys of a tile: factor of the scores, 2^(log2 vs + m - mv)
-  __shared__ __align__(16) float s_by_k[kSoft][2][CW], s_ratio[kSoft][2][CW];
-  __shared__ float2 s_red[G][4][CW];
+  __shared__ __align__(16) float s_by_k[L::soft][2][16], s_ratio[L::soft][2][16];
+  __shared__ float2 s_red[L::units][4][16];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -282,21 +302,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
 
   grid_dep_launch();  // the rows' own tokens need nothing of this launch until their join
-  if (warp == 0) tmem_alloc(&tmem_slot, kCols);
+  if (warp == 0) tmem_alloc(&tmem_slot, L::cols);
   if (tid == 32) {
     for (int i = 0; i < R::raws; ++i) {
       mbar_init(&kin[i], 1), mbar_init(&vin[i], 1);
-      mbar_init(&kout[i], F8 ? 1 : 4), mbar_init(&vout[i], F8 ? 8 : 4);
+      mbar_init(&kout[i], F8 ? 1 : 4), mbar_init(&vout[i], 4);
     }
-    for (int i = 0; i < R::vtiles; ++i) mbar_init(&vfull[i], F8 ? 8 : 4), mbar_init(&vfree[i], 1);
+    for (int i = 0; i < R::vtiles; ++i) mbar_init(&vfull[i], 4), mbar_init(&vfree[i], 1);
     for (int i = 0; i < kKTiles; ++i) mbar_init(&kfull[i], 4), mbar_init(&kfree[i], 1);
-    for (int i = 0; i < G; ++i) mbar_init(&sfull[i], 1), mbar_init(&sfree[i], 4), mbar_init(&pready[i], 4), mbar_init(&odone[i], 1);
-    mbar_init(&qready, kSoft);
+    for (int i = 0; i < 2 * G; ++i) mbar_init(&sfull[i], 1), mbar_init(&sfree[i], 4 * L::per_tile);
+    for (int i = 0; i < G; ++i) mbar_init(&pready[i], 4 * L::per_tile), mbar_init(&odone[i], 1);
+    mbar_init(&qready, L::soft);
     abort_flag = 0;
     fence_mbar_init();
   }
   if constexpr (DIM == 64) {
-    for (int i = tid; i < kKeys * 8; i += kThreads) reinterpret_cast<uint4*>(smem + R::zero)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kKeys * 8; i += L::threads) reinterpret_cast<uint4*>(smem + R::zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
   }
   Walk w(a, blockIdx.x, lane);
@@ -317,23 +338,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     if (lane == 0) mbar_arrive(bar);
   };
 
-  if (warp < kSoft) {
-    set_regs_up<kSoftRegs>();
+  if (warp < L::soft) {
+    set_regs_up<L::soft_regs>();
     // ======================= keys =======================
-    const int g = warp / 4, quad = warp & 3, key = quad * 32 + lane, sub = lane >> 4;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), s_col = lanes + g * CW, o_col = lanes + (G + g) * CW;
-    unsigned char *sQ = smem + R::q, *sP = smem + R::pt + g * R::ptile;
+    // A thread has a key, and 16 columns of its set's tiles.
+    const int unit = warp / 4, quad = warp & 3, key = quad * 32 + lane, half = lane >> 4, l16 = lane & 15;
+    const int set = unit / L::per_tile, c0 = unit % L::per_tile * 16;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + c0, o_col = lanes + L::s_cols + set * N;
+    unsigned char *sQ = smem + R::q, *sP = smem + R::pt + set * R::ptile + key * (2 * N);
+    const int swap = N == 64 ? key & 7 : key >> 1 & 3, u0 = c0 / 8;
     const int per_row = p.tokens * p.group, all_q = a.beams * per_row;
-    float *ratio = s_ratio[warp][sub], *by_k = s_by_k[warp][sub], *fm = s_m[g], *fmv = s_mv[g], *neg = s_neg[g];
+    float *by_k = s_by_k[warp][half], *ratio = s_ratio[warp][half], *neg = s_neg[unit];
     bool ok = true;
-    uint32_t n = 0, mine = 0;  // tiles so far, and this group's
+    uint32_t n = 0, mine = 0;  // tiles so far, and this set's
     for (; w.left > 0; w.next(a)) {
-      const int nt = w.count(), h = w.hq / a.blocks, q0 = w.hq % a.blocks * CW;
-      const int here = min(all_q - q0, CW), hc = (here + 15) / 16 * 16;  // columns in use, in chunks of 16
+      const int nt = w.count(), h = w.hq / a.blocks, q0 = w.hq % a.blocks * CW, here = min(all_q - q0, CW);  // columns in use
       // ---- queries: DIM / 8 lanes to a row ----
       {
         constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;
-        for (int c = warp * kAt + lane / kLanes; c < hc; c += kSoft * kAt) {
+#pragma unroll 1
+        for (int c = warp * kAt + lane / kLanes; c < CW; c += L::soft * kAt) {
           const int i = q0 + c, r_in = i / per_row, x_in = i - r_in * per_row, u = lane % kLanes;
           const int64_t r = w.g * a.beams + r_in;
           uint4 raw = make_uint4(0, 0, 0, 0);
@@ -359,11 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
               hi[e] = kv8_q_first(f + 4 * e, up, rest);
               lo[e] = kv8_e5m2x4(rest);
             }
-            unsigned char* to = sQ + (u & 1) * 8 + (DIM == 128 ? unit_at(c, u >> 1, CW) : c * 64 + (((u >> 1) ^ (c >> 1 & 3)) << 4));
+            unsigned char* to = sQ + (u & 1) * 8 + (DIM == 128 ? unit_at(c, u >> 1, N) : c * 64 + (((u >> 1) ^ (c >> 1 & 3)) << 4));
             *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(to + CW * DIM) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(to + N * DIM) = make_uint2(lo[0], lo[1]);
           } else {
-            *reinterpret_cast<uint4*>(sQ + unit_at(c, u, CW)) =
+            *reinterpret_cast<uint4*>(sQ + unit_at(c, u, N)) =
                 make_uint4(pack_f16(f[0] * up, f[2] * up), pack_f16(f[1] * up, f[3] * up),
                            pack_f16(f[4] * up, f[6] * up), pack_f16(f[5] * up, f[7] * up));
           }
@@ -371,225 +395,191 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
         fence_proxy_async();
         if (ok) warp_arrive(&qready);
       }
-      groups_sync<G * 128>();  // the columns' limits and factors
-      if (quad == 0) {
-        int least = 0x7fffffff;
-        for (int c = lane; c < hc; c += 32) {
-          if (c < here) least = min(least, s_lim[c]);
-          fm[c] = fmv[c] = -INFINITY, neg[c] = INFINITY;  // no score yet: any is too large
-        }
-        least = __reduce_min_sync(0xffffffffu, least);
-        if (lane == 0) s_min[g] = least;
+      if (quad == 0 && half == 0) {
+        s_m[unit][l16] = s_mv[unit][l16] = -INFINITY, neg[l16] = INFINITY;  // no score yet: any is too large
       }
-      group_sync(g);
-      const int least = s_min[g];
-      float sum[kChunks][16];
+      units_sync<L::soft * 32>();  // the columns' limits and factors
+      const int col = c0 + l16;
+      const float my_fac = s_fac[col];  // (of the column that a lane does for its half-warp)
+      const int least = (int)__reduce_min_sync(0xffffffffu, (unsigned)(col < here ? s_lim[col] : 0x7fffffff));
+      float sum[16];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[c][e] = 0.f;
+      for (int e = 0; e < 16; ++e) sum[e] = 0.f;
 
-      const int first = (int)((g - n) & (G - 1));  // this group's first tile of the piece
+      const int first = (int)((set - n) & (G - 1));  // this set's first tile of the piece
       for (int i = first; i < nt; i += G, ++mine) {
-        ok = ok && all_wait(&sfull[g], mine & 1);
-        if (!ok) {  // a wait gave up: only the barrier that others may stand at
-          if (i == first) group_sync(g), group_sync(g);
-          if (group_any(g, false)) group_sync(g), group_sync(g);
+        const uint32_t buf = (mine & 1) * G + set;
+        ok = ok && all_wait(&sfull[buf], mine >> 1 & 1);
+        if (i > first) ok = ok && all_wait(&odone[set], (mine - 1) & 1);  // P and O are free
+        if (!ok) {  // a wait gave up: only the barriers that others may stand at
+          if (unit_any(unit, false)) unit_sync(unit), unit_sync(unit);
           continue;
         }
         tc_fence_after();
+        float v[16], y[16];
+        tmem_ld16(lanes + buf * N, v);
         const int j0 = (w.t + i) * kKeys, at = j0 + key, slot = (n + i) & 15;
         const float2 sc = meta[slot][key >> 4];
-        const bool there = valid[slot] >> (key >> 4) & 1;
-        const bool mask = valid[slot] != 255 || j0 + kKeys > least;
-        auto gone = [&](int col) { return !there || at >= s_lim[col]; };
-        auto tables = [&]() {
-          for (int c = lane & 15; c < hc; c += 16) {
-            const float mv = fmv[c];
-            by_k[c] = s_fac[c] * sc.x;
-            ratio[c] = ex2_approx_f(fminf(sc.y - neg[c] - (mv == -INFINITY ? 0.f : mv), 126.f));
-          }
-          __syncwarp();
-        };
-        // Probabilities against the references as they are; over: the largest number.  (Two forms,
-        // with a mask and without: predicates for it take half of the instructions.)
-        float over = 0.f;
-        auto probs = [&](auto masked, auto add) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (16 * c >= hc) break;
-            float v[16];
-            tmem_ld16(s_col + 16 * c, v);
-            uint32_t pk[8];
+        // columns that see this key
+        uint32_t see = 0xffffu;
+        if (valid[slot] != 255 || j0 + kKeys > least) {
+          see = 0;
+          if (valid[slot] >> (key >> 4) & 1) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&by_k[16 * c + e]);
-              const float4 m = *reinterpret_cast<const float4*>(&neg[16 * c + e]);
-              const float4 r = *reinterpret_cast<const float4*>(&ratio[16 * c + e]);
-              float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
-              float2 y = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
-              if constexpr (decltype(masked)::value) {
-                if (gone(16 * c + e)) x.x = -INFINITY;
-                if (gone(16 * c + e + 1)) x.y = -INFINITY;
-                if (gone(16 * c + e + 2)) y.x = -INFINITY;
-                if (gone(16 * c + e + 3)) y.y = -INFINITY;
-              }
-              x = make_float2(ex2_approx_f(x.x), ex2_approx_f(x.y)), y = make_float2(ex2_approx_f(y.x), ex2_approx_f(y.y));
-              if constexpr (decltype(add)::value) {
-                const float2 s0 = add2(make_float2(sum[c][e], sum[c][e + 1]), x), s1 = add2(make_float2(sum[c][e + 2], sum[c][e + 3]), y);
-                sum[c][e] = s0.x, sum[c][e + 1] = s0.y, sum[c][e + 2] = s1.x, sum[c][e + 3] = s1.y;
-                over = max3(over, x.x, x.y), over = max3(over, y.x, y.y);
-              } else {
-                // what was too large for a sum stands alone in it
-                if (sum[c][e] == INFINITY) sum[c][e] = x.x;
-                if (sum[c][e + 1] == INFINITY) sum[c][e + 1] = x.y;
-                if (sum[c][e + 2] == INFINITY) sum[c][e + 2] = y.x;
-                if (sum[c][e + 3] == INFINITY) sum[c][e + 3] = y.y;
-              }
-              x = mul2(x, make_float2(r.x, r.y)), y = mul2(y, make_float2(r.z, r.w));
-              if constexpr (decltype(add)::value) over = max3(over, x.x, x.y), over = max3(over, y.x, y.y);
-              pk[e / 2] = pack_f16(x.x, x.y), pk[e / 2 + 1] = pack_f16(y.x, y.y);
+              const int4 x = *reinterpret_cast<const int4*>(&s_lim[c0 + e]);
+              see |= (uint32_t)(at < x.x) << e | (uint32_t)(at < x.y) << (e + 1) | (uint32_t)(at < x.z) << (e + 2) | (uint32_t)(at < x.w) << (e + 3);
             }
-            unsigned char* to = sP + key * (2 * CW);
-            const int swap = CW == 64 ? key & 7 : key >> 1 & 3;
-            *reinterpret_cast<uint4*>(to + (((2 * c) ^ swap) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ swap) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           }
-        };
-        // Maxima; columns that outgrew a reference by 2^8 get a new one.
-        auto references = [&]() {
+        }
+        const float f16 = my_fac * sc.x;
+        by_k[l16] = f16;
+        for (int again = 0;; ++again) {
+          const float mv = s_mv[unit][l16], um = neg[l16];
+          // (not 0, so that a score too large shows in P whatever V's scale)
+          ratio[l16] = um == INFINITY ? 1.f : fmaxf(ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f)), 1.17549435e-38f);
+          __syncwarp();
+          uint32_t pk[8];
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (16 * c >= hc) break;
-            float v[16];
-            tmem_ld16(s_col + 16 * c, v);
-            if (mask) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (gone(16 * c + e)) v[e] = -INFINITY;
+          for (int e = 0; e < 16; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&by_k[e]);
+            const float4 m = *reinterpret_cast<const float4*>(&neg[e]);
+            const float4 r = *reinterpret_cast<const float4*>(&ratio[e]);
+            float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
+            float2 z = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
+            y[e] = ex2_approx_f(x.x), y[e + 1] = ex2_approx_f(x.y), y[e + 2] = ex2_approx_f(z.x), y[e + 3] = ex2_approx_f(z.y);
+            if (see != 0xffffu) {
+              if (!(see >> e & 1)) y[e] = 0.f;
+              if (!(see >> (e + 1) & 1)) y[e + 1] = 0.f;
+              if (!(see >> (e + 2) & 1)) y[e + 2] = 0.f;
+              if (!(see >> (e + 3) & 1)) y[e + 3] = 0.f;
             }
-            const float x = half_reduce<false>(v, lane);
-            const int col = 16 * c + (lane & 15);
+            x = mul2(make_float2(y[e], y[e + 1]), make_float2(r.x, r.y)), z = mul2(make_float2(y[e + 2], y[e + 3]), make_float2(r.z, r.w));
+            pk[e / 2] = pack_f16(x.x, x.y), pk[e / 2 + 1] = pack_f16(z.x, z.y);
+          }
+          *reinterpret_cast<uint4*>(sP + ((u0 ^ swap) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(sP + (((u0 + 1) ^ swap) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          const uint32_t most = max2(max2(max2(pk[0], pk[1]), max2(pk[2], pk[3])), max2(max2(pk[4], pk[5]), max2(pk[6], pk[7])));
+          const bool over = (most & 0xffffu) > 0x5c00u || most >> 16 > 0x5c00u;  // of numbers >= 0: above 256
+          // Does a score outgrow its column's references by 2^8?  (fp16 and the sums have the room for
+          // that.)  Then columns that do get new ones, from their maxima, and it goes once more; what is too
+          // large after that is no number.
+          if (again || !unit_any(unit, over)) break;
+          {
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = see >> e & 1 ? v[e] : -INFINITY;
+            const float top = half_reduce<false>(x, lane);
             // (a factor of 0 would make -inf a NaN)
-            float nm = x == -INFINITY ? x : x * (sc.x * s_fac[col]);
+            float nm = top == -INFINITY ? top : top * f16;
             float nv = nm + sc.y;
             nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 16));
             nv = fmaxf(nv, __shfl_xor_sync(0xffffffffu, nv, 16));
-            if (lane < 16) s_red[g][quad][col] = make_float2(nm, nv);
+            if (half == 0) s_red[unit][quad][l16] = make_float2(nm, nv);
           }
-          group_sync(g);
-          for (int c = quad * 32 + lane; c < hc; c += 128) {
+          unit_sync(unit);
+          if (quad == 0 && half == 0) {
             float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[g][q][c].x), nv = fmaxf(nv, s_red[g][q][c].y);
-            const float m = fm[c], mv = fmv[c];
+            for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[unit][q][l16].x), nv = fmaxf(nv, s_red[unit][q][l16].y);
+            const float m = s_m[unit][l16];
             float by = 1.f, by_o = 1.f;
-            if (nm > m + 8.f) by = ex2_approx_f(m - nm), fm[c] = nm, neg[c] = -nm;
-            if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), fmv[c] = nv;
-            s_by[g][0][c] = by, s_by[g][1][c] = by_o;
+            if (nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][l16] = nm, neg[l16] = -nm;
+            if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[unit][l16] = nv;
+            s_by[unit][0][l16] = by, s_by[unit][1][l16] = by_o;
           }
-          group_sync(g);
-        };
-        if (i == first) {
-          references();
-        } else {
-          ok = all_wait(&odone[g], (mine - 1) & 1);  // P and O are free
-          tc_fence_after();
+          unit_sync(unit);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[e] *= s_by[unit][0][e];
+          if (i > first) {
+            float o[16];
+            tmem_ld16(o_col, o);
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * s_by[unit][1][e]);
+            tmem_st16(o_col, u);
+            tmem_wait_st();
+          }
         }
-        tables();
-        if (mask) probs(std::true_type(), std::true_type());
-        else probs(std::false_type(), std::true_type());
-        // a score that outgrew its column's references by 2^8: fp16 and the sums have the room for that
-        if (group_any(g, over > 256.f)) {
-          references();
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (16 * c >= hc) break;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (sum[c][e] != INFINITY) sum[c][e] *= s_by[g][0][16 * c + e];
-            if (i > first && ok) {
-              float v[16];
-              tmem_ld16(o_col + 16 * c, v);
-              uint32_t u[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * s_by[g][1][16 * c + e]);
-              tmem_st16(o_col + 16 * c, u);
-            }
-          }
-          tmem_wait_st();
-          tables();
-          probs(std::true_type(), std::false_type());
+        for (int e = 0; e < 16; e += 2) {
+          const float2 x = add2(make_float2(sum[e], sum[e + 1]), make_float2(y[e], y[e + 1]));
+          sum[e] = x.x, sum[e + 1] = x.y;
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&pready[g]), mbar_arrive(&sfree[g]);
+        if (lane == 0) mbar_arrive(&pready[set]), mbar_arrive(&sfree[buf]);
       }
 
       // ---- the part: outputs over the piece's keys, and log2 of the sums ----
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (16 * c >= hc) break;
-        float l = half_reduce<true>(sum[c], lane);
+      {
+        float l = half_reduce<true>(sum, lane);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (lane < 16) s_red[g][quad][16 * c + lane].x = l;
+        if (half == 0) s_red[unit][quad][l16].x = l;
       }
       if (first < nt) {
-        ok = ok && all_wait(&odone[g], (mine - 1) & 1);
+        ok = ok && all_wait(&odone[set], (mine - 1) & 1);
         tc_fence_after();
       }
-      group_sync(g);
-      for (int c = quad * 32 + lane; c < hc; c += 128)
-        s_sum[g][c] = (s_red[g][0][c].x + s_red[g][1][c].x) + (s_red[g][2][c].x + s_red[g][3][c].x);
+      unit_sync(unit);
+      if (quad == 0 && half == 0)
+        s_sum[unit][l16] = (s_red[unit][0][l16].x + s_red[unit][1][l16].x) + (s_red[unit][2][l16].x + s_red[unit][3][l16].x);
       tc_fence_before();
-      groups_sync<G * 128>();
+      units_sync<L::soft * 32>();
       tc_fence_after();
+      // the first set's units join the others' to their own
       const int64_t slot = w.slot(a, blockIdx.x);
-      for (int c = warp * 32 + lane; c < hc; c += kSoft * 32) {
-        float m = -INFINITY, l = 0.f;
+      if (set == 0) {
+        if (quad == 0 && half == 0) {
+          float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int x = 0; x < G; ++x) m = fmaxf(m, s_m[x][c]);
+          for (int x = 0; x < G; ++x) m = fmaxf(m, s_m[x * L::per_tile + unit][l16]);
 #pragma unroll
-        for (int x = 0; x < G; ++x) l += m == -INFINITY ? s_sum[x][c] : s_sum[x][c] * ex2_approx_f(s_m[x][c] - m);
-        // l is 0 where no key is seen, and NaN where a score is
+          for (int x = 0; x < G; ++x) {
+            const float part = s_sum[x * L::per_tile + unit][l16];
+            l += m == -INFINITY ? part : part * ex2_approx_f(s_m[x * L::per_tile + unit][l16] - m);
+          }
+          // l is 0 where no key is seen, and NaN where a score is  (V as it is: no power of two is left)
 #pragma unroll
-        for (int x = 0; x < G; ++x) s_out[x][c] = kv8_out_factor<GDN_QDQ_INT8>(s_mv[x][c], m, l);  // (V as it is)
-        if (c < here) a.lses[slot * a.stride + c] = l == 0.f ? -INFINITY : m + log2f(l);
-      }
-      groups_sync<G * 128>();
-      // with INT8 codes lane d of O is dim 4 (d / 4) + (0 2 1 3)[d % 4]
-      const int dim = F8 ? key : (key & ~3) | (key & 1) << 1 | (key >> 1 & 1);
-      for (int c = 16 * g; c < hc && ok; c += 16 * G) {
-        float o[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
-#pragma unroll
-        for (int x = 0; x < G; ++x) {
-          if ((int)((x - n) & (G - 1)) >= nt) continue;  // no tile of the piece was this group's
-          float v[16];
-          tmem_ld16(lanes + (G + x) * CW + c, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], s_out[x][c + e], o[e]);
+          for (int x = 0; x < G; ++x)
+            s_out[x * L::per_tile + unit][l16] = kv8_out_factor<GDN_QDQ_INT8>(s_mv[x * L::per_tile + unit][l16], m, l);
+          if (col < here) a.lses[slot * a.stride + col] = l == 0.f ? -INFINITY : m + log2f(l);
         }
-        if (key < DIM) {
-          float* to = a.parts + (slot * a.stride + c) * DIM + dim;
+        unit_sync(unit);
+        if (ok) {
+          float o[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c + e < here) to[e * DIM] = o[e];
+          for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 1
+          for (int x = 0; x < G; ++x) {
+            if ((int)((x - n) & (G - 1)) >= nt) continue;  // no tile of the piece was this set's
+            float v[16];
+            tmem_ld16(lanes + L::s_cols + x * N, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], s_out[x * L::per_tile + unit][e], o[e]);
+          }
+          // with INT8 codes lane d of O is dim 4 (d / 4) + (0 2 1 3)[d % 4]
+          const int dim = F8 ? key : (key & ~3) | (key & 1) << 1 | (key >> 1 & 1);
+          if (key < DIM) {
+            float* to = a.parts + (slot * a.stride + c0) * DIM + dim;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e < here) to[e * DIM] = o[e];
+          }
         }
       }
       n += nt;
       tc_fence_before();  // O has been read: the next piece's products may write it (after P's signal)
-      groups_sync<G * 128>();  // every column's values have been read
+      units_sync<L::soft * 32>();       // every column's values have been read
       tc_fence_after();
     }
-  } else if (warp < kIssueQK) {
-    set_regs_down<kConvRegs>();
+  } else if (warp < L::issue_qk) {
+    set_regs_down<L::conv_regs>();
     // ======================= codes to fp16 =======================
     // a lane takes 16 codes at a time; the two rows of eight neighbouring lanes are
     // chosen so that their loads and their stores each fall on different banks
-    const int cw = (warp - kSoft) % 4, second = (warp - kSoft) / 4;
+    const int cw = (warp - L::soft) % 4, second = (warp - L::soft) / 4;
     constexpr int kPer = DIM / 16, kStep = 2048 / DIM;
     const int unit = DIM == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const int r8 = DIM == 128 ? (lane >> 4 & 1) * 2 : lane >> 2;
@@ -599,73 +589,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     const int from0 = DIM == 128 ? row0c * 128 + ((unit ^ (row0c & 7)) << 4)
                                  : row0c * 64 + ((unit ^ (row0c >> 1 & 3)) << 4);
     const uint32_t to0 = unit_at(row0c, 2 * unit, kKeys), to1 = unit_at(row0c, 2 * unit + 1, kKeys);
-    constexpr int kMine = F8 ? kPer / 2 : kPer;  // (rows kStep apart: the swizzle is the same)
-    const int e_first = F8 ? second * kMine : 0;
-    auto read = [&](uint4 (&u)[kMine], const unsigned char* from) {
-#pragma unroll
-      for (int e = 0; e < kMine; ++e) u[e] = *reinterpret_cast<const uint4*>(from + from0 + (e_first + e) * kStep * DIM);
-    };
-    auto write = [&](const uint4 (&u)[kMine], unsigned char* to) {
-#pragma unroll
-      for (int e = 0; e < kMine; ++e) {
-        uint4 lo, hi;
-        if constexpr (F8) {
-          lo.x = half2_of(u[e].x), lo.y = half2_of(u[e].x >> 16), lo.z = half2_of(u[e].y), lo.w = half2_of(u[e].y >> 16);
-          hi.x = half2_of(u[e].z), hi.y = half2_of(u[e].z >> 16), hi.z = half2_of(u[e].w), hi.w = half2_of(u[e].w >> 16);
-        } else {
-          kv8_half2<MODE>(u[e].x, lo.x, lo.y);
-          kv8_half2<MODE>(u[e].y, lo.z, lo.w);
-          kv8_half2<MODE>(u[e].z, hi.x, hi.y);
-          kv8_half2<MODE>(u[e].w, hi.z, hi.w);
-        }
-        *reinterpret_cast<uint4*>(to + to0 + (e_first + e) * kStep * 128) = lo;
-        *reinterpret_cast<uint4*>(to + to1 + (e_first + e) * kStep * 128) = hi;
-      }
-      fence_proxy_async();
-    };
+    // Tiles of V, or of K and V in turn (K is one ahead); every step is the same code, which stays
+    // where instructions are near.  (Rows kStep apart: the swizzle is the same.)
     const uint32_t all = (uint32_t)w.left;
-    Ring<R::raws> in;
-    if (F8 || second) {
-      Ring<R::vtiles> out;
-      for (uint32_t n = 0; n < all; ++n, in.next(), out.next()) {
-        if (!all_wait(&vin[in.at], in.turn)) break;
-        uint4 u[kMine];
-        read(u, smem + R::v + in.at * R::raw);
-        const int2 what = vinfo[n & 15];
-        warp_arrive(&vout[in.at]);
+    const bool has_k = !F8 && (L::both || !second), has_v = F8 || L::both || second;
+    uint32_t ks = has_k ? 0 : all, vs = has_v ? 0 : all;  // tiles so far
+    while (ks < all || vs < all) {
+      const bool is_k = ks < all && (vs == all || ks < vs + 2);
+      const uint32_t n = is_k ? ks++ : vs++;
+      const uint32_t outs = is_k ? kKTiles : R::vtiles, in = n % R::raws, out = n % outs;
+      if (!all_wait((is_k ? kin : vin) + in, n / R::raws & 1)) break;
+      const unsigned char* from = smem + (is_k ? R::k : R::v) + in * R::raw + from0;
+      unsigned char* to = smem + (is_k ? R::kt : R::vt) + out * R::tile;
+      const int2 what = vinfo[n & 15];
+      if (!all_wait((is_k ? kfree : vfree) + out, (n / outs & 1) ^ 1)) break;
+      constexpr int kAt = 4;
+#pragma unroll 1
+      for (int e0 = 0; e0 < kPer; e0 += kAt) {
+        uint4 u[kAt];
+#pragma unroll
+        for (int e = 0; e < kAt; ++e) u[e] = *reinterpret_cast<const uint4*>(from + (e0 + e) * kStep * DIM);
         if (F8 && (what.x < kKeys || what.y != 255)) {
           // E4M3 bytes that are no number may stand where no token is
 #pragma unroll
-          for (int e = 0; e < kMine; ++e) {
-            const int row = row0c + (e_first + e) * kStep;
+          for (int e = 0; e < kAt; ++e) {
+            const int row = row0c + (e0 + e) * kStep;
             if (row >= what.x || !(what.y >> (row >> 4) & 1)) u[e] = make_uint4(0, 0, 0, 0);
           }
         }
-        if (!all_wait(&vfree[out.at], out.turn ^ 1)) break;
-        write(u, smem + R::vt + out.at * R::tile);
-        warp_arrive(&vfull[out.at]);
+#pragma unroll
+        for (int e = 0; e < kAt; ++e) {
+          uint4 lo, hi;
+          if constexpr (F8) {
+            lo.x = half2_of(u[e].x), lo.y = half2_of(u[e].x >> 16), lo.z = half2_of(u[e].y), lo.w = half2_of(u[e].y >> 16);
+            hi.x = half2_of(u[e].z), hi.y = half2_of(u[e].z >> 16), hi.z = half2_of(u[e].w), hi.w = half2_of(u[e].w >> 16);
+          } else {
+            kv8_half2<MODE>(u[e].x, lo.x, lo.y);
+            kv8_half2<MODE>(u[e].y, lo.z, lo.w);
+            kv8_half2<MODE>(u[e].z, hi.x, hi.y);
+            kv8_half2<MODE>(u[e].w, hi.z, hi.w);
+          }
+          *reinterpret_cast<uint4*>(to + to0 + (e0 + e) * kStep * 128) = lo;
+          *reinterpret_cast<uint4*>(to + to1 + (e0 + e) * kStep * 128) = hi;
+        }
       }
-    } else {
-      Ring<kKTiles> out;
-      for (uint32_t n = 0; n < all; ++n, in.next(), out.next()) {
-        if (!all_wait(&kin[in.at], in.turn)) break;
-        uint4 u[kMine];
-        read(u, smem + R::k + in.at * R::raw);
-        warp_arrive(&kout[in.at]);
-        if (!all_wait(&kfree[out.at], out.turn ^ 1)) break;
-        write(u, smem + R::kt + out.at * R::tile);
-        warp_arrive(&kfull[out.at]);
-      }
+      warp_arrive((is_k ? kout : vout) + in);
+      fence_proxy_async();
+      warp_arrive((is_k ? kfull : vfull) + out);
     }
   } else {
-    set_regs_down<kRestRegs>();
+    set_regs_down<L::rest_regs>();
   }
-  if (warp == kLoadK || warp == kLoadV) {
+  if (warp == L::load_k || warp == L::load_v) {
     // ======================= codes by TMA =======================
     // A warp for K, which says what the tile has, and one for V.
     // Lane l has page l of a window of 32, and its scales; those of the next window are asked for
     // while this one's tiles are loaded.
-    const bool is_v = warp == kLoadV;
+    const bool is_v = warp == L::load_v;
     const int boxes = kKeys >> p.shift, shift = 31 - __clz(boxes), span = 32 >> shift;  // pages of a tile; tiles of a window
     uint64_t *in = is_v ? vin : kin, *free = is_v ? vout : kout;
     constexpr int bufs = R::raws;
@@ -717,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     }
     // no copy is in flight when the CTA ends, whatever ended the loop
     for (uint32_t i = issued > bufs ? issued - bufs : 0; i < issued; ++i) mbar_wait(&in[i % bufs], (i / bufs) & 1);
-  } else if (warp == kIssueQK || warp == kIssuePV) {
+  } else if (warp == L::issue_qk || warp == L::issue_pv) {
     // ======================= products =======================
     // A warp for Q K^T, one for P V.  Each goes through this as a whole, and what it goes by comes
     // from one lane, so that descriptors stay in uniform registers; one elected lane issues.  (One
@@ -728,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
     uint32_t left = (uint32_t)__shfl_sync(0xffffffffu, (int)w.left, 0);
     bool ok = true;
     uint32_t n = 0;
-    if (warp == kIssueQK) {
+    if (warp == L::issue_qk) {
       const uint32_t dk = desc_lo(base + (F8 ? R::k : R::kt), 16), dq = desc_lo(base + R::q, 16);
       Ring<F8 ? R::raws : kKTiles> kb;
       uint64_t *there = F8 ? kin : kfull, *gone = F8 ? kout : kfree;
@@ -736,24 +716,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
         const uint32_t nt = (uint32_t)__shfl_sync(0xffffffffu, w.count(), 0);
         ok = all_wait(&qready, pieces & 1);
         for (uint32_t i = 0; i < nt; ++i, ++n) {
-          const uint32_t g = n & (G - 1);
-          ok = ok && all_wait(&there[kb.at], kb.turn) && all_wait(&sfree[g], (n / G & 1) ^ 1);
+          const uint32_t buf = (n / G & 1) * G + (n & (G - 1));
+          ok = ok && all_wait(&there[kb.at], kb.turn) && all_wait(&sfree[buf], (n / G >> 1 & 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
           if (lead) {
-            const uint32_t d = tm + g * CW, k = dk + kb.at * ((F8 ? R::raw : R::tile) >> 4);
+            const uint32_t d = tm + buf * N, k = dk + kb.at * ((F8 ? R::raw : R::tile) >> 4);
             if constexpr (F8) {
               constexpr int kRow = DIM / 32;
 #pragma unroll
               for (int s = 0; s < 2 * kRow; ++s)  // q's first parts, then its second ones, with the same codes
-                umma_ss_f8<DIM>(d, k + s % kRow * 2, dq + (s / kRow * (CW * DIM) >> 4) + s % kRow * 2, kIdQK | (s < kRow ? 0 : kBE5M2), s > 0);
+                umma_ss_f8<DIM>(d, k + s % kRow * 2, dq + (s / kRow * (N * DIM) >> 4) + s % kRow * 2, kIdQK | (s < kRow ? 0 : kBE5M2), s > 0);
             } else {
 #pragma unroll
               for (int s = 0; s < DIM / 16; ++s)
-                umma_ss(d, k + (s / 4 * (kKeys * 128) >> 4) + (s % 4) * 2, dq + (s / 4 * (CW * 128) >> 4) + (s % 4) * 2, kIdQK, s > 0);
+                umma_ss(d, k + (s / 4 * (kKeys * 128) >> 4) + (s % 4) * 2, dq + (s / 4 * (N * 128) >> 4) + (s % 4) * 2, kIdQK, s > 0);
             }
             umma_commit(&gone[kb.at]);
-            umma_commit(&sfull[g]);  // (the one that is waited for at the end)
+            umma_commit(&sfull[buf]);  // (the one that is waited for at the end)
           }
           __syncwarp();
           kb.next();
@@ -775,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
           if (lead) {
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
-              umma_pv<CW>(tm + (G + g) * CW, dv + s * (2048 >> 4), dp + g * (R::ptile >> 4) + s * (CW * 32 >> 4), kIdPV, i >= G || s > 0);
+              umma_pv<N>(tm + L::s_cols + g * N, dv + s * (2048 >> 4), dp + g * (R::ptile >> 4) + s * (N * 32 >> 4), kIdPV, i >= G || s > 0);
             umma_commit(&vfree[vb.at]);
             umma_commit(&odone[g]);
           }
@@ -786,16 +766,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_common_kernel(const __grid_co
       }
     }
     // every product issued has completed before the CTA ends
-    for (uint32_t g = 0; g < G; ++g) {
-      const uint32_t tiles = (n + G - 1 - g) / G;
-      if (tiles > 0) wait(warp == kIssueQK ? &sfull[g] : &odone[g], (tiles - 1) & 1);
+    if (warp == L::issue_qk) {
+      for (uint32_t buf = 0; buf < 2 * G; ++buf) {
+        // tiles n with (n / G & 1) * G + (n & (G - 1)) == buf
+        const uint32_t uses = (n + 2 * G - 1 - buf) / (2 * G);
+        if (uses > 0) wait(&sfull[buf], (uses - 1) & 1);
+      }
+    } else {
+      for (uint32_t g = 0; g < G; ++g) {
+        const uint32_t tiles = (n + G - 1 - g) / G;
+        if (tiles > 0) wait(&odone[g], (tiles - 1) & 1);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && abort_flag) atomicOr(&g_kv8_shared_error, 1);
-  if (warp == 0) tmem_dealloc(tmem, kCols);
+  if (warp == 0) tmem_dealloc(tmem, L::cols);
 }
 
 // 16 bytes (or 8) of codes
@@ -1149,7 +1137,7 @@ SharedArgs sized(const Kv8Params& p, int beams) {
   a.p = p;
   a.beams = beams;
   const int64_t rows = (int64_t)beams * p.tokens * p.group;
-  a.cw = rows <= 32 ? 32 : 64;
+  a.cw = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   a.blocks = (int)((rows + a.cw - 1) / a.cw);
   a.stride = (int)(rows < a.cw ? rows : a.cw);
   const int64_t tiles = ((int64_t)p.cols * p.page + kKeys - 1) / kKeys * (p.rows / beams) * p.heads * a.blocks;
@@ -1159,11 +1147,15 @@ SharedArgs sized(const Kv8Params& p, int beams) {
 // Parts: one for each (group, head, block), and one more for each CTA.
 int64_t slots_of(const SharedArgs& a) { return a.p.rows / a.beams * a.p.heads * a.blocks + a.grid; }
 
-gdn_status launch_common(void (*kern)(SharedArgs), int bytes, const SharedArgs& a, cudaStream_t st) {
+template <int MODE, int DIM, int CW>
+gdn_status run_common(const SharedArgs& a, cudaStream_t st) {
+  auto kern = kv8_common_kernel<MODE, DIM, CW>;
+  constexpr int bytes = Room<MODE, DIM, CW>::bytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GDN_ERR_CUDA;
-  kern<<<a.grid, kThreads, bytes, st>>>(a);
+  kern<<<a.grid, Plan<MODE, CW>::threads, bytes, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
+
 template <int MODE, int DIM>
 gdn_status run(SharedArgs& a, cudaStream_t st) {
   const Kv8Params& p = a.p;
@@ -1176,8 +1168,9 @@ gdn_status run(SharedArgs& a, cudaStream_t st) {
                                   DIM == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return GDN_ERR_CUDA;
   if (a.grid > 0) {
-    const gdn_status s = a.cw == 32 ? launch_common(kv8_common_kernel<MODE, DIM, 32>, Room<MODE, DIM, 32>::bytes, a, st)
-                                    : launch_common(kv8_common_kernel<MODE, DIM, 64>, Room<MODE, DIM, 64>::bytes, a, st);
+    const gdn_status s = a.cw == 16   ? run_common<MODE, DIM, 16>(a, st)
+                         : a.cw == 32 ? run_common<MODE, DIM, 32>(a, st)
+                                      : run_common<MODE, DIM, 64>(a, st);
     if (s != GDN_OK) return s;
   }
   cudaLaunchConfig_t cfg = {};
