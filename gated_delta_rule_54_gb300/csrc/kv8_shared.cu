@@ -41,26 +41,25 @@ __device__ int g_kv8_shared_error;
 constexpr int kWarps = 4;   // own tokens: warps of a CTA
 constexpr int kKeys = 128;  // the group's tokens: keys of a tile
 
-// The first kernel: CW query rows (columns) of a block, N of a product.  Units of four warps have 16
-// columns of a tile each, so that what they go through per tile is short (a unit with all
-// columns spent its time on fetching instructions); the units that this leaves take other
-// tiles: `sets` tiles are worked on at a time.  Warps turn codes into fp16: V's (E4M3), or K's
-// and V's, by the same four in turn or by four each.  More warps than these would leave a thread
-// fewer registers than it takes.
+// The first kernel: CW query rows (columns) of a block, N of a product.  Two units of four warps
+// have 16 (or 32) columns of a tile each, so that what they go through per tile is short, or
+// take tiles in turn: `sets` tiles are worked on at a time.  (With four units a thread had too few
+// registers, and all columns in one unit spent its time on fetching instructions.)  Warps turn codes
+// into fp16: four do V's, and with INT8 codes four more K's.
 template <int MODE, int CW>
 struct Plan {
-  static constexpr bool f8 = MODE == GDN_QDQ_E4M3, both = !f8 && CW == 64;
-  static constexpr int units = CW == 64 ? 4 : 2, soft = 4 * units, conv = CW == 64 || f8 ? 4 : 8;
+  static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
+  static constexpr int units = 2, soft = 4 * units, conv = f8 ? 4 : 8;
   static constexpr int issue_qk = soft + conv, issue_pv = issue_qk + 1, load_k = issue_qk + 2, load_v = issue_qk + 3;
   static constexpr int threads = (soft + conv + 4) * 32;
   // registers per thread of the warpgroups: together no more than the launch gave
-  static constexpr int launch_regs = units == 4 ? 80 : conv == 4 ? 120 : 96;
-  static constexpr int soft_regs = units == 4 ? 96 : 144, conv_regs = units == 4 ? 48 : 64, rest_regs = conv_regs;
+  static constexpr int launch_regs = f8 ? 128 : 96, soft_regs = f8 ? 192 : 144, conv_regs = 64, rest_regs = 64;
   static_assert(units * soft_regs + conv / 4 * conv_regs + rest_regs <= threads / 128 * launch_regs, "register shares");
   static_assert(threads * launch_regs <= 65536, "registers");
-  static constexpr int per_tile = CW / 16, sets = units / per_tile, n = CW < 32 ? 32 : CW;
+  static constexpr int chunks = CW == 64 ? 2 : 1, cols_of = 16 * chunks;  // 16 columns, of a unit
+  static constexpr int per_tile = CW / cols_of, sets = units / per_tile, n = CW < 32 ? 32 : CW;
   static constexpr int s_cols = 2 * sets * n;  // S: two of each set; then O, one of each
-  static constexpr uint32_t cols = s_cols + sets * n > 256 ? 512 : 256;
+  static constexpr uint32_t cols = s_cols + sets * n > 128 ? 256 : 128;
 };
 
 struct SharedArgs {
@@ -251,7 +250,7 @@ struct Room {
   using L = Plan<MODE, CW>;
   static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
   static constexpr int raw = kKeys * DIM, tile = 2 * raw, ptile = kKeys * L::n * 2;
-  static constexpr int raws = f8 ? (CW == 32 ? 4 : 3) : 2, vtiles = 2, ktiles = f8 ? 0 : CW == 64 ? 1 : 2;
+  static constexpr int raws = f8 ? (CW == 64 ? 3 : 4) : 2, vtiles = 2, ktiles = f8 ? 0 : CW == 64 ? 1 : 2;
   static constexpr int k = 0, v = raws * raw, vt = v + raws * raw, zero = vt + vtiles * tile;
   static constexpr int kt = zero + (DIM == 64 ? kKeys * 128 : 0), q = kt + ktiles * tile, pt = q + L::n * DIM * 2;
   static constexpr int bytes = pt + L::sets * ptile + 1024;
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
   using R = Room<MODE, DIM, CW>;
   using L = Plan<MODE, CW>;
   constexpr bool F8 = R::f8;
-  constexpr int G = L::sets, N = L::n;
+  constexpr int G = L::sets, N = L::n, UC = L::cols_of, KC = L::chunks;
   constexpr uint32_t kIdQK = idesc_f16(128, N, 0, 0), kIdPV = idesc_f16(128, N, 1, 1);
   constexpr uint32_t kBE5M2 = 1u << 10;
   constexpr int kKTiles = F8 ? 1 : R::ktiles;
@@ -289,11 +288,11 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
   __shared__ __align__(16) float s_fac[CW];  // factor of a column's scores
   // of a unit's column: references of s and of s + log2 of V's scale; -m; sum; factor of its
   // output; what a move makes of its sums, and of O
-  __shared__ __align__(16) float s_m[L::units][16], s_mv[L::units][16], s_neg[L::units][16], s_sum[L::units][16], s_out[L::units][16];
-  __shared__ __align__(16) float s_by[L::units][2][16];
+  __shared__ __align__(16) float s_m[L::units][UC], s_mv[L::units][UC], s_neg[L::units][UC], s_sum[L::units][UC], s_out[L::units][UC];
+  __shared__ __align__(16) float s_by[L::units][2][UC];
   // for 16 keys of a tile: factor of the scores, 2^(log2 vs + m - mv)
-  __shared__ __align__(16) float s_by_k[L::soft][2][16], s_ratio[L::soft][2][16];
-  __shared__ float2 s_red[L::units][4][16];
+  __shared__ __align__(16) float s_by_k[L::soft][2][UC], s_ratio[L::soft][2][UC];
+  __shared__ float2 s_red[L::units][4][UC];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -341,9 +340,9 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
   if (warp < L::soft) {
     set_regs_up<L::soft_regs>();
     // ======================= keys =======================
-    // A thread has a key, and 16 columns of its set's tiles.
+    // A thread has a key, and its unit's columns of the set's tiles.
     const int unit = warp / 4, quad = warp & 3, key = quad * 32 + lane, half = lane >> 4, l16 = lane & 15;
-    const int set = unit / L::per_tile, c0 = unit % L::per_tile * 16;
+    const int set = unit / L::per_tile, c0 = unit % L::per_tile * UC;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + c0, o_col = lanes + L::s_cols + set * N;
     unsigned char *sQ = smem + R::q, *sP = smem + R::pt + set * R::ptile + key * (2 * N);
     const int swap = N == 64 ? key & 7 : key >> 1 & 3, u0 = c0 / 8;
@@ -396,15 +395,23 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
         if (ok) warp_arrive(&qready);
       }
       if (quad == 0 && half == 0) {
-        s_m[unit][l16] = s_mv[unit][l16] = -INFINITY, neg[l16] = INFINITY;  // no score yet: any is too large
+        for (int c = l16; c < UC; c += 16) s_m[unit][c] = s_mv[unit][c] = -INFINITY, neg[c] = INFINITY;  // no score yet: any is too large
       }
       units_sync<L::soft * 32>();  // the columns' limits and factors
-      const int col = c0 + l16;
-      const float my_fac = s_fac[col];  // (of the column that a lane does for its half-warp)
-      const int least = (int)__reduce_min_sync(0xffffffffu, (unsigned)(col < here ? s_lim[col] : 0x7fffffff));
-      float sum[16];
+      float my_fac[KC];  // (of the columns that a lane does for its half-warp)
+      unsigned least_u = 0x7fffffff;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+      for (int c = 0; c < KC; ++c) {
+        const int col = c0 + 16 * c + l16;
+        my_fac[c] = s_fac[col];
+        if (col < here) least_u = min(least_u, (unsigned)s_lim[col]);
+      }
+      const int least = (int)__reduce_min_sync(0xffffffffu, least_u);
+      float sum[KC][16];
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[c][e] = 0.f;
 
       const int first = (int)((set - n) & (G - 1));  // this set's first tile of the piece
       for (int i = first; i < nt; i += G, ++mine) {
@@ -416,96 +423,115 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           continue;
         }
         tc_fence_after();
-        float v[16], y[16];
-        tmem_ld16(lanes + buf * N, v);
+        float y[KC][16];
         const int j0 = (w.t + i) * kKeys, at = j0 + key, slot = (n + i) & 15;
         const float2 sc = meta[slot][key >> 4];
         // columns that see this key
-        uint32_t see = 0xffffu;
+        uint32_t see = 0xffffffffu;
         if (valid[slot] != 255 || j0 + kKeys > least) {
           see = 0;
           if (valid[slot] >> (key >> 4) & 1) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
+            for (int e = 0; e < UC; e += 4) {
               const int4 x = *reinterpret_cast<const int4*>(&s_lim[c0 + e]);
               see |= (uint32_t)(at < x.x) << e | (uint32_t)(at < x.y) << (e + 1) | (uint32_t)(at < x.z) << (e + 2) | (uint32_t)(at < x.w) << (e + 3);
             }
           }
         }
-        const float f16 = my_fac * sc.x;
-        by_k[l16] = f16;
-        for (int again = 0;; ++again) {
-          const float mv = s_mv[unit][l16], um = neg[l16];
-          // (not 0, so that a score too large shows in P whatever V's scale)
-          ratio[l16] = um == INFINITY ? 1.f : fmaxf(ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f)), 1.17549435e-38f);
-          __syncwarp();
-          uint32_t pk[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&by_k[e]);
-            const float4 m = *reinterpret_cast<const float4*>(&neg[e]);
-            const float4 r = *reinterpret_cast<const float4*>(&ratio[e]);
-            float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
-            float2 z = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
-            y[e] = ex2_approx_f(x.x), y[e + 1] = ex2_approx_f(x.y), y[e + 2] = ex2_approx_f(z.x), y[e + 3] = ex2_approx_f(z.y);
-            if (see != 0xffffu) {
-              if (!(see >> e & 1)) y[e] = 0.f;
-              if (!(see >> (e + 1) & 1)) y[e + 1] = 0.f;
-              if (!(see >> (e + 2) & 1)) y[e + 2] = 0.f;
-              if (!(see >> (e + 3) & 1)) y[e + 3] = 0.f;
-            }
-            x = mul2(make_float2(y[e], y[e + 1]), make_float2(r.x, r.y)), z = mul2(make_float2(y[e + 2], y[e + 3]), make_float2(r.z, r.w));
-            pk[e / 2] = pack_f16(x.x, x.y), pk[e / 2 + 1] = pack_f16(z.x, z.y);
+        for (int c = 0; c < KC; ++c) by_k[16 * c + l16] = my_fac[c] * sc.x;
+        for (int again = 0;; ++again) {
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const float mv = s_mv[unit][16 * c + l16], um = neg[16 * c + l16];
+            // (not 0, so that a score too large shows in P whatever V's scale)
+            ratio[16 * c + l16] = um == INFINITY ? 1.f : fmaxf(ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f)), 1.17549435e-38f);
           }
-          *reinterpret_cast<uint4*>(sP + ((u0 ^ swap) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(sP + (((u0 + 1) ^ swap) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          const uint32_t most = max2(max2(max2(pk[0], pk[1]), max2(pk[2], pk[3])), max2(max2(pk[4], pk[5]), max2(pk[6], pk[7])));
-          const bool over = (most & 0xffffu) > 0x5c00u || most >> 16 > 0x5c00u;  // of numbers >= 0: above 256
+          __syncwarp();
+          bool over = false;
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            float v[16];
+            tmem_ld16(lanes + buf * N + 16 * c, v);
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&by_k[16 * c + e]);
+              const float4 m = *reinterpret_cast<const float4*>(&neg[16 * c + e]);
+              const float4 r = *reinterpret_cast<const float4*>(&ratio[16 * c + e]);
+              float2 x = fma2(make_float2(v[e], v[e + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
+              float2 z = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
+              float* yy = y[c] + e;
+              yy[0] = ex2_approx_f(x.x), yy[1] = ex2_approx_f(x.y), yy[2] = ex2_approx_f(z.x), yy[3] = ex2_approx_f(z.y);
+              if (see != 0xffffffffu) {
+                if (!(see >> (16 * c + e) & 1)) yy[0] = 0.f;
+                if (!(see >> (16 * c + e + 1) & 1)) yy[1] = 0.f;
+                if (!(see >> (16 * c + e + 2) & 1)) yy[2] = 0.f;
+                if (!(see >> (16 * c + e + 3) & 1)) yy[3] = 0.f;
+              }
+              x = mul2(make_float2(yy[0], yy[1]), make_float2(r.x, r.y)), z = mul2(make_float2(yy[2], yy[3]), make_float2(r.z, r.w));
+              pk[e / 2] = pack_f16(x.x, x.y), pk[e / 2 + 1] = pack_f16(z.x, z.y);
+            }
+            *reinterpret_cast<uint4*>(sP + (((u0 + 2 * c) ^ swap) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(sP + (((u0 + 2 * c + 1) ^ swap) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            const uint32_t most = max2(max2(max2(pk[0], pk[1]), max2(pk[2], pk[3])), max2(max2(pk[4], pk[5]), max2(pk[6], pk[7])));
+            over |= (most & 0xffffu) > 0x5c00u || most >> 16 > 0x5c00u;  // of numbers >= 0: above 256
+          }
           // Does a score outgrow its column's references by 2^8?  (fp16 and the sums have the room for
           // that.)  Then columns that do get new ones, from their maxima, and it goes once more; what is too
           // large after that is no number.
           if (again || !unit_any(unit, over)) break;
-          {
-            float x[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = see >> e & 1 ? v[e] : -INFINITY;
+          for (int c = 0; c < KC; ++c) {
+            float x[16];
+            tmem_ld16(lanes + buf * N + 16 * c, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (!(see >> (16 * c + e) & 1)) x[e] = -INFINITY;
             const float top = half_reduce<false>(x, lane);
             // (a factor of 0 would make -inf a NaN)
-            float nm = top == -INFINITY ? top : top * f16;
+            float nm = top == -INFINITY ? top : top * (my_fac[c] * sc.x);
             float nv = nm + sc.y;
             nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, 16));
             nv = fmaxf(nv, __shfl_xor_sync(0xffffffffu, nv, 16));
-            if (half == 0) s_red[unit][quad][l16] = make_float2(nm, nv);
+            if (half == 0) s_red[unit][quad][16 * c + l16] = make_float2(nm, nv);
           }
           unit_sync(unit);
-          if (quad == 0 && half == 0) {
-            float nm = -INFINITY, nv = -INFINITY;
+          if (quad == 0) {
+            for (int c = lane; c < UC; c += 32) {
+              float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[unit][q][l16].x), nv = fmaxf(nv, s_red[unit][q][l16].y);
-            const float m = s_m[unit][l16];
-            float by = 1.f, by_o = 1.f;
-            if (nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][l16] = nm, neg[l16] = -nm;
-            if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[unit][l16] = nv;
-            s_by[unit][0][l16] = by, s_by[unit][1][l16] = by_o;
+              for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[unit][q][c].x), nv = fmaxf(nv, s_red[unit][q][c].y);
+              const float m = s_m[unit][c], mv = s_mv[unit][c];
+              float by = 1.f, by_o = 1.f;
+              if (nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][c] = nm, neg[c] = -nm;
+              if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[unit][c] = nv;
+              s_by[unit][0][c] = by, s_by[unit][1][c] = by_o;
+            }
           }
           unit_sync(unit);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sum[e] *= s_by[unit][0][e];
-          if (i > first) {
-            float o[16];
-            tmem_ld16(o_col, o);
-            uint32_t u[16];
+          for (int c = 0; c < KC; ++c) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * s_by[unit][1][e]);
-            tmem_st16(o_col, u);
-            tmem_wait_st();
+            for (int e = 0; e < 16; ++e) sum[c][e] *= s_by[unit][0][16 * c + e];
+            if (i > first) {
+              float o[16];
+              tmem_ld16(o_col + 16 * c, o);
+              uint32_t u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * s_by[unit][1][16 * c + e]);
+              tmem_st16(o_col + 16 * c, u);
+            }
           }
+          tmem_wait_st();
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float2 x = add2(make_float2(sum[e], sum[e + 1]), make_float2(y[e], y[e + 1]));
-          sum[e] = x.x, sum[e + 1] = x.y;
-        }
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float2 x = add2(make_float2(sum[c][e], sum[c][e + 1]), make_float2(y[c][e], y[c][e + 1]));
+            sum[c][e] = x.x, sum[c][e + 1] = x.y;
+          }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
@@ -513,41 +539,46 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
       }
 
       // ---- the part: outputs over the piece's keys, and log2 of the sums ----
-      {
-        float l = half_reduce<true>(sum, lane);
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        float l = half_reduce<true>(sum[c], lane);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (half == 0) s_red[unit][quad][l16].x = l;
+        if (half == 0) s_red[unit][quad][16 * c + l16].x = l;
       }
       if (first < nt) {
         ok = ok && all_wait(&odone[set], (mine - 1) & 1);
         tc_fence_after();
       }
       unit_sync(unit);
-      if (quad == 0 && half == 0)
-        s_sum[unit][l16] = (s_red[unit][0][l16].x + s_red[unit][1][l16].x) + (s_red[unit][2][l16].x + s_red[unit][3][l16].x);
+      if (quad == 0)
+        for (int c = lane; c < UC; c += 32)
+          s_sum[unit][c] = (s_red[unit][0][c].x + s_red[unit][1][c].x) + (s_red[unit][2][c].x + s_red[unit][3][c].x);
       tc_fence_before();
       units_sync<L::soft * 32>();
       tc_fence_after();
       // the first set's units join the others' to their own
       const int64_t slot = w.slot(a, blockIdx.x);
       if (set == 0) {
-        if (quad == 0 && half == 0) {
-          float m = -INFINITY, l = 0.f;
+        if (quad == 0) {
+          for (int c = lane; c < UC; c += 32) {
+            float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int x = 0; x < G; ++x) m = fmaxf(m, s_m[x * L::per_tile + unit][l16]);
+            for (int x = 0; x < G; ++x) m = fmaxf(m, s_m[x * L::per_tile + unit][c]);
 #pragma unroll
-          for (int x = 0; x < G; ++x) {
-            const float part = s_sum[x * L::per_tile + unit][l16];
-            l += m == -INFINITY ? part : part * ex2_approx_f(s_m[x * L::per_tile + unit][l16] - m);
+            for (int x = 0; x < G; ++x) {
+              const float part = s_sum[x * L::per_tile + unit][c];
+              l += m == -INFINITY ? part : part * ex2_approx_f(s_m[x * L::per_tile + unit][c] - m);
+            }
+            // l is 0 where no key is seen, and NaN where a score is  (V as it is: no power of two is left)
+#pragma unroll
+            for (int x = 0; x < G; ++x)
+              s_out[x * L::per_tile + unit][c] = kv8_out_factor<GDN_QDQ_INT8>(s_mv[x * L::per_tile + unit][c], m, l);
+            if (c0 + c < here) a.lses[slot * a.stride + c0 + c] = l == 0.f ? -INFINITY : m + log2f(l);
           }
-          // l is 0 where no key is seen, and NaN where a score is  (V as it is: no power of two is left)
-#pragma unroll
-          for (int x = 0; x < G; ++x)
-            s_out[x * L::per_tile + unit][l16] = kv8_out_factor<GDN_QDQ_INT8>(s_mv[x * L::per_tile + unit][l16], m, l);
-          if (col < here) a.lses[slot * a.stride + col] = l == 0.f ? -INFINITY : m + log2f(l);
         }
         unit_sync(unit);
-        if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < KC && ok; ++c) {
           float o[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = 0.f;
@@ -555,17 +586,17 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           for (int x = 0; x < G; ++x) {
             if ((int)((x - n) & (G - 1)) >= nt) continue;  // no tile of the piece was this set's
             float v[16];
-            tmem_ld16(lanes + L::s_cols + x * N, v);
+            tmem_ld16(lanes + L::s_cols + x * N + 16 * c, v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], s_out[x * L::per_tile + unit][e], o[e]);
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], s_out[x * L::per_tile + unit][16 * c + e], o[e]);
           }
           // with INT8 codes lane d of O is dim 4 (d / 4) + (0 2 1 3)[d % 4]
           const int dim = F8 ? key : (key & ~3) | (key & 1) << 1 | (key >> 1 & 1);
           if (key < DIM) {
-            float* to = a.parts + (slot * a.stride + c0) * DIM + dim;
+            float* to = a.parts + (slot * a.stride + c0 + 16 * c) * DIM + dim;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (c0 + e < here) to[e * DIM] = o[e];
+              if (c0 + 16 * c + e < here) to[e * DIM] = o[e];
           }
         }
       }
@@ -589,14 +620,11 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
     const int from0 = DIM == 128 ? row0c * 128 + ((unit ^ (row0c & 7)) << 4)
                                  : row0c * 64 + ((unit ^ (row0c >> 1 & 3)) << 4);
     const uint32_t to0 = unit_at(row0c, 2 * unit, kKeys), to1 = unit_at(row0c, 2 * unit + 1, kKeys);
-    // Tiles of V, or of K and V in turn (K is one ahead); every step is the same code, which stays
-    // where instructions are near.  (Rows kStep apart: the swizzle is the same.)
+    // Tiles of V, or (INT8, the first four warps) of K: the same code, which stays where instructions
+    // are near.  (Rows kStep apart: the swizzle is the same.)
     const uint32_t all = (uint32_t)w.left;
-    const bool has_k = !F8 && (L::both || !second), has_v = F8 || L::both || second;
-    uint32_t ks = has_k ? 0 : all, vs = has_v ? 0 : all;  // tiles so far
-    while (ks < all || vs < all) {
-      const bool is_k = ks < all && (vs == all || ks < vs + 2);
-      const uint32_t n = is_k ? ks++ : vs++;
+    const bool is_k = !F8 && !second;
+    for (uint32_t n = 0; n < all; ++n) {
       const uint32_t outs = is_k ? kKTiles : R::vtiles, in = n % R::raws, out = n % outs;
       if (!all_wait((is_k ? kin : vin) + in, n / R::raws & 1)) break;
       const unsigned char* from = smem + (is_k ? R::k : R::v) + in * R::raw + from0;
