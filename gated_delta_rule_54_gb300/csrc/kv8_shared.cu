@@ -29,6 +29,8 @@
 // neighbouring keys.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "kv8_tc.cuh"
 #include "launch.h"
 
@@ -354,16 +356,26 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
       const int nt = w.count(), h = w.hq / a.blocks, q0 = w.hq % a.blocks * CW, here = min(all_q - q0, CW);  // columns in use
       // ---- queries: DIM / 8 lanes to a row ----
       {
-        constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;
-#pragma unroll 1
-        for (int c = warp * kAt + lane / kLanes; c < CW; c += L::soft * kAt) {
-          const int i = q0 + c, r_in = i / per_row, x_in = i - r_in * per_row, u = lane % kLanes;
-          const int64_t r = w.g * a.beams + r_in;
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (c < here)
-            raw = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_row + (x_in / p.group) * p.x_token +
-                                                       (int64_t)(h * p.group + x_in % p.group) * p.x_head + 8 * u));
-          if (u == 0) s_lim[c] = c < here ? min(seen_end(p, p.lengths[r], x_in / p.group), w.common) : 0;
+        constexpr int kLanes = DIM / 8, kAt = 32 / kLanes, kTimes = (CW + L::soft * kAt - 1) / (L::soft * kAt);
+        const int u = lane % kLanes;
+        uint4 raws[kTimes];  // (all on their way together)
+#pragma unroll
+        for (int x = 0; x < kTimes; ++x) {
+          const int c = warp * kAt + lane / kLanes + x * L::soft * kAt;
+          raws[x] = make_uint4(0, 0, 0, 0);
+          if (c < CW) {
+            const int i = q0 + c, r_in = i / per_row, x_in = i - r_in * per_row;
+            const int64_t r = w.g * a.beams + r_in;
+            if (c < here)
+              raws[x] = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_row + (x_in / p.group) * p.x_token +
+                                                             (int64_t)(h * p.group + x_in % p.group) * p.x_head + 8 * u));
+            if (u == 0) s_lim[c] = c < here ? min(seen_end(p, p.lengths[r], x_in / p.group), w.common) : 0;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kTimes; ++x) {
+          const int c = warp * kAt + lane / kLanes + x * L::soft * kAt;
+          const uint4 raw = raws[x];
           float f[8], most = 0.f;
           bf16x8(raw, f);
 #pragma unroll
@@ -372,6 +384,7 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
           float up, back;
           kv8_q_factor<F8 ? 7 : 8>(most, up, back);
+          if (c >= CW) break;  // (all rows of a warp's or none)
           if (u == 0) s_fac[c] = back * fabsf(p.scale) * kLog2eF;
           if (p.scale < 0.f) up = -up;
           if constexpr (F8) {  // an E4M3 number and an E5M2 one (kv8.cuh)
@@ -1179,7 +1192,15 @@ template <int MODE, int DIM, int CW>
 gdn_status run_common(const SharedArgs& a, cudaStream_t st) {
   auto kern = kv8_common_kernel<MODE, DIM, CW>;
   constexpr int bytes = Room<MODE, DIM, CW>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GDN_ERR_CUDA;
+  // once for a device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return GDN_ERR_CUDA;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   kern<<<a.grid, Plan<MODE, CW>::threads, bytes, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

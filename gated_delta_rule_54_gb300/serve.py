@@ -277,7 +277,7 @@ def kv8_attention_shared(q, codes, scales, table, lengths, shared, beams, mode="
     else:
         _say(dev, ("out", out, _bf16))
         _need(out.shape == q.shape, "out must have q's shape")
-    lse = torch.empty_like(q[..., 0], dtype=_f32, memory_format=_contiguous) if need_lse else None
+    lse = torch.empty(*q.shape[:-1], dtype=_f32, device=codes.device) if need_lse else None
     lib = _fns()
     if workspace is None:
         need = _shared_bytes.get((p, beams))
