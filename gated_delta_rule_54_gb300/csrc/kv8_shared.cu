@@ -1126,49 +1126,79 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_own_kernel(const __grid_const
   const Shares shares(all * per, a.grid);
   __syncthreads();
   grid_dep_wait();  // the parts of the group's tokens
-  for (int i = warp; i < rows_in; i += kWarps) {
-    // this row's parts: those of the CTAs whose shares meet its (group, head, block)
-    const int qi = (int)(r - grp * a.beams) * (p.tokens * p.group) + i0 + i, hq = h * a.blocks + qi / a.cw, col = qi % a.cw;
-    int64_t c0 = 0;
-    int n = 0;
-    if (tiles > 0) {
-      const int64_t u0 = before + (int64_t)hq * tiles;
-      c0 = shares.cta_of(u0), n = (int)(shares.cta_of(u0 + tiles - 1) - c0) + 1;
+  // With sixteen rows a warp's four go side by side, so that their loads are in flight together (30
+  // (row, head) of 15 rows: 33 us one after the other, 29 so).
+  constexpr int kMine = NB == 1 ? 1 : ROWS / kWarps;
+#pragma unroll 1
+  for (int i1 = warp; i1 < rows_in; i1 += kMine * kWarps) {
+    int64_t slot[kMine];  // of the row's first part in the workspace, and every a.stride from there
+    int n[kMine], most_n = 0;
+    float top[kMine], l[kMine];
+    float4 o[kMine];
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      // this row's parts: those of the CTAs whose shares meet its (group, head, block)
+      const int i = i1 + x * kWarps;
+      const int qi = (int)(r - grp * a.beams) * (p.tokens * p.group) + i0 + i, hq = h * a.blocks + qi / a.cw;
+      int64_t c0 = 0;
+      n[x] = 0;
+      if (tiles > 0 && i < rows_in) {
+        const int64_t u0 = before + (int64_t)hq * tiles;
+        c0 = shares.cta_of(u0), n[x] = (int)(shares.cta_of(u0 + tiles - 1) - c0) + 1;
+      }
+      slot[x] = (grp * per + hq + c0) * a.stride + qi % a.cw;
+      most_n = max(most_n, n[x]);
+      top[x] = -INFINITY, l[x] = 0.f, o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int64_t slot = (grp * per + hq + c0) * a.stride + col;  // and every a.stride from there
-    float top = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) top = max_nan(top, s_lse[w][i]);
-    for (int k = lane; k < n; k += 32) top = max_nan(top, a.lses[slot + (int64_t)k * a.stride]);
-    for (int d = 16; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    auto add = [&](float c, float4 x) {
-      l += c;
-      o.x = fmaf(c, x.x, o.x), o.y = fmaf(c, x.y, o.y), o.z = fmaf(c, x.z, o.z), o.w = fmaf(c, x.w, o.w);
+    auto lse_of = [&](int x, int k) { return k < n[x] ? a.lses[slot[x] + (int64_t)k * a.stride] : -INFINITY; };
+    for (int k = lane; k - lane < most_n; k += 32)
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) top[x] = max_nan(top[x], lse_of(x, k));
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      for (int w = 0; w < kWarps; ++w) top[x] = max_nan(top[x], s_lse[w][i1 + x * kWarps]);
+      for (int d = 16; d; d >>= 1) top[x] = max_nan(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
+    }
+    // (a weight of 0 for rows without a score)
+    auto add = [&](int x, float lse, float4 v) {
+      const float c = top[x] == -INFINITY ? 0.f : ex2_approx_f(lse - top[x]);
+      l[x] += c;
+      o[x].x = fmaf(c, v.x, o[x].x), o[x].y = fmaf(c, v.y, o[x].y), o[x].z = fmaf(c, v.z, o[x].z), o[x].w = fmaf(c, v.w, o[x].w);
     };
-    if (top != -INFINITY) {
-      for (int w = 0; w < kWarps; ++w)
-        add(ex2_approx_f(s_lse[w][i] - top), lane < DIM / 4 ? *reinterpret_cast<const float4*>(&s_o[w][i][4 * lane]) : o);
-      // four parts at a time, so that their loads are in flight together
-      for (int k0 = 0; k0 < n; k0 += 4) {
-        float c[4];
-        float4 x[4];
+    const int at4 = 4 * (lane % (DIM / 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t at = slot + (int64_t)min(k0 + k, n - 1) * a.stride;
-          c[k] = k0 + k < n ? a.lses[at] : -INFINITY;
-          x[k] = lane < DIM / 4 ? *reinterpret_cast<const float4*>(a.parts + at * DIM + 4 * lane) : o;
-        }
+    for (int x = 0; x < kMine; ++x)
+      for (int w = 0; w < kWarps; ++w) add(x, s_lse[w][i1 + x * kWarps], *reinterpret_cast<const float4*>(&s_o[w][i1 + x * kWarps][at4]));
+    for (int k0 = 0; k0 < most_n; k0 += 32) {
+      float lse[kMine];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add(ex2_approx_f(c[k] - top), x[k]);
+      for (int x = 0; x < kMine; ++x) lse[x] = lse_of(x, k0 + lane);
+      constexpr int J = NB == 1 ? 4 : 2;
+      for (int k = k0; k < min(k0 + 32, most_n); k += J) {
+        float4 v[kMine][J];
+#pragma unroll
+        for (int x = 0; x < kMine; ++x)
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            v[x][j] = k + j < n[x] ? *reinterpret_cast<const float4*>(a.parts + (slot[x] + (int64_t)(k + j) * a.stride) * DIM + at4)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kMine; ++x)
+#pragma unroll
+          for (int j = 0; j < J; ++j) add(x, __shfl_sync(0xffffffffu, lse[x], (k + j) & 31), v[x][j]);
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = (r * p.tokens + (i0 + i) / p.group) * (p.heads * p.group) + h * p.group + (i0 + i) % p.group;
-    if (lane < DIM / 4)
-      *reinterpret_cast<uint2*>(p.o + at * DIM + 4 * lane) =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      const int i = i1 + x * kWarps;
+      if (i >= rows_in) break;
+      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
+      const int64_t at = (r * p.tokens + (i0 + i) / p.group) * (p.heads * p.group) + h * p.group + (i0 + i) % p.group;
+      if (lane < DIM / 4)
+        *reinterpret_cast<uint2*>(p.o + at * DIM + at4) =
+            make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
+      if (p.lse && lane == 0) p.lse[at] = l[x] == 0.f ? -INFINITY : (top[x] + log2f(l[x])) * 0.6931471805599453f;
+    }
   }
 }
 
