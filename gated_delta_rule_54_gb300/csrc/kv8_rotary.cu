@@ -10,6 +10,12 @@
 // other's partners (or two neighbouring chunks, where pairs are neighbours or nothing turns), so
 // that a pair meets in registers.  Its angles stay there while it goes through the heads of
 // its token.  The bytes of q, k, v and the codes bound it.
+//
+// Measured on a GB300: eight uneven prompts of up to 4096 tokens, 8 K/V heads of 128 and 32 query
+// heads, E4M3, 446 MB: 88 us, 5.1 TB/s (copying: 6.8), DRAM and issue (0.51 a clock and scheduler)
+// together, two CTAs of 123 registers per SM.  With one chunk pair per thread, 512 threads, 112 to
+// 124; with three CTAs per SM (registers spilled) 143; four heads per CTA 95, sixteen 92.  64
+// single tokens: 2.7 us, launch and latency.
 #include <math.h>
 
 #include "kv8.cuh"
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(NT) kv8_rotary_kernel(const __grid_constant__ 
   }
 }
 
-// One token per row: DIM / 16 lanes take a head of it, so a warp 4 (or 8) heads.
+// One token per row: DIM / 16 lanes take a head of it, so a warp 4 (or 8) heads.  (64 rows x 48 heads 2.7 us.)
 template <int MODE, int DIM>
 __global__ void __launch_bounds__(128) kv8_rotary_one_kernel(const __grid_constant__ RotaryParams a, int groups) {
   constexpr int UN = DIM / 16, G = 32 / UN;
@@ -305,7 +311,8 @@ gdn_status run(const RotaryParams& a, cudaStream_t st) {
   // pages that n consecutive positions can touch
   const int blocks = (p.tokens + p.page - 2) / p.page + 1;
   if (p.rows * blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-  // heads per CTA, whose loads overlap and which share the angles: up to 8 while 152 SMs still get eight CTAs each
+  // heads per CTA, whose loads overlap and which share the angles: up to 8 while 152 SMs still get eight
+  // CTAs each (8 prompts to 4096 tokens: four 95.5 us, eight 88.7, sixteen 92.5)
   int per = 1;
   while (per < 8 && per < heads && p.rows * blocks * heads / (2 * per) >= 152 * 8) per *= 2;
   const int64_t runs = (heads + per - 1) / per;

@@ -4,29 +4,46 @@
 //
 // The group's tokens.  The query rows of a (group, K/V head) are its rows times their
 // queries times the query heads that share the head; they are few, so the products are laid
-// out with the keys as the long side.  Per 128 keys and up to NQ query rows:
-//     S = K Q^T      (tcgen05, fp16 -> fp32 in TMEM: lane = key, column = query)
+// out with the keys as the long side.  Per 128 keys and up to 64 query rows:
+//     S = K Q^T      (tcgen05, E4M3 or fp16 -> fp32 in TMEM: lane = key, column = query)
 //     P = 2^(s - reference), fp16 to shared memory
 //     O += V^T P     (lane = dim, column = query)
-// and only the columns in use cost exponentials.  All tiles of all (group, head, block of query
-// rows) form one line, of which every CTA takes an equal, contiguous share; what it has of a
-// (group, head, block) is a part: outputs over its own keys, and their log-sum-exp.
-// One warp brings the codes of a tile by TMA (a box per page), four turn K's into fp16 (exact)
-// and four V's, one lane issues the products, and eight warps are the keys: a thread
-// has one key, and half of the queries.
+// and only the columns in use (16, 32 or 64) cost exponentials.  All tiles of all (group, head,
+// block of query rows) form one line, of which every CTA takes an equal, contiguous share; what it
+// has of a (group, head, block) is a part: outputs over its own keys, and their log-sum-exp.
+// A warp brings the codes of K by TMA (a box per page) and one those of V, into rings of their
+// own; four turn V's into fp16 and, with INT8 codes, four K's; one lane of a warp issues Q K^T,
+// one of another P V; and eight warps are the keys: a thread has one key, and 16 or 32 of the
+// queries.  E4M3 codes of K are an operand as they are, q being the sum of two 8-bit numbers.
 //
-// A column's maxima (of s, and of s + log2 of V's scale, which is one for 16 lanes) come by exchanges
-// within half-warps and through shared memory.  The references follow them, per column, only
-// when they grow by more than 2^8, which fp16 has the room for; so a row's result does not
-// depend on the rows beside it.
+// A score is taken against its column's references (the largest s, and s + log2 of V's scale,
+// which is one for 16 lanes) as they are; where one outgrows them by 2^8, which fp16 and the
+// sums have the room for, the columns that did get new ones from their maxima and the tile is done
+// again.  Each column decides for itself, so a row's result does not depend on the rows
+// beside it.
 //
-// A row's own tokens.  A CTA takes 16 query rows of a (row, K/V head): its warps go through
-// tiles of 32 keys from registers, and their parts are joined with those of the group's tokens.
-// Codes go from global memory into the lanes that need them.  A score is a sum over dims in
-// any order, so a lane's 16 bytes of a key are four steps of a warp product whose other operand,
-// q, is laid out alike; and the columns of P V are dims in any order, so a lane's 16 bytes
-// of each of four keys are its column of 16 products, after an exchange of bytes between
-// neighbouring keys.
+// A row's own tokens.  A CTA takes 8 (or 16) query rows of a (row, K/V head): its warps go through
+// 16 keys at a time from registers, again with the keys, and the dims, as the long side of
+// warp products, and their parts are joined with those of the group's tokens.  Codes go from global
+// memory into the lanes that need them: a score is a sum over dims in any order, so a lane's 16
+// bytes of a key are steps of a product whose other operand, q, is laid out alike; and the rows of
+// V^T P are dims in any order, so a lane's bytes of each of four keys are its rows of eight
+// products, after an exchange of bytes between neighbouring keys.
+//
+// Measured on a GB300 (both launches, replayed): 16 x 8 beams behind 1096 .. 4096 tokens with 90 .. 150
+// of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 63 us (kv8_attention 148);
+// 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 90 us (344); 8 beams behind 131072 tokens,
+// 4 heads, INT8, 135 MB: 61 us (188); 4 beams behind 1472: 11 us (16.5).  DRAM is at 30 % in the
+// first launch.  What bounds it is the chain of a tile from S by P to the next: about 2300 cycles
+// for the keys' warps, whose instructions take 5 to 7 cycles each, and what a role runs per tile has
+// to stay near: a form with all columns in one unit, and one with a code for each use, missed
+// the instruction cache 130 times a tile (now 46) and took 78 to 85 us of the first case.  Taking
+// the tiles apart gave: without conversions 53 of 70 us (third case), without the softmax 58,
+// without both 44, without loads as well 30.  Four groups of warps instead of two were slower (73 us
+// beside 69), for want of registers; deeper rings of codes changed nothing.  Warp products from
+// rings in shared memory instead of tcgen05, for up to 32 rows, took 124 us of the third case.
+// A row's own tokens take 10 us of the first case and 23 of the second (latency: three CTAs per
+// SM; with products that have the queries as the long side, half of each empty, 31 and 32).
 #include <cuda.h>
 
 #include <atomic>
