@@ -198,7 +198,9 @@ gdn_status validate_logits(const gdn_logits_problem* p) {
     return p->dtype == GDN_DTYPE_FP16 ? GDN_ERR_UNSUPPORTED_DTYPE : GDN_ERR_INVALID_ARG;
   if ((p->bias_row != 0 && p->bias_row < p->vocab) || (p->mask_row != 0 && p->mask_row < ((int64_t)p->vocab + 31) / 32))
     return GDN_ERR_INVALID_ARG;
-  if (p->stride > 1LL << 36 || p->rows > 0x7fffffffLL >> 8 || p->vocab > 0x7fffffff - 65536) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (p->stride > 1LL << 36 || p->rows > 0x7fffffffLL >> 8 || p->vocab > 0x7fffffff - 65536 ||
+      p->cols > 0x7fffffff - 65536)  // (indices are 32-bit, some thousand ahead)
+    return GDN_ERR_UNSUPPORTED_SHAPE;
   return GDN_OK;
 }
 

@@ -683,8 +683,8 @@ typedef struct {
   int64_t stride;       /* elements from one row of logits to the next            */
   int64_t bias_row;     /* 0 or >= vocab                                          */
   int64_t mask_row;     /* 0 or >= ceil(vocab / 32)                               */
-  int32_t vocab;        /* >= 1                                                   */
-  int32_t cols;         /* columns of tokens                                      */
+  int32_t vocab;        /* 1 .. 2^31 - 2^16 - 1                                   */
+  int32_t cols;         /* columns of tokens, up to 2^31 - 2^16 - 1               */
   int32_t dtype;        /* GDN_DTYPE_BF16 or GDN_DTYPE_FP32                       */
 } gdn_logits_problem;
 

@@ -101,6 +101,15 @@ def test_logits_refusals():
     assert f(prob(rows=0), *[None] * 9) == 0
 
 
+def test_logits_history_stays_in_32_bits():
+    """A thread goes through a history by 32-bit indices, some thousand tokens ahead of it."""
+    lib = _lib.load()
+    prob = lambda cols: GdnLogitsProblem(rows=1, stride=100, bias_row=0, mask_row=0, vocab=100, cols=cols, dtype=0)
+    assert lib.gdn_beam_logits_validate(ctypes.byref(prob(0x7fffffff - 65536))) == 0
+    for cols in (0x7fffffff - 65535, 0x7fffffff):
+        assert lib.gdn_beam_logits_validate(ctypes.byref(prob(cols))) == -3
+
+
 def test_dependent_launches_wait_before_any_return():
     """A kernel that may start before its predecessor ends orders the rest of the stream behind it
     only by its own wait, so no thread leaves before that."""
