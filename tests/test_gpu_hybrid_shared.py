@@ -110,3 +110,39 @@ def test_shared_and_plain_attention_agree():
     a, b = (x.float() for x in out)
     # an attention layer and two layers behind it: a few bf16 roundings of the largest logit
     assert (a - b).abs().max() <= 8 * 2.0 ** -8 * a.abs().max()
+
+
+def test_two_streams_at_once():
+    """A step's three operators on two streams at once, each with rows of its own, as one after the other."""
+    rows, beams, heads, group, dim, page, vocab = 8, 4, 2, 4, 128, 64, 40000
+    todo = []
+    for seed in (3, 4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rand = lambda *shape, t=torch.bfloat16: torch.randn(*shape, generator=g, device="cuda").to(t)
+        kv = gdn.kv8_pool(1, rows * 40, heads, dim, page=page)
+        table = torch.arange(rows * 40, device="cuda", dtype=torch.int32).view(rows, 40)
+        at, shared = torch.full((rows,), 2300, dtype=torch.int32, device="cuda"), torch.full((rows // beams,), 2176, dtype=torch.int32, device="cuda")
+        gdn.kv8_append(rand(rows, 2300, heads, dim), rand(rows, 2300, heads, dim), kv[0][0], kv[1][0], table, torch.zeros_like(at))
+        angles = torch.rand(2400, dim // 2, generator=g, device="cuda")
+        q, k, v = rand(rows, 1, heads * group, dim), rand(rows, 1, heads, dim), rand(rows, 1, heads, dim)
+        logits, cost = rand(2, beams, vocab), torch.rand(2, beams, generator=g, device="cuda")
+        said = torch.randint(0, vocab, (2, beams, 900), generator=g, device="cuda", dtype=torch.int32)
+
+        def step(codes=kv[0][0], scales=kv[1][0], table=table, at=at, shared=shared, cos=angles.cos(), sin=angles.sin(),
+                 q=q, k=k, v=v, logits=logits, said=said, cost=cost):
+            turned = gdn.kv8_append_rotary(q, k, v, codes, scales, table, at, cos, sin)
+            o, lse = gdn.kv8_attention_shared(turned, codes, scales, table, at + 1, shared, beams, need_lse=True)
+            return turned, o, lse, gdn.beam_logits(logits, said, frequency=cost)
+        todo.append((step, step()))
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in todo]
+    got = [[] for _ in todo]
+    for _ in range(10):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(todo[i][0]())  # (the same tokens at the same places: nothing changes)
+    torch.cuda.synchronize()
+    for (_, want), many in zip(todo, got):
+        for one in many:
+            assert all(torch.equal(a, b) for a, b in zip(one, want))
+    assert gdn.load().gdn_device_error(0) == 0
