@@ -13,9 +13,9 @@
 //
 // Measured on a GB300: eight uneven prompts of up to 4096 tokens, 8 K/V heads of 128 and 32 query
 // heads, E4M3, 446 MB: 88 us, 5.1 TB/s (copying: 6.8), DRAM and issue (0.51 a clock and scheduler)
-// together, two CTAs of 123 registers per SM.  With one chunk pair per thread, 512 threads, 112 to
-// 124; with three CTAs per SM (registers spilled) 143; four heads per CTA 95, sixteen 92.  64
-// single tokens: 2.7 us, launch and latency.
+// together, two CTAs of 123 registers per SM.  With 512 threads of one unit each 124, or 112 with two
+// such CTAs per SM; 256 of two units with three CTAs per SM 143, with four 161; 128 of four units 90.
+// 64 single tokens: 2.7 us, launch and latency.
 #include <math.h>
 
 #include "kv8.cuh"
