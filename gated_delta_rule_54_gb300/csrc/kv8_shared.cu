@@ -20,7 +20,8 @@
 // which is one for 16 lanes) as they are; where one outgrows them by 2^8, which fp16 and the
 // sums have the room for, the columns that did get new ones from their maxima and the tile is done
 // again.  Each column decides for itself, so a row's result does not depend on the rows
-// beside it.
+// beside it; nor on its place, where a group's query rows of a K/V head fit one block of 64.  (Blocks lie
+// at different places of the line, where CTAs' shares cut their keys differently.)
 //
 // A row's own tokens.  A CTA takes 8 (or 16) query rows of a (row, K/V head): its warps go through
 // 16 keys at a time from registers, again with the keys, and the dims, as the long side of
@@ -31,19 +32,22 @@
 // products, after an exchange of bytes between neighbouring keys.
 //
 // Measured on a GB300 (both launches, replayed): 16 x 8 beams behind 1096 .. 4096 tokens with 90 .. 150
-// of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 63 us (kv8_attention 148);
+// of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 62 us (kv8_attention 148);
 // 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 90 us (344); 8 beams behind 131072 tokens,
-// 4 heads, INT8, 135 MB: 61 us (188); 4 beams behind 1472: 11 us (16.5).  DRAM is at 30 % in the
-// first launch.  What bounds it is the chain of a tile from S by P to the next: about 2300 cycles
-// for the keys' warps, whose instructions take 5 to 7 cycles each, and what a role runs per tile has
-// to stay near: a form with all columns in one unit, and one with a code for each use, missed
-// the instruction cache 130 times a tile (now 46) and took 78 to 85 us of the first case.  Taking
-// the tiles apart gave: without conversions 53 of 70 us (third case), without the softmax 58,
-// without both 44, without loads as well 30.  Four groups of warps instead of two were slower (73 us
-// beside 69), for want of registers; deeper rings of codes changed nothing.  Warp products from
-// rings in shared memory instead of tcgen05, for up to 32 rows, took 124 us of the third case.
-// A row's own tokens take 10 us of the first case and 23 of the second (latency: three CTAs per
-// SM; with products that have the queries as the long side, half of each empty, 31 and 32).
+// 4 heads, INT8, 135 MB: 61 us (188); 4 beams behind 1472: 11 us (16.5).  Where little is in common
+// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 29 us (19).
+//
+// DRAM is at 30 % in the first launch, issue at 36 %.  What bounds it is the chain of a tile from S by P
+// to the next: in the first case (an earlier form, 67 us) 46.8 of a keys' warp's 73.6 thousand cycles were its own,
+// 2200 for each of 21 tiles, and the rest waits for S and O.  On an earlier form (80 us in the first case,
+// 70 in the third) with parts of the work left out the third took: without conversions 53 us, without
+// the softmax 59, without both 44, and without loads and products as well 30.  Four units of warps
+// instead of two, with 80 registers a thread, spilled and missed the instruction cache 131 times a tile
+// instead of 46: 80, 129 and 78 us.  Two that take whole tiles of 32 columns in turn: 69, 104 and 68.
+// Warp products from rings in shared memory instead of tcgen05, for up to 32 rows: 133 and 124 in the
+// first and the third.
+// A row's own tokens take 9 us of the first case and 23 of the second (latency; products that had the
+// queries as the long side, half of each empty, took 31 and 32 of an earlier form).
 #include <cuda.h>
 
 #include <atomic>
@@ -62,9 +66,8 @@ constexpr int kKeys = 128;  // the group's tokens: keys of a tile
 
 // The first kernel: CW query rows (columns) of a block, N of a product.  Two units of four warps
 // have 16 (or 32) columns of a tile each, so that what they go through per tile is short, or
-// take tiles in turn: `sets` tiles are worked on at a time.  (With four units a thread had too few
-// registers, and all columns in one unit spent its time on fetching instructions.)  Warps turn codes
-// into fp16: four do V's, and with INT8 codes four more K's.
+// take tiles in turn: `sets` tiles are worked on at a time.  Warps turn codes into fp16: four do V's,
+// and with INT8 codes four more K's.
 template <int MODE, int CW>
 struct Plan {
   static constexpr bool f8 = MODE == GDN_QDQ_E4M3;
@@ -262,7 +265,7 @@ struct Ring {
 
 // Shared memory of the first kernel: codes of K and of V as they arrive, as many tiles of them as
 // there is room for, since what is on its way is what DRAM's latency leaves; fp16 tiles of V and
-// (INT8; E4M3 codes are an operand as they are) of K; the queries, and the groups' P.
+// (INT8; E4M3 codes are an operand as they are) of K; the queries, and the sets' P.
 // V with 64 dims has a panel of zeros for the other 64 lanes of O.
 template <int MODE, int DIM, int CW>
 struct Room {
@@ -1225,6 +1228,12 @@ SharedArgs sized(const Kv8Params& p, int beams) {
   a.p = p;
   a.beams = beams;
   const int64_t rows = (int64_t)beams * p.tokens * p.group;
+  // As few columns as the rows need: 16 query rows behind 65536 tokens 28 us, in blocks of 32 columns 33;
+  // 32 behind 131072 62 us, in blocks of 64 76.  More rows go in blocks of 64, since tiles are
+  // loaded and turned into fp16 for each (256 rows behind 16384 tokens 90 us, in blocks of 32 106).  For short
+  // lines two blocks of 32 would be faster (45 rows behind 1000 .. 5000 25.5 us, in one of 64 28), but blocks are
+  // cut at different keys: a row's roundings would depend on its place in a group of more than 32, not
+  // of more than 64, and beams change places.
   a.cw = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   a.blocks = (int)((rows + a.cw - 1) / a.cw);
   a.stride = (int)(rows < a.cw ? rows : a.cw);
@@ -1256,8 +1265,13 @@ template <int MODE, int DIM>
 gdn_status run(SharedArgs& a, cudaStream_t st) {
   const Kv8Params& p = a.p;
   const int64_t rows = (int64_t)p.tokens * p.group;
-  const bool few = rows <= 8;
-  const int64_t y = few ? 1 : (rows + 15) / 16;
+  // Eight query rows to a CTA where there are no more, or where all CTAs have an SM of their own (15 rows of
+  // 30 (row, head) 26.7 us, in one CTA of sixteen 28.2; 16 of 16 16.2 and 18.5), else sixteen, for
+  // which a row's own tokens are read once (16 rows of 512 (row, head) with 1000 tokens 95 us, by eights 104; 16 of
+  // 128 49.3 and 50.5).
+  const int64_t eights = (rows + 7) / 8;
+  const bool few = rows <= 8 || p.rows * p.heads * eights <= 152;
+  const int64_t y = few ? eights : (rows + 15) / 16;
   if (y > 65535) return GDN_ERR_UNSUPPORTED_SHAPE;
   if (p.pages > 0 && !make_map_3d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, DIM, p.page,
                                   (uint64_t)(2 * p.pages * p.heads), DIM, DIM, p.page,

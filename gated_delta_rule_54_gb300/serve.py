@@ -263,8 +263,11 @@ def kv8_attention_shared(q, codes, scales, table, lengths, shared, beams, mode="
     that a group has in common (the prompt of its beams: with kv8_fork its whole pages; all rows'
     system prompt with beams = rows).  Positions below it are looked up in the table row of the
     group's first row (which has no more of them in common than it has), the others in the row's
-    own, so the result is kv8_attention's where the rows hold the same tokens there.  q bf16 [rows, tokens, query heads, dim], for a few tokens each:
-    whole prompts gain nothing from sharing.  The rest as for kv8_attention."""
+    own, so the result is kv8_attention's, up to roundings, where the rows hold the same tokens there.
+    q bf16 [rows, tokens, query heads, dim], for a few tokens each: whole prompts gain nothing from
+    sharing, nor do groups with little in common.  A row's bits do not depend on what its group's other
+    rows hold, nor on its place among them while beams * tokens * query heads / K/V heads <= 64.  The
+    rest as for kv8_attention."""
     p = _problem(q, None, codes, scales, table, lengths, None, None, mode,
                  codes.shape[-1] ** -0.5 if scale is None else scale, 1 if causal else 0, 0)
     dev, beams = codes.get_device(), int(beams)

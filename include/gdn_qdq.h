@@ -560,7 +560,8 @@ gdn_status gdn_kv8_append_rotary(const gdn_kv8_problem* p, const gdn_kv8_rotary*
  * shared counts tokens; it is cut to what the first row has (0 .. lengths, and the
  * table's columns).  What a query sees, NaNs and infinities, and the fewer bits of
  * the probabilities and of q are as for gdn_kv8_attention.  A row's result does not
- * depend on its group's other rows, but for the tokens of the first.
+ * depend on its group's other rows, but for the tokens of the first; and where
+ * beams * tokens * group <= 64 its bits do not depend on its place in the group.
  * Not packed (cu_seqlens NULL: GDN_ERR_INVALID_ARG), no window
  * (GDN_ERR_UNSUPPORTED_MODE), rows a multiple of beams.
  *   shared i32 [rows / beams]; the others as for gdn_kv8_attention
