@@ -35,7 +35,7 @@
 // of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 62 us (kv8_attention 148);
 // 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 90 us (344); 8 beams behind 131072 tokens,
 // 4 heads, INT8, 135 MB: 61 us (188); 4 beams behind 1472: 11 us (16.5).  Where little is in common
-// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 29 us (19).
+// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 27 us (19).
 //
 // DRAM is at 30 % in the first launch, issue at 36 %.  What bounds it is the chain of a tile from S by P
 // to the next: in the first case (an earlier form, 67 us) 46.8 of a keys' warp's 73.6 thousand cycles were its own,
