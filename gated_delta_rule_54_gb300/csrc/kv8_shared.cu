@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
   // for 16 keys of a tile: factor of the scores, 2^(log2 vs + m - mv)
   __shared__ __align__(16) float s_by_k[L::soft][2][UC], s_ratio[L::soft][2][UC];
   __shared__ float2 s_red[L::units][4][UC];
+  __shared__ uint32_t s_over[L::units][4];  // columns of which a P is too large, by warp
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const Kv8Params& p = a.p;
@@ -512,8 +513,21 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           }
           // Does a score outgrow its column's references by 2^8?  (fp16 and the sums have the room for
           // that.)  Then columns that do get new ones, from their maxima, and it goes once more; what is too
-          // large after that is no number.
+          // large after that is no number.  Only columns with a P too large of their own: another's scores may
+          // have outgrown theirs where V's scale is small, and would move or not as its neighbours do.
           if (again || !unit_any(unit, over)) break;
+          uint32_t too = 0;
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 r = *reinterpret_cast<const float2*>(&ratio[16 * c + e]);
+              const float2 x = mul2(make_float2(y[c][e], y[c][e + 1]), r);
+              const uint32_t both = pack_f16(x.x, x.y);
+              too |= (uint32_t)((both & 0xffffu) > 0x5c00u) << (16 * c + e) | (uint32_t)(both >> 16 > 0x5c00u) << (16 * c + e + 1);
+            }
+          too = __reduce_or_sync(0xffffffffu, too);
+          if (lane == 0) s_over[unit][quad] = too;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             float x[16];
@@ -531,14 +545,15 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           }
           unit_sync(unit);
           if (quad == 0) {
+            const uint32_t moves = s_over[unit][0] | s_over[unit][1] | s_over[unit][2] | s_over[unit][3];
             for (int c = lane; c < UC; c += 32) {
               float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
               for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[unit][q][c].x), nv = fmaxf(nv, s_red[unit][q][c].y);
               const float m = s_m[unit][c], mv = s_mv[unit][c];
               float by = 1.f, by_o = 1.f;
-              if (nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][c] = nm, neg[c] = -nm;
-              if (nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[unit][c] = nv;
+              if ((moves >> c & 1) && nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][c] = nm, neg[c] = -nm;
+              if ((moves >> c & 1) && nv > mv + 8.f) by_o = ex2_approx_f(mv - nv), s_mv[unit][c] = nv;
               s_by[unit][0][c] = by, s_by[unit][1][c] = by_o;
             }
           }

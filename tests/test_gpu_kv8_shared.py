@@ -204,6 +204,54 @@ def test_a_rows_result_does_not_depend_on_its_neighbours():
         assert torch.equal(o3[::2], o[::2]) and torch.equal(lse3[::2], lse[::2])
 
 
+@pytest.mark.parametrize("beams,tokens,group", [(12, 1, 4), (16, 2, 2), (7, 3, 3)])
+def test_a_place_in_the_group_does_not_count_where_ctas_have_uneven_shares(beams, tokens, group):
+    """Up to 64 query rows of a K/V head, more tiles than CTAs: 2 groups x 4 heads x 40 tiles and more."""
+    rng = np.random.default_rng(31)
+    codes, scales, table, lens, common, beams, q = _inputs(rng, [5056, 6016], [40] * (2 * beams), tokens, 4, group, 128, 64, "e4m3")
+    c, s, t, n, p = _cuda(codes, scales, table, lens, common)
+    o, lse = kv8_attention_shared(q, c, s, t, n, p, beams, need_lse=True)
+    order = torch.from_numpy(np.concatenate([rng.permutation(beams), beams + rng.permutation(beams)])).cuda()
+    o2, lse2 = kv8_attention_shared(q[order], c, s, t[order].contiguous(), n[order], p, beams, need_lse=True)
+    assert torch.equal(o2, o[order]) and torch.equal(lse2, lse[order])
+
+
+@pytest.mark.parametrize("mode,beams,group", [("e4m3", 4, 4), ("int8", 8, 4), ("e4m3", 16, 4), ("int8", 40, 4)])
+def test_neighbours_do_not_count_whatever_the_scales_of_v(mode, beams, group):
+    """Scores of a row may outgrow its earlier ones where V's scale is small; rows beside it that are
+    spoilt, or have far larger scores, or none, change no bit of it."""
+    rng = np.random.default_rng(33)
+    codes, scales, table, lens, common, n, q = _inputs(rng, [6016], [40] * beams, 1, 2, group, 128, 64, mode, qstd=4.0)
+    scales[1] *= np.exp2(rng.integers(-30, 5, scales[1].shape)).astype(np.float32)
+    c, s, t, l, p = _cuda(codes, scales, table, lens, common)
+    q = q.clone()
+    o, lse = kv8_attention_shared(q, c, s, t, l, p, n, mode=mode, need_lse=True)
+    for change in (30.0, 0.0, float("nan")):
+        q2 = q.clone()
+        q2[1::2] *= change
+        o2, lse2 = kv8_attention_shared(q2, c, s, t, l, p, n, mode=mode, need_lse=True)
+        assert torch.equal(o2[::2], o[::2]) and torch.equal(lse2[::2], lse[::2]), change
+
+
+@pytest.mark.parametrize("mode,beams", [("e4m3", 4), ("int8", 8), ("e4m3", 16), ("int8", 12)])
+def test_a_columns_references_move_for_itself(mode, beams):
+    """From page 20 on scores are three times as large and V's scale 2^-25: they outgrow the earlier ones
+    by more than 2^8 but their products with V's scale do not, unless a row's q is eight times as large."""
+    rng = np.random.default_rng(35)
+    codes, scales, table, lens, common, n, q = _inputs(rng, [6016], [40] * beams, 1, 2, 4, 128, 64, mode)
+    late = np.unique(table[:, 20:94])
+    scales[0][late] *= 3
+    scales[1][late] *= np.float32(2.0 ** -25)
+    c, s, t, l, p = _cuda(codes, scales, table, lens, common)
+    q = q.clone()
+    want = kv8_attention_shared(q, c, s, t, l, p, n, mode=mode, need_lse=True)
+    _check(want, q, codes, scales, table, lens, common, n, mode, 128 ** -0.5)
+    q[1::2] *= 8
+    got = kv8_attention_shared(q, c, s, t, l, p, n, mode=mode, need_lse=True)
+    assert torch.equal(got[0][::2], want[0][::2]) and torch.equal(got[1][::2], want[1][::2])
+    assert load().gdn_device_error(0) == 0
+
+
 def test_stream_graph_workspace_and_far_pages():
     rng = np.random.default_rng(29)
     heads, page, dim = 8, 128, 128
