@@ -32,10 +32,10 @@
 // products, after an exchange of bytes between neighbouring keys.
 //
 // Measured on a GB300 (both launches, replayed): 16 x 8 beams behind 1096 .. 4096 tokens with 90 .. 150
-// of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 62 us (kv8_attention 148);
-// 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 90 us (344); 8 beams behind 131072 tokens,
-// 4 heads, INT8, 135 MB: 61 us (188); 4 beams behind 1472: 11 us (16.5).  Where little is in common
-// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 27 us (19).
+// of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 63 us (kv8_attention 148);
+// 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 92 us (344); 8 beams behind 131072 tokens,
+// 4 heads, INT8, 135 MB: 62 us (188); 4 beams behind 1472: 11 us (16.5).  Where little is in common
+// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 27.5 us (19).
 //
 // DRAM is at 30 % in the first launch, issue at 36 %.  What bounds it is the chain of a tile from S by P
 // to the next: in the first case (an earlier form, 67 us) 46.8 of a keys' warp's 73.6 thousand cycles were its own,
