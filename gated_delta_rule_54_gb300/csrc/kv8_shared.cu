@@ -17,9 +17,9 @@
 // queries.  E4M3 codes of K are an operand as they are, q being the sum of two 8-bit numbers.
 //
 // A score is taken against its column's references (the largest s, and s + log2 of V's scale,
-// which is one for 16 lanes) as they are; where one outgrows them by 2^8, which fp16 and the
-// sums have the room for, the columns that did get new ones from their maxima and the tile is done
-// again.  Each column decides for itself, so a row's result does not depend on the rows
+// which is one for 16 lanes) as they are.  Where P, which fp16 has to hold, outgrows them by 2^8, or where the
+// second has been missing (V scales of 0 give none), the columns concerned get new ones from their maxima
+// and the tile is done again.  Each column decides for itself, so a row's result does not depend on the rows
 // beside it; nor on its place, where a group's query rows of a K/V head fit one block of 64.  (Blocks lie
 // at different places of the line, where CTAs' shares cut their keys differently.)
 //
@@ -433,11 +433,12 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
       }
       units_sync<L::soft * 32>();  // the columns' limits and factors
       float my_fac[KC];  // (of the columns that a lane does for its half-warp)
+      int my_lim[KC];
       unsigned least_u = 0x7fffffff;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         const int col = c0 + 16 * c + l16;
-        my_fac[c] = s_fac[col];
+        my_fac[c] = s_fac[col], my_lim[c] = s_lim[col];
         if (col < here) least_u = min(least_u, (unsigned)s_lim[col]);
       }
       const int least = (int)__reduce_min_sync(0xffffffffu, least_u);
@@ -475,14 +476,18 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
 #pragma unroll
         for (int c = 0; c < KC; ++c) by_k[16 * c + l16] = my_fac[c] * sc.x;
         for (int again = 0;; ++again) {
+          // A column that has seen V scales of 0 only has no reference for s + log2 of V's scale, and gets
+          // one with the first other scale it sees.  (P would not tell: without a reference it is of any size.)
+          uint32_t start = 0;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const float mv = s_mv[unit][16 * c + l16], um = neg[16 * c + l16];
+            if (mv == -INFINITY && sc.y > -INFINITY && j0 + (key & ~15) < my_lim[c]) start |= 1u << (16 * c + l16);
             // (not 0, so that a score too large shows in P whatever V's scale)
             ratio[16 * c + l16] = um == INFINITY ? 1.f : fmaxf(ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f)), 1.17549435e-38f);
           }
           __syncwarp();
-          bool over = false;
+          bool over = start != 0;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             float v[16];
@@ -511,12 +516,12 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
             const uint32_t most = max2(max2(max2(pk[0], pk[1]), max2(pk[2], pk[3])), max2(max2(pk[4], pk[5]), max2(pk[6], pk[7])));
             over |= (most & 0xffffu) > 0x5c00u || most >> 16 > 0x5c00u;  // of numbers >= 0: above 256
           }
-          // Does a score outgrow its column's references by 2^8?  (fp16 and the sums have the room for
-          // that.)  Then columns that do get new ones, from their maxima, and it goes once more; what is too
-          // large after that is no number.  Only columns with a P too large of their own: another's scores may
-          // have outgrown theirs where V's scale is small, and would move or not as its neighbours do.
+          // Does a column need other references?  (fp16 and the sums have the room for 2^8.)  Then it gets
+          // them from its maxima, and the tile goes once more; what is too large after that is no number.  Only
+          // columns with a need of their own: another's scores may have outgrown theirs where V's scale is
+          // small, and would move or not as its neighbours do.
           if (again || !unit_any(unit, over)) break;
-          uint32_t too = 0;
+          uint32_t too = start;
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll

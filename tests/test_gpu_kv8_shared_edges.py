@@ -1,0 +1,117 @@
+"""GPU: corners of the attention over shared tokens, on lines of several tiles for each CTA.
+
+Tolerances are those that test_gpu_kv8_shared.py derives.  A line has more tiles than any GPU of this kind has
+SMs, so that every CTA goes through some tiles one after the other and carries what it has from one to the
+next: two tiles at least, and with up to 16 query rows, where tiles go in turn to two sets, four."""
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_54_gb300 import kv8_attention_shared, load
+from oracle import serve as ref
+from test_gpu_kv8_shared import _check, _cuda
+
+pytestmark = pytest.mark.gpu
+
+SMS = 152
+# query rows of a K/V head as rows x query heads, which decide between 16, 32 and 64 of a block; 64-wide blocks also two
+FORMS = [("e4m3", 128, 64, 4, 4), ("int8", 64, 16, 4, 3), ("int8", 128, 128, 2, 8), ("e4m3", 64, 32, 3, 5),
+         ("e4m3", 128, 16, 8, 4), ("int8", 64, 64, 10, 3), ("int8", 128, 32, 8, 4), ("e4m3", 64, 128, 30, 1),
+         ("e4m3", 128, 128, 16, 4), ("int8", 64, 32, 9, 5), ("int8", 128, 16, 11, 4), ("e4m3", 64, 64, 16, 4),
+         ("e4m3", 128, 32, 18, 4), ("int8", 64, 128, 13, 8)]
+
+
+class Line:
+    """One group whose first tokens are tiles of 128 keys, the same for all rows, with a few tokens of each row's own."""
+
+    def __init__(self, seed, mode, dim, page, beams, group, tokens=1, ragged=0):
+        self.mode, self.dim, self.page, self.beams, self.group, self.heads = mode, dim, page, beams, group, 8
+        rows = beams * group * tokens
+        self.tiles = 80 if rows <= 16 else 48
+        assert self.heads * self.tiles > (4 if rows <= 16 else 2) * SMS
+        self.rng = np.random.default_rng(seed)
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.common = self.tiles * 128 - ragged
+        self.lens = self.common + 20 + 7 * np.arange(beams) % 50 + tokens
+        first, own = self.tiles * 128 // page, -(-int(self.lens.max()) // page) - self.common // page + 1
+        pages = first + beams * own
+        ids = self.rng.permutation(pages).astype(np.int32)
+        self.table = np.full((beams, first + own), -1, np.int32)
+        self.table[:, :first] = ids[:first]
+        whole = self.common // page
+        for r in range(beams):
+            use = slice(first + r * own, first + (r + 1) * own)
+            self.table[r, whole:whole + own] = ids[use]
+            if r == 0:                                       # (the last page in common, where it is not whole)
+                self.table[0, whole:first], self.table[0, first:] = ids[whole:first], ids[use][:self.table.shape[1] - first]
+        # scores of a few units; dim 0 is for what a test adds to them
+        self.q = torch.randn(beams, tokens, self.heads * group, dim, generator=self.gen, device="cuda")
+        self.q *= 0.5
+        self.q[..., 0] = 8.0
+        self.q = self.q.to(torch.bfloat16)
+        self.x = torch.randn(2, pages, self.heads, page, dim, generator=self.gen, device="cuda")
+        self.x[0, ..., 0] = 0
+        self.factor = torch.ones(pages, self.heads, device="cuda")  # of V's scales
+
+    def of(self, per_tile):
+        """[tiles, heads] as [pages of these, heads], in the table's order."""
+        return np.repeat(per_tile, 128 // self.page, 0), torch.from_numpy(self.table[0, :self.tiles * 128 // self.page].astype(np.int64)).cuda()
+
+    def levels(self, log2):
+        """Adds to the scores of tile t for head h, in powers of two."""
+        x, ids = self.of(log2)
+        c = self.dim ** -0.5 * 1.4426950408889634 * 8.0
+        self.x[0, ids, ..., 0] = torch.from_numpy((x / c).astype(np.float32)).cuda()[..., None]
+
+    def v_scales(self, by):
+        x, ids = self.of(by)
+        self.factor[ids] = torch.from_numpy(x.astype(np.float32)).cuda()
+
+    def cache(self):
+        s = self.x.abs().amax((-2, -1)) / ref.CODE_MAX[self.mode]
+        u = self.x / s.clamp(min=1e-37)[..., None, None]
+        if self.mode == "e4m3":
+            codes = u.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        else:
+            codes = u.round().clamp(-127, 127).to(torch.int8).view(torch.uint8)
+        s[1] *= self.factor
+        return codes.contiguous(), s.contiguous()
+
+    def run(self, codes, scales, q=None, table=None, lens=None):
+        t, n, p = _cuda(self.table if table is None else table, (self.lens if lens is None else lens).astype(np.int32),
+                        np.array([self.common], np.int32))
+        got = kv8_attention_shared(self.q if q is None else q, codes, scales, t, n, p, self.beams, mode=self.mode, need_lse=True)
+        assert load().gdn_device_error(0) == 0
+        return got
+
+    def check(self, got, codes, scales, table=None, lens=None):
+        """Some rows, the first among them."""
+        rows = sorted({0, self.beams // 2, self.beams - 1})
+        table, lens = (self.table if table is None else table)[rows], (self.lens if lens is None else lens)[rows]
+        _check([x[rows] for x in got], self.q[rows], codes.cpu().numpy(), scales.cpu().numpy(), table, lens, [self.common], len(rows),
+               self.mode, self.dim ** -0.5)
+
+    def alone(self, got, codes, scales):
+        """Bits of every other row are the same beside rows of any other kind."""
+        for change in (float("nan"), -30.0):
+            q = self.q.clone()
+            q[1::2] *= change
+            o, lse = self.run(codes, scales, q)
+            assert torch.equal(o[::2], got[0][::2]) and torch.equal(lse[::2], got[1][::2]), change
+
+
+# ---- V scales of 0 -----------------------------------------------------
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS)
+def test_tiles_whose_v_is_zero(mode, dim, page, beams, group):
+    """V of whole tiles is 0, with the scale 0 that append gives it: two of four, so that a CTA's share, and each set of
+    tiles in turn, begins with such a tile and goes on with others."""
+    for phase in range(4):
+        a = Line(40 + phase, mode, dim, page, beams, group)
+        t = (np.arange(a.tiles)[:, None] + np.arange(a.heads)) % 4
+        a.v_scales(np.where((t == phase) | (t == (phase + 1) % 4), 0.0, 1.0))
+        codes, scales = a.cache()
+        codes[1][(scales[1] == 0)] = 0
+        got = a.run(codes, scales)
+        a.check(got, codes, scales)
+        if phase == 0:
+            a.alone(got, codes, scales)
