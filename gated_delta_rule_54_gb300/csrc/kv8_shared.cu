@@ -288,6 +288,14 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
   return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
+// The same of V, where bytes that are no number become 448, the largest.  Such bytes stand where no token
+// is, and in blocks whose scale is no number, whose keys have a weight of 0 (and not of NaN) for the
+// queries that do not see them: 0 times any number is 0.
+__device__ __forceinline__ uint32_t v_half2_of(uint32_t codes) {
+  const uint32_t x = half2_of(codes);
+  const __half2 y = __hmin2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x5f00)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
 
 template <int MODE, int DIM, int CW>
 __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(const __grid_constant__ SharedArgs a) {
@@ -305,7 +313,6 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
   __shared__ __align__(8) uint64_t sfull[2 * G], sfree[2 * G], pready[G], odone[G], qready;  // of S by buffer, by set
   __shared__ float2 meta[16][8];  // [tile]: per 16 keys K scale, log2 of V scale
   __shared__ int valid[16];       // bit c: they have a page
-  __shared__ int2 vinfo[16];      // the tile's tokens, and the same for those who have V
   __shared__ __align__(16) int s_lim[CW];    // keys that a column sees
   __shared__ __align__(16) float s_fac[CW];  // factor of a column's scores
   // of a unit's column: references of s and of s + log2 of V's scale; -m; sum; factor of its
@@ -682,7 +689,6 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
       if (!all_wait((is_k ? kin : vin) + in, n / R::raws & 1)) break;
       const unsigned char* from = smem + (is_k ? R::k : R::v) + in * R::raw + from0;
       unsigned char* to = smem + (is_k ? R::kt : R::vt) + out * R::tile;
-      const int2 what = vinfo[n & 15];
       if (!all_wait((is_k ? kfree : vfree) + out, (n / outs & 1) ^ 1)) break;
       constexpr int kAt = 4;
 #pragma unroll 1
@@ -690,20 +696,12 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
         uint4 u[kAt];
 #pragma unroll
         for (int e = 0; e < kAt; ++e) u[e] = *reinterpret_cast<const uint4*>(from + (e0 + e) * kStep * DIM);
-        if (F8 && (what.x < kKeys || what.y != 255)) {
-          // E4M3 bytes that are no number may stand where no token is
-#pragma unroll
-          for (int e = 0; e < kAt; ++e) {
-            const int row = row0c + (e0 + e) * kStep;
-            if (row >= what.x || !(what.y >> (row >> 4) & 1)) u[e] = make_uint4(0, 0, 0, 0);
-          }
-        }
 #pragma unroll
         for (int e = 0; e < kAt; ++e) {
           uint4 lo, hi;
           if constexpr (F8) {
-            lo.x = half2_of(u[e].x), lo.y = half2_of(u[e].x >> 16), lo.z = half2_of(u[e].y), lo.w = half2_of(u[e].y >> 16);
-            hi.x = half2_of(u[e].z), hi.y = half2_of(u[e].z >> 16), hi.z = half2_of(u[e].w), hi.w = half2_of(u[e].w >> 16);
+            lo.x = v_half2_of(u[e].x), lo.y = v_half2_of(u[e].x >> 16), lo.z = v_half2_of(u[e].y), lo.w = v_half2_of(u[e].y >> 16);
+            hi.x = v_half2_of(u[e].z), hi.y = v_half2_of(u[e].z >> 16), hi.z = v_half2_of(u[e].w), hi.w = v_half2_of(u[e].w >> 16);
           } else {
             kv8_half2<MODE>(u[e].x, lo.x, lo.y);
             kv8_half2<MODE>(u[e].y, lo.z, lo.w);
@@ -758,7 +756,7 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           tma_load_3d(smem + (is_v ? R::v : R::k) + b * R::raw + ((lane & (boxes - 1)) << p.shift) * DIM, &a.map, 0, 0,
                       (int)((is_v * p.pages + id) * p.heads + h), &in[b]);
         issued = n + 1;
-        {
+        if (!is_v) {
           // 16 keys c lie in page c >> (log2 of 16ths of a page) of the tile
           const int from = (at << shift) + ((lane * 16 >> p.shift) & (boxes - 1));
           const float k1 = __shfl_sync(0xffffffffu, sc.x, from), v1 = __shfl_sync(0xffffffffu, sc.y, from);
@@ -766,9 +764,8 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           const unsigned bits = __ballot_sync(0xffffffffu, there && lane < 8);
           // (this buffer of codes is free, so its last tile is multiplied, or its fp16 form waits for
           // that of the tile before: tiles 16 back have been through everything)
-          if (lane < 8 && !is_v) meta[n & 15][lane] = there ? kv8_scales(k1, v1) : make_float2(0.f, -INFINITY);
-          if (lane == 0 && !is_v) valid[n & 15] = (int)bits;
-          if (lane == 0 && is_v) vinfo[n & 15] = make_int2((int)min((int64_t)kKeys, w.common - (int64_t)(w.t + i) * kKeys), (int)bits);
+          if (lane < 8) meta[n & 15][lane] = there ? kv8_scales(k1, v1) : make_float2(0.f, -INFINITY);
+          if (lane == 0) valid[n & 15] = (int)bits;
         }
         const unsigned bytes = __popc(__ballot_sync(0xffffffffu, have && now)) * (DIM << p.shift);
         __syncwarp();
@@ -911,10 +908,12 @@ struct Rows {
 #pragma unroll
       for (int e = 0; e < 2; ++e) l[b][e] = 0.f, m[b][e] = mv[b][e] = -INFINITY;
   }
-  // Four codes of one key (two of each of two) as fp16.
+  // Four codes of a key of K, or two of each of two of V, as fp16.
+  template <bool OF_V>
   static __device__ __forceinline__ void two(uint32_t w, uint32_t& first, uint32_t& second) {
-    if constexpr (F8) first = half2_of(w), second = half2_of(w >> 16);
-    else kv8_half2<MODE>(w, first, second);
+    if constexpr (!F8) kv8_half2<MODE>(w, first, second);
+    else if constexpr (OF_V) first = v_half2_of(w), second = v_half2_of(w >> 16);
+    else first = half2_of(w), second = half2_of(w >> 16);
   }
   // The products' other operand: eight queries, of which a lane has row g, by step.
   static __device__ __forceinline__ uint2 query_of(uint2 raw, float to) {
@@ -927,7 +926,7 @@ struct Rows {
   // 16 keys from position j0: K of keys g and g + 8, V of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9.
   // part: not every query sees all of them, or they are not all of [from, to) or there.
   template <class Q>
-  __device__ __forceinline__ void step(const uint4 (&kc)[2][KC], V (&vc)[4], const Q& query, float ks, float lv,
+  __device__ __forceinline__ void step(const uint4 (&kc)[2][KC], const V (&vc)[4], const Q& query, float ks, float lv,
                                        bool part, int j0, int from, int to, bool there, int g, int t) {
     float s[NB][4];
 #pragma unroll
@@ -939,8 +938,8 @@ struct Rows {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a[4];
-        two(x[w], a[0], a[2]);
-        two(y[w], a[1], a[3]);
+        two<false>(x[w], a[0], a[2]);
+        two<false>(y[w], a[1], a[3]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint2 q = query(4 * c + w, b);
@@ -966,14 +965,6 @@ struct Rows {
           over |= x > most;
         }
       }
-    if (F8 && part) {
-      // E4M3 bytes that are no number may stand where no token is
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int j = j0 + 2 * t + (x & 1) + 8 * (x >> 1);
-        if (j < from || j >= to || !there) vc[x] = V();
-      }
-    }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -1023,8 +1014,8 @@ struct Rows {
         // of two neighbouring keys a, b: a0 b0 a1 b1 (E4M3), a0 a1 b0 b1 (INT8), then those of 2 and 3
         const uint32_t sel = F8 ? (z ? 0x7362 : 0x5140) : (z ? 0x7632 : 0x5410);
         uint32_t a[4];
-        two(__byte_perm(w[0][i], w[1][i], sel), a[0], a[1]);
-        two(__byte_perm(w[2][i], w[3][i], sel), a[2], a[3]);
+        two<true>(__byte_perm(w[0][i], w[1][i], sel), a[0], a[1]);
+        two<true>(__byte_perm(w[2][i], w[3][i], sel), a[2], a[3]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) mma_f16(o[2 * i + z][b], a, pb[b][0], pb[b][1]);
       }

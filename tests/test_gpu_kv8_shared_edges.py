@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_54_gb300 import kv8_attention_shared, load
+from gated_delta_rule_54_gb300 import kv8_append, kv8_attention_shared, load
 from oracle import serve as ref
 from test_gpu_kv8_shared import _check, _cuda
 
@@ -115,3 +115,82 @@ def test_tiles_whose_v_is_zero(mode, dim, page, beams, group):
         a.check(got, codes, scales)
         if phase == 0:
             a.alone(got, codes, scales)
+
+
+# ---- V codes that are no number ----------------------------------------
+def _random_cache(gen, pages, heads, page, dim, mode):
+    x = torch.randn(2, pages, heads, page, dim, generator=gen, device="cuda")
+    s = x.abs().amax((-2, -1)) / ref.CODE_MAX[mode]
+    u = x / s[..., None, None]
+    if mode == "e4m3":
+        return u.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), s
+    return u.round().clamp(-127, 127).to(torch.int8).view(torch.uint8), s
+
+
+@pytest.mark.parametrize("spoilt", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("mode,dim,page,group", [("e4m3", 128, 64, 1), ("e4m3", 128, 16, 4), ("e4m3", 64, 32, 2), ("e4m3", 64, 16, 3),
+                                                 ("int8", 128, 32, 2), ("int8", 64, 16, 4)])
+def test_a_draft_whose_v_is_no_number(mode, dim, page, group, spoilt):
+    """It, or it and the one before, opens a new page, whose codes and scale append makes of such a V: the drafts before
+    it do not see that page, and are the same to the bit as without it."""
+    gen, heads, tokens = torch.Generator(device="cuda").manual_seed(50), 2, 4
+    opens = [1, 2, 1]                                  # drafts on the new page, by row
+    lens = [6 * page + 1, 5 * page + 2, 9 * page + 1]
+    table = torch.full((3, 10), -1, dtype=torch.int32)
+    table[:, :2], at = torch.tensor([0, 1]), 2         # two pages in common
+    for r, n in enumerate(lens):
+        own = -(-n // page) - 2
+        table[r, 2:2 + own] = torch.arange(at, at + own)
+        at += own
+    codes, scales = _random_cache(gen, at, heads, page, dim, mode)
+    table, n, p = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.tensor([2 * page], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(3, tokens, heads, dim, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(3, tokens, heads * group, dim, generator=gen, device="cuda").to(torch.bfloat16)
+    got = []
+    for bad in (False, True):
+        if bad:
+            v[:, tokens - 1, 1, 5] = spoilt
+        c, s = codes.clone(), scales.clone()
+        kv8_append(k, v, c, s, table, n - tokens, mode=mode)
+        got.append(kv8_attention_shared(q, c, s, table, n, p, 3, mode=mode, need_lse=True))
+    (o, lse), (o2, lse2) = got
+    lost = torch.zeros(3, tokens, heads * group, dtype=torch.bool, device="cuda")
+    for r, x in enumerate(opens):
+        lost[r, tokens - x:, group:] = True
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert torch.equal(torch.isnan(o2), lost[..., None].expand_as(o2)) and torch.equal(torch.isnan(lse2), lost)
+    assert torch.equal(o2[~lost], o[~lost]) and torch.equal(lse2[~lost], lse[~lost])
+
+
+@pytest.mark.parametrize("spoilt", [float("nan"), float("inf")])
+@pytest.mark.parametrize("mode,dim,page,beams,group", [("e4m3", 128, 64, 4, 4), ("e4m3", 64, 16, 4, 3), ("e4m3", 128, 32, 8, 4),
+                                                       ("e4m3", 64, 64, 10, 3), ("e4m3", 128, 16, 16, 4), ("e4m3", 64, 32, 18, 4),
+                                                       ("int8", 128, 16, 8, 4), ("int8", 64, 32, 4, 4)])
+def test_tokens_in_common_whose_v_is_no_number(mode, dim, page, beams, group, spoilt):
+    """Rows that end before such a token's page, though in its tile, are the same to the bit as without it."""
+    gen, heads = torch.Generator(device="cuda").manual_seed(51), 2
+    common, bad_at = 1400, 128 * 7 + page              # (a page that is not its tile's first one, where it has more)
+    cols = -(-common // page) + 2
+    table = torch.arange(cols, dtype=torch.int32).repeat(beams, 1)
+    table[:, common // page:] = cols + torch.arange(beams * (cols - common // page), dtype=torch.int32).view(beams, -1)
+    table[0, common // page:] = torch.arange(common // page, cols)
+    codes, scales = _random_cache(gen, int(table.max()) + 1, heads, page, dim, mode)
+    short = torch.arange(beams) % 2 == 1
+    n = torch.where(short, bad_at - torch.arange(beams) % 3 * 5, common + 9).int().cuda()
+    p = torch.tensor([common], dtype=torch.int32, device="cuda")
+    table = table.cuda()
+    q = torch.randn(beams, 1, heads * group, dim, generator=gen, device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn(1, page, heads, dim, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    got, first = [], torch.tensor([bad_at], dtype=torch.int32, device="cuda")
+    for bad in (False, True):
+        if bad:
+            v[0, page // 2, 0, 3] = spoilt
+        c, s = codes.clone(), scales.clone()
+        kv8_append(k, v, c, s, table[:1].contiguous(), first, mode=mode)
+        got.append(kv8_attention_shared(q, c, s, table, n, p, beams, mode=mode, need_lse=True))
+    (o, lse), (o2, lse2) = got
+    lost = torch.zeros(beams, 1, heads * group, dtype=torch.bool, device="cuda")
+    lost[~short.cuda(), :, :group] = True
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert torch.equal(torch.isnan(o2), lost[..., None].expand_as(o2)) and torch.equal(torch.isnan(lse2), lost)
+    assert torch.equal(o2[~lost], o[~lost]) and torch.equal(lse2[~lost], lse[~lost])
