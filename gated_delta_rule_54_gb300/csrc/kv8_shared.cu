@@ -17,11 +17,12 @@
 // queries.  E4M3 codes of K are an operand as they are, q being the sum of two 8-bit numbers.
 //
 // A score is taken against its column's references (the largest s, and s + log2 of V's scale,
-// which is one for 16 lanes) as they are.  Where P, which fp16 has to hold, outgrows them by 2^8, or where the
-// second has been missing (V scales of 0 give none), the columns concerned get new ones from their maxima
-// and the tile is done again.  Each column decides for itself, so a row's result does not depend on the rows
-// beside it; nor on its place, where a group's query rows of a K/V head fit one block of 64.  (Blocks lie
-// at different places of the line, where CTAs' shares cut their keys differently.)
+// which is one for 16 lanes) as they are.  Where P, which fp16 has to hold, outgrows them by 2^8, where the
+// second has been missing (V scales of 0 give none), or where V's scale is so small that a score outgrows the
+// first by 2^60 unseen, the columns concerned get new ones from their maxima and the tile is done
+// again.  Each column decides for itself, so a row's result does not depend on the rows beside it; nor on
+// its place, where a group's query rows of a K/V head fit one block of 64.  (Blocks lie at different places of
+// the line, where CTAs' shares cut their keys differently.)
 //
 // A row's own tokens.  A CTA takes 8 (or 16) query rows of a (row, K/V head): its warps go through
 // 16 keys at a time from registers, again with the keys, and the dims, as the long side of
@@ -297,6 +298,10 @@ __device__ __forceinline__ uint32_t v_half2_of(uint32_t codes) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Where V's scale, against its reference, is below this P does not tell whether a score outgrows its own, and the
+// exponential has to: above it one of 2^60 gives a P of 2^8 at least.  So the sums, of less than 2^31 keys, stay below 2^100.
+constexpr float kLittle = 0x1p-52f;
+
 template <int MODE, int DIM, int CW>
 __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(const __grid_constant__ SharedArgs a) {
   using R = Room<MODE, DIM, CW>;
@@ -486,15 +491,18 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           // A column that has seen V scales of 0 only has no reference for s + log2 of V's scale, and gets
           // one with the first other scale it sees.  (P would not tell: without a reference it is of any size.)
           uint32_t start = 0;
+          bool little = false;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const float mv = s_mv[unit][16 * c + l16], um = neg[16 * c + l16];
-            if (mv == -INFINITY && sc.y > -INFINITY && j0 + (key & ~15) < my_lim[c]) start |= 1u << (16 * c + l16);
-            // (not 0, so that a score too large shows in P whatever V's scale)
-            ratio[16 * c + l16] = um == INFINITY ? 1.f : fmaxf(ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f)), 1.17549435e-38f);
+            const bool sees = j0 + (key & ~15) < my_lim[c];
+            if (mv == -INFINITY && sc.y > -INFINITY && sees) start |= 1u << (16 * c + l16);
+            const float by = um == INFINITY ? 1.f : ex2_approx_f(fminf(sc.y - um - (mv == -INFINITY ? 0.f : mv), 126.f));
+            ratio[16 * c + l16] = by, little |= by < kLittle && sees;
           }
           __syncwarp();
-          bool over = start != 0;
+          // (tiles with such scales are looked at below, which tells who needs what; they are few)
+          bool over = start != 0 || (little && (valid[slot] >> (key >> 4) & 1));
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             float v[16];
@@ -529,6 +537,10 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           // small, and would move or not as its neighbours do.
           if (again || !unit_any(unit, over)) break;
           uint32_t too = start;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < KC; ++c) ratio[16 * c + l16] = fmaxf(ratio[16 * c + l16], kLittle);
+          __syncwarp();
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll

@@ -194,3 +194,38 @@ def test_tokens_in_common_whose_v_is_no_number(mode, dim, page, beams, group, sp
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
     assert torch.equal(torch.isnan(o2), lost[..., None].expand_as(o2)) and torch.equal(torch.isnan(lse2), lost)
     assert torch.equal(o2[~lost], o[~lost]) and torch.equal(lse2[~lost], lse[~lost])
+
+
+# ---- scores that outgrow earlier ones where V's scale is little --------
+@pytest.mark.parametrize("by", [0.0, 2.0 ** -120, 2.0 ** -75])
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS[:8:2] + FORMS[9::2])
+def test_scores_that_rise_where_v_is_little(mode, dim, page, beams, group, by):
+    """One tile of four lies 2^124 above the others, and has a V scale that does not show it; the last tiles' V does."""
+    for phase in (0, 2):
+        a = Line(60 + phase, mode, dim, page, beams, group)
+        t = (np.arange(a.tiles)[:, None] + np.arange(a.heads)) % 4
+        late = (np.arange(a.tiles) >= a.tiles - 3)[:, None]
+        a.levels(np.where((t == phase) | late, np.where(late, 122.0, 124.0), 0.0))
+        a.v_scales(np.where((t == phase) & ~late, by, 1.0))
+        a.q[1::4, ..., 0] = 4.0                        # (half of all that, for other rows)
+        codes, scales = a.cache()
+        got = a.run(codes, scales)
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+        a.check(got, codes, scales)
+        if phase == 0:
+            a.alone(got, codes, scales)
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS[:13:3] + FORMS[1::6])
+def test_scores_and_v_scales_of_all_sizes(mode, dim, page, beams, group, seed):
+    """Any of them after any other, by tile and head."""
+    a = Line(70 + seed, mode, dim, page, beams, group)
+    shape = (a.tiles, a.heads)
+    a.levels(a.rng.choice([0.0, 0.0, 40.0, 90.0, 124.0, 127.0], shape) * a.rng.choice([1.0, -1.0, 2.0], (1, a.heads)))
+    a.v_scales(a.rng.choice([0.0, 0.0, 2.0 ** -135, 2.0 ** -110, 2.0 ** -60, 1.0, 2.0 ** 60], shape))
+    a.q[1::3, ..., 0] = 6.0
+    codes, scales = a.cache()
+    got = a.run(codes, scales)
+    a.check(got, codes, scales)
+    a.alone(got, codes, scales)
