@@ -574,6 +574,8 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
               float nm = -INFINITY, nv = -INFINITY;
 #pragma unroll
               for (int q = 0; q < 4; ++q) nm = fmaxf(nm, s_red[unit][q][c].x), nv = fmaxf(nv, s_red[unit][q][c].y);
+              // (scores that are all below fp32's range have a weight of 0, for which the reference has to be a number)
+              nm = fmaxf(nm, -3.402823466e38f);
               const float m = s_m[unit][c], mv = s_mv[unit][c];
               float by = 1.f, by_o = 1.f;
               if ((moves >> c & 1) && nm > m + 8.f) by = ex2_approx_f(m - nm), s_m[unit][c] = nm, neg[c] = -nm;

@@ -229,3 +229,27 @@ def test_scores_and_v_scales_of_all_sizes(mode, dim, page, beams, group, seed):
     got = a.run(codes, scales)
     a.check(got, codes, scales)
     a.alone(got, codes, scales)
+
+
+# ---- scores below what 32 bits hold ------------------------------------
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS[:13:2])
+def test_scores_below_fp32s_range(mode, dim, page, beams, group):
+    """Such a key has a weight of 0: the result is, to the bit, that of a table without its page, in which a
+    CTA's share may begin, or consist, or all that the group has."""
+    a = Line(80, mode, dim, page, beams, group)
+    a.q[..., 0] = 64.0
+    clean = a.cache()
+    tile = np.arange(a.tiles)
+    for far in ((tile % 4 == 0) | (tile % 4 == 3), tile % 8 < 6, tile >= 0):
+        codes, scales = (x.clone() for x in clean)
+        x, ids = a.of(far)
+        ids = ids[torch.from_numpy(x).cuda()]
+        codes[0, ids] = 0
+        codes[0, ids, ..., 0] = 0xfe if mode == "e4m3" else 0x81     # -448, -127
+        scales[0, ids] = 3e38 / ref.CODE_MAX[mode]
+        got = a.run(codes, scales)
+        table = a.table.copy()
+        table[:, :len(x)][:, x] = -1
+        want = a.run(codes, scales, table=table)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        a.check(want, codes, scales, table)
