@@ -253,3 +253,48 @@ def test_scores_below_fp32s_range(mode, dim, page, beams, group):
         want = a.run(codes, scales, table=table)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         a.check(want, codes, scales, table)
+
+
+# ---- what the other tests have, on long lines --------------------------
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS)
+def test_long_lines(mode, dim, page, beams, group, tokens):
+    """Pages that are missing, an end inside a page with bytes that are no numbers behind it, uneven V scales, rows that
+    end before the group's tokens do, several queries to a row."""
+    a = Line(90 + tokens, mode, dim, page, beams, group, tokens, ragged=37)
+    a.v_scales(np.exp2(a.rng.integers(-12, 3, (a.tiles, a.heads)).astype(float)) * (a.rng.random((a.tiles, a.heads)) > 0.1))
+    codes, scales = a.cache()
+    table, lens = a.table.copy(), a.lens.copy()
+    holes = a.rng.choice(a.common // page, 9, replace=False)
+    table[0, holes[:5]], table[0, holes[5:]] = -1, len(scales[0]) + 3
+    if beams > 1:
+        lens[beams - 1] = a.common - 500
+    if beams // 2 > 0 and beams // 2 != beams - 1:
+        lens[beams // 2] = tokens - 1                  # a query before the row's begin
+    for r, n in enumerate(lens):
+        if n % page and n >= a.common:
+            codes[:, int(table[r, n // page]), :, n % page:] = 0x7f if mode == "e4m3" else 0x80
+    got = a.run(codes, scales, table=table, lens=lens)
+    a.check(got, codes, scales, table, lens)
+    o, lse = a.run(codes, scales, table=table, lens=lens)
+    assert torch.equal(o, got[0]) and torch.equal(lse, got[1])
+
+
+@pytest.mark.parametrize("power", [-127.5, -120, 110])
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS[::5])
+def test_v_scales_near_the_ends_of_their_range(mode, dim, page, beams, group, power):
+    a = Line(95, mode, dim, page, beams, group)
+    codes, scales = a.cache()
+    scales[1] = 2.0 ** power
+    a.check(a.run(codes, scales), codes, scales)
+
+
+@pytest.mark.parametrize("power", [-110, 110])
+@pytest.mark.parametrize("mode,dim,page,beams,group", FORMS[2::5])
+def test_q_near_the_ends_of_its_range(mode, dim, page, beams, group, power):
+    """Scores of ordinary size from a q and a K far from 1."""
+    a = Line(96, mode, dim, page, beams, group)
+    a.q = (a.q.float() * 2.0 ** power).to(torch.bfloat16)
+    codes, scales = a.cache()
+    scales[0] *= 2.0 ** -power
+    a.check(a.run(codes, scales), codes, scales)
