@@ -21,12 +21,25 @@ _i32, _u8, _f32, _bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _MODES = {k: v for k, v in QDQ_MODES.items() if v}
 _XTYPES = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"], torch.float32: DTYPES["fp32"]}
-# the problems' structures as the C compiler lays them out
-_KV8 = struct.Struct("@3q10ifP6q").pack
-_POOL = struct.Struct("@2q5i0q").pack
-_BEAM = struct.Struct("@2q5i0q").pack
-_ROTARY = struct.Struct("@4q2i").pack
-_LOGITS = struct.Struct("@4q3i0q").pack
+
+
+def _structure(layout):
+    """Packs a problem as the C compiler lays it out."""
+    pack = struct.Struct(layout).pack
+
+    def packed(*fields):
+        try:
+            return pack(*fields)
+        except (struct.error, OverflowError) as e:
+            raise ValueError("a size or number of the call does not fit its C structure: %s" % e) from None
+    return packed
+
+
+_KV8 = _structure("@3q10ifP6q")
+_POOL = _structure("@2q5i0q")
+_BEAM = _structure("@2q5i0q")
+_ROTARY = _structure("@4q2i")
+_LOGITS = _structure("@4q3i0q")
 _TOO_SMALL = -5  # GDN_ERR_WORKSPACE_TOO_SMALL
 _contiguous = torch.contiguous_format
 _shared_bytes = {}  # of the workspace, by the problem's sizes
