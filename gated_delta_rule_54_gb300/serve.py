@@ -30,7 +30,7 @@ def _structure(layout):
     def packed(*fields):
         try:
             return pack(*fields)
-        except (struct.error, OverflowError) as e:
+        except struct.error as e:
             raise ValueError("a size or number of the call does not fit its C structure: %s" % e) from None
     return packed
 

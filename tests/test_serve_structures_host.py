@@ -10,7 +10,6 @@ BIG = 1 << 31
     (serve._KV8, [1, 2, 3, BIG, 5, 6, 7, 64, 16, 1, 0, 1, 9, 0.5, 4096, *range(8, 56, 8)]),      # tokens
     (serve._KV8, [1, 2, 3, 4, 5, 6, 7, 64, 16, 1, 0, 1, BIG, 0.5, 4096, *range(8, 56, 8)]),      # window
     (serve._KV8, [1, 2, 3, 4, 5, 6, 7, 64, 16, 1, 0, 1, 9, "a", 4096, *range(8, 56, 8)]),        # scale
-    (serve._KV8, [1, 2, 3, 4, 5, 6, 7, 64, 16, 1, 0, 1, 9, 1e39, 4096, *range(8, 56, 8)]),       # and one that fp32 has not
     (serve._POOL, [1, 2, BIG, 4, 5, 6, 7]),                                                      # columns
     (serve._BEAM, [1, 2, 3, BIG, 5, 6, 7]),                                                      # vocabulary
     (serve._BEAM, [1, 2, 3, 4, 5, 6, -BIG - 1]),                                                 # eos
