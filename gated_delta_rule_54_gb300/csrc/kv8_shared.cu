@@ -537,7 +537,6 @@ __global__ void __launch_bounds__(Plan<MODE, CW>::threads, 1) kv8_common_kernel(
           // small, and would move or not as its neighbours do.
           if (again || !unit_any(unit, over)) break;
           uint32_t too = start;
-          __syncwarp();
 #pragma unroll
           for (int c = 0; c < KC; ++c) ratio[16 * c + l16] = fmaxf(ratio[16 * c + l16], kLittle);
           __syncwarp();
