@@ -35,20 +35,25 @@
 // Measured on a GB300 (both launches, replayed): 16 x 8 beams behind 1096 .. 4096 tokens with 90 .. 150
 // of their own, 8 K/V heads of 128, four query heads each, E4M3, 132 MB: 63 us (kv8_attention 148);
 // 64 rows behind 16384 with 24 .. 1024 of their own, 102 MB: 92 us (344); 8 beams behind 131072 tokens,
-// 4 heads, INT8, 135 MB: 62 us (188); 4 beams behind 1472: 11 us (16.5).  Where little is in common
-// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 27.5 us (19).
+// 4 heads, INT8, 135 MB: 62 us (188); 4 beams behind 1472: 11.6 us (16.5).  Where little is in common
+// both launches cost more than they save: 5 x 3 beams of five drafts, 4 MB, 28 us (19).  So do a few rows
+// with many tokens of their own, which one CTA goes through for each row and K/V head: 4 rows x 4 heads with
+// 8000 behind 1024 take 177 us (21), with 2000 27 (17), with 500 12 (14).
 //
-// DRAM is at 30 % in the first launch, issue at 36 %.  What bounds it is the chain of a tile from S by P
-// to the next: in the first case (an earlier form, 67 us) 46.8 of a keys' warp's 73.6 thousand cycles were its own,
-// 2200 for each of 21 tiles, and the rest waits for S and O.  On an earlier form (80 us in the first case,
-// 70 in the third) with parts of the work left out the third took: without conversions 53 us, without
-// the softmax 59, without both 44, and without loads and products as well 30.  Four units of warps
-// instead of two, with 80 registers a thread, spilled and missed the instruction cache 131 times a tile
-// instead of 46: 80, 129 and 78 us.  Two that take whole tiles of 32 columns in turn: 69, 104 and 68.
-// Warp products from rings in shared memory instead of tcgen05, for up to 32 rows: 133 and 124 in the
-// first and the third.
-// A row's own tokens take 9 us of the first case and 23 of the second (latency; products that had the
-// queries as the long side, half of each empty, took 31 and 32 of an earlier form).
+// DRAM is at 30 % in the first launch, issue at 38 %.  What bounds it is the chain of a tile from S by P
+// to the next.  In the first case 30 to 37 of a keys' warp's 65 to 73 thousand cycles are its own, 1500 to 1850
+// for each of 20 tiles; 12 go by before its first scores, 11 to 13 in waits for S, and as many in waits for the
+// product of the tile before, since a set has one buffer of P.  In the second (64 columns) 63 of 102 are its
+// own, 2350 a tile, in the third 56 to 60 of 93.  A tile that is done again takes about half as long again:
+// where V's scale is 0 throughout, 64 rows behind 16384 tokens 102 us beside 67, for a tenth of the pages 75.
+// Earlier forms differ from the present one in more than what is named here.  One of 80 us in the first
+// case and 70 in the third with parts of the work left out took in the third: without conversions 53, without the
+// softmax 59, without both 44, and without loads and products as well 30.  Four units of warps instead of two,
+// with 80 registers a thread, spilled and missed the instruction cache 131 times a tile (46 with two then, 51
+// now): 80, 129 and 78.  Two that take whole tiles of 32 columns in turn: 69, 104 and 68.  Warp products from rings in
+// shared memory instead of tcgen05, for up to 32 rows: 133 and 124 in the first and the third.
+// A row's own tokens took 9 us of the first case and 23 of the second behind the first launch (latency; alone 30
+// and 31 with cold caches; products that had the queries as the long side, half of each empty, 31 and 32).
 #include <cuda.h>
 
 #include <atomic>

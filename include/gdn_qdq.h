@@ -532,8 +532,8 @@ gdn_status gdn_kv8_attention(const gdn_kv8_problem* p, const void* q, const uint
  * (x_2j, x_{2j+1}) where interleaved; with c = cos[t, j], s = sin[t, j]
  *   a' = fl(fl(a c) - fl(b s))     b' = fl(fl(b c) + fl(a s))      in fp32
  * and the other dims stay as they are.  Keys are quantized from these fp32 numbers;
- * q' is rounded to bf16.  Where cos and sin have no row t, c = s = NaN: the queries are
- * NaN there, and the scales of the key blocks that are written.  Which keys and values
+ * q' is rounded to bf16.  Where cos and sin have no row t, c = s = NaN: the dims of the
+ * queries that turn are NaN there, and the scales of the key blocks that are written.  Which keys and values
  * are written is as for gdn_kv8_append.  In a packed call queries of no row are 0,
  * and all those of a row with more than `tokens` tokens are NaN.
  *   q    bf16 [rows, tokens, heads * group, dim] or packed [total, ...], strided
@@ -559,7 +559,9 @@ gdn_status gdn_kv8_append_rotary(const gdn_kv8_problem* p, const gdn_kv8_rotary*
  * the table row of the group's first row, those from there on in the row's own.
  * shared counts tokens; it is cut to what the first row has (0 .. lengths, and the
  * table's columns).  What a query sees, NaNs and infinities, and the fewer bits of
- * the probabilities and of q are as for gdn_kv8_attention.  A row's result does not
+ * the probabilities and of q are as for gdn_kv8_attention.  A row's own tokens are
+ * gone through by one CTA for each K/V head: a few rows with thousands of them are
+ * faster by gdn_kv8_attention.  A row's result does not
  * depend on its group's other rows, but for the tokens of the first; and where
  * beams * tokens * group <= 64 its bits do not depend on its place in the group.
  * Not packed (cu_seqlens NULL: GDN_ERR_INVALID_ARG), no window
